@@ -1,7 +1,8 @@
 """Builds the in-tree CUDA library ``liblocks_gb300.so`` (sm_103a only).
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
-linked into one shared library exporting the C ABI of ``include/locks.h``.
+linked into one shared library exporting the C ABI of ``include/locks.h`` and
+``include/locks_cache.h``.
 Run as ``python -m sparse_kv_page_gb300.build`` or through
 ``__graft_entry__.build()``.
 """
@@ -43,7 +44,7 @@ def _sources() -> List[str]:
 def _fingerprint() -> str:
     h = hashlib.sha256()
     files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
-        glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "locks.h")]
+        glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         with open(f, "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())

@@ -6,7 +6,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "locks_internal.h"
+#include "cache_internal.h"
 
 namespace {
 
@@ -275,6 +275,17 @@ int select_attend_impl(const locks_dims_t* dims, const float* q, const uint16_t*
 }
 
 }  // namespace
+
+// The checks above, for the entry points of the cache operators (api_cache.cu).
+namespace locks {
+int check_dims(const locks_dims_t* d) { return validate_dims(d); }
+int check_workspace(void* ws, size_t bytes, size_t need) { return check_ws(ws, bytes, need); }
+int current_sms() { return num_sms(current_device()); }
+DeviceStatus device_status(void* ws) { return status_of(ws); }
+int scorer_partials_row(const locks_dims_t* d, int sms) {
+    return scorer_grid(d, sms) * slot_warps(d->num_kv_heads, d->num_q_heads / d->num_kv_heads);
+}
+}  // namespace locks
 
 extern "C" {
 

@@ -1,0 +1,111 @@
+// cache_internal.h - launchers of the paged-cache operators (locks_cache.h), and the
+// argument checks of the C ABI that their entry points share with api.cu.
+#pragma once
+
+#include "../../include/locks_cache.h"
+#include "locks_internal.h"
+
+namespace locks {
+
+// ------------------------------------------------- shared argument checks (api.cu)
+int check_dims(const locks_dims_t* d);
+int check_workspace(void* ws, size_t bytes, size_t need);
+int current_sms();                       // SMs of the current device; 0: no device
+DeviceStatus device_status(void* ws);    // with the process's wait limit
+int scorer_partials_row(const locks_dims_t* d, int sms);   // (max, sum exp) pairs per (sequence, query head)
+
+// ------------------------------------------------------------------ launchers
+struct AppendArgs {
+    const void* q;               // nullable, with q_out
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;   // elements per token
+    const int32_t* positions;    // [axes][num_tokens]
+    const int32_t* token_seq;    // nullable
+    const int32_t* cache_index;
+    const int32_t* page_table;
+    const float* q_weight;       // nullable
+    const float* k_weight;       // nullable
+    float eps;
+    void* q_out;
+    uint16_t* k_cache;
+    uint16_t* v_cache;
+    int num_tokens, batch, hq, hkv, max_pages, num_phys;
+    int in_type, q_type;
+    int rot_dim, interleaved;    // rot_dim 0: no rotation
+    float rope_scale;
+    uint64_t turns[64];          // pair i: inv_freq / (2 pi) turns per position, as a fraction of 2^64 (wraps)
+    uint8_t axis[64];
+    DeviceStatus st;
+};
+cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
+
+struct MassArgs {
+    const float* scores;
+    const int32_t* seq_pages;
+    const float* mass;
+    float* mass_out;
+    float decay;
+    int batch, hq, max_pages;
+    const float2* partials;      // [batch][hq][row]
+    int row;
+    DeviceStatus st;
+};
+// Pairs per (sequence, query head) that launch_mass_partials writes.
+int mass_partials_row(int max_pages);
+cudaError_t launch_mass_partials(const MassArgs& a, float2* partials, cudaStream_t stream);
+cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream);
+
+struct EvictArgs {
+    const float* mass;
+    const int32_t* page_table;
+    const int32_t* seq_pages;
+    float* mass_out;
+    int32_t* page_table_out;
+    int32_t* seq_pages_out;
+    int32_t* evicted;
+    int32_t* n_evicted;
+    int batch, max_pages, keep, sink, recent, extra, evict_cap;
+    DeviceStatus st;
+};
+constexpr int kMaxEvictPages = 393216;
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
+}  // namespace locks
+
+namespace locks {
+
+struct PrefixArgs {
+    const void* q;                 // fp32 or bf16 [batch][hq][128]
+    const uint16_t* k_cache;
+    const uint16_t* v_cache;
+    const int32_t* prefix_table;   // [num_groups][max_prefix_pages]
+    const int32_t* prefix_tokens;  // [num_groups]
+    const int32_t* group_start;    // [num_groups + 1]
+    const int32_t* page_table;     // [batch][max_pages]
+    const int32_t* seq_tokens;     // [batch]
+    uint16_t* out;
+    float* lse;                    // nullable
+    int num_groups, max_prefix_pages, batch, hq, hkv, max_pages, num_phys, q_type;
+    // workspace regions (prefix_layout)
+    int64_t* total;                // tiles of the whole call
+    struct PrefixUnit* units;      // [num_groups + batch]
+    float2* part_ml;               // (max, sum) per partial row
+    float* part_o;                 // [partial row][128]
+    DeviceStatus st;
+    CUtensorMap tm_k, tm_v;        // 64 x 16 boxes with 128-byte swizzle (filled by the launcher)
+};
+// A group's prefix or a sequence's own tokens: where its tiles begin on the line of all
+// tiles and its rows on the line of all partial rows.
+struct PrefixUnit {
+    int64_t tile0;
+    int32_t row0, tiles, seq0, num_seqs;
+};
+constexpr int kMaxPrefixCtas = 256;
+struct PrefixLayout {
+    size_t units, ml, o, bytes;    // offsets from the workspace (total at 256)
+};
+PrefixLayout prefix_layout(int batch, int hq, int num_groups);
+cudaError_t launch_prefix(const PrefixArgs& a, int num_sms, cudaStream_t stream);
+
+}  // namespace locks
