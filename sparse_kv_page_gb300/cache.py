@@ -26,12 +26,13 @@ from typing import Optional, Sequence
 import torch
 
 from . import locks as _locks
-from .locks import LocksError, _STATUS, _check, locks_dims_t  # noqa: F401
+from .locks import LocksError, _check, locks_dims_t
 
 LOCKS_BF16, LOCKS_FP16, LOCKS_FP32 = 0, 1, 2
 LOCKS_MAX_AXES = 4
 _TYPES = {torch.bfloat16: LOCKS_BF16, torch.int16: LOCKS_BF16, torch.float16: LOCKS_FP16, torch.float32: LOCKS_FP32}
 _BF16 = (torch.bfloat16, torch.int16)
+_QUERY = (torch.float32,) + _BF16
 
 
 class locks_rope_t(ctypes.Structure):
@@ -66,59 +67,69 @@ def _library() -> ctypes.CDLL:
 
 
 # ----------------------------------------------------------------- arguments
+# These run before every launch, and for a decode step's small calls they are most of the
+# call's time: one chained test per tensor, and its reason found only when it fails.
 
-def _arg(name: str, t: Optional[torch.Tensor], device: torch.device, dtypes, shape) -> Optional[int]:
-    """The address of a contiguous tensor of the given kind and shape (None: null)."""
-    if t is None:
-        return None
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+def _refuse(name: str, t: torch.Tensor, device: int, dtypes, shape) -> None:
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call is on device {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has type {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError("LOCKS buffers must be contiguous")
+    raise ValueError("LOCKS buffers must be contiguous")
+
+
+def _arg(name: str, t: Optional[torch.Tensor], device: int, dtypes, shape) -> Optional[int]:
+    """The address of a contiguous tensor of the given kind and shape (None: null)."""
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, device, dtypes, shape)
     return t.data_ptr()
 
 
-def _ws(t: Optional[torch.Tensor], device: torch.device):
+def _ws(t: Optional[torch.Tensor], device: int):
     if t is None:
         return None, 0
-    if t.device != device:
-        raise ValueError(f"workspace is on {t.device}, the call is on {device}")
-    return _locks._ws(t)
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse("workspace", t, device, (t.dtype,), t.shape)
+    return t.data_ptr(), t.nbytes
 
 
-def _rows(name: str, t: torch.Tensor, device: torch.device, dtype, tokens: int, heads: int):
+def _rows(name: str, t: torch.Tensor, device: int, dtype, tokens: int, heads: int):
     """(address, elements from token to token) of [tokens][heads][128] rows; only the token
     axis may be strided."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has type {t.dtype}, q or k has {dtype}")
-    if t.shape != (tokens, heads, 128):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(tokens, heads, 128)}")
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != 128):
+    if t.get_device() != device or t.dtype != dtype or t.shape != (tokens, heads, 128):
+        _refuse(name, t, device, (dtype,), (tokens, heads, 128))
+    step, head, one = t.stride()
+    if one != 1 or (head != 128 and heads > 1):
         raise ValueError(f"{name}: the heads of a token must lie beside each other")
-    return t.data_ptr(), stride[0] if tokens > 1 else 0
+    return t.data_ptr(), step if tokens > 1 else 0
 
 
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    if device.type != "cuda":
-        raise ValueError(f"{name} takes CUDA tensors, not {device}")
-    lib = _library()
+def _call(name: str, device: int, stream, *args) -> None:
+    if device < 0:
+        raise ValueError(f"{name} takes CUDA tensors")
+    fn = getattr(_lib or _library(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        status = getattr(lib, name)(*args, stream)
+    if torch.cuda.current_device() == device:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            status = getattr(lib, name)(*args, stream)
-    _check(name, status)
+            status = fn(*args, stream)
+    if status != 0:
+        raise LocksError(name, status)
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)   # the same without a Stream object
 
 
 _I32 = (torch.int32,)
@@ -149,8 +160,9 @@ def locks_append_tokens(dims: locks_dims_t, rope: Optional[locks_rope_t], q: Opt
                         eps: float = 1e-6, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """q, k, v: [tokens][heads][128], bf16, fp16 or fp32, the token axis strided as it likes (slices
     of one projection's output). positions int32 [axes][tokens] (or [tokens] for one axis)."""
-    dev, n, hq, hkv = k.device, k.shape[0], dims.num_q_heads, dims.num_kv_heads
-    if k.dtype not in _TYPES:
+    dev, n, hq, hkv = k.get_device(), k.shape[0], dims.num_q_heads, dims.num_kv_heads
+    in_type = _TYPES.get(k.dtype)
+    if in_type is None:
         raise TypeError(f"k has type {k.dtype}")
     kp, ks = _rows("k", k, dev, k.dtype, n, hkv)
     vp, vs = _rows("v", v, dev, k.dtype, n, hkv)
@@ -167,11 +179,11 @@ def locks_append_tokens(dims: locks_dims_t, rope: Optional[locks_rope_t], q: Opt
     cache = (dims.num_phys_pages, hkv, 16, 128)
     ws, nws = _ws(workspace, dev)
     _call("locks_append_tokens", dev, stream, ctypes.byref(dims), ctypes.byref(rope) if rope is not None else None,
-          qp, kp, vp, _TYPES[k.dtype], qs, ks, vs, n, pos, _arg("token_seq", token_seq, dev, _I32, (n,)),
+          qp, kp, vp, in_type, qs, ks, vs, n, pos, _arg("token_seq", token_seq, dev, _I32, (n,)),
           _arg("cache_index", cache_index, dev, _I32, (n,)),
           _arg("page_table", page_table, dev, _I32, (dims.batch, dims.max_pages_per_seq)),
           _arg("q_weight", q_weight, dev, _F32, (128,)), _arg("k_weight", k_weight, dev, _F32, (128,)), eps,
-          _arg("q_out", q_out, dev, (torch.float32,) + _BF16, (n, hq, 128)), qtype,
+          _arg("q_out", q_out, dev, _QUERY, (n, hq, 128)), qtype,
           _arg("k_cache", k_cache, dev, _BF16, cache), _arg("v_cache", v_cache, dev, _BF16, cache), ws, nws)
 
 
@@ -195,12 +207,12 @@ def locks_prefix_attention(dims: locks_dims_t, q: torch.Tensor, k_cache: torch.T
                            seq_tokens: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                            lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """prefix_table None: no prefixes. page_table may be None when dims.max_pages_per_seq is 0."""
-    dev, b, hq = q.device, dims.batch, dims.num_q_heads
+    dev, b, hq = q.get_device(), dims.batch, dims.num_q_heads
     cache = (dims.num_phys_pages, dims.num_kv_heads, 16, 128)
     groups, pages = (0, 0) if prefix_table is None else prefix_table.shape
     ws, nws = _ws(workspace, dev)
     _call("locks_prefix_attention", dev, stream, ctypes.byref(dims),
-          _arg("q", q, dev, (torch.float32,) + _BF16, (b, hq, 128)),
+          _arg("q", q, dev, _QUERY, (b, hq, 128)),
           LOCKS_FP32 if q.dtype == torch.float32 else LOCKS_BF16, _arg("k_cache", k_cache, dev, _BF16, cache),
           _arg("v_cache", v_cache, dev, _BF16, cache),
           _arg("prefix_table", prefix_table, dev, _I32, (groups, pages)),
@@ -228,7 +240,7 @@ def locks_accumulate_mass(dims: locks_dims_t, scores: torch.Tensor, seq_pages: t
                           mass_out: torch.Tensor, workspace: Optional[torch.Tensor] = None, decay: float = 1.0,
                           lse_partials: Optional[torch.Tensor] = None, stream=None) -> None:
     """mass_out may be mass. Without lse_partials the workspace is needed (alloc_mass_workspace)."""
-    dev, b, p = scores.device, dims.batch, dims.max_pages_per_seq
+    dev, b, p = scores.get_device(), dims.batch, dims.max_pages_per_seq
     ws, nws = _ws(workspace, dev)
     partials = None
     if lse_partials is not None:
@@ -246,7 +258,7 @@ def locks_evict_pages(dims: locks_dims_t, mass: torch.Tensor, page_table: torch.
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """The outputs mass_out, page_table_out and seq_pages_out may be the inputs. evicted: int32
     [batch][at least max(1, max_pages_per_seq - keep_pages)]."""
-    dev, b, p = mass.device, dims.batch, dims.max_pages_per_seq
+    dev, b, p = mass.get_device(), dims.batch, dims.max_pages_per_seq
     ws, nws = _ws(workspace, dev)
     cap = evicted.shape[-1]
     _call("locks_evict_pages", dev, stream, ctypes.byref(dims), _arg("mass", mass, dev, _F32, (b, p)),

@@ -11,21 +11,27 @@
 // Work: "units" (a group's prefix, a sequence's own tokens), each an item per kv head and
 // block of 128 rows, each item a run of tiles of 128 tokens. All tiles of the call form one
 // line, split evenly over one CTA per SM whatever the items are; an item cut by a CTA
-// boundary gives one partial (m, l, O) per piece. The line is found on the device from the
+// boundary gives two partials (m, l, O) per piece. The line is found on the device from the
 // token counts, so a captured graph follows them.
 //
-// CTA (12 warps): warp 0 loads, warp 1 issues the products, warps 4-7 and 8-11 are two
-// softmax groups that take alternate tiles, each with its own running maximum, sum and
-// accumulator, so neither waits for the other. Tensor memory: scores of the two groups
-// (2 x 128 columns; the bf16 weights overwrite them) and their accumulators (2 x 128).
-// Shared memory: Q as a bf16 high and low part (64 KB; fp32 queries keep 16 significant
-// bits) and a ring of five 32 KB slots, each a K or a V tile: eight pages of two 64-dim
-// halves, one 2 KB TMA box each.
+// CTA (12 warps): warp 0 loads K and V, warp 1 issues the products, warps 2-3 bring the
+// queries, warps 4-7 and 8-11 are two softmax groups. The CTA's tiles are one stream,
+// whatever pieces they belong to: the scores of tile t + 1 are formed while the groups
+// weigh tile t, group x its 64 tokens x * 64.., each with a running maximum, sum and
+// accumulator of its own, so neither waits for the other, and each leaves a partial of its
+// own. A piece's accumulators are read while the next piece's scores are formed.
+// Tensor memory: two score tiles (2 x 128 columns; the bf16 weights overwrite them) and the
+// groups' accumulators (2 x 128). Shared memory: the queries as a bf16 high part and, for
+// fp32, a low part (32 KB each; 16 significant bits together), and a ring of 32 KB slots,
+// each a K or a V tile: eight pages of two 64-dim halves, one 2 KB TMA box each.
+// Pieces of up to 16 rows (a sequence's own tokens, small groups) take an eighth of the
+// query space each, so their queries come ahead of time; the products read 128 rows all the
+// same, and what the rows behind a piece's own hold reaches no row but theirs.
 //
 // Bound: per 128 x 128 tile the products take 128 * 128 * 128 * (2 + 1) multiply-adds (high
-// and low scores, then the values), 1536 cycles at the SM's 4096 a cycle; its 64 KB take
-// about 2800 cycles at an SM's share of HBM. Up to 128 rows HBM bounds it, above that the
-// tensor cores.
+// and low scores, then the values; one less for bf16 queries), 1536 cycles at the SM's 4096
+// a cycle; its 64 KB take about 2800 cycles at an SM's share of HBM. Up to 128 rows HBM
+// bounds it, above that the tensor cores.
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -42,29 +48,37 @@ constexpr int kTilePages = kTile / kPage;
 constexpr int kHalfBytes = kTile * 128;           // 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kBoxBytes = kPage * 128;
-constexpr int kSlots = 5;
+constexpr int kGroupTokens = kTile / 2;           // of a tile, per softmax group
+constexpr int kNarrow = 16;                       // rows of a piece that takes one query unit
+constexpr int kQueryUnits = kTile / kNarrow;
 constexpr int kThreads = 384;
-constexpr int kSoftmaxThreads = 128;              // per group
+constexpr int kQueryThreads = 64;
 constexpr float kScaleLog2 = kInvSqrtD * kLog2e;  // raw score -> exponent of 2
 constexpr float kRescale = 8.f / kScaleLog2;      // a running maximum may lag by 2^8
 
+// Ring slots: what the queries leave of shared memory.
+template <bool kSplitQ>
+constexpr int kSlots = kSplitQ ? 5 : 6;
+template <bool kSplitQ>
+constexpr int kQueryBytes = (kSplitQ ? 2 : 1) * kTileBytes;
+
 struct Control {
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t scores[2];                           // a group's score tile is in tensor memory
-    uint64_t weights[2];                          // ... its weights are, and its V rows are ready
-    uint64_t queries;                             // Q of the piece is in shared memory
-    uint64_t done;                                // every product of the piece has completed
-    uint64_t joined;                              // both groups' (m, l) of the piece are in ml
-    uint64_t drained;                             // its accumulators and ml have been read
+    uint64_t full[6], empty[6];
+    uint64_t scores[2];                           // a score tile is in tensor memory
+    uint64_t weights[2][2];                       // [group][score tile] its weights are
+    uint64_t values[2];                           // [score tile] their products with V have completed
+    uint64_t q_full[kQueryUnits];                 // a piece's queries are in shared memory
+    uint64_t q_free[kQueryUnits];                 // its last scores have been formed
+    uint64_t last;                                // every product of the CTA has completed
     uint32_t tmem;
     int abort;
-    float2 ml[2][kTile];
 };
-constexpr int kSmemBytes = 2 * kTileBytes + kSlots * kTileBytes + static_cast<int>(sizeof(Control));
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+template <bool kSplitQ>
+constexpr int kSmemBytes = kQueryBytes<kSplitQ> + kSlots<kSplitQ> * kTileBytes + static_cast<int>(sizeof(Control));
+static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024, "shared memory of one CTA");
 
-// Tensor-memory columns.
-__host__ __device__ constexpr uint32_t score_col(int x) { return x * 128; }
+// Tensor-memory columns: score tile b, accumulator of group x.
+__host__ __device__ constexpr uint32_t score_col(int b) { return b * 128; }
 __host__ __device__ constexpr uint32_t acc_col(int x) { return 256 + x * 128; }
 
 // A wait that gives up after the limit, or once another warp of the CTA has.
@@ -189,36 +203,45 @@ struct Piece {                      // a run of tiles of one item
     int tokens, kvh, seq0, row0;    // row r of the block: sequence seq0 + (row0 + r) / g, head kvh * g + (row0 + r) % g
     int rows, tile0, tiles;
     int64_t part;                   // its first partial row
+    uint32_t n;                     // pieces of this CTA before it
+
+    __device__ __forceinline__ bool wide() const { return rows > kNarrow; }
+    // tokens of its tile i
+    __device__ __forceinline__ int valid(int i) const { return min(kTile, tokens - (tile0 + i) * kTile); }
 };
 
 struct Walk {
     int64_t t, t_end;
     Cursor at;
     int first;                      // of the chunk in hand
+    uint32_t pieces;                // so far
     Chunk c;
 };
 
-// Positions the walk at this CTA's first tile; false if it has none.
+// Positions the walk at this CTA's first tile; false if it has none. Calls of up to 32 units
+// know the whole line from their first chunk.
 __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
     const int lane = threadIdx.x & 31;
+    w.at = Cursor{0, 0, 0};
+    w.first = 0;
+    w.pieces = 0;
+    w.c = load_chunk(a, 0, w.at);
     int64_t sum = 0;
-    int bound = 0;
-    for (int u0 = 0; u0 < a.num_groups; u0 += 32) {
+    int bound = w.at.bound;
+    for (int u0 = 32; u0 < a.num_groups; u0 += 32) {
         const int u = u0 + lane;
         const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, bound);
         if (u < a.num_groups) sum += unit_tiles(a, group_unit(a, u, before));
     }
 #pragma unroll 4
-    for (int b = lane; b < a.batch; b += 32) sum += unit_tiles(a, own_unit(a, b));
+    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_tiles(a, own_unit(a, b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum += w.at.tiles;
     const int n = ctas_of(sum, gridDim.x), cta = blockIdx.x;
     if (cta >= n) return false;
     w.t = cta_first(sum, cta, n);
     w.t_end = cta_first(sum, cta + 1, n);
-    w.at = Cursor{0, 0, 0};
-    w.first = 0;
-    w.c = load_chunk(a, 0, w.at);
     return true;
 }
 
@@ -249,311 +272,349 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
     p.row0 = rb * kTile;
     p.rows = min(kTile, rows - p.row0);
     p.part = static_cast<int64_t>(part0) + p.kvh * rows + p.row0 + static_cast<int64_t>(blockIdx.x) * kTile;
+    p.n = w.pieces++;
     w.t += p.tiles;
     return true;
 }
 
-// A piece of n tiles passes through the ring as K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), the
-// order in which the products use it.
-__device__ __forceinline__ void ring_entry(int j, int n, bool& is_v, int& tile) {
-    if (j < 2 && j < n) {
-        is_v = false;
-        tile = j;
-    } else if (j == 2 * n - 1) {
-        is_v = true;
-        tile = n - 1;
-    } else {
-        is_v = (j & 1) == 0;
-        tile = is_v ? (j - 2) / 2 : (j + 1) / 2;
-    }
-}
+// The order of the stream, the same for all roles: K of tile t + 1 comes before V of tile t.
+// Around a wide piece, whose queries need the whole space, V of the tile before comes first:
+// its product must not wait for queries that wait for it.
+__device__ __forceinline__ bool flush_before(const Piece& p, bool before_wide) { return p.wide() || before_wide; }
 
 // ----------------------------------------------------------------------- the loads
 
+template <bool kSplitQ>
 __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl, Walk& w) {
+    constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
     uint32_t seq = 0;
-    bool ok = true;
+    // loads `live` pages of a tile; lanes 0-7 (and 8-15 for the other half) hold their ids
+    auto load = [&](const CUtensorMap* map, int id, int kvh, int live) {
+        const int slot = seq % kN;
+        bool ok = wait_or_abort(&ctl->empty[slot], ((seq / kN) & 1) ^ 1, ctl, a.st);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], live * 2 * kBoxBytes);
+        __syncwarp();
+        if (lane < 2 * kTilePages && (lane & 7) < live) {
+            const int half = lane >> 3;
+            tma_load_2d(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes, map, half * 64,
+                        (id * a.hkv + kvh) * kPage, &ctl->full[slot]);
+        }
+        __syncwarp();
+        ++seq;
+        return true;
+    };
+    bool ok = true, pending = false, before_wide = false;
+    int v_id = 0, v_kvh = 0, v_live = 0;
     Piece p;
     while (ok && walk_next(a, w, p)) {
-        // page ids of four tiles at a time, a page a lane: those of the K tile in hand, and
-        // the four before for V, which runs at most two tiles behind
-        int ids = 0, ids_before = 0, batch = -1;
         const int pages = (p.tokens + kPage - 1) / kPage;
-        for (int j = 0; ok && j < 2 * p.tiles; ++j) {
-            bool is_v;
-            int tile;
-            ring_entry(j, p.tiles, is_v, tile);
-            if (!is_v && (tile >> 2) != batch) {
-                batch = tile >> 2;
-                ids_before = ids;
-                const int page = (p.tile0 + batch * 4) * kTilePages + lane;
+        int ids = 0;                              // of four tiles, a page a lane
+        for (int i = 0; ok && i < p.tiles; ++i) {
+            if ((i & 3) == 0) {
+                const int page = (p.tile0 + i) * kTilePages + lane;
                 ids = page < pages ? p.table[page] : 0;
                 if (ids < 0 || ids >= a.num_phys) {
                     report_error(a.st, LOCKS_ERR_BAD_INDEX);
                     ids = 0;
                 }
             }
-            const int from = (tile & 3) * kTilePages + (lane & 7);
-            const int id_now = __shfl_sync(0xffffffffu, ids, from);
-            const int id_before = __shfl_sync(0xffffffffu, ids_before, from);
-            const int id = (tile >> 2) == batch ? id_now : id_before;
-            const int slot = seq % kSlots;
-            const uint32_t parity = ((seq / kSlots) & 1) ^ 1;
-            ok = wait_or_abort(&ctl->empty[slot], parity, ctl, a.st);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const int live = min(kTilePages, pages - (p.tile0 + tile) * kTilePages);
-            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], live * 2 * kBoxBytes);
-            __syncwarp();
-            if (lane < 2 * kTilePages && (lane & 7) < live) {
-                const int half = lane >> 3;
-                tma_load_2d(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes,
-                            is_v ? &a.tm_v : &a.tm_k, half * 64, (id * a.hkv + p.kvh) * kPage, &ctl->full[slot]);
+            const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kTilePages + (lane & 7));
+            if (pending && i == 0 && flush_before(p, before_wide)) {
+                ok = load(&a.tm_v, v_id, v_kvh, v_live);
+                pending = false;
             }
-            __syncwarp();
-            ++seq;
+            const int live = min(kTilePages, pages - (p.tile0 + i) * kTilePages);
+            ok = ok && load(&a.tm_k, id, p.kvh, live);
+            if (ok && pending) ok = load(&a.tm_v, v_id, v_kvh, v_live);
+            v_id = id;
+            v_kvh = p.kvh;
+            v_live = live;
+            pending = true;
         }
+        before_wide = p.wide();
     }
+    if (ok && pending) ok = load(&a.tm_v, v_id, v_kvh, v_live);
     if (!ok) {
         // giving up: the loads in flight write to this CTA's shared memory, so wait for them
-        for (uint32_t s = seq > kSlots ? seq - kSlots : 0; s < seq; ++s)
-            mbar_wait_bounded(&ctl->full[s % kSlots], (s / kSlots) & 1, a.st.wait_limit_ns);
+        for (uint32_t s = seq > kN ? seq - kN : 0; s < seq; ++s)
+            mbar_wait_bounded(&ctl->full[s % kN], (s / kN) & 1, a.st.wait_limit_ns);
+    }
+}
+
+// --------------------------------------------------------------------- the queries
+
+// Rows of a piece's queries as bf16 high parts (and low parts behind them) in the 128-byte
+// swizzle: a narrow piece in unit p.n % 8 (16 rows), a wide one from the first unit on. Rows
+// past the piece's keep what they held.
+template <bool kSplitQ>
+__device__ __forceinline__ void write_queries(const PrefixArgs& a, const Piece& p, uint8_t* q_s, int tid) {
+    constexpr int kInFlight = kSplitQ ? 4 : 8;
+    const int g = a.hq / a.hkv, chunks = p.rows * 16;
+    q_s += p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128);
+    for (int i0 = tid; i0 < chunks; i0 += kQueryThreads * kInFlight) {
+        uint4 in[kInFlight][kSplitQ ? 2 : 1];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int i = i0 + u * kQueryThreads;
+            if (i >= chunks) break;
+            const int row = p.row0 + (i >> 4);
+            const int64_t src = (static_cast<int64_t>(p.seq0 + row / g) * a.hq + p.kvh * g + row % g) * kD + (i & 15) * 8;
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + src * (kSplitQ ? 4 : 2));
+            in[u][0] = s[0];
+            if (kSplitQ) in[u][kSplitQ ? 1 : 0] = s[1];
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int i = i0 + u * kQueryThreads;
+            if (i >= chunks) break;
+            const int r = i >> 4, c = i & 15;
+            uint8_t* dst = q_s + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            if (kSplitQ) {
+                const uint4 v0 = in[u][0], v1 = in[u][kSplitQ ? 1 : 0];
+                const float x[8] = {__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z),
+                                    __uint_as_float(v0.w), __uint_as_float(v1.x), __uint_as_float(v1.y),
+                                    __uint_as_float(v1.z), __uint_as_float(v1.w)};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                    lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
+                                        x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                }
+                *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(dst + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                *reinterpret_cast<uint4*>(dst) = in[u][0];
+            }
+        }
+    }
+}
+
+template <bool kSplitQ>
+__device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl, Walk& w) {
+    const int tid = threadIdx.x - 64;
+    uint32_t freed = 0;                           // pieces whose scores are known to be formed
+    uint32_t after_wide = 0;                      // 1 + the last wide piece
+    Piece p;
+    while (walk_next(a, w, p)) {
+        // a narrow piece follows its unit's last user and any wide piece; a wide one, all
+        uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
+        for (; freed < need; ++freed) {
+            bool ok = wait_or_abort(&ctl->q_free[freed % kQueryUnits], (freed / kQueryUnits) & 1, ctl, a.st);
+            if (!__all_sync(0xffffffffu, ok)) return;
+        }
+        write_queries<kSplitQ>(a, p, q_s, tid);
+        fence_proxy_async_smem();
+        mbar_arrive(&ctl->q_full[p.n % kQueryUnits]);
+        if (p.wide()) after_wide = p.n + 1;
     }
 }
 
 // -------------------------------------------------------------------- the products
 
+// The whole warp keeps step; its first lane issues.
 template <bool kSplitQ>
-__device__ __forceinline__ void run_products(const PrefixArgs& a, uint32_t q_addr, uint32_t ring_addr, Control* ctl,
+__device__ __forceinline__ void run_products(const PrefixArgs& a, uint32_t q_addr, uint8_t* ring, Control* ctl,
                                              Walk& w) {
+    constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = ctl->tmem;
-    constexpr uint32_t kScores = bf16_idesc(kTile, kTile, false), kValues = bf16_idesc(kTile, kD, true);
-    uint32_t seq = 0, pieces = 0, ready[2] = {0, 0};
-    bool ok = true;
+    const uint32_t tmem = ctl->tmem, ring_addr = smem_u32(ring);
+    uint32_t seq = 0, t = 0;                      // ring entries and tiles so far
+    // the tile whose values come next
+    bool pending = false, v_first = false;
+    int v_valid = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_or_abort(bar, parity, ctl, a.st);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto scores = [&](const Piece& p, int i) {    // S = Q K^T of the ring's next tile, its live pages alone
+        const int slot = seq % kN, b = t & 1;
+        if (i == 0 && !wait(&ctl->q_full[p.n % kQueryUnits], (p.n / kQueryUnits) & 1)) return false;
+        if (!wait(&ctl->full[slot], (seq / kN) & 1)) return false;
+        tc_fence_after_sync();
+        if (lane == 0) {
+            const uint32_t idesc = bf16_idesc(kTile, (p.valid(i) + kPage - 1) / kPage * kPage, false);
+            const uint32_t k_addr = ring_addr + slot * kTileBytes;
+            const uint32_t q_at = q_addr + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128));
+#pragma unroll
+            for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+                    mma_ss(tmem + score_col(b), sw128_desc(q_at + part * kTileBytes + off, 16, 1024),
+                           sw128_desc(k_addr + off, 16, 1024), idesc, part + k > 0);
+                }
+            mma_commit(&ctl->scores[b]);
+            mma_commit(&ctl->empty[slot]);
+            if (i == p.tiles - 1) mma_commit(&ctl->q_free[p.n % kQueryUnits]);
+        }
+        ++seq;
+        ++t;
+        return true;
+    };
+    auto values = [&](uint32_t vt) {              // O_x += P_x V of tile vt, its live pages alone
+        constexpr uint32_t kValues = bf16_idesc(kTile, kD, true);
+        const int slot = seq % kN, b = vt & 1;
+        const int live = (v_valid + kPage - 1) / kPage;
+        if (!wait(&ctl->full[slot], (seq / kN) & 1)) return false;
+        if (v_valid % kPage != 0) {
+            // rows of the last page past the end weigh 0, but 0 * NaN would still reach the sums
+            uint8_t* rows = ring + slot * kTileBytes + v_valid * 128;
+            for (int i = lane; i < (live * kPage - v_valid) * 16; i += 32)
+                *reinterpret_cast<uint4*>(rows + (i & 8) * (kHalfBytes / 8) + (i >> 4) * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        const uint32_t v_addr = ring_addr + slot * kTileBytes;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (!wait(&ctl->weights[x][b], (vt >> 1) & 1)) return false;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < kTilePages / 2; ++k)  // 16 tokens: one page
+                    if (x * (kTilePages / 2) + k < live)
+                        mma_ts(tmem + acc_col(x), tmem + score_col(b) + x * kGroupTokens + 8 * k,
+                               sw128_desc(v_addr + (x * (kTilePages / 2) + k) * kBoxBytes, kHalfBytes, 1024), kValues,
+                               !v_first || k > 0);
+            }
+        }
+        if (lane == 0) {
+            mma_commit(&ctl->values[b]);
+            mma_commit(&ctl->empty[slot]);
+        }
+        ++seq;
+        return true;
+    };
+    bool ok = true, before_wide = false;
     Piece p;
     while (ok && walk_next(a, w, p)) {
-        if (lane == 0) {
-            auto scores = [&](int x) {            // S_x = Q K^T of the ring's next tile
-                const int slot = seq % kSlots;
-                if (!wait_or_abort(&ctl->full[slot], (seq / kSlots) & 1, ctl, a.st)) return false;
-                tc_fence_after_sync();
-                const uint32_t k_addr = ring_addr + slot * kTileBytes;
-#pragma unroll
-                for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-                        mma_ss(tmem + score_col(x), sw128_desc(q_addr + part * kTileBytes + off, 16, 1024),
-                               sw128_desc(k_addr + off, 16, 1024), kScores, part + k > 0);
-                    }
-                mma_commit(&ctl->empty[slot]);
-                mma_commit(&ctl->scores[x]);
-                ++seq;
-                return true;
-            };
-            ok = wait_or_abort(&ctl->queries, pieces & 1, ctl, a.st);
-            if (ok) {
-                tc_fence_after_sync();
-                ok = scores(0);
+        for (int i = 0; ok && i < p.tiles; ++i) {
+            if (pending && i == 0 && flush_before(p, before_wide)) {
+                ok = values(t - 1);
+                pending = false;
             }
-            if (ok && p.tiles > 1) ok = scores(1);
-            if (ok && pieces > 0) ok = wait_or_abort(&ctl->drained, (pieces - 1) & 1, ctl, a.st);
-            for (int i = 0; ok && i < p.tiles; ++i) {
-                const int x = i & 1, slot = seq % kSlots;
-                ok = wait_or_abort(&ctl->weights[x], ready[x]++ & 1, ctl, a.st) &&
-                     wait_or_abort(&ctl->full[slot], (seq / kSlots) & 1, ctl, a.st);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t v_addr = ring_addr + slot * kTileBytes;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)       // 16 tokens: one page
-                    mma_ts(tmem + acc_col(x), tmem + score_col(x) + 8 * k,
-                           sw128_desc(v_addr + k * kBoxBytes, kHalfBytes, 1024), kValues, i >= 2 || k > 0);
-                mma_commit(&ctl->empty[slot]);
-                ++seq;
-                if (i + 2 < p.tiles) ok = scores(x);
-            }
-            mma_commit(&ctl->done);
+            ok = ok && scores(p, i);
+            if (ok && pending) ok = values(t - 2);
+            v_first = i == 0;
+            v_valid = p.valid(i);
+            pending = true;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        ++pieces;
+        before_wide = p.wide();
     }
-    // Products may still read shared memory after a wait ran out: their end, bounded.
-    if (!ok && lane == 0) mbar_wait_bounded(&ctl->done, (pieces - 1) & 1, a.st.wait_limit_ns);
+    if (ok && pending) values(t - 1);
+    if (lane == 0) {
+        // whatever was issued reads shared and tensor memory: see its end
+        mma_commit(&ctl->last);
+        mbar_wait_bounded(&ctl->last, 0, a.st.wait_limit_ns);
+    }
     __syncwarp();
 }
 
 // --------------------------------------------------------------------- the softmax
 
-// Rows of the piece's queries as bf16 high parts (and low parts behind them) in the
-// 128-byte swizzle. Rows past p.rows keep what they held: no other row sees them.
-template <bool kSplitQ>
-__device__ __forceinline__ void write_queries(const PrefixArgs& a, const Piece& p, uint8_t* q_s, int tid) {
-    const int g = a.hq / a.hkv;
-    for (int i = tid; i < p.rows * 16; i += 2 * kSoftmaxThreads) {
-        const int r = i >> 4, c = i & 15;
-        const int row = p.row0 + r;
-        const int64_t src = (static_cast<int64_t>(p.seq0 + row / g) * a.hq + p.kvh * g + row % g) * kD + c * 8;
-        uint8_t* dst = q_s + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        if (kSplitQ) {
-            const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + src);
-            const float4 u = s[0], v = s[1];
-            const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-                lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
-                                    x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
-            }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        } else {
-            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + src);
-        }
-    }
-}
-
-template <bool kSplitQ>
-__device__ __forceinline__ void run_softmax(const PrefixArgs& a, uint8_t* q_s, uint8_t* ring, Control* ctl, Walk& w) {
+__device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl, Walk& w) {
     const int tid = threadIdx.x - 128;            // 0..255
     const int x = tid >> 7, row = tid & 127;      // softmax group, row of the block (= tensor-memory lane)
+    const int lane = tid & 31;
     const uint32_t lane_base = ctl->tmem + (static_cast<uint32_t>((tid >> 5) & 3) << 21);
-    const int warp_row = row & ~31;
-    uint32_t seq = 0, pieces = 0, tiles = 0;
-    bool ok = true;
+    const uint32_t acc = lane_base + acc_col(x);
+    uint32_t t = 0;                               // tiles so far
     Piece p;
-    while (ok && walk_next(a, w, p)) {
-        write_queries<kSplitQ>(a, p, q_s, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(&ctl->queries);
-        const bool busy = warp_row < p.rows;      // some row of this warp is real
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_or_abort(bar, parity, ctl, a.st);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    while (walk_next(a, w, p)) {
+        const bool busy = (row & ~31) < p.rows;   // some row of this warp is real
         float m = -INFINITY, l = 0.f;
-        for (int i = x; i < p.tiles; i += 2) {
-            ok = wait_or_abort(&ctl->scores[x], tiles++ & 1, ctl, a.st);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+        for (int i = 0; i < p.tiles; ++i, ++t) {
+            const int b = t & 1;
+            const int valid = p.valid(i) - x * kGroupTokens;      // tokens of this group; may be none
+            if (!wait(&ctl->scores[b], (t >> 1) & 1)) return;
             tc_fence_after_sync();
-            const int valid = min(kTile, p.tokens - (p.tile0 + i) * kTile);
-            if (busy) {
-                // first pass: the rows' maxima; the scores are read again below (they would take
-                // 128 registers in between)
-                float top = -INFINITY;
+            if (busy && valid > 0) {
+                const uint32_t tile = lane_base + score_col(b) + x * kGroupTokens;
+                float s[kGroupTokens];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t r[32];
-                    tmem_load(r, lane_base + score_col(x) + c * 32);
-                    float mx[2] = {-INFINITY, -INFINITY};
+                    tmem_load(r, tile + c * 32);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        mx[e & 1] = fmaxf(mx[e & 1], c * 32 + e < valid ? __uint_as_float(r[e]) : -INFINITY);
-                    top = fmaxf(top, fmaxf(mx[0], mx[1]));
+                    for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[e]);
                 }
-                if (i < 2) {
+                if (valid < kGroupTokens) {
+#pragma unroll
+                    for (int e = 0; e < kGroupTokens; ++e) s[e] = e < valid ? s[e] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int e = 4; e < kGroupTokens; ++e) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (i == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, row < p.rows && top > m + kRescale)) {
                     // some row's maximum grew enough to matter: bring its sums over (the other
-                    // rows' stay, so that no row's rounding depends on its neighbours)
+                    // rows' stay, so that no row's rounding depends on its neighbours), once the
+                    // values of the tile before are in
                     const float to = top > m + kRescale ? top : m;
                     const float f = to == m ? 1.f : fast_exp2((m - to) * kScaleLog2);
+                    if (!wait(&ctl->values[b ^ 1], ((t - 1) >> 1) & 1)) return;
+                    tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t r[32];
-                        tmem_load(r, lane_base + acc_col(x) + c * 32);
+                        tmem_load(r, acc + c * 32);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                        tmem_store(lane_base + acc_col(x) + c * 32, r);
+                        tmem_store(acc + c * 32, r);
                     }
                     l *= f;
                     m = to;
                 }
                 const float base = m == -INFINITY ? 0.f : m * kScaleLog2;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                // 32 scores become 16 columns of weights, which lie in columns already read
+                uint32_t r[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32], w16[16];
-                    tmem_load(r, lane_base + score_col(x) + c * 32);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float u = fast_exp2(fmaf(__uint_as_float(r[2 * e]), kScaleLog2, -base));
-                        float v = fast_exp2(fmaf(__uint_as_float(r[2 * e + 1]), kScaleLog2, -base));
-                        if (c * 32 + 2 * e >= valid) u = 0.f;
-                        if (c * 32 + 2 * e + 1 >= valid) v = 0.f;
-                        sum[e & 3] += u + v;
-                        w16[e] = pack_bf16x2(u, v);
-                    }
-                    tmem_store(lane_base + score_col(x) + c * 16, w16);
+                for (int e = 0; e < 32; ++e) {
+                    const float u = fast_exp2(fmaf(s[2 * e], kScaleLog2, -base));
+                    const float v = fast_exp2(fmaf(s[2 * e + 1], kScaleLog2, -base));
+                    sum[e & 3] += u + v;
+                    r[e] = pack_bf16x2(u, v);
                 }
+                tmem_store(tile, r);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_store();
             }
-            if (valid < kTile) {
-                // rows of V past the end weigh 0, but 0 * NaN would still reach the sum
-                const uint32_t at = seq + 2 * p.tiles - 1;
-                ok = wait_or_abort(&ctl->full[at % kSlots], (at / kSlots) & 1, ctl, a.st);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (row >= valid) {
-                    uint8_t* v_row = ring + (at % kSlots) * kTileBytes + row * 128;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        *reinterpret_cast<uint4*>(v_row + (c >> 3) * kHalfBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-            }
             tc_fence_before_sync();
-            mbar_arrive(&ctl->weights[x]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->weights[x][b]);
         }
-        if (!ok) break;
-        seq += 2 * p.tiles;
-        ok = wait_or_abort(&ctl->done, pieces & 1, ctl, a.st);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        // the group's partial of the piece, once its last products are in
+        if (!wait(&ctl->values[(t - 1) & 1], ((t - 1) >> 1) & 1)) return;
         tc_fence_after_sync();
-        // the two groups' parts of a row: group x writes its 64 dims of both
-        ctl->ml[x][row] = make_float2(m, l);
-        mbar_arrive(&ctl->joined);
-        ok = wait_or_abort(&ctl->joined, pieces & 1, ctl, a.st);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         if (busy) {
-            const float2 o0 = ctl->ml[0][row], o1 = ctl->ml[1][row];
-            const float top = fmaxf(o0.x, o1.x), at = top == -INFINITY ? 0.f : top;
-            const float f0 = fast_exp2((o0.x - at) * kScaleLog2);
-            const float f1 = p.tiles > 1 ? fast_exp2((o1.x - at) * kScaleLog2) : 0.f;
-            float* dst = a.part_o + (p.part + row) * kD + x * 64;
+            const int64_t at = (p.part + row) * 2 + x;
+            if (row < p.rows) a.part_ml[at] = make_float2(m, l);
+            if (p.tiles > 1 || p.valid(0) > x * kGroupTokens) {   // else the accumulator holds nothing
+                float* dst = a.part_o + at * kD;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r0[32], r1[32];
-                tmem_load(r0, lane_base + acc_col(0) + x * 64 + c * 32);
-                if (p.tiles > 1) {
-                    tmem_load(r1, lane_base + acc_col(1) + x * 64 + c * 32);
-                } else {
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tmem_load(r, acc + c * 32);
+                    if (row < p.rows) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r1[e] = 0;
-                }
-                if (row < p.rows) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float4 o;
-                        o.x = __uint_as_float(r0[e]) * f0 + __uint_as_float(r1[e]) * f1;
-                        o.y = __uint_as_float(r0[e + 1]) * f0 + __uint_as_float(r1[e + 1]) * f1;
-                        o.z = __uint_as_float(r0[e + 2]) * f0 + __uint_as_float(r1[e + 2]) * f1;
-                        o.w = __uint_as_float(r0[e + 3]) * f0 + __uint_as_float(r1[e + 3]) * f1;
-                        *reinterpret_cast<float4*>(dst + c * 32 + e) = o;
+                        for (int e = 0; e < 32; e += 8) store_v8(dst + c * 32 + e, &r[e]);
                     }
                 }
+                // the next piece's products overwrite the accumulator once its weights have arrived
+                tc_fence_before_sync();
             }
-            if (x == 0 && row < p.rows)
-                a.part_ml[p.part + row] = make_float2(top, o0.y * f0 + (p.tiles > 1 ? o1.y * f1 : 0.f));
         }
-        // the next piece's values, and so its (m, l), wait for this
-        tc_fence_before_sync();
-        mbar_arrive(&ctl->drained);
-        ++pieces;
     }
 }
 
@@ -575,22 +636,24 @@ __device__ __forceinline__ void write_plan(const PrefixArgs& a) {
 template <bool kSplitQ>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ __align__(1024) uint8_t q_s[];   // swizzle atoms: 1024-byte aligned
-    uint8_t* ring = q_s + 2 * kTileBytes;
-    Control* ctl = reinterpret_cast<Control*>(ring + kSlots * kTileBytes);
+    uint8_t* ring = q_s + kQueryBytes<kSplitQ>;
+    Control* ctl = reinterpret_cast<Control*>(ring + kSlots<kSplitQ> * kTileBytes);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kSlots<kSplitQ>; ++i) {
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->empty[i], 1);
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&ctl->scores[x], 1);
-            mbar_init(&ctl->weights[x], kSoftmaxThreads);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->scores[b], 1);
+            mbar_init(&ctl->values[b], 1);
+            for (int x = 0; x < 2; ++x) mbar_init(&ctl->weights[x][b], 4);   // a warp each
         }
-        mbar_init(&ctl->queries, 2 * kSoftmaxThreads);
-        mbar_init(&ctl->done, 1);
-        mbar_init(&ctl->joined, 2 * kSoftmaxThreads);
-        mbar_init(&ctl->drained, 2 * kSoftmaxThreads);
+        for (int i = 0; i < kQueryUnits; ++i) {
+            mbar_init(&ctl->q_full[i], kQueryThreads);
+            mbar_init(&ctl->q_free[i], 1);
+        }
+        mbar_init(&ctl->last, 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -600,16 +663,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     tc_fence_after_sync();
     grid_dependency_wait();
     allow_dependent_launch();
-    if (warp == 2) {
-        if (blockIdx.x == 0) write_plan(a);
-    } else if (warp != 3) {
-        Walk w;
-        if (walk_begin(a, w)) {
-            if (warp == 0) run_loads(a, ring, ctl, w);
-            else if (warp == 1) run_products<kSplitQ>(a, smem_u32(q_s), smem_u32(ring), ctl, w);
-            else run_softmax<kSplitQ>(a, q_s, ring, ctl, w);
-        }
+    Walk w;
+    if (walk_begin(a, w)) {
+        if (warp == 0) run_loads<kSplitQ>(a, ring, ctl, w);
+        else if (warp == 1) run_products<kSplitQ>(a, smem_u32(q_s), ring, ctl, w);
+        else if (warp < 4) run_queries<kSplitQ>(a, q_s, ctl, w);
+        else run_softmax(a, ctl, w);
     }
+    if (warp == 0 && blockIdx.x == 0) write_plan(a);      // its loads are out: the groups still work
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -655,12 +716,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
             first_p = cta_of(total, t, n);
             count_p = cta_of(total, t + pre.tiles - 1, n) - first_p + 1;
         }
-        const int count = count_p + count_o;
+        const int count = 2 * (count_p + count_o);          // a piece has one of each softmax group
         const int64_t row_p = static_cast<int64_t>(pre.row0) + kvh * rows + row_in;
         const int64_t row_o = static_cast<int64_t>(own.row0) + kvh * g + h;
         auto part_row = [&](int i) {
-            return i < count_p ? row_p + static_cast<int64_t>(first_p + i) * kTile
-                               : row_o + static_cast<int64_t>(first_o + i - count_p) * kTile;
+            const int c = i >> 1;
+            const int64_t r = c < count_p ? row_p + static_cast<int64_t>(first_p + c) * kTile
+                                          : row_o + static_cast<int64_t>(first_o + c - count_p) * kTile;
+            return 2 * r + (i & 1);
         };
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -685,7 +748,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 #pragma unroll 8
             for (int k = 0; k < here; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, wgt, k);
-                const float4 v = *reinterpret_cast<const float4*>(a.part_o + part_row(i0 + k) * kD + lane * 4);
+                // a part without weight may never have been written
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wk != 0.f) v = *reinterpret_cast<const float4*>(a.part_o + part_row(i0 + k) * kD + lane * 4);
                 o.x += wk * v.x, o.y += wk * v.y, o.z += wk * v.z, o.w += wk * v.w;
             }
         }
@@ -728,7 +793,7 @@ cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows) {
 
 template <bool kSplitQ>
 cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) {
-    cudaError_t e = ensure_kernel_attrs<prefix_kernel<kSplitQ>>(kSmemBytes);
+    cudaError_t e = ensure_kernel_attrs<prefix_kernel<kSplitQ>>(kSmemBytes<kSplitQ>);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -736,7 +801,7 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes<kSplitQ>;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -753,7 +818,8 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
 PrefixLayout prefix_layout(int batch, int hq, int num_groups) {
     // Partial rows: every unit has its own (the groups' are disjoint sequences, so at most
     // batch * hq, and as many for the own tokens), and each CTA boundary moves on by a block.
-    const size_t rows = 2 * static_cast<size_t>(batch) * hq + static_cast<size_t>(kMaxPrefixCtas + 1) * kTile;
+    // Each holds a partial of either softmax group.
+    const size_t rows = 2 * (2 * static_cast<size_t>(batch) * hq + static_cast<size_t>(kMaxPrefixCtas + 1) * kTile);
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     PrefixLayout w;
     w.units = 512;

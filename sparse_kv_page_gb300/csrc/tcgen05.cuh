@@ -61,6 +61,13 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes to global memory (32-byte aligned): one whole sector.
+__device__ __forceinline__ void store_v8(float* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // ----------------------------------------------------------------- products
 // Shared-memory operand in the 128-byte swizzle, 1024-byte aligned atoms of 8 rows x 128
 // bytes. K-major operands (rows of 64 K elements): `stride` bytes between groups of 8 rows,
