@@ -66,8 +66,8 @@ typedef struct {
  * - q_out: q_type LOCKS_FP32 (as locks_decode_step takes it) or LOCKS_BF16,
  *   contiguous [num_tokens][num_q_heads][128], 16-byte aligned; it may not
  *   overlap q, k or v. q and q_out may both be NULL (keys and values only).
- * - A negative cache_index marks a row of padding: nothing is read or written
- *   for it. A token_seq, cache_index or page id out of range records
+ * - A negative cache_index marks a row of padding: nothing is written for it,
+ *   whatever it holds. A token_seq, cache_index or page id out of range records
  *   LOCKS_ERR_BAD_INDEX and nothing is written for that token.
  * - No two tokens of a call may name the same cache row: each of its 16-byte
  *   pieces would hold either token's values.

@@ -152,7 +152,7 @@ int locks_prefix_workspace_size(const locks_dims_t* dims, int32_t num_groups, si
     if (s != LOCKS_OK) return s;
     if (num_groups < 0) return LOCKS_ERR_INVALID_ARG;
     if (dims->batch > kMaxBatch || num_groups > kMaxBatch) return LOCKS_ERR_UNSUPPORTED;
-    *bytes = locks::prefix_layout(dims->batch, dims->num_q_heads, num_groups).bytes;
+    *bytes = locks::prefix_layout(dims->batch, dims->num_q_heads).bytes;
     return LOCKS_OK;
 }
 
@@ -172,7 +172,7 @@ int locks_prefix_attention(const locks_dims_t* dims, const void* q, int32_t q_ty
     // cache rows are TMA coordinates (int32)
     if (static_cast<int64_t>(dims->num_phys_pages) * dims->num_kv_heads * LOCKS_PAGE_SIZE > INT_MAX)
         return LOCKS_ERR_UNSUPPORTED;
-    const locks::PrefixLayout w = locks::prefix_layout(dims->batch, dims->num_q_heads, num_groups);
+    const locks::PrefixLayout w = locks::prefix_layout(dims->batch, dims->num_q_heads);
     if ((s = locks::check_workspace(workspace, workspace_bytes, w.bytes)) != LOCKS_OK) return s;
     if (dims->batch == 0) return LOCKS_OK;
     if (!q || !k_cache || !v_cache || !seq_tokens || !out) return LOCKS_ERR_INVALID_ARG;
@@ -206,7 +206,7 @@ int locks_prefix_attention(const locks_dims_t* dims, const void* q, int32_t q_ty
     a.max_pages = dims->max_pages_per_seq;
     a.num_phys = dims->num_phys_pages;
     a.total = reinterpret_cast<int64_t*>(base + kStatusBytes);
-    a.units = reinterpret_cast<locks::PrefixUnit*>(base + w.units);
+    a.seqs = reinterpret_cast<locks::PrefixSeq*>(base + w.seqs);
     a.part_ml = reinterpret_cast<float2*>(base + w.ml);
     a.part_o = reinterpret_cast<float*>(base + w.o);
     a.st = locks::device_status(workspace);

@@ -88,24 +88,25 @@ struct PrefixArgs {
     float* lse;                    // nullable
     int num_groups, max_prefix_pages, batch, hq, hkv, max_pages, num_phys, q_type;
     // workspace regions (prefix_layout)
-    int64_t* total;                // tiles of the whole call
-    struct PrefixUnit* units;      // [num_groups + batch]
-    float2* part_ml;               // (max, sum) per partial row
-    float* part_o;                 // [partial row][128]
+    int64_t* total;                // steps of the whole call
+    struct PrefixSeq* seqs;        // [batch]
+    float2* part_ml;               // (max, sum) per partial
+    float* part_o;                 // [partial][128]
     DeviceStatus st;
     CUtensorMap tm_k, tm_v;        // 64 x 16 boxes with 128-byte swizzle (filled by the launcher)
 };
-// A group's prefix or a sequence's own tokens: where its tiles begin on the line of all
-// tiles and its rows on the line of all partial rows.
-struct PrefixUnit {
-    int64_t tile0;
-    int32_t row0, tiles, seq0, num_seqs;
+// Where a sequence's own tokens and its group's prefix lie on the line of all steps and on
+// the line of all partial rows (written by the first launch for the second).
+struct PrefixSeq {
+    int64_t own_step0, pre_step0;
+    int32_t own_row0, own_tiles;
+    int32_t pre_row0, pre_tiles, pre_seq0, pre_num_seqs;   // pre_tiles 0: no prefix
 };
 constexpr int kMaxPrefixCtas = 256;
 struct PrefixLayout {
-    size_t units, ml, o, bytes;    // offsets from the workspace (total at 256)
+    size_t seqs, ml, o, bytes;    // offsets from the workspace (total at 256)
 };
-PrefixLayout prefix_layout(int batch, int hq, int num_groups);
+PrefixLayout prefix_layout(int batch, int hq);
 cudaError_t launch_prefix(const PrefixArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace locks

@@ -100,6 +100,10 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Co
 
 // ----------------------------------------------------------------- the line of tiles
 
+// The line is counted in steps: one per tile and kItemCost per item, about what the first
+// tile of an item costs over the others (its queries, its partial, a pipeline that fills).
+constexpr int kItemCost = 1;
+
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
 
 struct Unit {
@@ -146,8 +150,9 @@ __device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b) {
 __device__ __forceinline__ int unit_tokens(const PrefixArgs& a, int u) {
     return u < a.num_groups ? a.prefix_tokens[u] : a.seq_tokens[u - a.num_groups];
 }
-__device__ __forceinline__ int64_t unit_tiles(const PrefixArgs& a, const Unit& u) {
-    return static_cast<int64_t>(u.tiles) * blocks_of(u.num_seqs * (a.hq / a.hkv)) * a.hkv;
+// Steps of a unit on the line: an item takes kItemCost before its tiles.
+__device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
+    return u.tiles == 0 ? 0 : static_cast<int64_t>(u.tiles + kItemCost) * blocks_of(u.num_seqs * (a.hq / a.hkv)) * a.hkv;
 }
 
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
@@ -155,11 +160,11 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) { return __shfl_s
 // 32 units, one a lane, with their places on the line. Whole warps call everything here.
 struct Chunk {
     Unit u;
-    int64_t tile0, count;           // the unit's first tile and its tiles
+    int64_t step0, count;           // the unit's first step and its steps
     int row0;                       // its first partial row
 };
 struct Cursor {                     // what lies before a chunk
-    int64_t tiles;
+    int64_t steps;
     int rows, bound;
 };
 __device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor& at) {
@@ -172,7 +177,7 @@ __device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Curs
         if (u < a.num_groups) c.u = group_unit(a, u, before);
     }
     if (u >= a.num_groups && u < units) c.u = own_unit(a, u - a.num_groups);
-    c.count = unit_tiles(a, c.u);
+    c.count = unit_steps(a, c.u);
     const int rows = c.u.num_seqs * a.hq;
     int64_t ts = c.count;
     int rs = rows;
@@ -182,19 +187,23 @@ __device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Curs
         const int ry = __shfl_up_sync(0xffffffffu, rs, o);
         if (lane >= o) ts += ty, rs += ry;
     }
-    c.tile0 = at.tiles + ts - c.count;
+    c.step0 = at.steps + ts - c.count;
     c.row0 = at.rows + rs - rows;
-    at.tiles += shfl64(ts, 31);
+    at.steps += shfl64(ts, 31);
     at.rows += __shfl_sync(0xffffffffu, rs, 31);
     return c;
 }
 
-// First tile of CTA c of n on a line of `total` tiles, and the CTA of a tile.
-__host__ __device__ __forceinline__ int64_t cta_first(int64_t total, int c, int n) { return total * c / n; }
-__host__ __device__ __forceinline__ int cta_of(int64_t total, int64_t tile, int n) {
-    return static_cast<int>(((tile + 1) * n - 1) / total);
+// First step of CTA c of n on a line of `total` steps, and the CTA of a step (32-bit division
+// where it will do: a 64-bit one is a long routine).
+__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
+    const int64_t v = (step + 1) * n - 1;
+    if (v < (1ll << 32) && total < (1ll << 32))
+        return static_cast<int>(static_cast<uint32_t>(v) / static_cast<uint32_t>(total));
+    return static_cast<int>(v / total);
 }
-__host__ __device__ __forceinline__ int ctas_of(int64_t total, int grid) {
+__device__ __forceinline__ int ctas_of(int64_t total, int grid) {
     return total < grid ? static_cast<int>(total) : grid;
 }
 
@@ -218,7 +227,7 @@ struct Walk {
     Chunk c;
 };
 
-// Positions the walk at this CTA's first tile; false if it has none. Calls of up to 32 units
+// Positions the walk at this CTA's first step; false if it has none. Calls of up to 32 units
 // know the whole line from their first chunk.
 __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
     const int lane = threadIdx.x & 31;
@@ -231,13 +240,13 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
     for (int u0 = 32; u0 < a.num_groups; u0 += 32) {
         const int u = u0 + lane;
         const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, bound);
-        if (u < a.num_groups) sum += unit_tiles(a, group_unit(a, u, before));
+        if (u < a.num_groups) sum += unit_steps(a, group_unit(a, u, before));
     }
 #pragma unroll 4
-    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_tiles(a, own_unit(a, b));
+    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_steps(a, own_unit(a, b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    sum += w.at.tiles;
+    sum += w.at.steps;
     const int n = ctas_of(sum, gridDim.x), cta = blockIdx.x;
     if (cta >= n) return false;
     w.t = cta_first(sum, cta, n);
@@ -246,24 +255,35 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
 }
 
 __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p) {
-    if (w.t >= w.t_end) return false;
     const int g = a.hq / a.hkv;
-    while (w.t >= w.at.tiles) {     // ends: t < t_end <= tiles of the line
-        w.first += 32;
-        w.c = load_chunk(a, w.first, w.at);
+    int at, tiles, rows, step;
+    int64_t item;
+    for (;;) {
+        if (w.t >= w.t_end) return false;
+        while (w.t >= w.at.steps) { // ends: t < t_end <= steps of the line
+            w.first += 32;
+            w.c = load_chunk(a, w.first, w.at);
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, w.c.step0 <= w.t && w.t < w.c.step0 + w.c.count);
+        at = __ffs(in) - 1;         // exactly one
+        tiles = __shfl_sync(0xffffffffu, w.c.u.tiles, at);
+        const int64_t off = w.t - shfl64(w.c.step0, at);
+        if (off < (1ll << 31)) {
+            item = static_cast<int>(off) / (tiles + kItemCost);
+        } else {
+            item = off / (tiles + kItemCost);
+        }
+        step = static_cast<int>(off - item * (tiles + kItemCost));
+        if (step >= kItemCost) break;
+        w.t += kItemCost - step;    // the item's first tile, if it is this CTA's
     }
-    const unsigned in = __ballot_sync(0xffffffffu, w.c.tile0 <= w.t && w.t < w.c.tile0 + w.c.count);
-    const int at = __ffs(in) - 1;   // exactly one
-    const int tiles = __shfl_sync(0xffffffffu, w.c.u.tiles, at);
+    rows = __shfl_sync(0xffffffffu, w.c.u.num_seqs, at) * g;
     const int seq0 = __shfl_sync(0xffffffffu, w.c.u.seq0, at);
-    const int rows = __shfl_sync(0xffffffffu, w.c.u.num_seqs, at) * g;
     const int part0 = __shfl_sync(0xffffffffu, w.c.row0, at);
-    const int64_t off = w.t - shfl64(w.c.tile0, at);
     const int u = w.first + at, blocks = blocks_of(rows);
-    const int item = static_cast<int>(off / tiles);
-    const int rb = item % blocks;
-    p.kvh = item / blocks;
-    p.tile0 = static_cast<int>(off - static_cast<int64_t>(item) * tiles);
+    const int rb = static_cast<int>(item) % blocks;
+    p.kvh = static_cast<int>(item) / blocks;
+    p.tile0 = step - kItemCost;
     p.tiles = static_cast<int>(min(static_cast<int64_t>(tiles - p.tile0), w.t_end - w.t));
     p.table = u < a.num_groups ? a.prefix_table + static_cast<int64_t>(u) * a.max_prefix_pages
                                : a.page_table + static_cast<int64_t>(u - a.num_groups) * a.max_pages;
@@ -600,37 +620,60 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl, W
         if (busy) {
             const int64_t at = (p.part + row) * 2 + x;
             if (row < p.rows) a.part_ml[at] = make_float2(m, l);
-            if (p.tiles > 1 || p.valid(0) > x * kGroupTokens) {   // else the accumulator holds nothing
-                float* dst = a.part_o + at * kD;
+            const bool some = p.tiles > 1 || p.valid(0) > x * kGroupTokens;   // else the accumulator holds nothing
+            float* dst = a.part_o + at * kD;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tmem_load(r, acc + c * 32);
-                    if (row < p.rows) {
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_load(r, acc + c * 32);
+                if (row < p.rows) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) store_v8(dst + c * 32 + e, &r[e]);
-                    }
+                    for (int e = 0; e < 32; ++e) r[e] = some ? r[e] : 0u;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) store_v8(dst + c * 32 + e, &r[e]);
                 }
-                // the next piece's products overwrite the accumulator once its weights have arrived
-                tc_fence_before_sync();
             }
+            // the next piece's products overwrite the accumulator once its weights have arrived
+            tc_fence_before_sync();
         }
     }
 }
 
-// Writes where every unit lies for the second launch, and reports bad lengths and bounds.
+// Writes where every sequence's tiles lie for the second launch, and reports bad lengths and
+// bounds. One warp.
 __device__ __forceinline__ void write_plan(const PrefixArgs& a) {
     const int lane = threadIdx.x & 31, units = a.num_groups + a.batch;
+    for (int b = lane; b < a.batch; b += 32) a.seqs[b].pre_tiles = 0;
+    __syncwarp();
     Cursor at{0, 0, 0};
     for (int first = 0; first < units; first += 32) {
         const Chunk c = load_chunk(a, first, at);
         const int u = first + lane;
-        if (u < units) {
-            a.units[u] = PrefixUnit{c.tile0, c.row0, c.u.tiles, c.u.seq0, c.u.num_seqs};
-            if (c.u.bad) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        if (u < units && c.u.bad) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        if (u >= a.num_groups && u < units) {
+            PrefixSeq& s = a.seqs[u - a.num_groups];
+            s.own_step0 = c.step0;
+            s.own_row0 = c.row0;
+            s.own_tiles = c.u.tiles;
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, u < a.num_groups && c.u.tiles > 0); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;               // a group: all lanes write its sequences
+            const int64_t step0 = shfl64(c.step0, from);
+            const int row0 = __shfl_sync(0xffffffffu, c.row0, from);
+            const int tiles = __shfl_sync(0xffffffffu, c.u.tiles, from);
+            const int seq0 = __shfl_sync(0xffffffffu, c.u.seq0, from);
+            const int num = __shfl_sync(0xffffffffu, c.u.num_seqs, from);
+            for (int i = lane; i < num; i += 32) {
+                PrefixSeq& s = a.seqs[seq0 + i];
+                s.pre_step0 = step0;
+                s.pre_row0 = row0;
+                s.pre_tiles = tiles;
+                s.pre_seq0 = seq0;
+                s.pre_num_seqs = num;
+            }
         }
     }
-    if (lane == 0) *a.total = at.tiles;
+    if (lane == 0) *a.total = at.steps;
 }
 
 template <bool kSplitQ>
@@ -679,87 +722,106 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
 // ------------------------------------------------------------------------ the join
 
-constexpr int kJoinWarps = 4;
+// kWarps warps join the partials of one (sequence, query head): each takes every kWarps-th
+// batch of 8, whose 4 KB are in flight together, and they meet in shared memory. The time
+// is the latency of a few dependent loads, so the registers are kept to 64: four CTAs an SM.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;
 
-// Grid: batch * hkv CTAs; a warp takes every kJoinWarps-th head of the GQA group.
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixArgs a, int grid) {
-    __shared__ int group_s;
+template <int kWarps>
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ PrefixArgs a, int grid) {
+    constexpr int kRowsPerCta = kJoinThreads / 32 / kWarps;
+    __shared__ float2 ml_s[kJoinThreads / 32];
+    __shared__ float4 o_s[kJoinThreads / 32][32];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int b = blockIdx.x / a.hkv, kvh = blockIdx.x % a.hkv;
-    const int lane = threadIdx.x & 31, g = a.hq / a.hkv;
-    if (threadIdx.x == 0) group_s = -1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.num_groups; i += kJoinWarps * 32) {
-        const PrefixUnit u = a.units[i];
-        if (b >= u.seq0 && b < u.seq0 + u.num_seqs) group_s = i;
-    }
-    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.hq / a.hkv;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + warp / kWarps;
+    const bool live = row < static_cast<int64_t>(a.batch) * a.hq;
+    const int b = live ? static_cast<int>(row / a.hq) : 0, head = static_cast<int>(row % a.hq);
+    const int kvh = head / g, h = head % g;
     const int64_t total = *a.total;
+    const PrefixSeq s = a.seqs[b];
     const int n = ctas_of(total, grid);
-    PrefixUnit pre = {0, 0, 0, 0, 0};
-    if (group_s >= 0) pre = a.units[group_s];
-    const int rows = pre.num_seqs * g;                      // of the group, per kv head
-    const PrefixUnit own = a.units[a.num_groups + b];
     int first_o = 0, count_o = 0;                           // CTAs with a piece of the own tokens
-    if (own.tiles > 0) {
-        const int64_t t = own.tile0 + static_cast<int64_t>(kvh) * own.tiles;
+    if (s.own_tiles > 0) {
+        const int64_t t = s.own_step0 + static_cast<int64_t>(kvh) * (s.own_tiles + kItemCost) + kItemCost;
         first_o = cta_of(total, t, n);
-        count_o = cta_of(total, t + own.tiles - 1, n) - first_o + 1;
+        count_o = cta_of(total, t + s.own_tiles - 1, n) - first_o + 1;
     }
-    for (int h = threadIdx.x >> 5; h < g; h += kJoinWarps) {
-        int first_p = 0, count_p = 0;                       // ... and of the prefix, for this row's block
-        const int row_in = (b - pre.seq0) * g + h;
-        if (pre.tiles > 0) {
-            const int64_t item = static_cast<int64_t>(kvh) * blocks_of(rows) + row_in / kTile;
-            const int64_t t = pre.tile0 + item * pre.tiles;
-            first_p = cta_of(total, t, n);
-            count_p = cta_of(total, t + pre.tiles - 1, n) - first_p + 1;
-        }
-        const int count = 2 * (count_p + count_o);          // a piece has one of each softmax group
-        const int64_t row_p = static_cast<int64_t>(pre.row0) + kvh * rows + row_in;
-        const int64_t row_o = static_cast<int64_t>(own.row0) + kvh * g + h;
-        auto part_row = [&](int i) {
-            const int c = i >> 1;
-            const int64_t r = c < count_p ? row_p + static_cast<int64_t>(first_p + c) * kTile
-                                          : row_o + static_cast<int64_t>(first_o + c - count_p) * kTile;
-            return 2 * r + (i & 1);
-        };
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < count; i0 += 32) {            // 32 pieces at a time, one a lane
-            const int i = i0 + lane;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i < count) ml = a.part_ml[part_row(i)];
-            float top = ml.x;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
-            const float f = fast_exp2((m - base) * kScaleLog2);
-            const float wgt = i < count ? fast_exp2((ml.x - base) * kScaleLog2) : 0.f;
-            float sum = wgt * ml.y;
-            if (i >= count) sum = 0.f;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-            l = l * f + sum;
-            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-            m = to;
-            const int here = min(32, count - i0);
-#pragma unroll 8
-            for (int k = 0; k < here; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wgt, k);
-                // a part without weight may never have been written
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wk != 0.f) v = *reinterpret_cast<const float4*>(a.part_o + part_row(i0 + k) * kD + lane * 4);
-                o.x += wk * v.x, o.y += wk * v.y, o.z += wk * v.z, o.w += wk * v.w;
-            }
-        }
-        const float inv = count > 0 ? 1.f / l : 0.f;
-        const int64_t row = static_cast<int64_t>(b) * a.hq + kvh * g + h;
-        *reinterpret_cast<uint2*>(a.out + row * kD + lane * 4) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (a.lse && lane == 0) a.lse[row] = count > 0 ? fmaf(m, kInvSqrtD, logf(l)) : -INFINITY;
+    int first_p = 0, count_p = 0;                           // ... and of the prefix, for this row's block
+    int64_t row_p = 0;
+    if (s.pre_tiles > 0) {
+        const int rows = s.pre_num_seqs * g, row_in = (b - s.pre_seq0) * g + h;
+        const int64_t item = static_cast<int64_t>(kvh) * blocks_of(rows) + row_in / kTile;
+        const int64_t t = s.pre_step0 + item * (s.pre_tiles + kItemCost) + kItemCost;
+        first_p = cta_of(total, t, n);
+        count_p = cta_of(total, t + s.pre_tiles - 1, n) - first_p + 1;
+        row_p = static_cast<int64_t>(s.pre_row0) + kvh * rows + row_in;
     }
+    const int count = live ? 2 * (count_p + count_o) : 0;   // a piece has one of each softmax group
+    const int64_t row_o = static_cast<int64_t>(s.own_row0) + kvh * g + h;
+    auto part_row = [&](int i) {
+        const int c = i >> 1;
+        const int64_t r = c < count_p ? row_p + static_cast<int64_t>(first_p + c) * kTile
+                                      : row_o + static_cast<int64_t>(first_o + c - count_p) * kTile;
+        return 2 * r + (i & 1);
+    };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = (warp % kWarps) * kJoinBatch; i0 < count; i0 += kWarps * kJoinBatch) {
+        const int here = min(kJoinBatch, count - i0);
+        const int64_t at = part_row(i0 + min(lane, here - 1));       // a partial a lane
+        float4 v[kJoinBatch];
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+            const int64_t r = shfl64(at, k);
+            if (k < here) v[k] = *reinterpret_cast<const float4*>(a.part_o + r * kD + lane * 4);
+        }
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < here) ml = a.part_ml[at];
+        float top = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
+        const float f = fast_exp2((m - base) * kScaleLog2);
+        const float wgt = lane < here ? fast_exp2((ml.x - base) * kScaleLog2) : 0.f;
+        float sum = lane < here ? wgt * ml.y : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l = l * f + sum;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        m = to;
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, wgt, k);
+            if (k < here) o.x += wk * v[k].x, o.y += wk * v[k].y, o.z += wk * v[k].z, o.w += wk * v[k].w;
+        }
+    }
+    if (kWarps > 1) {
+        if (lane == 0) ml_s[warp] = make_float2(m, l);
+        o_s[warp][lane] = o;
+        __syncthreads();
+        if (warp != 0) return;
+        m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_s[w].x);
+        const float base = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = fast_exp2((ml_s[w].x - base) * kScaleLog2);
+            const float4 v = o_s[w][lane];
+            l += f * ml_s[w].y;
+            o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+        }
+    }
+    if (!live) return;
+    const float inv = count > 0 ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(a.out + row * kD + lane * 4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[row] = count > 0 ? fmaf(m, kInvSqrtD, logf(l)) : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tiled_encoder() {
@@ -806,24 +868,29 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, prefix_kernel<kSplitQ>, a)) != cudaSuccess) return e;
-    cfg.gridDim = dim3(a.batch * a.hkv, 1, 1);
-    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    // The fewer rows, the more pieces each has. 16 or more rows per SM are at least 19 blocks
+    // of 128, so a prefix row has at most 9 pieces: a warp per row will do.
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.hq;
+    const bool many = rows >= 16 * static_cast<int64_t>(grid);
+    cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows), 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, join_kernel, a, grid)) != cudaSuccess) return e;
+    e = many ? cudaLaunchKernelEx(&cfg, join_kernel<1>, a, grid) : cudaLaunchKernelEx(&cfg, join_kernel<8>, a, grid);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 }  // namespace
 
-PrefixLayout prefix_layout(int batch, int hq, int num_groups) {
+PrefixLayout prefix_layout(int batch, int hq) {
     // Partial rows: every unit has its own (the groups' are disjoint sequences, so at most
     // batch * hq, and as many for the own tokens), and each CTA boundary moves on by a block.
     // Each holds a partial of either softmax group.
     const size_t rows = 2 * (2 * static_cast<size_t>(batch) * hq + static_cast<size_t>(kMaxPrefixCtas + 1) * kTile);
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     PrefixLayout w;
-    w.units = 512;
-    w.ml = w.units + up((static_cast<size_t>(num_groups) + batch) * sizeof(PrefixUnit));
+    w.seqs = 512;
+    w.ml = w.seqs + up(static_cast<size_t>(batch) * sizeof(PrefixSeq));
     w.o = w.ml + up(rows * sizeof(float2));
     w.bytes = w.o + rows * kD * sizeof(float);
     return w;
