@@ -14,12 +14,15 @@
 // boundary gives two partials (m, l, O) per piece. The line is found on the device from the
 // token counts, so a captured graph follows them.
 //
-// CTA (12 warps): warp 0 loads K and V, warp 1 issues the products, warps 2-3 bring the
-// queries, warps 4-7 and 8-11 are two softmax groups. The CTA's tiles are one stream,
-// whatever pieces they belong to: the scores of tile t + 1 are formed while the groups
-// weigh tile t, group x its 64 tokens x * 64.., each with a running maximum, sum and
-// accumulator of its own, so neither waits for the other, and each leaves a partial of its
-// own. A piece's accumulators are read while the next piece's scores are formed.
+// CTA (14 warps): warp 0 loads K and warp 3 V, warp 1 issues the products with K, warp 2 those
+// with V, warps 4-7 and 8-11 are two softmax groups, warps 12-13 bring the queries. The CTA's
+// tiles are one stream, whatever pieces they belong to: the scores of tile t + 1 are formed
+// while the groups weigh tile t, group x its 64 tokens x * 64.., each with a running maximum,
+// sum and accumulator of its own, so neither waits for the other, and each leaves a partial
+// of its own. A piece's accumulators are read while the next piece's scores are formed. (One
+// warp for both products was the bottleneck: issuing a product blocks until the tensor core
+// takes it, so its waits for K, V and the weights added up to a third of a tile's 3600
+// cycles; 1M x 8: REPLACE.)
 // Tensor memory: two score tiles (2 x 128 columns; the bf16 weights overwrite them) and the
 // groups' accumulators (2 x 128). Shared memory: the queries as a bf16 high part and, for
 // fp32, a low part (32 KB each; 16 significant bits together), and a ring of 32 KB slots,
@@ -51,7 +54,7 @@ constexpr int kBoxBytes = kPage * 128;
 constexpr int kGroupTokens = kTile / 2;           // of a tile, per softmax group
 constexpr int kNarrow = 16;                       // rows of a piece that takes one query unit
 constexpr int kQueryUnits = kTile / kNarrow;
-constexpr int kThreads = 384;
+constexpr int kThreads = 448;
 constexpr int kQueryThreads = 64;
 constexpr float kScaleLog2 = kInvSqrtD * kLog2e;  // raw score -> exponent of 2
 constexpr float kRescale = 8.f / kScaleLog2;      // a running maximum may lag by 2^8
@@ -69,7 +72,7 @@ struct Control {
     uint64_t values[2];                           // [score tile] their products with V have completed
     uint64_t q_full[kQueryUnits];                 // a piece's queries are in shared memory
     uint64_t q_free[kQueryUnits];                 // its last scores have been formed
-    uint64_t last;                                // every product of the CTA has completed
+    uint64_t last[2];                             // every product with K (with V) of the CTA has completed
     uint32_t tmem;
     int abort;
 };
@@ -297,42 +300,26 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
     return true;
 }
 
-// The order of the stream, the same for all roles: K of tile t + 1 comes before V of tile t.
-// Around a wide piece, whose queries need the whole space, V of the tile before comes first:
-// its product must not wait for queries that wait for it.
-__device__ __forceinline__ bool flush_before(const Piece& p, bool before_wide) { return p.wide() || before_wide; }
+// The order of the ring: K of tile t + 1 comes before V of tile t. (The entry of the K that
+// would follow the last tile stays empty.)
+__device__ __forceinline__ uint32_t k_entry(uint32_t t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ uint32_t v_entry(uint32_t t) { return 2 * t + 2; }
 
 // ----------------------------------------------------------------------- the loads
 
-template <bool kSplitQ>
+// The loads of K (kValues false) or of V, a warp each: a box takes about 75 cycles to issue,
+// so one warp for the 32 boxes of a tile would bound the supply.
+template <bool kSplitQ, bool kValues>
 __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl, Walk& w) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
-    uint32_t seq = 0;
-    // loads `live` pages of a tile; lanes 0-7 (and 8-15 for the other half) hold their ids
-    auto load = [&](const CUtensorMap* map, int id, int kvh, int live) {
-        const int slot = seq % kN;
-        bool ok = wait_or_abort(&ctl->empty[slot], ((seq / kN) & 1) ^ 1, ctl, a.st);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], live * 2 * kBoxBytes);
-        __syncwarp();
-        if (lane < 2 * kTilePages && (lane & 7) < live) {
-            const int half = lane >> 3;
-            tma_load_2d(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes, map, half * 64,
-                        (id * a.hkv + kvh) * kPage, &ctl->full[slot]);
-        }
-        __syncwarp();
-        ++seq;
-        return true;
-    };
-    bool ok = true, pending = false, before_wide = false;
-    int v_id = 0, v_kvh = 0, v_live = 0;
+    uint32_t t = 0;                               // tiles so far
+    bool ok = true;
     Piece p;
     while (ok && walk_next(a, w, p)) {
         const int pages = (p.tokens + kPage - 1) / kPage;
         int ids = 0;                              // of four tiles, a page a lane
-        for (int i = 0; ok && i < p.tiles; ++i) {
+        for (int i = 0; i < p.tiles; ++i) {
             if ((i & 3) == 0) {
                 const int page = (p.tile0 + i) * kTilePages + lane;
                 ids = page < pages ? p.table[page] : 0;
@@ -341,26 +328,30 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
                     ids = 0;
                 }
             }
+            // lanes 0-7 load the pages' first halves, lanes 8-15 the second
             const int id = __shfl_sync(0xffffffffu, ids, (i & 3) * kTilePages + (lane & 7));
-            if (pending && i == 0 && flush_before(p, before_wide)) {
-                ok = load(&a.tm_v, v_id, v_kvh, v_live);
-                pending = false;
-            }
             const int live = min(kTilePages, pages - (p.tile0 + i) * kTilePages);
-            ok = ok && load(&a.tm_k, id, p.kvh, live);
-            if (ok && pending) ok = load(&a.tm_v, v_id, v_kvh, v_live);
-            v_id = id;
-            v_kvh = p.kvh;
-            v_live = live;
-            pending = true;
+            const uint32_t seq = kValues ? v_entry(t) : k_entry(t), slot = seq % kN;
+            ok = wait_or_abort(&ctl->empty[slot], ((seq / kN) & 1) ^ 1, ctl, a.st);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], live * 2 * kBoxBytes);
+            __syncwarp();
+            if (lane < 2 * kTilePages && (lane & 7) < live) {
+                const int half = lane >> 3;
+                tma_load_2d(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes,
+                            kValues ? &a.tm_v : &a.tm_k, half * 64, (id * a.hkv + p.kvh) * kPage, &ctl->full[slot]);
+            }
+            __syncwarp();
+            ++t;
         }
-        before_wide = p.wide();
     }
-    if (ok && pending) ok = load(&a.tm_v, v_id, v_kvh, v_live);
     if (!ok) {
         // giving up: the loads in flight write to this CTA's shared memory, so wait for them
-        for (uint32_t s = seq > kN ? seq - kN : 0; s < seq; ++s)
-            mbar_wait_bounded(&ctl->full[s % kN], (s / kN) & 1, a.st.wait_limit_ns);
+        for (uint32_t i = t > kN ? t - kN : 0; i < t; ++i) {
+            const uint32_t seq = kValues ? v_entry(i) : k_entry(i);
+            mbar_wait_bounded(&ctl->full[seq % kN], (seq / kN) & 1, a.st.wait_limit_ns);
+        }
     }
 }
 
@@ -415,7 +406,7 @@ __device__ __forceinline__ void write_queries(const PrefixArgs& a, const Piece& 
 
 template <bool kSplitQ>
 __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl, Walk& w) {
-    const int tid = threadIdx.x - 64;
+    const int tid = threadIdx.x - (kThreads - kQueryThreads);
     uint32_t freed = 0;                           // pieces whose scores are known to be formed
     uint32_t after_wide = 0;                      // 1 + the last wide piece
     Piece p;
@@ -435,104 +426,109 @@ __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, C
 
 // -------------------------------------------------------------------- the products
 
-// The whole warp keeps step; its first lane issues.
-template <bool kSplitQ>
-__device__ __forceinline__ void run_products(const PrefixArgs& a, uint32_t q_addr, uint8_t* ring, Control* ctl,
-                                             Walk& w) {
-    constexpr uint32_t kN = kSlots<kSplitQ>;
-    const int lane = threadIdx.x & 31;
-    const uint32_t tmem = ctl->tmem, ring_addr = smem_u32(ring);
-    uint32_t seq = 0, t = 0;                      // ring entries and tiles so far
-    // the tile whose values come next
-    bool pending = false, v_first = false;
-    int v_valid = 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_or_abort(bar, parity, ctl, a.st);
-        return __all_sync(0xffffffffu, ok) != 0;
-    };
-    auto scores = [&](const Piece& p, int i) {    // S = Q K^T of the ring's next tile, its live pages alone
-        const int slot = seq % kN, b = t & 1;
-        if (i == 0 && !wait(&ctl->q_full[p.n % kQueryUnits], (p.n / kQueryUnits) & 1)) return false;
-        if (!wait(&ctl->full[slot], (seq / kN) & 1)) return false;
-        tc_fence_after_sync();
-        if (lane == 0) {
-            const uint32_t idesc = bf16_idesc(kTile, (p.valid(i) + kPage - 1) / kPage * kPage, false);
-            const uint32_t k_addr = ring_addr + slot * kTileBytes;
-            const uint32_t q_at = q_addr + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128));
-#pragma unroll
-            for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-                    mma_ss(tmem + score_col(b), sw128_desc(q_at + part * kTileBytes + off, 16, 1024),
-                           sw128_desc(k_addr + off, 16, 1024), idesc, part + k > 0);
-                }
-            mma_commit(&ctl->scores[b]);
-            mma_commit(&ctl->empty[slot]);
-            if (i == p.tiles - 1) mma_commit(&ctl->q_free[p.n % kQueryUnits]);
-        }
-        ++seq;
-        ++t;
-        return true;
-    };
-    auto values = [&](uint32_t vt) {              // O_x += P_x V of tile vt, its live pages alone
-        constexpr uint32_t kValues = bf16_idesc(kTile, kD, true);
-        const int slot = seq % kN, b = vt & 1;
-        const int live = (v_valid + kPage - 1) / kPage;
-        if (!wait(&ctl->full[slot], (seq / kN) & 1)) return false;
-        if (v_valid % kPage != 0) {
-            // rows of the last page past the end weigh 0, but 0 * NaN would still reach the sums
-            uint8_t* rows = ring + slot * kTileBytes + v_valid * 128;
-            for (int i = lane; i < (live * kPage - v_valid) * 16; i += 32)
-                *reinterpret_cast<uint4*>(rows + (i & 8) * (kHalfBytes / 8) + (i >> 4) * 128 + (i & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        const uint32_t v_addr = ring_addr + slot * kTileBytes;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            if (!wait(&ctl->weights[x][b], (vt >> 1) & 1)) return false;
-            tc_fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < kTilePages / 2; ++k)  // 16 tokens: one page
-                    if (x * (kTilePages / 2) + k < live)
-                        mma_ts(tmem + acc_col(x), tmem + score_col(b) + x * kGroupTokens + 8 * k,
-                               sw128_desc(v_addr + (x * (kTilePages / 2) + k) * kBoxBytes, kHalfBytes, 1024), kValues,
-                               !v_first || k > 0);
-            }
-        }
-        if (lane == 0) {
-            mma_commit(&ctl->values[b]);
-            mma_commit(&ctl->empty[slot]);
-        }
-        ++seq;
-        return true;
-    };
-    bool ok = true, before_wide = false;
-    Piece p;
-    while (ok && walk_next(a, w, p)) {
-        for (int i = 0; ok && i < p.tiles; ++i) {
-            if (pending && i == 0 && flush_before(p, before_wide)) {
-                ok = values(t - 1);
-                pending = false;
-            }
-            ok = ok && scores(p, i);
-            if (ok && pending) ok = values(t - 2);
-            v_first = i == 0;
-            v_valid = p.valid(i);
-            pending = true;
-        }
-        before_wide = p.wide();
-    }
-    if (ok && pending) values(t - 1);
-    if (lane == 0) {
-        // whatever was issued reads shared and tensor memory: see its end
-        mma_commit(&ctl->last);
-        mbar_wait_bounded(&ctl->last, 0, a.st.wait_limit_ns);
+// In both the whole warp keeps step and its first lane issues.
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
+    const bool ok = wait_or_abort(bar, parity, ctl, st);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Whatever the warp issued reads shared and tensor memory: sees its end.
+__device__ __forceinline__ void end_products(uint64_t* bar, const DeviceStatus& st) {
+    if ((threadIdx.x & 31) == 0) {
+        mma_commit(bar);
+        mbar_wait_bounded(bar, 0, st.wait_limit_ns);
     }
     __syncwarp();
+}
+
+// S = Q K^T, over each tile's live pages alone.
+template <bool kSplitQ>
+__device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr, uint32_t ring_addr, Control* ctl,
+                                           Walk& w) {
+    constexpr uint32_t kN = kSlots<kSplitQ>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = ctl->tmem;
+    uint32_t t = 0;                               // tiles so far
+    bool ok = true;
+    Piece p;
+    while (ok && walk_next(a, w, p)) {
+        ok = warp_wait(&ctl->q_full[p.n % kQueryUnits], (p.n / kQueryUnits) & 1, ctl, a.st);
+        const uint32_t q_at = q_addr + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128));
+        for (int i = 0; ok && i < p.tiles; ++i, ++t) {
+            const uint32_t seq = k_entry(t), slot = seq % kN, b = t & 1;
+            // the weights of tile t - 2 lie where these scores go
+            if (t >= 2) ok = warp_wait(&ctl->values[b], ((t >> 1) - 1) & 1, ctl, a.st);
+            ok = ok && warp_wait(&ctl->full[slot], (seq / kN) & 1, ctl, a.st);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+                const uint32_t idesc = bf16_idesc(kTile, (p.valid(i) + kPage - 1) / kPage * kPage, false);
+                const uint32_t k_addr = ring_addr + slot * kTileBytes;
+#pragma unroll
+                for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+                        mma_ss(tmem + score_col(b), sw128_desc(q_at + part * kTileBytes + off, 16, 1024),
+                               sw128_desc(k_addr + off, 16, 1024), idesc, part + k > 0);
+                    }
+                mma_commit(&ctl->scores[b]);
+                mma_commit(&ctl->empty[slot]);
+                if (i == p.tiles - 1) mma_commit(&ctl->q_free[p.n % kQueryUnits]);
+            }
+        }
+    }
+    end_products(&ctl->last[0], a.st);
+}
+
+// O_x += P_x V, over each tile's live pages alone.
+template <bool kSplitQ>
+__device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, Control* ctl, Walk& w) {
+    constexpr uint32_t kN = kSlots<kSplitQ>;
+    constexpr uint32_t kValues = bf16_idesc(kTile, kD, true);
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = ctl->tmem;
+    uint32_t t = 0;                               // tiles so far
+    bool ok = true;
+    Piece p;
+    while (ok && walk_next(a, w, p)) {
+        for (int i = 0; ok && i < p.tiles; ++i, ++t) {
+            const uint32_t seq = v_entry(t), slot = seq % kN, b = t & 1;
+            const int valid = p.valid(i), live = (valid + kPage - 1) / kPage;
+            ok = warp_wait(&ctl->full[slot], (seq / kN) & 1, ctl, a.st);
+            if (!ok) break;
+            if (valid % kPage != 0) {
+                // rows of the last page past the end weigh 0, but 0 * NaN would still reach the sums
+                uint8_t* rows = ring + slot * kTileBytes + valid * 128;
+                for (int j = lane; j < (live * kPage - valid) * 16; j += 32)
+                    *reinterpret_cast<uint4*>(rows + (j & 8) * (kHalfBytes / 8) + (j >> 4) * 128 + (j & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const uint32_t v_addr = smem_u32(ring) + slot * kTileBytes;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ok = ok && warp_wait(&ctl->weights[x][b], (t >> 1) & 1, ctl, a.st);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kTilePages / 2; ++k)      // 16 tokens: one page
+                        if (x * (kTilePages / 2) + k < live)
+                            mma_ts(tmem + acc_col(x), tmem + score_col(b) + x * kGroupTokens + 8 * k,
+                                   sw128_desc(v_addr + (x * (kTilePages / 2) + k) * kBoxBytes, kHalfBytes, 1024),
+                                   kValues, i > 0 || k > 0);
+                }
+            }
+            if (ok && lane == 0) {
+                mma_commit(&ctl->values[b]);
+                mma_commit(&ctl->empty[slot]);
+            }
+        }
+    }
+    end_products(&ctl->last[1], a.st);
 }
 
 // --------------------------------------------------------------------- the softmax
@@ -545,10 +541,7 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl, W
     const uint32_t acc = lane_base + acc_col(x);
     uint32_t t = 0;                               // tiles so far
     Piece p;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_or_abort(bar, parity, ctl, a.st);
-        return __all_sync(0xffffffffu, ok) != 0;
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl, a.st); };
     while (walk_next(a, w, p)) {
         const bool busy = (row & ~31) < p.rows;   // some row of this warp is real
         float m = -INFINITY, l = 0.f;
@@ -696,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(&ctl->q_full[i], kQueryThreads);
             mbar_init(&ctl->q_free[i], 1);
         }
-        mbar_init(&ctl->last, 1);
+        mbar_init(&ctl->last[0], 1);
+        mbar_init(&ctl->last[1], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -708,10 +702,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     allow_dependent_launch();
     Walk w;
     if (walk_begin(a, w)) {
-        if (warp == 0) run_loads<kSplitQ>(a, ring, ctl, w);
-        else if (warp == 1) run_products<kSplitQ>(a, smem_u32(q_s), ring, ctl, w);
-        else if (warp < 4) run_queries<kSplitQ>(a, q_s, ctl, w);
-        else run_softmax(a, ctl, w);
+        if (warp == 0) run_loads<kSplitQ, false>(a, ring, ctl, w);
+        else if (warp == 3) run_loads<kSplitQ, true>(a, ring, ctl, w);
+        else if (warp == 1) run_scores<kSplitQ>(a, smem_u32(q_s), smem_u32(ring), ctl, w);
+        else if (warp == 2) run_values<kSplitQ>(a, ring, ctl, w);
+        else if (warp >= 12) run_queries<kSplitQ>(a, q_s, ctl, w);
+        else if (warp >= 4) run_softmax(a, ctl, w);
     }
     if (warp == 0 && blockIdx.x == 0) write_plan(a);      // its loads are out: the groups still work
     tc_fence_before_sync();
