@@ -14,8 +14,9 @@
 // boundary gives two partials (m, l, O) per piece. The line is found on the device from the
 // token counts, so a captured graph follows them.
 //
-// CTA (14 warps): warp 0 loads K and warp 3 V, warp 1 issues the products with K, warp 2 those
-// with V, warps 4-7 and 8-11 are two softmax groups, warps 12-13 bring the queries. The CTA's
+// CTA (16 warps): warp 14 finds the CTA's pieces and announces them to the others, warp 0
+// loads K and warp 3 V, warp 1 issues the products with K, warp 2 those with V, warps 4-7 and
+// 8-11 are two softmax groups, the other three bring the queries. The CTA's
 // tiles are one stream, whatever pieces they belong to: the scores of tile t + 1 are formed
 // while the groups weigh tile t, group x its 64 tokens x * 64.., each with a running maximum,
 // sum and accumulator of its own, so neither waits for the other, and each leaves a partial
@@ -54,8 +55,10 @@ constexpr int kBoxBytes = kPage * 128;
 constexpr int kGroupTokens = kTile / 2;           // of a tile, per softmax group
 constexpr int kNarrow = 16;                       // rows of a piece that takes one query unit
 constexpr int kQueryUnits = kTile / kNarrow;
-constexpr int kThreads = 448;
-constexpr int kQueryThreads = 64;
+constexpr int kThreads = 512;
+constexpr int kQueryThreads = 96;
+constexpr int kPieces = 8;                        // pieces announced ahead
+constexpr int kPieceReaders = 15;                 // warps that follow them
 constexpr float kScaleLog2 = kInvSqrtD * kLog2e;  // raw score -> exponent of 2
 constexpr float kRescale = 8.f / kScaleLog2;      // a running maximum may lag by 2^8
 
@@ -65,16 +68,30 @@ constexpr int kSlots = kSplitQ ? 5 : 6;
 template <bool kSplitQ>
 constexpr int kQueryBytes = (kSplitQ ? 2 : 1) * kTileBytes;
 
+struct Piece {                      // a run of tiles of one item
+    const int32_t* table;
+    int tokens, kvh, seq0, row0;    // row r of the block: sequence seq0 + (row0 + r) / g, head kvh * g + (row0 + r) % g
+    int rows, tile0, tiles;         // no tiles: the end
+    int64_t part;                   // its first partial row
+    uint32_t n;                     // pieces of this CTA before it
+
+    __device__ __forceinline__ bool wide() const { return rows > kNarrow; }
+    // tokens of its tile i
+    __device__ __forceinline__ int valid(int i) const { return min(kTile, tokens - (tile0 + i) * kTile); }
+};
+
 struct Control {
     uint64_t full[6], empty[6];
     uint64_t scores[2];                           // a score tile is in tensor memory
     uint64_t weights[2][2];                       // [group][score tile] its weights are
     uint64_t values[2];                           // [score tile] their products with V have completed
+    uint64_t p_full[kPieces], p_free[kPieces];    // a piece is announced; every role has read it
     uint64_t q_full[kQueryUnits];                 // a piece's queries are in shared memory
     uint64_t q_free[kQueryUnits];                 // its last scores have been formed
     uint64_t last[2];                             // every product with K (with V) of the CTA has completed
     uint32_t tmem;
     int abort;
+    Piece pieces[kPieces];
 };
 template <bool kSplitQ>
 constexpr int kSmemBytes = kQueryBytes<kSplitQ> + kSlots<kSplitQ> * kTileBytes + static_cast<int>(sizeof(Control));
@@ -101,6 +118,22 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Co
     }
 }
 
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
+    const bool ok = wait_or_abort(bar, parity, ctl, st);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// The next piece of the CTA, as warp 14 announced it; false after the last. Whole warps.
+__device__ __forceinline__ bool next_piece(Control* ctl, uint32_t& n, Piece& p, const DeviceStatus& st) {
+    const int slot = n % kPieces;
+    if (!warp_wait(&ctl->p_full[slot], (n / kPieces) & 1, ctl, st)) return false;
+    p = ctl->pieces[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->p_free[slot]);
+    ++n;
+    return p.tiles > 0;
+}
+
 // ----------------------------------------------------------------- the line of tiles
 
 // The line is counted in steps: one per tile and kItemCost per item, about what the first
@@ -110,7 +143,7 @@ constexpr int kItemCost = 1;
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
 
 struct Unit {
-    int tiles, seq0, num_seqs;      // tiles per item
+    int tokens, tiles, seq0, num_seqs;            // tiles per item
     bool bad;
 };
 // The largest group bound ahead of this lane's, given the largest one before the warp's
@@ -136,7 +169,8 @@ __device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int u, int befor
     Unit r;
     r.seq0 = span ? s : 0;
     r.num_seqs = span ? e - s : 0;
-    r.tiles = span && len ? (n + kTile - 1) / kTile : 0;
+    r.tokens = span && len ? n : 0;
+    r.tiles = (r.tokens + kTile - 1) / kTile;
     r.bad = !span || !len;
     return r;
 }
@@ -146,12 +180,10 @@ __device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b) {
     Unit r;
     r.seq0 = b;
     r.num_seqs = 1;
-    r.tiles = len ? (n + kTile - 1) / kTile : 0;
+    r.tokens = len ? n : 0;
+    r.tiles = (r.tokens + kTile - 1) / kTile;
     r.bad = !len;
     return r;
-}
-__device__ __forceinline__ int unit_tokens(const PrefixArgs& a, int u) {
-    return u < a.num_groups ? a.prefix_tokens[u] : a.seq_tokens[u - a.num_groups];
 }
 // Steps of a unit on the line: an item takes kItemCost before its tiles.
 __device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
@@ -174,7 +206,7 @@ __device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Curs
     const int lane = threadIdx.x & 31, u = first + lane;
     const int units = a.num_groups + a.batch;
     Chunk c;
-    c.u = Unit{0, 0, 0, false};
+    c.u = Unit{0, 0, 0, 0, false};
     if (first < a.num_groups) {
         const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, at.bound);
         if (u < a.num_groups) c.u = group_unit(a, u, before);
@@ -209,18 +241,6 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
 __device__ __forceinline__ int ctas_of(int64_t total, int grid) {
     return total < grid ? static_cast<int>(total) : grid;
 }
-
-struct Piece {                      // a run of tiles of one item
-    const int32_t* table;
-    int tokens, kvh, seq0, row0;    // row r of the block: sequence seq0 + (row0 + r) / g, head kvh * g + (row0 + r) % g
-    int rows, tile0, tiles;
-    int64_t part;                   // its first partial row
-    uint32_t n;                     // pieces of this CTA before it
-
-    __device__ __forceinline__ bool wide() const { return rows > kNarrow; }
-    // tokens of its tile i
-    __device__ __forceinline__ int valid(int i) const { return min(kTile, tokens - (tile0 + i) * kTile); }
-};
 
 struct Walk {
     int64_t t, t_end;
@@ -290,7 +310,7 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
     p.tiles = static_cast<int>(min(static_cast<int64_t>(tiles - p.tile0), w.t_end - w.t));
     p.table = u < a.num_groups ? a.prefix_table + static_cast<int64_t>(u) * a.max_prefix_pages
                                : a.page_table + static_cast<int64_t>(u - a.num_groups) * a.max_pages;
-    p.tokens = unit_tokens(a, u);
+    p.tokens = __shfl_sync(0xffffffffu, w.c.u.tokens, at);
     p.seq0 = seq0;
     p.row0 = rb * kTile;
     p.rows = min(kTile, rows - p.row0);
@@ -310,13 +330,13 @@ __device__ __forceinline__ uint32_t v_entry(uint32_t t) { return 2 * t + 2; }
 // The loads of K (kValues false) or of V, a warp each: a box takes about 75 cycles to issue,
 // so one warp for the 32 boxes of a tile would bound the supply.
 template <bool kSplitQ, bool kValues>
-__device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl, Walk& w) {
+__device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
-    uint32_t t = 0;                               // tiles so far
+    uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     bool ok = true;
     Piece p;
-    while (ok && walk_next(a, w, p)) {
+    while (ok && next_piece(ctl, pieces, p, a.st)) {
         const int pages = (p.tokens + kPage - 1) / kPage;
         int ids = 0;                              // of four tiles, a page a lane
         for (int i = 0; i < p.tiles; ++i) {
@@ -405,12 +425,14 @@ __device__ __forceinline__ void write_queries(const PrefixArgs& a, const Piece& 
 }
 
 template <bool kSplitQ>
-__device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl, Walk& w) {
-    const int tid = threadIdx.x - (kThreads - kQueryThreads);
+__device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl) {
+    // warps 12, 13 and 15
+    const int tid = threadIdx.x < 14 * 32 ? threadIdx.x - 12 * 32 : threadIdx.x - 13 * 32;
+    uint32_t pieces = 0;
     uint32_t freed = 0;                           // pieces whose scores are known to be formed
     uint32_t after_wide = 0;                      // 1 + the last wide piece
     Piece p;
-    while (walk_next(a, w, p)) {
+    while (next_piece(ctl, pieces, p, a.st)) {
         // a narrow piece follows its unit's last user and any wide piece; a wide one, all
         uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
         for (; freed < need; ++freed) {
@@ -428,11 +450,6 @@ __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, C
 
 // In both the whole warp keeps step and its first lane issues.
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
-    const bool ok = wait_or_abort(bar, parity, ctl, st);
-    return __all_sync(0xffffffffu, ok) != 0;
-}
-
 // Whatever the warp issued reads shared and tensor memory: sees its end.
 __device__ __forceinline__ void end_products(uint64_t* bar, const DeviceStatus& st) {
     if ((threadIdx.x & 31) == 0) {
@@ -444,15 +461,14 @@ __device__ __forceinline__ void end_products(uint64_t* bar, const DeviceStatus& 
 
 // S = Q K^T, over each tile's live pages alone.
 template <bool kSplitQ>
-__device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr, uint32_t ring_addr, Control* ctl,
-                                           Walk& w) {
+__device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr, uint32_t ring_addr, Control* ctl) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = ctl->tmem;
-    uint32_t t = 0;                               // tiles so far
+    uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     bool ok = true;
     Piece p;
-    while (ok && walk_next(a, w, p)) {
+    while (ok && next_piece(ctl, pieces, p, a.st)) {
         ok = warp_wait(&ctl->q_full[p.n % kQueryUnits], (p.n / kQueryUnits) & 1, ctl, a.st);
         const uint32_t q_at = q_addr + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128));
         for (int i = 0; ok && i < p.tiles; ++i, ++t) {
@@ -484,15 +500,15 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
 
 // O_x += P_x V, over each tile's live pages alone.
 template <bool kSplitQ>
-__device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, Control* ctl, Walk& w) {
+__device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, Control* ctl) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
     constexpr uint32_t kValues = bf16_idesc(kTile, kD, true);
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = ctl->tmem;
-    uint32_t t = 0;                               // tiles so far
+    uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     bool ok = true;
     Piece p;
-    while (ok && walk_next(a, w, p)) {
+    while (ok && next_piece(ctl, pieces, p, a.st)) {
         for (int i = 0; ok && i < p.tiles; ++i, ++t) {
             const uint32_t seq = v_entry(t), slot = seq % kN, b = t & 1;
             const int valid = p.valid(i), live = (valid + kPage - 1) / kPage;
@@ -533,16 +549,16 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
 
 // --------------------------------------------------------------------- the softmax
 
-__device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl, Walk& w) {
+__device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
     const int tid = threadIdx.x - 128;            // 0..255
     const int x = tid >> 7, row = tid & 127;      // softmax group, row of the block (= tensor-memory lane)
     const int lane = tid & 31;
     const uint32_t lane_base = ctl->tmem + (static_cast<uint32_t>((tid >> 5) & 3) << 21);
     const uint32_t acc = lane_base + acc_col(x);
-    uint32_t t = 0;                               // tiles so far
+    uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     Piece p;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl, a.st); };
-    while (walk_next(a, w, p)) {
+    while (next_piece(ctl, pieces, p, a.st)) {
         const bool busy = (row & ~31) < p.rows;   // some row of this warp is real
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < p.tiles; ++i, ++t) {
@@ -632,6 +648,26 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl, W
     }
 }
 
+// Announces the CTA's pieces, and their end.
+__device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
+    const int lane = threadIdx.x & 31;
+    Walk w;
+    Piece p;
+    bool more = walk_begin(a, w);
+    for (uint32_t n = 0;; ++n) {
+        more = more && walk_next(a, w, p);
+        const int slot = n % kPieces;
+        if (!warp_wait(&ctl->p_free[slot], ((n / kPieces) & 1) ^ 1, ctl, a.st)) return;
+        if (lane == 0) {
+            if (!more) p.tiles = 0;
+            ctl->pieces[slot] = p;
+            mbar_arrive(&ctl->p_full[slot]);
+        }
+        __syncwarp();
+        if (!more) return;
+    }
+}
+
 // Writes where every sequence's tiles lie for the second launch, and reports bad lengths and
 // bounds. One warp.
 __device__ __forceinline__ void write_plan(const PrefixArgs& a) {
@@ -685,6 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(&ctl->values[b], 1);
             for (int x = 0; x < 2; ++x) mbar_init(&ctl->weights[x][b], 4);   // a warp each
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&ctl->p_full[i], 1);
+            mbar_init(&ctl->p_free[i], kPieceReaders);
+        }
         for (int i = 0; i < kQueryUnits; ++i) {
             mbar_init(&ctl->q_full[i], kQueryThreads);
             mbar_init(&ctl->q_free[i], 1);
@@ -700,16 +740,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     tc_fence_after_sync();
     grid_dependency_wait();
     allow_dependent_launch();
-    Walk w;
-    if (walk_begin(a, w)) {
-        if (warp == 0) run_loads<kSplitQ, false>(a, ring, ctl, w);
-        else if (warp == 3) run_loads<kSplitQ, true>(a, ring, ctl, w);
-        else if (warp == 1) run_scores<kSplitQ>(a, smem_u32(q_s), smem_u32(ring), ctl, w);
-        else if (warp == 2) run_values<kSplitQ>(a, ring, ctl, w);
-        else if (warp >= 12) run_queries<kSplitQ>(a, q_s, ctl, w);
-        else if (warp >= 4) run_softmax(a, ctl, w);
+    if (warp == 0) run_loads<kSplitQ, false>(a, ring, ctl);
+    else if (warp == 1) run_scores<kSplitQ>(a, smem_u32(q_s), smem_u32(ring), ctl);
+    else if (warp == 2) run_values<kSplitQ>(a, ring, ctl);
+    else if (warp == 3) run_loads<kSplitQ, true>(a, ring, ctl);
+    else if (warp < 12) run_softmax(a, ctl);
+    else if (warp != 14) run_queries<kSplitQ>(a, q_s, ctl);
+    else {
+        run_pieces(a, ctl);
+        if (blockIdx.x == 0) write_plan(a);               // off the way: the others still work
     }
-    if (warp == 0 && blockIdx.x == 0) write_plan(a);      // its loads are out: the groups still work
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
