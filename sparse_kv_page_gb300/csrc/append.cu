@@ -5,14 +5,14 @@
 // of y turns by its angle, (a cos - b sin, b cos + a sin), and the row is rounded
 // once into q_out or into its cache row. Values are copied (rounded) beside them.
 //
-// Half a warp holds a row, eight consecutive elements a lane: one 16-byte load for
-// 16-bit types, the mean by four shuffles, a pair's partner (i, i + rot/2) from the
-// lane rot/16 away, one 16-byte cache store. A warp takes a token's rows two at a time,
-// four such loads ahead, and shares nothing with other warps: a token's cosines and
-// sines are computed once by its warp, and each lane keeps those of its own elements.
-// The pass reads its inputs once and writes its outputs once, so HBM bounds it at prompt
-// lengths and latency at decode. (A CTA per token that met at a barrier after the angles
-// had too few loads in flight: 514 us for 65,536 tokens of 32 + 2 x 8 heads.)
+// Half a warp holds a row, a lane eight of its elements in two runs of four such that both
+// elements of a pair are in one lane: (4l.., rot/2 + 4l..) when pairs lie half the rotated
+// part apart, eight in a row when they are neighbours or not rotated. So a row costs four
+// shuffles (the mean) and no exchange. A warp takes a token's rows two at a time, several
+// loads ahead, and shares nothing with other warps: a token's cosines and sines are computed
+// once by its warp, and each lane keeps the four pairs that are its own. The pass reads its
+// inputs once and writes its outputs once, so HBM bounds it at prompt lengths and latency at
+// decode.
 //
 // Angles: a pair turns by position * inv_freq / (2 pi) turns, of which only the
 // fraction matters. The host rounds inv_freq / (2 pi) to a multiple of 2^-64 turns;
@@ -28,68 +28,51 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;                // row pairs in flight per warp
 
-// Inputs are read once: past L1.
-__device__ __forceinline__ uint4 load_once(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
+// Four consecutive elements; inputs are read once, past L1.
 template <typename T>
-struct Row8;                             // eight consecutive elements of a row
-
+struct Run4;
 template <>
-struct Row8<float> {
-    uint4 a, b;
+struct Run4<float> {
+    uint4 a;
     __device__ __forceinline__ void load(const float* p) {
-        a = load_once(p);
-        b = load_once(p + 4);
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w)
+                     : "l"(p));
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z);
-        x[3] = __uint_as_float(a.w), x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
-        x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+    }
+};
+struct Run4Half {
+    uint2 a;
+    __device__ __forceinline__ void load_raw(const void* p) {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(a.x), "=r"(a.y) : "l"(p));
     }
 };
 template <>
-struct Row8<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = load_once(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+struct Run4<__nv_bfloat16> : Run4Half {
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { load_raw(p); }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xffff0000u);
+        x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xffff0000u);
     }
 };
 template <>
-struct Row8<__half> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __half* p) { a = load_once(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+struct Run4<__half> : Run4Half {
+    __device__ __forceinline__ void load(const __half* p) { load_raw(p); }
+    __device__ __forceinline__ void get(float* x) const {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a.x));
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&a.y));
+        x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
     }
 };
 
-__device__ __forceinline__ void store_row8(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
-__device__ __forceinline__ void store_row8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // cos and sin (times scale) of a position's pair.
@@ -106,132 +89,158 @@ __device__ __forceinline__ float2 turn(int64_t pos, uint64_t turns, float scale)
     return make_float2(r.x * scale, r.y * scale);
 }
 
+// What a lane does to its eight elements of a row.
+struct Lane {
+    int o1, o2;                      // its runs of four
+    bool turned, neighbours;         // its pairs are rotated; they are (x[2i], x[2i + 1]), else (x[i], x[i + 4])
+    float c[4], s[4];
+    float w[8];                      // norm weights
+
+    template <bool kNorm>
+    __device__ __forceinline__ void apply(float (&x)[8], float eps) const {
+        if (kNorm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float scale = rsqrtf(ss * (1.f / kD) + eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * w[e];
+        }
+        if (turned) {
+            if (neighbours) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = x[2 * e], m = x[2 * e + 1];
+                    x[2 * e] = p * c[e] - m * s[e];
+                    x[2 * e + 1] = m * c[e] + p * s[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = x[e], m = x[e + 4];
+                    x[e] = p * c[e] - m * s[e];
+                    x[e + 4] = m * c[e] + p * s[e];
+                }
+            }
+        }
+    }
+};
+
+// Rows first + half, first + half + 2, ... < last of `src` (128 elements apart) through
+// `lane` (kTouch) into `dst` (dst_step elements apart), kAhead row pairs in flight.
+template <bool kTouch, bool kNorm, typename T, typename TO>
+__device__ __forceinline__ void rows(const T* src, TO* dst, int64_t dst_step, int first, int last, const Lane& lane,
+                                     float eps) {
+    constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
+    const int half = (threadIdx.x >> 4) & 1;
+    Run4<T> in[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int r = first + 2 * i + half;
+        if (r < last) {
+            in[i][0].load(src + r * kD + lane.o1);
+            in[i][1].load(src + r * kD + lane.o2);
+        }
+    }
+#pragma unroll 1
+    for (int r0 = first; r0 < last; r0 += 2 * kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + 2 * i + half;
+            float x[8];
+            in[i][0].get(x);
+            in[i][1].get(x + 4);
+            if (r + 2 * kAhead < last) {
+                in[i][0].load(src + (r + 2 * kAhead) * kD + lane.o1);
+                in[i][1].load(src + (r + 2 * kAhead) * kD + lane.o2);
+            }
+            if (kTouch) lane.apply<kNorm>(x, eps);
+            if (r < last) {
+                store4(dst + r * dst_step + lane.o1, x);
+                store4(dst + r * dst_step + lane.o2, x + 4);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void load_weights(Lane& lane, const float* w) {
+    const float4 a = *reinterpret_cast<const float4*>(w + lane.o1), b = *reinterpret_cast<const float4*>(w + lane.o2);
+    lane.w[0] = a.x, lane.w[1] = a.y, lane.w[2] = a.z, lane.w[3] = a.w;
+    lane.w[4] = b.x, lane.w[5] = b.y, lane.w[6] = b.z, lane.w[7] = b.w;
+}
+
 // A unit of work is `per_unit` head rows (even) of one token, heads of q first, then k, then v;
-// the warps of the grid stride over tokens * units_per_token of them.
+// a warp each.
 template <typename T, typename TQ>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, int units_per_token,
-                                                          int per_unit) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a,
+                                                             int units_per_token, int per_unit) {
     __shared__ __align__(16) float turn_s[kWarps][2][64];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & 15;                              // of the row; rows alternate between half warps
-    const int nq = a.q ? a.hq : 0, total = nq + 2 * a.hkv;
-    const int half_rot = a.rot_dim / 2, reach = half_rot >> 3;        // lanes per half of the rotated part
-    const bool upper = sub >= reach;
-    const int pair = a.interleaved ? 4 * sub : 8 * (upper ? sub - reach : sub);   // first pair of this lane
-    const bool turned = a.interleaved ? 8 * sub < a.rot_dim : sub < 2 * reach;
-    const int partner = (lane & 16) | (turned ? (upper ? sub - reach : sub + reach) : sub);
-    float* cos_s = turn_s[warp][0];
-    float* sin_s = turn_s[warp][1];
-    const int64_t units = static_cast<int64_t>(a.num_tokens) * units_per_token;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units; u += step) {
-        const int t = static_cast<int>(u / units_per_token);
-        const int first = static_cast<int>(u - static_cast<int64_t>(t) * units_per_token) * per_unit;
-        const int last = min(first + per_unit, total);
-        const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(t) * a.q_stride + sub * 8;
-        const T* k = static_cast<const T*>(a.k) + static_cast<int64_t>(t) * a.k_stride + sub * 8;
-        const T* v = static_cast<const T*>(a.v) + static_cast<int64_t>(t) * a.v_stride + sub * 8;
-        auto src = [&](int r) {
-            return r < nq ? q + r * kD : r < nq + a.hkv ? k + (r - nq) * kD : v + (r - nq - a.hkv) * kD;
-        };
-        Row8<T> in[kAhead];
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (u >= static_cast<int64_t>(a.num_tokens) * units_per_token) return;
+    const int t = static_cast<int>(u / units_per_token);
+    const int first = static_cast<int>(u - static_cast<int64_t>(t) * units_per_token) * per_unit;
+    const int index = a.cache_index[t];
+    const int seq = a.token_seq ? a.token_seq[t] : t;
+    const int l = threadIdx.x & 31, sub = l & 15;           // rows alternate between half warps
+    const int nq = a.q ? a.hq : 0, last = min(first + per_unit, nq + 2 * a.hkv);
+    const int pairs = a.rot_dim / 2;
+    float* cos_s = turn_s[threadIdx.x >> 5][0];
+    float* sin_s = turn_s[threadIdx.x >> 5][1];
+    Lane lane;
+    lane.neighbours = a.interleaved;
+    lane.turned = 8 * sub < a.rot_dim;
+    const bool apart = lane.turned && !a.interleaved;       // 4 * sub < pairs, as pairs is a multiple of 8
+    lane.o1 = apart ? 4 * sub : 8 * sub;
+    lane.o2 = apart ? pairs + 4 * sub : 8 * sub + 4;
+    for (int i = l; i < pairs; i += 32) {
+        const int64_t pos = a.positions[static_cast<int64_t>(a.axis[i]) * a.num_tokens + t];
+        const float2 cs = turn(pos, a.turns[i], a.rope_scale);
+        cos_s[i] = cs.x;
+        sin_s[i] = cs.y;
+    }
+    if (index < 0) return;                                  // padding; uniform: the warp has one token
+    const int lpage = index / kPage;
+    int page = -1;
+    if (seq >= 0 && seq < a.batch && lpage < a.max_pages)
+        page = a.page_table[static_cast<int64_t>(seq) * a.max_pages + lpage];
+    if (page < 0 || page >= a.num_phys) {
+        if (l == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        return;
+    }
+    __syncwarp();
+    if (lane.turned) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int r = first + 2 * i + (lane >> 4);
-            if (r < last) in[i].load(src(r));
+        for (int e = 0; e < 4; ++e) lane.c[e] = cos_s[4 * sub + e], lane.s[e] = sin_s[4 * sub + e];
+    }
+    if (first < nq) {
+        const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(t) * a.q_stride;
+        TQ* dst = static_cast<TQ*>(a.q_out) + static_cast<int64_t>(t) * a.hq * kD;
+        if (a.q_weight) {
+            load_weights(lane, a.q_weight);
+            rows<true, true>(src, dst, kD, first, min(last, nq), lane, a.eps);
+        } else {
+            rows<true, false>(src, dst, kD, first, min(last, nq), lane, a.eps);
         }
-        const int index = a.cache_index[t];
-        const int seq = a.token_seq ? a.token_seq[t] : t;
-        const int lpage = index / kPage;
-        int page = -1;
-        if (index >= 0 && seq >= 0 && seq < a.batch && lpage < a.max_pages)
-            page = a.page_table[static_cast<int64_t>(seq) * a.max_pages + lpage];
-        for (int i = lane; i < half_rot; i += 32) {
-            const int64_t pos = a.positions[static_cast<int64_t>(a.axis[i]) * a.num_tokens + t];
-            const float2 cs = turn(pos, a.turns[i], a.rope_scale);
-            cos_s[i] = cs.x;
-            sin_s[i] = cs.y;
+    }
+    const int64_t at = (static_cast<int64_t>(page) * a.hkv * kPage + index % kPage) * kD;
+    if (last > nq && first < nq + a.hkv) {
+        const T* src = static_cast<const T*>(a.k) + static_cast<int64_t>(t) * a.k_stride;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.k_cache) + at;
+        if (a.k_weight) {
+            load_weights(lane, a.k_weight);
+            rows<true, true>(src, dst, kPage * kD, max(first - nq, 0), min(last - nq, a.hkv), lane, a.eps);
+        } else {
+            rows<true, false>(src, dst, kPage * kD, max(first - nq, 0), min(last - nq, a.hkv), lane, a.eps);
         }
-        __syncwarp();
-        float c[8], s[8];
-        if (turned) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const bool used = e < 4 || !a.interleaved;
-                c[e] = used ? cos_s[pair + e] : 0.f;
-                s[e] = used ? sin_s[pair + e] : 0.f;
-            }
-        }
-        __syncwarp();
-        if (page < 0 || page >= a.num_phys) {               // uniform: the warp has one token
-            if (index >= 0 && lane == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-            continue;
-        }
-        const int64_t cache_row = static_cast<int64_t>(page) * a.hkv * kPage + index % kPage;
-#pragma unroll 1
-        for (int r0 = first; r0 < last; r0 += 2 * kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (r0 + 2 * i >= last) break;              // uniform
-                const int r = r0 + 2 * i + (lane >> 4);
-                const bool live = r < last;
-                const bool is_q = r < nq, is_v = r >= nq + a.hkv;
-                float x[8];
-                in[i].get(x);
-                {
-                    const int next = r + 2 * kAhead;
-                    if (next < last) in[i].load(src(next));
-                }
-                const float* w = is_q ? a.q_weight : a.k_weight;
-                const bool normed = live && !is_v && w;
-                if (__any_sync(0xffffffffu, normed)) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    if (normed) {
-                        const float scale = rsqrtf(ss * (1.f / kD) + a.eps);
-                        const float4 w0 = reinterpret_cast<const float4*>(w + sub * 8)[0];
-                        const float4 w1 = reinterpret_cast<const float4*>(w + sub * 8)[1];
-                        const float we[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * we[e];
-                    }
-                }
-                if (half_rot > 0 && __any_sync(0xffffffffu, live && !is_v)) {
-                    if (a.interleaved) {
-                        if (!is_v && turned) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float p = x[2 * e], m = x[2 * e + 1];
-                                x[2 * e] = p * c[e] - m * s[e];
-                                x[2 * e + 1] = m * c[e] + p * s[e];
-                            }
-                        }
-                    } else {
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
-                        if (!is_v && turned) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = x[e] * c[e] + (upper ? y[e] : -y[e]) * s[e];
-                        }
-                    }
-                }
-                if (live) {
-                    if (is_q) {
-                        store_row8(static_cast<TQ*>(a.q_out) + (static_cast<int64_t>(t) * a.hq + r) * kD + sub * 8, x);
-                    } else {
-                        const int h = is_v ? r - nq - a.hkv : r - nq;
-                        __nv_bfloat16* cache = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache);
-                        store_row8(cache + (cache_row + h * kPage) * kD + sub * 8, x);
-                    }
-                }
-            }
-        }
+    }
+    if (last > nq + a.hkv) {
+        const T* src = static_cast<const T*>(a.v) + static_cast<int64_t>(t) * a.v_stride;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.v_cache) + at;
+        rows<false, false>(src, dst, kPage * kD, max(first - nq - a.hkv, 0), last - nq - a.hkv, lane, a.eps);
     }
 }
 
