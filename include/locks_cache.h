@@ -140,11 +140,10 @@ LOCKS_API int locks_mass_workspace_size(const locks_dims_t* dims, size_t* bytes)
  *   (but may not overlap it otherwise). decay: finite; 1 sums, less forgets.
  *   With decay 0 the old mass is not read.
  * - lse_partials (may be NULL): the partials locks_score_pages wrote for these
- *   same scores and dims on this device; L_bh is then reduced from them (their
- *   sums hold +inf scores too) in one launch. Without them the scores are read
- *   twice, in two launches.
+ *   same scores and dims on this device; L_bh is then joined from them (their
+ *   sums hold +inf scores too) and the scores are read once instead of twice.
  * - seq_pages[b] out of [0, max_pages_per_seq] records LOCKS_ERR_BAD_INDEX and
- *   the sequence is skipped.
+ *   the sequence is skipped. Two kernel launches.
  */
 LOCKS_API int locks_accumulate_mass(const locks_dims_t* dims, const float* scores, const float* lse_partials,
                                     const int32_t* seq_pages, const float* mass, float* mass_out, float decay,

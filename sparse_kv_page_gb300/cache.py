@@ -237,9 +237,9 @@ def alloc_mass_workspace(dims: locks_dims_t, device="cuda") -> torch.Tensor:
 
 
 def locks_accumulate_mass(dims: locks_dims_t, scores: torch.Tensor, seq_pages: torch.Tensor, mass: torch.Tensor,
-                          mass_out: torch.Tensor, workspace: Optional[torch.Tensor] = None, decay: float = 1.0,
+                          mass_out: torch.Tensor, workspace: torch.Tensor, decay: float = 1.0,
                           lse_partials: Optional[torch.Tensor] = None, stream=None) -> None:
-    """mass_out may be mass. Without lse_partials the workspace is needed (alloc_mass_workspace)."""
+    """mass_out may be mass. lse_partials: those locks_score_pages wrote beside these scores."""
     dev, b, p = scores.get_device(), dims.batch, dims.max_pages_per_seq
     ws, nws = _ws(workspace, dev)
     partials = None

@@ -229,10 +229,7 @@ int locks_accumulate_mass(const locks_dims_t* dims, const float* scores, const f
     if (!std::isfinite(decay)) return LOCKS_ERR_INVALID_ARG;
     if (dims->batch > 65535) return LOCKS_ERR_UNSUPPORTED;              // a grid dimension
     const MassLayout w = mass_layout(dims);
-    if (!lse_partials || workspace) {
-        const size_t need = lse_partials ? kStatusBytes : w.total;
-        if ((s = locks::check_workspace(workspace, workspace_bytes, need)) != LOCKS_OK) return s;
-    }
+    if ((s = locks::check_workspace(workspace, workspace_bytes, w.total)) != LOCKS_OK) return s;
     if (dims->batch == 0 || dims->max_pages_per_seq == 0) return LOCKS_OK;
     if (!scores || !seq_pages || !mass || !mass_out) return LOCKS_ERR_INVALID_ARG;
     if (!aligned(scores, 4) || !aligned(mass, 4) || !aligned(mass_out, 4)) return LOCKS_ERR_INVALID_ARG;
@@ -252,15 +249,18 @@ int locks_accumulate_mass(const locks_dims_t* dims, const float* scores, const f
     a.max_pages = dims->max_pages_per_seq;
     a.st = locks::device_status(workspace);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float2* own = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.partials);
+    a.partials = own;
     if (lse_partials) {
-        a.partials = reinterpret_cast<const float2*>(lse_partials);
-        a.row = locks::scorer_partials_row(dims, sms);
+        a.row = 1;
+        s = cuda_status(locks::launch_mass_reduce(reinterpret_cast<const float2*>(lse_partials),
+                                                  locks::scorer_partials_row(dims, sms),
+                                                  static_cast<int64_t>(dims->batch) * dims->num_q_heads, own, st));
     } else {
-        float2* own = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.partials);
-        a.partials = own;
         a.row = locks::mass_partials_row(dims->max_pages_per_seq);
-        if ((s = cuda_status(locks::launch_mass_partials(a, own, st))) != LOCKS_OK) return s;
+        s = cuda_status(locks::launch_mass_partials(a, own, st));
     }
+    if (s != LOCKS_OK) return s;
     return cuda_status(locks::launch_mass(a, st));
 }
 

@@ -12,7 +12,8 @@
 // loads ahead, and shares nothing with other warps: a token's cosines and sines are computed
 // once by its warp, and each lane keeps the four pairs that are its own. The pass reads its
 // inputs once and writes its outputs once, so HBM bounds it at prompt lengths and latency at
-// decode.
+// decode. 24 warps an SM in CTAs of two: 269 us for 65,536 tokens of 32 + 2 x 8 heads, 88% of
+// the copy rate (32 warps of 64 registers spill: 286; CTAs of eight warps: 283).
 //
 // Angles: a pair turns by position * inv_freq / (2 pi) turns, of which only the
 // fraction matters. The host rounds inv_freq / (2 pi) to a multiple of 2^-64 turns;
@@ -21,12 +22,14 @@
 // the rounding of the factor. fp32 angles instead would be off by position * 2^-24
 // radians, 0.06 at 1M tokens. The nearest quarter turn is taken off in integers and
 // sincospi sees at most an eighth of a turn.
+#include <algorithm>
+
 #include "cache_internal.h"
 
 namespace locks {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 constexpr int kWarps = kThreads / 32;
 
 // Four consecutive elements; inputs are read once, past L1.
@@ -174,7 +177,7 @@ __device__ __forceinline__ void load_weights(Lane& lane, const float* w) {
 // A unit of work is `per_unit` head rows (even) of one token, heads of q first, then k, then v;
 // a warp each.
 template <typename T, typename TQ>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a,
+__global__ void __launch_bounds__(kThreads, 12) append_kernel(const __grid_constant__ AppendArgs a,
                                                              int units_per_token, int per_unit) {
     __shared__ __align__(16) float turn_s[kWarps][2][64];
     grid_dependency_wait();
@@ -247,10 +250,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 template <typename T, typename TQ>
 cudaError_t launch_t(const AppendArgs& a, int num_sms, cudaStream_t stream) {
     const int total = (a.q ? a.hq : 0) + 2 * a.hkv;
-    // Few tokens: a warp per pair of rows, so that the call is one round of loads. Many: a warp
-    // per token, which computes the token's angles once.
-    const bool few = static_cast<int64_t>(a.num_tokens) * total <= static_cast<int64_t>(num_sms) * 8 * kWarps;
-    const int per_unit = few ? 2 : (total + 1) / 2 * 2;
+    // Many tokens: a warp per token, which computes the token's angles once. Few: a token's rows
+    // spread over as many warps as are resident (a pair of rows each at least), so that the
+    // call is one round of loads.
+    const int64_t share = static_cast<int64_t>(a.num_tokens) * total / (12 * static_cast<int64_t>(num_sms));
+    const int per_unit = static_cast<int>(std::min<int64_t>((share + 3) / 2 * 2, (total + 1) / 2 * 2));
     const int units_per_token = (total + per_unit - 1) / per_unit;
     const int64_t ctas = (static_cast<int64_t>(a.num_tokens) * units_per_token + kWarps - 1) / kWarps;
     cudaLaunchConfig_t cfg = {};

@@ -54,6 +54,9 @@ struct MassArgs {
 // Pairs per (sequence, query head) that launch_mass_partials writes.
 int mass_partials_row(int max_pages);
 cudaError_t launch_mass_partials(const MassArgs& a, float2* partials, cudaStream_t stream);
+// Joins `row` pairs per (sequence, query head) to one.
+cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2* out, cudaStream_t stream);
+// Follows one of the two on the same stream.
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream);
 
 struct EvictArgs {

@@ -3,21 +3,21 @@
 //
 // Mass: share_h(j) = exp(s_hj - L_h), L_h = log sum_j exp(s_hj) over the sequence's
 // pages, added to each page's mass as the mean over the query heads. L_h needs every
-// score before the first share, so the scores are read twice: one launch takes a
-// (max, sum exp) pair per (query head, slice of pages), the next joins a head's pairs
-// and streams the scores again, this time from L2 (the score tables of 4 x 1M tokens at
-// 32 heads, 33.5 MB, fit in it several times). With the scorer's own pairs the first
-// launch falls away.
+// score before the first share, so the scores are read twice: the first launch takes a
+// (max, sum exp) pair per (query head, slice of pages), the second joins a head's pairs
+// and reads the scores again, this time from L2 (the score tables of 4 x 1M tokens at
+// 32 heads, 33.5 MB, fit in it several times). The scorer's own pairs, where given, are
+// joined to one per head by a first launch that does not touch the scores.
 #include "cache_internal.h"
 
 namespace locks {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSlicePages = 2048;        // pages per pair
+constexpr int kWarps = kThreads / 32;
+constexpr int kSlicePages = 8192;        // pages per pair
 constexpr int kPerThread = kSlicePages / kThreads;
-constexpr int kMassThreads = 128;
-constexpr int kMassPages = 4 * kMassThreads;   // pages per CTA of the second pass
+constexpr int kMassPages = 128;          // pages per CTA of the second launch, four a lane
 
 __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
     const float M = fmaxf(m, m2);
@@ -83,70 +83,103 @@ __global__ void __launch_bounds__(kThreads) partials_kernel(const MassArgs a, fl
     }
 }
 
-// Grid: (blocks of kMassPages pages, batch). Dynamic shared memory: a float2 per head,
-// its maximum and (1 / Hq) / sum.
-__global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a, bool vec) {
-    extern __shared__ float2 norm[];
+// The scorer's pairs, `row` per (sequence, query head), joined to one: a warp each.
+__global__ void __launch_bounds__(kThreads) reduce_kernel(const float2* in, int row, int64_t heads, float2* out) {
     grid_dependency_wait();
     allow_dependent_launch();
-    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    const int n = pages_of(a.seq_pages, b, a.max_pages);
-    if (n < 0) {
-        if (tid == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-        return;
+    const int64_t h = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (h >= heads) return;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < row; i += 32) {
+        const float2 v = in[h * row + i];
+        join(m, l, v.x, v.y);
     }
-    const int first = blockIdx.x * kMassPages;
-    if (first >= n) return;
-    for (int h = tid >> 5; h < a.hq; h += kMassThreads / 32) {
-        const float2* p = a.partials + (static_cast<int64_t>(b) * a.hq + h) * a.row;
-        float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < a.row; i += 32) {
-            const float2 v = p[i];
-            join(m, l, v.x, v.y);
-        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-        // no score above -inf, or a normaliser that is no number: the head adds nothing
-        const bool ok = m > -INFINITY && m < INFINITY && l > 0.f && l < INFINITY;
-        if (lane == 0) norm[h] = ok ? make_float2(m, 1.f / (l * a.hq)) : make_float2(0.f, 0.f);
-    }
-    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1)
+        join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+    if (lane == 0) out[h] = make_float2(m, l);
+}
+
+// Grid: (blocks of kMassPages pages, batch). Warp w adds up heads w, w + 8, ... of the CTA's
+// pages, and the warps' sums meet in shared memory. The scores were there before the first
+// launch began (it starts this one only after waiting for its own predecessor), so the
+// first of them are loaded before its pairs are waited for.
+__global__ void __launch_bounds__(kThreads) mass_kernel(const MassArgs a, bool vec) {
+    __shared__ float sums[kWarps][kMassPages];
+    constexpr int kBatch = 4;                               // heads in flight per warp
+    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = pages_of(a.seq_pages, b, a.max_pages);
+    const int first = blockIdx.x * kMassPages;
+    // a lane's four pages: side by side where the rows are whole 16-byte pieces
+    const int j0 = vec ? first + 4 * lane : first + lane, step = vec ? 1 : 32;
     const float* s = a.scores + static_cast<int64_t>(b) * a.hq * a.max_pages;
     const int64_t base = static_cast<int64_t>(b) * a.max_pages;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-        const int j = first + 4 * tid;
-        if (j >= n) return;
-#pragma unroll 8
-        for (int h = 0; h < a.hq; ++h) {
-            const float4 v = *reinterpret_cast<const float4*>(s + static_cast<int64_t>(h) * a.max_pages + j);
-            const float2 c = norm[h];
-            acc[0] += fast_exp2((score_of(v.x) - c.x) * kLog2e) * c.y;
-            acc[1] += fast_exp2((score_of(v.y) - c.x) * kLog2e) * c.y;
-            acc[2] += fast_exp2((score_of(v.z) - c.x) * kLog2e) * c.y;
-            acc[3] += fast_exp2((score_of(v.w) - c.x) * kLog2e) * c.y;
-        }
+    float4 x[kBatch];
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < n)
-                a.mass_out[base + j + e] = a.decay != 0.f ? a.mass[base + j + e] * a.decay + acc[e] : acc[e];
-    } else {
-#pragma unroll 4
-        for (int h = 0; h < a.hq; ++h) {
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = h0 + i * kWarps;
+            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (h >= a.hq) continue;
             const float* r = s + static_cast<int64_t>(h) * a.max_pages;
-            const float2 c = norm[h];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = first + e * kMassThreads + tid;
-                if (j < n) acc[e] += fast_exp2((score_of(r[j]) - c.x) * kLog2e) * c.y;
+            if (vec) {
+                if (j0 < n) x[i] = *reinterpret_cast<const float4*>(r + j0);
+            } else {
+                if (j0 < n) x[i].x = r[j0];
+                if (j0 + 32 < n) x[i].y = r[j0 + 32];
+                if (j0 + 64 < n) x[i].z = r[j0 + 64];
+                if (j0 + 96 < n) x[i].w = r[j0 + 96];
+            }
+        }
+    };
+    load(warp);
+    const int mine = first + tid;                           // threads 0..127 finish a page each
+    const bool writes = tid < kMassPages && mine < n;
+    const float old = writes && a.decay != 0.f ? a.mass[base + mine] * a.decay : 0.f;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (n < 0 && tid == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+    if (first >= n) return;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int h0 = warp; h0 < a.hq; h0 += kBatch * kWarps) {
+        if (h0 != warp) load(h0);
+        // eight lanes join the pairs of one of the four heads
+        float m = -INFINITY, l = 0.f;
+        const int h = h0 + (lane >> 3) * kWarps;
+        if (h < a.hq) {
+            const float2* p = a.partials + (static_cast<int64_t>(b) * a.hq + h) * a.row;
+            for (int i = lane & 7; i < a.row; i += 8) {
+                const float2 v = p[i];
+                join(m, l, v.x, v.y);
             }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = first + e * kMassThreads + tid;
-            if (j < n) a.mass_out[base + j] = a.decay != 0.f ? a.mass[base + j] * a.decay + acc[e] : acc[e];
+        for (int o = 4; o > 0; o >>= 1)
+            join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+        // no score above -inf, or a normaliser that is no number: the head adds nothing
+        const bool ok = m > -INFINITY && m < INFINITY && l > 0.f && l < INFINITY;
+        const float inv = ok ? 1.f / (l * a.hq) : 0.f;
+        m = ok ? m : 0.f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float mi = __shfl_sync(0xffffffffu, m, 8 * i), w = __shfl_sync(0xffffffffu, inv, 8 * i);
+            if (w == 0.f) continue;                         // also heads past the last; uniform
+            acc[0] += fast_exp2((score_of(x[i].x) - mi) * kLog2e) * w;
+            acc[1] += fast_exp2((score_of(x[i].y) - mi) * kLog2e) * w;
+            acc[2] += fast_exp2((score_of(x[i].z) - mi) * kLog2e) * w;
+            acc[3] += fast_exp2((score_of(x[i].w) - mi) * kLog2e) * w;
         }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[warp][j0 - first + e * step] = acc[e];
+    __syncthreads();
+    if (writes) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += sums[w][tid];
+        a.mass_out[base + mine] = old + sum;
     }
 }
 
@@ -174,18 +207,30 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, 
 
 // One cluster of CL CTAs per sequence. A CTA keeps its share of the sequence's masses and
 // table entries in shared memory: the inputs are read once, and all of them before the
-// first write, so the outputs may be the inputs. The e-th smallest key is found by a radix
-// select, most significant 8 bits first, on the order-preserving image of the mass; the
-// CTAs' histograms are joined through distributed shared memory.
+// first write, so the outputs may be the inputs. The e-th smallest key (order-preserving
+// image of the mass) is found by a radix select; the CTAs' histograms are joined through
+// distributed shared memory. What it costs is those exchanges (about 2.4 us each over 16
+// CTAs), so it stops as soon as it can: when all keys of the chosen bin are equal (pages
+// that never drew any mass), or when they are few enough for every CTA to gather and rank
+// them. One CTA alone takes 11 bits a pass; clusters take 8, as the bytes of 16 histograms
+// of 2048 bins cost more than the passes they save (4 x 65,536 pages: 26.6 us).
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kMaxBins = 2048;               // two 16-bit counts to a word
+template <int CL>
+constexpr int kDigit = CL == 1 ? 11 : 8;     // bits a pass
+constexpr int kGather = 256;
 
 struct EvictShared {
-    uint32_t hist[2][256];
-    uint32_t sum[256];
-    int wsum[2][kEvictWarps];
-    int digit, below;
-    int cnt[2];                          // this CTA's pages below / at the threshold
+    uint32_t hist[2][kMaxBins / 2];
+    uint32_t kmin[2], kmax[2];           // of the keys counted
+    uint32_t list[kGather], all[kGather];
+    int listed;
+    uint32_t wsum[kEvictWarps];
+    int digit, below, inside;
+    uint32_t key;
+    int want;
+    uint32_t cnt;                        // this CTA's pages below (high half) and at (low) the threshold
 };
 
 __device__ __forceinline__ uint32_t mass_key(float m) { return orderable_key(m + 0.f); }   // -0 counts as 0
@@ -195,31 +240,38 @@ __device__ __forceinline__ void join_sync() {
     if (CL == 1) __syncthreads();
     else cluster_sync_all();
 }
+template <int CL>
+__device__ __forceinline__ uint32_t of_cta(const uint32_t* p, int r) {
+    return CL == 1 ? *p : ld_dsmem_u32(dsmem_addr(p, r));
+}
 
-// Exclusive scan of two flags over the CTA (in thread order) and their totals.
-__device__ __forceinline__ void scan_flags(bool f0, bool f1, int (&pos)[2], int (&tot)[2], EvictShared& sh) {
+// Exclusive scan over the CTA in thread order, and the total. Two barriers.
+__device__ __forceinline__ uint32_t scan_cta(uint32_t v, uint32_t& total, EvictShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned b0 = __ballot_sync(0xffffffffu, f0), b1 = __ballot_sync(0xffffffffu, f1);
-    if (lane == 0) sh.wsum[0][warp] = __popc(b0), sh.wsum[1][warp] = __popc(b1);
+    uint32_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) sh.wsum[warp] = upto;
     __syncthreads();
-    int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
+    uint32_t before = 0, sum = 0;
 #pragma unroll
     for (int w = 0; w < kEvictWarps; ++w) {
-        const int c0 = sh.wsum[0][w], c1 = sh.wsum[1][w];
-        p0 += w < warp ? c0 : 0;
-        p1 += w < warp ? c1 : 0;
-        t0 += c0;
-        t1 += c1;
+        const uint32_t c = sh.wsum[w];
+        before += w < warp ? c : 0;
+        sum += c;
     }
     __syncthreads();
-    pos[0] = p0 + __popc(b0 & lanemask_lt());
-    pos[1] = p1 + __popc(b1 & lanemask_lt());
-    tot[0] = t0;
-    tot[1] = t1;
+    total = sum;
+    return before + upto - v;
 }
 
 template <int CL>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a, int share) {
+    constexpr int kBits = kDigit<CL>, kWords = (1 << kBits) / 2;
+    constexpr int kPer = (kWords + kEvictThreads - 1) / kEvictThreads;   // words of the histogram a thread
     __shared__ EvictShared sh;
     extern __shared__ float mass_s[];
     int32_t* table_s = reinterpret_cast<int32_t*>(mass_s + share);
@@ -239,120 +291,159 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a,
     const int end = n + min(a.extra, a.max_pages - n);      // entries that stay or leave
     const int64_t base = static_cast<int64_t>(b) * a.max_pages;
     const int first = rank * share, mine = max(0, min(share, end - first));
+#pragma unroll 4
     for (int i = tid; i < mine; i += kEvictThreads) {
         mass_s[i] = a.mass[base + first + i];
         table_s[i] = a.page_table[base + first + i];
     }
     // candidates: logical pages [lo, hi) of this CTA's share
     const int lo = max(0, a.sink - first), hi = min(mine, n - a.recent - first);
-    uint32_t prefix = 0;
-    int want = e;                                           // rank of the threshold among the candidates left
+    uint32_t key = 0;                                       // the threshold (its known high bits at first)
+    int want = e;                                           // its rank among the candidates left
     if (e > 0) {
+        if (tid == 0) sh.listed = 0;
 #pragma unroll 1
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
+        for (int pass = 0, shift = 32; shift > 0; ++pass) {
+            const int upto = shift, bits = min(kBits, shift);
+            shift -= bits;
             uint32_t* hist = sh.hist[pass & 1];
-            for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
+            for (int i = tid; i < kWords; i += kEvictThreads) hist[i] = 0;
+            if (tid == 0) sh.kmin[pass & 1] = 0xffffffffu, sh.kmax[pass & 1] = 0;
             __syncthreads();
+            uint32_t kmin = 0xffffffffu, kmax = 0;
             for (int i = lo + tid; i < hi; i += kEvictThreads) {
-                const uint32_t key = mass_key(mass_s[i]);
-                if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+                const uint32_t k = mass_key(mass_s[i]);
+                if (pass == 0 || k >> upto == key) {
+                    const uint32_t d = (k >> shift) & ((1u << bits) - 1);
+                    atomicAdd(&hist[d >> 1], 1u << (16 * (d & 1)));
+                    kmin = min(kmin, k);
+                    kmax = max(kmax, k);
+                }
+            }
+            if (pass > 0) {
+                kmin = __reduce_min_sync(0xffffffffu, kmin);
+                kmax = __reduce_max_sync(0xffffffffu, kmax);
+                if ((tid & 31) == 0) atomicMin(&sh.kmin[pass & 1], kmin), atomicMax(&sh.kmax[pass & 1], kmax);
             }
             join_sync<CL>();
-            if (tid < 256) {
-                uint32_t c = 0;
-                if (CL == 1) {
-                    c = hist[tid];
-                } else {
+            uint32_t c[2 * kPer] = {};                      // this thread's bins
+            if (tid * kPer < kWords) {
 #pragma unroll
-                    for (int r = 0; r < CL; ++r) c += ld_dsmem_u32(dsmem_addr(&hist[tid], r));
-                }
-                sh.sum[tid] = c;
-            }
-            __syncthreads();
-            if (tid < 32) {                                 // the bin that holds rank `want` (1-based)
-                uint32_t c[8], t = 0;
+                for (int r = 0; r < CL; ++r)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t += c[i] = sh.sum[tid * 8 + i];
-                uint32_t upto = t;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (tid >= o) upto += y;
-                }
-                uint32_t before = upto - t;
-                if (before < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= upto) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (before < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= before + c[i]) {
-                            sh.digit = tid * 8 + i;
-                            sh.below = static_cast<int>(before);
-                        }
-                        before += c[i];
+                    for (int i = 0; i < kPer; ++i) {
+                        const uint32_t u = of_cta<CL>(&hist[tid * kPer + i], r);
+                        c[2 * i] += u & 0xffffu;
+                        c[2 * i + 1] += u >> 16;
                     }
+            }
+            kmin = 0xffffffffu, kmax = 0;
+            if (pass > 0) {                                 // every warp learns the range of the keys
+                const int r = tid & 31;
+                if (r < CL) kmin = of_cta<CL>(&sh.kmin[pass & 1], r), kmax = of_cta<CL>(&sh.kmax[pass & 1], r);
+                kmin = __reduce_min_sync(0xffffffffu, kmin);
+                kmax = __reduce_max_sync(0xffffffffu, kmax);
+            }
+            if (pass > 0 && kmin == kmax) {                 // uniform in the cluster
+                key = kmin;
+                break;
+            }
+            uint32_t sum = 0, total;
+#pragma unroll
+            for (int i = 0; i < 2 * kPer; ++i) sum += c[i];
+            uint32_t before = scan_cta(sum, total, sh);
+#pragma unroll
+            for (int i = 0; i < 2 * kPer; ++i) {
+                if (before < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= before + c[i]) {
+                    sh.digit = 2 * kPer * tid + i;
+                    sh.below = static_cast<int>(before);
+                    sh.inside = static_cast<int>(c[i]);
                 }
+                before += c[i];
             }
             __syncthreads();
-            prefix = (prefix << 8) | static_cast<uint32_t>(sh.digit);
+            key = (key << bits) | static_cast<uint32_t>(sh.digit);
             want -= sh.below;
-        }
-        // prefix is now the threshold key; `want` of the pages at it leave, lowest first
-        int c0 = 0, c1 = 0;
-        for (int i = lo + tid; i < hi; i += kEvictThreads) {
-            const uint32_t key = mass_key(mass_s[i]);
-            c0 += key < prefix;
-            c1 += key == prefix;
-        }
-        c0 = __reduce_add_sync(0xffffffffu, c0);
-        c1 = __reduce_add_sync(0xffffffffu, c1);
-        if ((tid & 31) == 0) sh.wsum[0][tid >> 5] = c0, sh.wsum[1][tid >> 5] = c1;
-        __syncthreads();
-        if (tid == 0) {
-            c0 = c1 = 0;
-            for (int w = 0; w < kEvictWarps; ++w) c0 += sh.wsum[0][w], c1 += sh.wsum[1][w];
-            sh.cnt[0] = c0;
-            sh.cnt[1] = c1;
-        }
-    }
-    join_sync<CL>();                                        // counts, and every CTA's inputs are read
-    int out_before = 0, eq_before = 0;                      // evicted / at the threshold in lower CTAs
-    if (e > 0 && CL > 1) {
-        int less = 0;
-        for (int r = 0; r < rank; ++r) {
-            less += static_cast<int>(ld_dsmem_u32(dsmem_addr(&sh.cnt[0], r)));
-            eq_before += static_cast<int>(ld_dsmem_u32(dsmem_addr(&sh.cnt[1], r)));
-        }
-        out_before = less + min(eq_before, want);
-    }
-#pragma unroll 1
-    for (int i0 = 0; i0 < mine; i0 += kEvictThreads) {
-        const int i = i0 + tid;
-        const bool cand = e > 0 && i >= lo && i < hi;
-        const uint32_t key = cand ? mass_key(mass_s[i]) : 0u;
-        const bool less = cand && key < prefix, eq = cand && key == prefix;
-        int pos[2], tot[2];
-        scan_flags(less, eq, pos, tot, sh);
-        // of the pages at the threshold, those before this one that leave
-        const int eq_out = min(max(want - eq_before, 0), pos[1]);
-        const bool gone = less || (eq && eq_before + pos[1] < want);
-        const int before = out_before + pos[0] + eq_out;
-        if (i < mine) {
-            const int at = first + i;
-            if (gone) {
-                if (before < a.evict_cap) a.evicted[static_cast<int64_t>(b) * a.evict_cap + before] = table_s[i];
-            } else {
-                a.page_table_out[base + at - before] = table_s[i];
-                a.mass_out[base + at - before] = mass_s[i];
+            const int inside = sh.inside;
+            if (shift > 0 && inside <= kGather) {            // uniform in the cluster: rank them here
+                for (int i = lo + tid; i < hi; i += kEvictThreads) {
+                    const uint32_t k = mass_key(mass_s[i]);
+                    if (k >> shift == key) sh.list[atomicAdd(&sh.listed, 1)] = k;
+                }
+                join_sync<CL>();
+                if (tid < kGather) {                        // the tid-th key of all lists
+                    int from = -1, at = tid;
+                    for (int r = 0; r < CL; ++r) {
+                        const int cr = static_cast<int>(of_cta<CL>(reinterpret_cast<const uint32_t*>(&sh.listed), r));
+                        if (from < 0) {
+                            if (at < cr) from = r;
+                            else at -= cr;
+                        }
+                    }
+                    sh.all[tid] = from < 0 ? 0xffffffffu : of_cta<CL>(&sh.list[at], from);
+                }
+                __syncthreads();
+                if (tid < inside) {
+                    const uint32_t k = sh.all[tid];
+                    int less = 0, same = 0;
+                    for (int i = 0; i < inside; ++i) {
+                        less += sh.all[i] < k;
+                        same += sh.all[i] == k;
+                    }
+                    if (less < want && want <= less + same) sh.key = k, sh.want = want - less;   // equal writers agree
+                }
+                __syncthreads();
+                key = sh.key;
+                want = sh.want;
+                break;
             }
         }
-        out_before += tot[0] + min(max(want - eq_before, 0), tot[1]);
-        eq_before += tot[1];
+    }
+    // `want` of the pages at the threshold leave, lowest first. A thread takes pages side by
+    // side (an odd number of them: no bank conflicts), so that one scan places them all.
+    const int per = (share + kEvictThreads - 1) / kEvictThreads | 1;
+    const int i0 = min(tid * per, mine), i1 = min(i0 + per, mine);
+    uint32_t mark = 0;                                      // below (high half) and at (low half) the threshold
+    if (e > 0) {
+        for (int i = max(i0, lo); i < min(i1, hi); ++i) {
+            const uint32_t k = mass_key(mass_s[i]);
+            mark += k < key ? 0x10000u : k == key ? 1u : 0u;
+        }
+    }
+    uint32_t total;
+    mark = scan_cta(mark, total, sh);
+    int less_before = mark >> 16, eq_before = mark & 0xffffu;
+    if (CL > 1) {
+        if (tid == 0) sh.cnt = total;
+        cluster_sync_all();                                 // also: every CTA has read its inputs
+        const int r = tid & 31;
+        const uint32_t c = r < rank ? ld_dsmem_u32(dsmem_addr(&sh.cnt, r)) : 0u;
+        less_before += __reduce_add_sync(0xffffffffu, c >> 16);
+        eq_before += __reduce_add_sync(0xffffffffu, c & 0xffffu);
+        // shared memory stays until every CTA has read it
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    for (int i = i0; i < i1; ++i) {
+        const float m = mass_s[i];
+        const int32_t t = table_s[i];
+        const bool cand = e > 0 && i >= lo && i < hi;
+        const uint32_t k = mass_key(m);
+        const bool less = cand && k < key, eq = cand && k == key;
+        const int before = less_before + min(eq_before, want);
+        if (less || (eq && eq_before < want)) {
+            if (before < a.evict_cap) a.evicted[static_cast<int64_t>(b) * a.evict_cap + before] = t;
+        } else {
+            a.page_table_out[base + first + i - before] = t;
+            a.mass_out[base + first + i - before] = m;
+        }
+        less_before += less;
+        eq_before += eq;
     }
     if (rank == 0 && tid == 0) {
         a.n_evicted[b] = e;
         a.seq_pages_out[b] = n - e;
     }
-    join_sync<CL>();                                        // shared memory stays until every reader is done
+    if (CL > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int CL>
@@ -389,8 +480,12 @@ cudaError_t launch_mass_partials(const MassArgs& a, float2* partials, cudaStream
 
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream) {
     const int blocks = (a.max_pages + kMassPages - 1) / kMassPages;
-    return launch_pdl(mass_kernel, dim3(blocks, a.batch, 1), kMassThreads, a.hq * sizeof(float2), stream, a,
-                      rows_aligned(a));
+    return launch_pdl(mass_kernel, dim3(blocks, a.batch, 1), kThreads, 0, stream, a, rows_aligned(a));
+}
+
+cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2* out, cudaStream_t stream) {
+    return launch_pdl(reduce_kernel, dim3(static_cast<unsigned>((heads + kWarps - 1) / kWarps)), kThreads, 0, stream, in,
+                      row, heads, out);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
