@@ -220,6 +220,8 @@ constexpr int kMaxBins = 2048;               // two 16-bit counts to a word
 template <int CL>
 constexpr int kDigit = CL == 1 ? 11 : 8;     // bits a pass
 constexpr int kGather = 256;
+constexpr int kMaxShare = 24576;             // pages of a CTA
+static_assert(16 * kMaxShare == kMaxEvictPages, "the longest table");
 
 struct EvictShared {
     uint32_t hist[2][kMaxBins / 2];
@@ -489,9 +491,12 @@ cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2*
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-    // A cluster barrier costs about as much as a pass over a few thousand pages: one CTA
-    // takes short tables, sixteen the long ones (24,576 pages each at most).
-    if (a.max_pages <= 4096) return launch_evict_t<1>(a, stream);
+    // More CTAs a sequence shorten the passes over its pages and lengthen every exchange.
+    // us a call with 1 / 8 / 16 CTAs a sequence: one sequence of 1024 pages 6.5 / 7.2 / 8.1, of
+    // 8192 15.9 / 6.2 / 7.8, of 16,384 - / 7.9 / 8.3, of 65,536 - / 18.3 / 14.0; eight of
+    // 65,536 - / 18.9 / 21.2. Sixteen also hold the longest tables (24,576 pages a CTA at most).
+    if (a.max_pages <= 1024) return launch_evict_t<1>(a, stream);
+    if (a.max_pages <= 16384 || (a.batch > 4 && a.max_pages <= 8 * kMaxShare)) return launch_evict_t<8>(a, stream);
     return launch_evict_t<16>(a, stream);
 }
 
