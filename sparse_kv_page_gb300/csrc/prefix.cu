@@ -74,6 +74,7 @@ struct Piece {                      // a run of tiles of one item
     int rows, tile0, tiles;         // no tiles: the end
     int64_t part;                   // its first partial row
     uint32_t n;                     // pieces of this CTA before it
+    bool once;                      // no other block of rows reads its K and V
 
     __device__ __forceinline__ bool wide() const { return rows > kNarrow; }
     // tokens of its tile i
@@ -136,9 +137,11 @@ __device__ __forceinline__ bool next_piece(Control* ctl, uint32_t& n, Piece& p, 
 
 // ----------------------------------------------------------------- the line of tiles
 
-// The line is counted in steps: one per tile and kItemCost per item, about what the first
-// tile of an item costs over the others (its queries, its partial, a pipeline that fills).
-constexpr int kItemCost = 1;
+// The line is counted in steps: one per tile, and ahead of an item's tiles what starting it
+// costs, in tiles: its queries, its partials, a pipeline that fills. A wide item's queries
+// wait for the ones before to be used up.
+constexpr int kNarrowCost = 1, kWideCost = 3;
+__device__ __forceinline__ int item_cost(int rows) { return rows > kNarrow ? kWideCost : kNarrowCost; }
 
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
 
@@ -185,9 +188,10 @@ __device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b) {
     r.bad = !len;
     return r;
 }
-// Steps of a unit on the line: an item takes kItemCost before its tiles.
+// Steps of a unit on the line: an item's cost goes before its tiles.
 __device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
-    return u.tiles == 0 ? 0 : static_cast<int64_t>(u.tiles + kItemCost) * blocks_of(u.num_seqs * (a.hq / a.hkv)) * a.hkv;
+    const int rows = u.num_seqs * (a.hq / a.hkv);
+    return u.tiles == 0 ? 0 : static_cast<int64_t>(u.tiles + item_cost(rows)) * blocks_of(rows) * a.hkv;
 }
 
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
@@ -279,7 +283,7 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
 
 __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p) {
     const int g = a.hq / a.hkv;
-    int at, tiles, rows, step;
+    int at, tiles, rows, cost, step;
     int64_t item;
     for (;;) {
         if (w.t >= w.t_end) return false;
@@ -290,23 +294,24 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
         const unsigned in = __ballot_sync(0xffffffffu, w.c.step0 <= w.t && w.t < w.c.step0 + w.c.count);
         at = __ffs(in) - 1;         // exactly one
         tiles = __shfl_sync(0xffffffffu, w.c.u.tiles, at);
+        rows = __shfl_sync(0xffffffffu, w.c.u.num_seqs, at) * g;
+        cost = item_cost(rows);
         const int64_t off = w.t - shfl64(w.c.step0, at);
         if (off < (1ll << 31)) {
-            item = static_cast<int>(off) / (tiles + kItemCost);
+            item = static_cast<int>(off) / (tiles + cost);
         } else {
-            item = off / (tiles + kItemCost);
+            item = off / (tiles + cost);
         }
-        step = static_cast<int>(off - item * (tiles + kItemCost));
-        if (step >= kItemCost) break;
-        w.t += kItemCost - step;    // the item's first tile, if it is this CTA's
+        step = static_cast<int>(off - item * (tiles + cost));
+        if (step >= cost) break;
+        w.t += cost - step;         // the item's first tile, if it is this CTA's
     }
-    rows = __shfl_sync(0xffffffffu, w.c.u.num_seqs, at) * g;
     const int seq0 = __shfl_sync(0xffffffffu, w.c.u.seq0, at);
     const int part0 = __shfl_sync(0xffffffffu, w.c.row0, at);
     const int u = w.first + at, blocks = blocks_of(rows);
     const int rb = static_cast<int>(item) % blocks;
     p.kvh = static_cast<int>(item) / blocks;
-    p.tile0 = step - kItemCost;
+    p.tile0 = step - cost;
     p.tiles = static_cast<int>(min(static_cast<int64_t>(tiles - p.tile0), w.t_end - w.t));
     p.table = u < a.num_groups ? a.prefix_table + static_cast<int64_t>(u) * a.max_prefix_pages
                                : a.page_table + static_cast<int64_t>(u - a.num_groups) * a.max_pages;
@@ -316,6 +321,7 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
     p.rows = min(kTile, rows - p.row0);
     p.part = static_cast<int64_t>(part0) + p.kvh * rows + p.row0 + static_cast<int64_t>(blockIdx.x) * kTile;
     p.n = w.pieces++;
+    p.once = blocks == 1;
     w.t += p.tiles;
     return true;
 }
@@ -333,6 +339,7 @@ template <bool kSplitQ, bool kValues>
 __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
     const int lane = threadIdx.x & 31;
+    const uint64_t first_out = policy_evict_first(), normal = policy_evict_normal();
     uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     bool ok = true;
     Piece p;
@@ -359,8 +366,9 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
             __syncwarp();
             if (lane < 2 * kTilePages && (lane & 7) < live) {
                 const int half = lane >> 3;
-                tma_load_2d(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes,
-                            kValues ? &a.tm_v : &a.tm_k, half * 64, (id * a.hkv + p.kvh) * kPage, &ctl->full[slot]);
+                tma_load_2d_hint(ring + slot * kTileBytes + half * kHalfBytes + (lane & 7) * kBoxBytes,
+                                 kValues ? &a.tm_v : &a.tm_k, half * 64, (id * a.hkv + p.kvh) * kPage,
+                                 &ctl->full[slot], p.once ? first_out : normal);
             }
             __syncwarp();
             ++t;
@@ -379,67 +387,67 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
 
 // Rows of a piece's queries as bf16 high parts (and low parts behind them) in the 128-byte
 // swizzle: a narrow piece in unit p.n % 8 (16 rows), a wide one from the first unit on. Rows
-// past the piece's keep what they held.
-template <bool kSplitQ>
-__device__ __forceinline__ void write_queries(const PrefixArgs& a, const Piece& p, uint8_t* q_s, int tid) {
-    constexpr int kInFlight = kSplitQ ? 4 : 8;
-    const int g = a.hq / a.hkv, chunks = p.rows * 16;
-    q_s += p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128);
-    for (int i0 = tid; i0 < chunks; i0 += kQueryThreads * kInFlight) {
-        uint4 in[kInFlight][kSplitQ ? 2 : 1];
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            const int i = i0 + u * kQueryThreads;
-            if (i >= chunks) break;
-            const int row = p.row0 + (i >> 4);
-            const int64_t src = (static_cast<int64_t>(p.seq0 + row / g) * a.hq + p.kvh * g + row % g) * kD + (i & 15) * 8;
-            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + src * (kSplitQ ? 4 : 2));
-            in[u][0] = s[0];
-            if (kSplitQ) in[u][kSplitQ ? 1 : 0] = s[1];
-        }
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            const int i = i0 + u * kQueryThreads;
-            if (i >= chunks) break;
-            const int r = i >> 4, c = i & 15;
-            uint8_t* dst = q_s + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            if (kSplitQ) {
-                const uint4 v0 = in[u][0], v1 = in[u][kSplitQ ? 1 : 0];
-                const float x[8] = {__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z),
-                                    __uint_as_float(v0.w), __uint_as_float(v1.x), __uint_as_float(v1.y),
-                                    __uint_as_float(v1.z), __uint_as_float(v1.w)};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-                    lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
-                                        x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
-                }
-                *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(dst + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-                *reinterpret_cast<uint4*>(dst) = in[u][0];
-            }
-        }
-    }
-}
-
+// past the piece's keep what they held. A thread takes one 16-byte chunk of every sixth row,
+// eight rows in flight; the first eight are loaded before the space is free.
 template <bool kSplitQ>
 __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl) {
+    constexpr int kInFlight = 8, kRowStep = kQueryThreads / 16;
+    constexpr int kWords = kSplitQ ? 2 : 1;                 // 16-byte loads a chunk
     // warps 12, 13 and 15
     const int tid = threadIdx.x < 14 * 32 ? threadIdx.x - 12 * 32 : threadIdx.x - 13 * 32;
+    const int c = tid & 15, row0 = tid >> 4, g = a.hq / a.hkv;
     uint32_t pieces = 0;
     uint32_t freed = 0;                           // pieces whose scores are known to be formed
     uint32_t after_wide = 0;                      // 1 + the last wide piece
     Piece p;
     while (next_piece(ctl, pieces, p, a.st)) {
+        uint8_t* dst = q_s + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128)) + (c >> 3) * kHalfBytes;
+        int r = row0;
+        int seq = (p.row0 + r) / g, h = (p.row0 + r) - seq * g;   // of row r, and of the next to load
+        uint4 in[kInFlight][kWords];
+        auto load = [&](int from) {
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                if (from + u * kRowStep >= p.rows) break;
+                const int64_t src = (static_cast<int64_t>(p.seq0 + seq) * a.hq + p.kvh * g + h) * kD + c * 8;
+                const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + src * (kSplitQ ? 4 : 2));
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) in[u][k] = s[k];
+                for (h += kRowStep; h >= g; h -= g) ++seq;
+            }
+        };
+        load(r);
         // a narrow piece follows its unit's last user and any wide piece; a wide one, all
-        uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
-        for (; freed < need; ++freed) {
-            bool ok = wait_or_abort(&ctl->q_free[freed % kQueryUnits], (freed / kQueryUnits) & 1, ctl, a.st);
-            if (!__all_sync(0xffffffffu, ok)) return;
+        const uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
+        for (; freed < need; ++freed)
+            if (!warp_wait(&ctl->q_free[freed % kQueryUnits], (freed / kQueryUnits) & 1, ctl, a.st)) return;
+        while (r < p.rows) {
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                const int at = r + u * kRowStep;
+                if (at >= p.rows) break;
+                uint8_t* to = dst + at * 128 + (((c & 7) ^ (at & 7)) << 4);
+                if (kSplitQ) {
+                    const uint4 v0 = in[u][0], v1 = in[u][kWords - 1];
+                    const float x[8] = {__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z),
+                                        __uint_as_float(v0.w), __uint_as_float(v1.x), __uint_as_float(v1.y),
+                                        __uint_as_float(v1.z), __uint_as_float(v1.w)};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                        lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
+                                            x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                    }
+                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                } else {
+                    *reinterpret_cast<uint4*>(to) = in[u][0];
+                }
+            }
+            r += kInFlight * kRowStep;
+            load(r);
         }
-        write_queries<kSplitQ>(a, p, q_s, tid);
         fence_proxy_async_smem();
         mbar_arrive(&ctl->q_full[p.n % kQueryUnits]);
         if (p.wide()) after_wide = p.n + 1;
@@ -649,15 +657,26 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
 }
 
 // Announces the CTA's pieces, and their end.
+template <bool kSplitQ>
 __device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
     const int lane = threadIdx.x & 31;
     Walk w;
     Piece p;
+    const uint64_t keep = policy_evict_last();
     bool more = walk_begin(a, w);
     for (uint32_t n = 0;; ++n) {
         more = more && walk_next(a, w, p);
         const int slot = n % kPieces;
         if (!warp_wait(&ctl->p_free[slot], ((n / kPieces) & 1) ^ 1, ctl, a.st)) return;
+        if (more) {
+            // its queries (g rows of each sequence, side by side) into L2, to stay: behind a
+            // saturated HBM a load takes several us, and a wide piece's come in three rounds
+            const int g = a.hq / a.hkv, bytes = g * kD * (kSplitQ ? 4 : 2);
+            for (int s = p.row0 / g + lane; s * g < p.row0 + p.rows; s += 32)
+                prefetch_l2_kept(static_cast<const uint8_t*>(a.q) +
+                                     (static_cast<int64_t>(p.seq0 + s) * a.hkv + p.kvh) * bytes,
+                                 bytes, keep);
+        }
         if (lane == 0) {
             if (!more) p.tiles = 0;
             ctl->pieces[slot] = p;
@@ -747,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     else if (warp < 12) run_softmax(a, ctl);
     else if (warp != 14) run_queries<kSplitQ>(a, q_s, ctl);
     else {
-        run_pieces(a, ctl);
+        run_pieces<kSplitQ>(a, ctl);
         if (blockIdx.x == 0) write_plan(a);               // off the way: the others still work
     }
     tc_fence_before_sync();
@@ -781,7 +800,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
     const int n = ctas_of(total, grid);
     int first_o = 0, count_o = 0;                           // CTAs with a piece of the own tokens
     if (s.own_tiles > 0) {
-        const int64_t t = s.own_step0 + static_cast<int64_t>(kvh) * (s.own_tiles + kItemCost) + kItemCost;
+        const int cost = item_cost(g);
+        const int64_t t = s.own_step0 + static_cast<int64_t>(kvh) * (s.own_tiles + cost) + cost;
         first_o = cta_of(total, t, n);
         count_o = cta_of(total, t + s.own_tiles - 1, n) - first_o + 1;
     }
@@ -790,7 +810,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
     if (s.pre_tiles > 0) {
         const int rows = s.pre_num_seqs * g, row_in = (b - s.pre_seq0) * g + h;
         const int64_t item = static_cast<int64_t>(kvh) * blocks_of(rows) + row_in / kTile;
-        const int64_t t = s.pre_step0 + item * (s.pre_tiles + kItemCost) + kItemCost;
+        const int cost = item_cost(rows);
+        const int64_t t = s.pre_step0 + item * (s.pre_tiles + cost) + cost;
         first_p = cta_of(total, t, n);
         count_p = cta_of(total, t + s.pre_tiles - 1, n) - first_p + 1;
         row_p = static_cast<int64_t>(s.pre_row0) + kvh * rows + row_in;
