@@ -140,7 +140,7 @@ __device__ __forceinline__ bool next_piece(Control* ctl, uint32_t& n, Piece& p, 
 // The line is counted in steps: one per tile, and ahead of an item's tiles what starting it
 // costs, in tiles: its queries, its partials, a pipeline that fills. A wide item's queries
 // wait for the ones before to be used up.
-constexpr int kNarrowCost = 1, kWideCost = 3;
+constexpr int kNarrowCost = 1, kWideCost = 6;
 __device__ __forceinline__ int item_cost(int rows) { return rows > kNarrow ? kWideCost : kNarrowCost; }
 
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
