@@ -203,6 +203,7 @@ int locks_prefix_attention(const locks_dims_t* dims, const void* q, int32_t q_ty
     a.batch = dims->batch;
     a.hq = dims->num_q_heads;
     a.hkv = dims->num_kv_heads;
+    a.group = a.hq / a.hkv;
     a.max_pages = dims->max_pages_per_seq;
     a.num_phys = dims->num_phys_pages;
     a.total = reinterpret_cast<int64_t*>(base + kStatusBytes);

@@ -90,6 +90,7 @@ struct PrefixArgs {
     uint16_t* out;
     float* lse;                    // nullable
     int num_groups, max_prefix_pages, batch, hq, hkv, max_pages, num_phys, q_type;
+    int group;                     // hq / hkv
     // workspace regions (prefix_layout)
     int64_t* total;                // steps of the whole call
     struct PrefixSeq* seqs;        // [batch]

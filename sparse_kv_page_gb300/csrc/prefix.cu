@@ -102,21 +102,35 @@ static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024,
 __host__ __device__ constexpr uint32_t score_col(int b) { return b * 128; }
 __host__ __device__ constexpr uint32_t acc_col(int x) { return 256 + x * 128; }
 
-// A wait that gives up after the limit, or once another warp of the CTA has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
-    if (mbar_try_wait(bar, parity)) return true;
+// A wait that gives up after the limit, or once another warp of the CTA has. Out of line: the
+// roles' code together is larger than the nearer instruction caches, and behind a saturated
+// HBM a fetch from L2 takes microseconds.
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                       uint64_t limit_ns) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
         if ((it & 63u) == 0) {
-            if (*static_cast<volatile int*>(&ctl->abort)) return false;
-            if (global_timer_ns() - t0 > st.wait_limit_ns) {
-                *static_cast<volatile int*>(&ctl->abort) = 1;
-                report_error(st, LOCKS_ERR_TIMEOUT);
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > limit_ns) {
+                *abort = 1;
+                if (status) atomicCAS(status, 0, LOCKS_ERR_TIMEOUT);
                 return false;
             }
         }
     }
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return slow_wait(smem_u32(bar), parity, &ctl->abort, st.word, st.wait_limit_ns);
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Control* ctl, const DeviceStatus& st) {
@@ -190,7 +204,7 @@ __device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b) {
 }
 // Steps of a unit on the line: an item's cost goes before its tiles.
 __device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
-    const int rows = u.num_seqs * (a.hq / a.hkv);
+    const int rows = u.num_seqs * (a.group);
     return u.tiles == 0 ? 0 : static_cast<int64_t>(u.tiles + item_cost(rows)) * blocks_of(rows) * a.hkv;
 }
 
@@ -206,7 +220,7 @@ struct Cursor {                     // what lies before a chunk
     int64_t steps;
     int rows, bound;
 };
-__device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor& at) {
+__device__ __noinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor& at) {
     const int lane = threadIdx.x & 31, u = first + lane;
     const int units = a.num_groups + a.batch;
     Chunk c;
@@ -233,14 +247,16 @@ __device__ __forceinline__ Chunk load_chunk(const PrefixArgs& a, int first, Curs
     return c;
 }
 
-// First step of CTA c of n on a line of `total` steps, and the CTA of a step (32-bit division
-// where it will do: a 64-bit one is a long routine).
-__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int n) { return total * c / n; }
+// First step of CTA c of n on a line of `total` steps, and the CTA of a step. (32-bit division
+// where it will do: a 64-bit one is a long routine, kept in one place.)
+__device__ __noinline__ int64_t divide64(int64_t x, int64_t y) { return x / y; }
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    if (x < (1ll << 32) && y < (1ll << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return divide64(x, y);
+}
+__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int n) { return divide(total * c, n); }
 __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
-    const int64_t v = (step + 1) * n - 1;
-    if (v < (1ll << 32) && total < (1ll << 32))
-        return static_cast<int>(static_cast<uint32_t>(v) / static_cast<uint32_t>(total));
-    return static_cast<int>(v / total);
+    return static_cast<int>(divide((step + 1) * n - 1, total));
 }
 __device__ __forceinline__ int ctas_of(int64_t total, int grid) {
     return total < grid ? static_cast<int>(total) : grid;
@@ -264,12 +280,13 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
     w.c = load_chunk(a, 0, w.at);
     int64_t sum = 0;
     int bound = w.at.bound;
+#pragma unroll 1
     for (int u0 = 32; u0 < a.num_groups; u0 += 32) {
         const int u = u0 + lane;
         const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, bound);
         if (u < a.num_groups) sum += unit_steps(a, group_unit(a, u, before));
     }
-#pragma unroll 4
+#pragma unroll 1
     for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_steps(a, own_unit(a, b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -282,7 +299,7 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
 }
 
 __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p) {
-    const int g = a.hq / a.hkv;
+    const int g = a.group;
     int at, tiles, rows, cost, step;
     int64_t item;
     for (;;) {
@@ -297,11 +314,7 @@ __device__ __forceinline__ bool walk_next(const PrefixArgs& a, Walk& w, Piece& p
         rows = __shfl_sync(0xffffffffu, w.c.u.num_seqs, at) * g;
         cost = item_cost(rows);
         const int64_t off = w.t - shfl64(w.c.step0, at);
-        if (off < (1ll << 31)) {
-            item = static_cast<int>(off) / (tiles + cost);
-        } else {
-            item = off / (tiles + cost);
-        }
+        item = divide(off, tiles + cost);
         step = static_cast<int>(off - item * (tiles + cost));
         if (step >= cost) break;
         w.t += cost - step;         // the item's first tile, if it is this CTA's
@@ -388,14 +401,15 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
 // Rows of a piece's queries as bf16 high parts (and low parts behind them) in the 128-byte
 // swizzle: a narrow piece in unit p.n % 8 (16 rows), a wide one from the first unit on. Rows
 // past the piece's keep what they held. A thread takes one 16-byte chunk of every sixth row,
-// eight rows in flight; the first eight are loaded before the space is free.
+// four rows in flight; the first four are loaded before the space is free.
 template <bool kSplitQ>
 __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl) {
-    constexpr int kInFlight = 8, kRowStep = kQueryThreads / 16;
+    constexpr int kInFlight = 4, kRowStep = kQueryThreads / 16;
     constexpr int kWords = kSplitQ ? 2 : 1;                 // 16-byte loads a chunk
     // warps 12, 13 and 15
     const int tid = threadIdx.x < 14 * 32 ? threadIdx.x - 12 * 32 : threadIdx.x - 13 * 32;
-    const int c = tid & 15, row0 = tid >> 4, g = a.hq / a.hkv;
+    const int c = tid & 15, row0 = tid >> 4, g = a.group;
+    const float per_g = 1.f / g;                            // rows stay below 2^20: (row + 1/2) / g is exact enough
     uint32_t pieces = 0;
     uint32_t freed = 0;                           // pieces whose scores are known to be formed
     uint32_t after_wide = 0;                      // 1 + the last wide piece
@@ -403,17 +417,18 @@ __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, C
     while (next_piece(ctl, pieces, p, a.st)) {
         uint8_t* dst = q_s + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128)) + (c >> 3) * kHalfBytes;
         int r = row0;
-        int seq = (p.row0 + r) / g, h = (p.row0 + r) - seq * g;   // of row r, and of the next to load
         uint4 in[kInFlight][kWords];
         auto load = [&](int from) {
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
-                if (from + u * kRowStep >= p.rows) break;
+                const int row = p.row0 + from + u * kRowStep;
+                const int seq = static_cast<int>((static_cast<float>(row) + 0.5f) * per_g), h = row - seq * g;
                 const int64_t src = (static_cast<int64_t>(p.seq0 + seq) * a.hq + p.kvh * g + h) * kD + c * 8;
                 const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + src * (kSplitQ ? 4 : 2));
+                if (from + u * kRowStep < p.rows) {
 #pragma unroll
-                for (int k = 0; k < kWords; ++k) in[u][k] = s[k];
-                for (h += kRowStep; h >= g; h -= g) ++seq;
+                    for (int k = 0; k < kWords; ++k) in[u][k] = s[k];
+                }
             }
         };
         load(r);
@@ -421,11 +436,12 @@ __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, C
         const uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
         for (; freed < need; ++freed)
             if (!warp_wait(&ctl->q_free[freed % kQueryUnits], (freed / kQueryUnits) & 1, ctl, a.st)) return;
+#pragma unroll 1
         while (r < p.rows) {
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
                 const int at = r + u * kRowStep;
-                if (at >= p.rows) break;
+                if (at >= p.rows) continue;
                 uint8_t* to = dst + at * 128 + (((c & 7) ^ (at & 7)) << 4);
                 if (kSplitQ) {
                     const uint4 v0 = in[u][0], v1 = in[u][kWords - 1];
@@ -489,7 +505,7 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
             if (lane == 0) {
                 const uint32_t idesc = bf16_idesc(kTile, (p.valid(i) + kPage - 1) / kPage * kPage, false);
                 const uint32_t k_addr = ring_addr + slot * kTileBytes;
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -532,7 +548,7 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
                 __syncwarp();
             }
             const uint32_t v_addr = smem_u32(ring) + slot * kTileBytes;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 ok = ok && warp_wait(&ctl->weights[x][b], (t >> 1) & 1, ctl, a.st);
                 if (!ok) break;
@@ -671,7 +687,7 @@ __device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
         if (more) {
             // its queries (g rows of each sequence, side by side) into L2, to stay: behind a
             // saturated HBM a load takes several us, and a wide piece's come in three rounds
-            const int g = a.hq / a.hkv, bytes = g * kD * (kSplitQ ? 4 : 2);
+            const int g = a.group, bytes = g * kD * (kSplitQ ? 4 : 2);
             for (int s = p.row0 / g + lane; s * g < p.row0 + p.rows; s += 32)
                 prefetch_l2_kept(static_cast<const uint8_t*>(a.q) +
                                      (static_cast<int64_t>(p.seq0 + s) * a.hkv + p.kvh) * bytes,
@@ -790,7 +806,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
     __shared__ float4 o_s[kJoinThreads / 32][32];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.hq / a.hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.group;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + warp / kWarps;
     const bool live = row < static_cast<int64_t>(a.batch) * a.hq;
     const int b = live ? static_cast<int>(row / a.hq) : 0, head = static_cast<int>(row % a.hq);
