@@ -94,8 +94,8 @@ struct PrefixArgs {
     // workspace regions (prefix_layout)
     int64_t* total;                // steps of the whole call
     struct PrefixSeq* seqs;        // [batch]
-    float2* part_ml;               // (max, sum) per partial
-    float* part_o;                 // [partial][128]
+    float2* part_ml;               // (max, sum) of either softmax group per partial row
+    float* part_o;                 // [partial row][128]
     DeviceStatus st;
     CUtensorMap tm_k, tm_v;        // 64 x 16 boxes with 128-byte swizzle (filled by the launcher)
 };

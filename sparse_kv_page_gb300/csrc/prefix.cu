@@ -11,7 +11,7 @@
 // Work: "units" (a group's prefix, a sequence's own tokens), each an item per kv head and
 // block of 128 rows, each item a run of tiles of 128 tokens. All tiles of the call form one
 // line, split evenly over one CTA per SM whatever the items are; an item cut by a CTA
-// boundary gives two partials (m, l, O) per piece. The line is found on the device from the
+// boundary gives one partial (m, l, O) per piece. The line is found on the device from the
 // token counts, so a captured graph follows them.
 //
 // CTA (16 warps): warp 14 finds the CTA's pieces and announces them to the others, warp 0
@@ -90,8 +90,10 @@ struct Control {
     uint64_t q_full[kQueryUnits];                 // a piece's queries are in shared memory
     uint64_t q_free[kQueryUnits];                 // its last scores have been formed
     uint64_t last[2];                             // every product with K (with V) of the CTA has completed
+    uint64_t joined;                              // both groups' maxima of a piece are in m
     uint32_t tmem;
     int abort;
+    float m[2][kTile];
     Piece pieces[kPieces];
 };
 template <bool kSplitQ>
@@ -548,6 +550,8 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
                 __syncwarp();
             }
             const uint32_t v_addr = smem_u32(ring) + slot * kTileBytes;
+            // both groups read both accumulators of the piece before
+            if (i == 0) ok = warp_wait(&ctl->weights[1][b], (t >> 1) & 1, ctl, a.st);
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 ok = ok && warp_wait(&ctl->weights[x][b], (t >> 1) & 1, ctl, a.st);
@@ -578,7 +582,7 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
     const int x = tid >> 7, row = tid & 127;      // softmax group, row of the block (= tensor-memory lane)
     const int lane = tid & 31;
     const uint32_t lane_base = ctl->tmem + (static_cast<uint32_t>((tid >> 5) & 3) << 21);
-    const uint32_t acc = lane_base + acc_col(x);
+    const uint32_t acc = lane_base + acc_col(x);  // of this group
     uint32_t t = 0, pieces = 0;                   // tiles and pieces so far
     Piece p;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl, a.st); };
@@ -647,26 +651,37 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->weights[x][b]);
         }
-        // the group's partial of the piece, once its last products are in
+        // the piece's partial, once its last products are in: group x brings 64 dims of both
+        // groups' sums to the larger maximum
+        ctl->m[x][row] = m;
+        const int64_t at = p.part + row;
+        if (row < p.rows) a.part_ml[at * 2 + x] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->joined);
         if (!wait(&ctl->values[(t - 1) & 1], ((t - 1) >> 1) & 1)) return;
+        if (!wait(&ctl->joined, p.n & 1)) return;
         tc_fence_after_sync();
         if (busy) {
-            const int64_t at = (p.part + row) * 2 + x;
-            if (row < p.rows) a.part_ml[at] = make_float2(m, l);
-            const bool some = p.tiles > 1 || p.valid(0) > x * kGroupTokens;   // else the accumulator holds nothing
-            float* dst = a.part_o + at * kD;
+            const float m0 = ctl->m[0][row], m1 = ctl->m[1][row], top = fmaxf(m0, m1);
+            const float base = top == -INFINITY ? 0.f : top;
+            const float f0 = fast_exp2((m0 - base) * kScaleLog2), f1 = fast_exp2((m1 - base) * kScaleLog2);
+            const bool second = p.tiles > 1 || p.valid(0) > kGroupTokens;     // else group 1 holds nothing
+            float* dst = a.part_o + at * kD + x * kGroupTokens;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_load(r, acc + c * 32);
+            for (int c = 0; c < kGroupTokens; c += 16) {
+                uint32_t r[16], r1[16];
+                tmem_load(r, lane_base + acc_col(0) + x * 64 + c);
+                tmem_load(r1, lane_base + acc_col(1) + x * 64 + c);
                 if (row < p.rows) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = some ? r[e] : 0u;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) store_v8(dst + c * 32 + e, &r[e]);
+                    for (int e = 0; e < 16; ++e)
+                        r[e] = __float_as_uint(__uint_as_float(r[e]) * f0 +
+                                               (second ? __uint_as_float(r1[e]) * f1 : 0.f));
+                    store_v8(dst + c, &r[0]);
+                    store_v8(dst + c + 8, &r[8]);
                 }
             }
-            // the next piece's products overwrite the accumulator once its weights have arrived
+            // the next piece's products overwrite the accumulators once both groups' weights have arrived
             tc_fence_before_sync();
         }
     }
@@ -764,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(&ctl->q_full[i], kQueryThreads);
             mbar_init(&ctl->q_free[i], 1);
         }
+        mbar_init(&ctl->joined, 8);                         // a warp each
         mbar_init(&ctl->last[0], 1);
         mbar_init(&ctl->last[1], 1);
         ctl->abort = 0;
@@ -832,13 +848,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
         count_p = cta_of(total, t + s.pre_tiles - 1, n) - first_p + 1;
         row_p = static_cast<int64_t>(s.pre_row0) + kvh * rows + row_in;
     }
-    const int count = live ? 2 * (count_p + count_o) : 0;   // a piece has one of each softmax group
+    const int count = live ? count_p + count_o : 0;
     const int64_t row_o = static_cast<int64_t>(s.own_row0) + kvh * g + h;
     auto part_row = [&](int i) {
-        const int c = i >> 1;
-        const int64_t r = c < count_p ? row_p + static_cast<int64_t>(first_p + c) * kTile
-                                      : row_o + static_cast<int64_t>(first_o + c - count_p) * kTile;
-        return 2 * r + (i & 1);
+        return i < count_p ? row_p + static_cast<int64_t>(first_p + i) * kTile
+                           : row_o + static_cast<int64_t>(first_o + i - count_p) * kTile;
     };
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -851,15 +865,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
             const int64_t r = shfl64(at, k);
             if (k < here) v[k] = *reinterpret_cast<const float4*>(a.part_o + r * kD + lane * 4);
         }
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < here) ml = a.part_ml[at];
-        float top = ml.x;
+        // either softmax group's maximum and sum; the accumulator goes by the larger maximum
+        float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (lane < here) ml = *reinterpret_cast<const float4*>(a.part_ml + at * 2);
+        const float mine = fmaxf(ml.x, ml.z);
+        float top = mine;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
         const float f = fast_exp2((m - base) * kScaleLog2);
-        const float wgt = lane < here ? fast_exp2((ml.x - base) * kScaleLog2) : 0.f;
-        float sum = lane < here ? wgt * ml.y : 0.f;
+        const float wgt = lane < here ? fast_exp2((mine - base) * kScaleLog2) : 0.f;
+        float sum = lane < here ? fast_exp2((ml.x - base) * kScaleLog2) * ml.y +
+                                      fast_exp2((ml.z - base) * kScaleLog2) * ml.w
+                                : 0.f;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         l = l * f + sum;
@@ -958,13 +976,12 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
 PrefixLayout prefix_layout(int batch, int hq) {
     // Partial rows: every unit has its own (the groups' are disjoint sequences, so at most
     // batch * hq, and as many for the own tokens), and each CTA boundary moves on by a block.
-    // Each holds a partial of either softmax group.
-    const size_t rows = 2 * (2 * static_cast<size_t>(batch) * hq + static_cast<size_t>(kMaxPrefixCtas + 1) * kTile);
+    const size_t rows = 2 * static_cast<size_t>(batch) * hq + static_cast<size_t>(kMaxPrefixCtas + 1) * kTile;
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     PrefixLayout w;
     w.seqs = 512;
     w.ml = w.seqs + up(static_cast<size_t>(batch) * sizeof(PrefixSeq));
-    w.o = w.ml + up(rows * sizeof(float2));
+    w.o = w.ml + up(rows * 2 * sizeof(float2));
     w.bytes = w.o + rows * kD * sizeof(float);
     return w;
 }
