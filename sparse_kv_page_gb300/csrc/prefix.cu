@@ -20,10 +20,11 @@
 // tiles are one stream, whatever pieces they belong to: the scores of tile t + 1 are formed
 // while the groups weigh tile t, group x its 64 tokens x * 64.., each with a running maximum,
 // sum and accumulator of its own, so neither waits for the other, and each leaves a partial
-// of its own. A piece's accumulators are read while the next piece's scores are formed. (One
-// warp for both products was the bottleneck: issuing a product blocks until the tensor core
-// takes it, so its waits for K, V and the weights added up to a third of a tile's 3600
-// cycles; 1M x 8: REPLACE.)
+// of its own. A piece's accumulators are read while the next piece's scores are formed.
+// The roles are apart because each would hold up another: issuing a product or a load box
+// blocks until it is taken (one warp for both products took 3600 cycles a tile, one for all
+// 32 boxes 2400), and every role finding its own pieces spilled. The code is kept small: behind
+// a saturated HBM an instruction fetch from L2 takes microseconds.
 // Tensor memory: two score tiles (2 x 128 columns; the bf16 weights overwrite them) and the
 // groups' accumulators (2 x 128). Shared memory: the queries as a bf16 high part and, for
 // fp32, a low part (32 KB each; 16 significant bits together), and a ring of 32 KB slots,
@@ -77,6 +78,8 @@ struct Piece {                      // a run of tiles of one item
     bool once;                      // no other block of rows reads its K and V
 
     __device__ __forceinline__ bool wide() const { return rows > kNarrow; }
+    // of its queries in shared memory
+    __device__ __forceinline__ int query_offset() const { return wide() ? 0 : (n % kQueryUnits) * (kNarrow * 128); }
     // tokens of its tile i
     __device__ __forceinline__ int valid(int i) const { return min(kTile, tokens - (tile0 + i) * kTile); }
 };
@@ -88,6 +91,7 @@ struct Control {
     uint64_t values[2];                           // [score tile] their products with V have completed
     uint64_t p_full[kPieces], p_free[kPieces];    // a piece is announced; every role has read it
     uint64_t q_full[kQueryUnits];                 // a piece's queries are in shared memory
+    uint64_t q_first;                             // ... what the softmax groups bring of the first
     uint64_t q_free[kQueryUnits];                 // its last scores have been formed
     uint64_t last[2];                             // every product with K (with V) of the CTA has completed
     uint64_t joined;                              // both groups' maxima of a piece are in m
@@ -180,9 +184,9 @@ __device__ __forceinline__ int bound_before(int mine, int& bound) {
     bound = max(bound, __shfl_sync(0xffffffffu, upto, 31));
     return lane == 0 ? at : max(before, at);
 }
-// Group u's prefix. Bounds may not fall: `before` is the largest one ahead (bound_before).
-__device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int u, int before) {
-    const int s = a.group_start[u], e = a.group_start[u + 1], n = a.prefix_tokens[u];
+// A group's prefix: sequences s..e, n tokens. Bounds may not fall: `before` is the largest one
+// ahead (bound_before).
+__device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int s, int e, int n, int before) {
     const bool span = s >= before && e >= s && e <= a.batch;
     const bool len = n >= 0 && n <= static_cast<int64_t>(a.max_prefix_pages) * kPage;
     Unit r;
@@ -193,8 +197,7 @@ __device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int u, int befor
     r.bad = !span || !len;
     return r;
 }
-__device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b) {
-    const int n = a.seq_tokens[b];
+__device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b, int n) {
     const bool len = n >= 0 && n <= static_cast<int64_t>(a.max_pages) * kPage;
     Unit r;
     r.seq0 = b;
@@ -227,11 +230,16 @@ __device__ __noinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor&
     const int units = a.num_groups + a.batch;
     Chunk c;
     c.u = Unit{0, 0, 0, 0, false};
+    const bool own = u >= a.num_groups && u < units;
+    const int own_tokens = own ? a.seq_tokens[u - a.num_groups] : 0;
     if (first < a.num_groups) {
-        const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, at.bound);
-        if (u < a.num_groups) c.u = group_unit(a, u, before);
+        const bool group = u < a.num_groups;
+        const int start = group ? a.group_start[u] : 0, end = group ? a.group_start[u + 1] : 0;
+        const int tokens = group ? a.prefix_tokens[u] : 0;
+        const int before = bound_before(start, at.bound);
+        if (group) c.u = group_unit(a, start, end, tokens, before);
     }
-    if (u >= a.num_groups && u < units) c.u = own_unit(a, u - a.num_groups);
+    if (own) c.u = own_unit(a, u - a.num_groups, own_tokens);
     c.count = unit_steps(a, c.u);
     const int rows = c.u.num_seqs * a.hq;
     int64_t ts = c.count;
@@ -285,11 +293,13 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
 #pragma unroll 1
     for (int u0 = 32; u0 < a.num_groups; u0 += 32) {
         const int u = u0 + lane;
-        const int before = bound_before(u < a.num_groups ? a.group_start[u] : 0, bound);
-        if (u < a.num_groups) sum += unit_steps(a, group_unit(a, u, before));
+        const int start = u < a.num_groups ? a.group_start[u] : 0;
+        const int before = bound_before(start, bound);
+        if (u < a.num_groups)
+            sum += unit_steps(a, group_unit(a, start, a.group_start[u + 1], a.prefix_tokens[u], before));
     }
 #pragma unroll 1
-    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_steps(a, own_unit(a, b));
+    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_steps(a, own_unit(a, b, a.seq_tokens[b]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sum += w.at.steps;
@@ -400,73 +410,78 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
 
 // --------------------------------------------------------------------- the queries
 
-// Rows of a piece's queries as bf16 high parts (and low parts behind them) in the 128-byte
-// swizzle: a narrow piece in unit p.n % 8 (16 rows), a wide one from the first unit on. Rows
-// past the piece's keep what they held. A thread takes one 16-byte chunk of every sixth row,
-// four rows in flight; the first four are loaded before the space is free.
+// Rows first, first + step, ... of a piece's queries as bf16 high parts (and low parts behind
+// them) in the 128-byte swizzle: a narrow piece in unit p.n % 8 (16 rows), a wide one from the
+// first unit on. Rows past the piece's keep what they held. Sixteen threads a row, a 16-byte
+// chunk each (thread % 16), four rows in flight.
+template <bool kSplitQ>
+__device__ __noinline__ void write_queries(const void* queries, int hq, int g, int kvh, int seq0, int row0, int rows,
+                                           uint8_t* dst, int first, int step) {
+    constexpr int kInFlight = 4;
+    constexpr int kWords = kSplitQ ? 2 : 1;                 // 16-byte loads a chunk
+    const int c = threadIdx.x & 15;
+    const float per_g = 1.f / g;                            // rows stay below 2^20: (row + 1/2) / g is exact enough
+    dst += (c >> 3) * kHalfBytes;
+#pragma unroll 1
+    for (int r = first; r < rows; r += kInFlight * step) {
+        uint4 in[kInFlight][kWords];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int row = row0 + r + u * step;
+            const int seq = static_cast<int>((static_cast<float>(row) + 0.5f) * per_g), h = row - seq * g;
+            const int64_t src = (static_cast<int64_t>(seq0 + seq) * hq + kvh * g + h) * kD + c * 8;
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(queries) + src * (kSplitQ ? 4 : 2));
+            if (r + u * step < rows) {
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) in[u][k] = s[k];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int at = r + u * step;
+            if (at >= rows) continue;
+            uint8_t* to = dst + at * 128 + (((c & 7) ^ (at & 7)) << 4);
+            if (kSplitQ) {
+                const uint4 v0 = in[u][0], v1 = in[u][kWords - 1];
+                const float x[8] = {__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z),
+                                    __uint_as_float(v0.w), __uint_as_float(v1.x), __uint_as_float(v1.y),
+                                    __uint_as_float(v1.z), __uint_as_float(v1.w)};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                    lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
+                                        x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                }
+                *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                *reinterpret_cast<uint4*>(to) = in[u][0];
+            }
+        }
+    }
+    fence_proxy_async_smem();
+}
+
+// The first piece's queries are brought by the softmax groups too, which have nothing else to
+// do yet: by the three query warps alone 128 rows take 6 us, longer than the ring lasts.
+constexpr int kFirstRows = (kQueryThreads + 256) / 16;      // rows that all of them take at once
+
 template <bool kSplitQ>
 __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl) {
-    constexpr int kInFlight = 4, kRowStep = kQueryThreads / 16;
-    constexpr int kWords = kSplitQ ? 2 : 1;                 // 16-byte loads a chunk
     // warps 12, 13 and 15
     const int tid = threadIdx.x < 14 * 32 ? threadIdx.x - 12 * 32 : threadIdx.x - 13 * 32;
-    const int c = tid & 15, row0 = tid >> 4, g = a.group;
-    const float per_g = 1.f / g;                            // rows stay below 2^20: (row + 1/2) / g is exact enough
     uint32_t pieces = 0;
     uint32_t freed = 0;                           // pieces whose scores are known to be formed
     uint32_t after_wide = 0;                      // 1 + the last wide piece
     Piece p;
     while (next_piece(ctl, pieces, p, a.st)) {
-        uint8_t* dst = q_s + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128)) + (c >> 3) * kHalfBytes;
-        int r = row0;
-        uint4 in[kInFlight][kWords];
-        auto load = [&](int from) {
-#pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int row = p.row0 + from + u * kRowStep;
-                const int seq = static_cast<int>((static_cast<float>(row) + 0.5f) * per_g), h = row - seq * g;
-                const int64_t src = (static_cast<int64_t>(p.seq0 + seq) * a.hq + p.kvh * g + h) * kD + c * 8;
-                const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + src * (kSplitQ ? 4 : 2));
-                if (from + u * kRowStep < p.rows) {
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) in[u][k] = s[k];
-                }
-            }
-        };
-        load(r);
         // a narrow piece follows its unit's last user and any wide piece; a wide one, all
         const uint32_t need = p.wide() ? p.n : max(after_wide, p.n >= kQueryUnits ? p.n - kQueryUnits + 1 : 0u);
         for (; freed < need; ++freed)
             if (!warp_wait(&ctl->q_free[freed % kQueryUnits], (freed / kQueryUnits) & 1, ctl, a.st)) return;
-#pragma unroll 1
-        while (r < p.rows) {
-#pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int at = r + u * kRowStep;
-                if (at >= p.rows) continue;
-                uint8_t* to = dst + at * 128 + (((c & 7) ^ (at & 7)) << 4);
-                if (kSplitQ) {
-                    const uint4 v0 = in[u][0], v1 = in[u][kWords - 1];
-                    const float x[8] = {__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z),
-                                        __uint_as_float(v0.w), __uint_as_float(v1.x), __uint_as_float(v1.y),
-                                        __uint_as_float(v1.z), __uint_as_float(v1.w)};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-                        lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
-                                            x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
-                    }
-                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                } else {
-                    *reinterpret_cast<uint4*>(to) = in[u][0];
-                }
-            }
-            r += kInFlight * kRowStep;
-            load(r);
-        }
-        fence_proxy_async_smem();
+        write_queries<kSplitQ>(a.q, a.hq, a.group, p.kvh, p.seq0, p.row0, p.rows, q_s + p.query_offset(), tid >> 4,
+                               p.n == 0 ? kFirstRows : kQueryThreads / 16);
         mbar_arrive(&ctl->q_full[p.n % kQueryUnits]);
         if (p.wide()) after_wide = p.n + 1;
     }
@@ -496,7 +511,8 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
     Piece p;
     while (ok && next_piece(ctl, pieces, p, a.st)) {
         ok = warp_wait(&ctl->q_full[p.n % kQueryUnits], (p.n / kQueryUnits) & 1, ctl, a.st);
-        const uint32_t q_at = q_addr + (p.wide() ? 0 : (p.n % kQueryUnits) * (kNarrow * 128));
+        const uint32_t q_at = q_addr + p.query_offset();
+        if (p.n == 0) ok = ok && warp_wait(&ctl->q_first, 0, ctl, a.st);
         for (int i = 0; ok && i < p.tiles; ++i, ++t) {
             const uint32_t seq = k_entry(t), slot = seq % kN, b = t & 1;
             // the weights of tile t - 2 lie where these scores go
@@ -576,6 +592,19 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
 }
 
 // --------------------------------------------------------------------- the softmax
+
+// The softmax groups' share of the first piece's queries. (The piece stays announced until they
+// have read it for themselves.)
+template <bool kSplitQ>
+__device__ __forceinline__ void help_queries(const PrefixArgs& a, uint8_t* q_s, Control* ctl) {
+    if (!warp_wait(&ctl->p_full[0], 0, ctl, a.st)) return;
+    const Piece& p = ctl->pieces[0];
+    if (p.tiles > 0)
+        write_queries<kSplitQ>(a.q, a.hq, a.group, p.kvh, p.seq0, p.row0, p.rows, q_s + p.query_offset(),
+                               kQueryThreads / 16 + ((threadIdx.x - 128) >> 4), kFirstRows);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->q_first);
+}
 
 __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
     const int tid = threadIdx.x - 128;            // 0..255
@@ -698,8 +727,13 @@ __device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
     for (uint32_t n = 0;; ++n) {
         more = more && walk_next(a, w, p);
         const int slot = n % kPieces;
-        if (!warp_wait(&ctl->p_free[slot], ((n / kPieces) & 1) ^ 1, ctl, a.st)) return;
-        if (more) {
+        if (n >= kPieces && !warp_wait(&ctl->p_free[slot], ((n / kPieces) & 1) ^ 1, ctl, a.st)) return;
+        if (lane == 0) {
+            if (!more) p.tiles = 0;
+            ctl->pieces[slot] = p;
+            mbar_arrive(&ctl->p_full[slot]);
+        }
+        if (more && n > 0) {
             // its queries (g rows of each sequence, side by side) into L2, to stay: behind a
             // saturated HBM a load takes several us, and a wide piece's come in three rounds
             const int g = a.group, bytes = g * kD * (kSplitQ ? 4 : 2);
@@ -707,11 +741,6 @@ __device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
                 prefetch_l2_kept(static_cast<const uint8_t*>(a.q) +
                                      (static_cast<int64_t>(p.seq0 + s) * a.hkv + p.kvh) * bytes,
                                  bytes, keep);
-        }
-        if (lane == 0) {
-            if (!more) p.tiles = 0;
-            ctl->pieces[slot] = p;
-            mbar_arrive(&ctl->p_full[slot]);
         }
         __syncwarp();
         if (!more) return;
@@ -779,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(&ctl->q_full[i], kQueryThreads);
             mbar_init(&ctl->q_free[i], 1);
         }
+        mbar_init(&ctl->q_first, 8);                        // a warp each
         mbar_init(&ctl->joined, 8);                         // a warp each
         mbar_init(&ctl->last[0], 1);
         mbar_init(&ctl->last[1], 1);
@@ -795,7 +825,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     else if (warp == 1) run_scores<kSplitQ>(a, smem_u32(q_s), smem_u32(ring), ctl);
     else if (warp == 2) run_values<kSplitQ>(a, ring, ctl);
     else if (warp == 3) run_loads<kSplitQ, true>(a, ring, ctl);
-    else if (warp < 12) run_softmax(a, ctl);
+    else if (warp < 12) {
+        help_queries<kSplitQ>(a, q_s, ctl);
+        run_softmax(a, ctl);
+    }
     else if (warp != 14) run_queries<kSplitQ>(a, q_s, ctl);
     else {
         run_pieces<kSplitQ>(a, ctl);
@@ -810,13 +843,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 // ------------------------------------------------------------------------ the join
 
 // kWarps warps join the partials of one (sequence, query head): each takes every kWarps-th
-// batch of 8, whose 4 KB are in flight together, and they meet in shared memory. The time
-// is the latency of a few dependent loads, so the registers are kept to 64: four CTAs an SM.
+// batch, whose partials are in flight together (8 of them, 16 where a row has a CTA to itself),
+// and they meet in shared memory. The time is the latency of a few dependent loads.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBatch = 8;
+
 
 template <int kWarps>
-__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ PrefixArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads, kWarps == 8 ? 2 : 4)
+    join_kernel(const __grid_constant__ PrefixArgs a, int grid) {
+    constexpr int kJoinBatch = kWarps == 8 ? 16 : 8;
     constexpr int kRowsPerCta = kJoinThreads / 32 / kWarps;
     __shared__ float2 ml_s[kJoinThreads / 32];
     __shared__ float4 o_s[kJoinThreads / 32][32];
@@ -893,18 +928,18 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
         if (lane == 0) ml_s[warp] = make_float2(m, l);
         o_s[warp][lane] = o;
         __syncthreads();
-        if (warp != 0) return;
+        if (warp % kWarps != 0) return;                     // else: ml_s[warp] on are the row's
         m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_s[w].x);
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_s[warp + w].x);
         const float base = m == -INFINITY ? 0.f : m;
         l = 0.f;
         o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = fast_exp2((ml_s[w].x - base) * kScaleLog2);
-            const float4 v = o_s[w][lane];
-            l += f * ml_s[w].y;
+            const float f = fast_exp2((ml_s[warp + w].x - base) * kScaleLog2);
+            const float4 v = o_s[warp + w][lane];
+            l += f * ml_s[warp + w].y;
             o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
         }
     }
@@ -959,14 +994,18 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, prefix_kernel<kSplitQ>, a)) != cudaSuccess) return e;
-    // The fewer rows, the more pieces each has. 16 or more rows per SM are at least 19 blocks
-    // of 128, so a prefix row has at most 9 pieces: a warp per row will do.
+    // The fewer rows, the more pieces each has: a prefix row of n blocks of 128 in all has about
+    // grid / n. A CTA per row up to two rows an SM, half a CTA up to sixteen, a warp beyond. The
+    // whole call, CTA / half CTA a row: 256 rows (1M x 8 sequences) 170.2 / 174.8 us, 2048 rows
+    // (64K x 64) 114.3 / 100.1.
     const int64_t rows = static_cast<int64_t>(a.batch) * a.hq;
-    const bool many = rows >= 16 * static_cast<int64_t>(grid);
-    cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows), 1, 1);
+    const int warps = rows <= 2 * grid ? 8 : rows < 16 * grid ? 4 : 1, per_cta = kJoinThreads / 32 / warps;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta), 1, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    e = many ? cudaLaunchKernelEx(&cfg, join_kernel<1>, a, grid) : cudaLaunchKernelEx(&cfg, join_kernel<8>, a, grid);
+    e = warps == 8   ? cudaLaunchKernelEx(&cfg, join_kernel<8>, a, grid)
+        : warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<4>, a, grid)
+                     : cudaLaunchKernelEx(&cfg, join_kernel<1>, a, grid);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
