@@ -144,6 +144,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Contro
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// What a role that gave up still has in flight: loads and products that were issued end by
+// themselves, so this wait is not cut short by a small limit.
+constexpr uint64_t kDrainNs = 500000000ull;
+
 // The next piece of the CTA, as warp 14 announced it; false after the last. Whole warps.
 __device__ __forceinline__ bool next_piece(Control* ctl, uint32_t& n, Piece& p, const DeviceStatus& st) {
     const int slot = n % kPieces;
@@ -403,7 +407,7 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
         // giving up: the loads in flight write to this CTA's shared memory, so wait for them
         for (uint32_t i = t > kN ? t - kN : 0; i < t; ++i) {
             const uint32_t seq = kValues ? v_entry(i) : k_entry(i);
-            mbar_wait_bounded(&ctl->full[seq % kN], (seq / kN) & 1, a.st.wait_limit_ns);
+            mbar_wait_bounded(&ctl->full[seq % kN], (seq / kN) & 1, kDrainNs);
         }
     }
 }
@@ -492,10 +496,10 @@ __device__ __forceinline__ void run_queries(const PrefixArgs& a, uint8_t* q_s, C
 // In both the whole warp keeps step and its first lane issues.
 
 // Whatever the warp issued reads shared and tensor memory: sees its end.
-__device__ __forceinline__ void end_products(uint64_t* bar, const DeviceStatus& st) {
+__device__ __forceinline__ void end_products(uint64_t* bar) {
     if ((threadIdx.x & 31) == 0) {
         mma_commit(bar);
-        mbar_wait_bounded(bar, 0, st.wait_limit_ns);
+        mbar_wait_bounded(bar, 0, kDrainNs);
     }
     __syncwarp();
 }
@@ -537,7 +541,7 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
             }
         }
     }
-    end_products(&ctl->last[0], a.st);
+    end_products(&ctl->last[0]);
 }
 
 // O_x += P_x V, over each tile's live pages alone.
@@ -588,7 +592,7 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
             }
         }
     }
-    end_products(&ctl->last[1], a.st);
+    end_products(&ctl->last[1]);
 }
 
 // --------------------------------------------------------------------- the softmax

@@ -304,6 +304,45 @@ def test_prefix_many_sequences_many_groups():
     check_prefix(prefix_case(groups, own, 4, 1, seed=8))
 
 
+def test_prefix_thousands_of_sequences():
+    groups = [(1 + i % 20, (i * 29) % 60) for i in range(260)]
+    n = sum(s for s, _ in groups)
+    check_prefix(prefix_case(groups, [(b * 7) % 41 if b % 3 else 0 for b in range(n + 300)], 2, 1, seed=18))
+
+
+def test_cache_of_more_than_2_31_elements():
+    """Rows appended to the last pages of a 9 GB pool, and attended there."""
+    phys, hkv, hq = 140001, 8, 32
+    kc = torch.empty((phys, hkv, 16, 128), dtype=torch.bfloat16, device=DEV)
+    vc = torch.empty_like(kc)
+    kc[-40:] = float("nan")
+    vc[-40:] = float("nan")
+    assert kc.numel() > 2 ** 31
+    dims = L.make_dims(2, hq, hkv, 3, phys)
+    table = (phys - 1 - torch.arange(6, device=DEV)).view(2, 3).int().contiguous()
+    own = [45, 20]
+    seq = torch.tensor([0] * 45 + [1] * 20, dtype=torch.int32, device=DEV)
+    index = torch.tensor(list(range(45)) + list(range(20)), dtype=torch.int32, device=DEV)
+    qkv = torch.randn((65, hq + 2 * hkv, 128), generator=gen(3), device=DEV).bfloat16()
+    L.locks_append_tokens(dims, None, None, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], None, index, table, None, kc, vc,
+                          token_seq=seq)
+    for t in (0, 44, 45, 64):
+        page, row = int(table[int(seq[t]), int(index[t]) // 16]), int(index[t]) % 16
+        assert torch.equal(kc[page, :, row], qkv[t, hq:hq + hkv]) and torch.equal(vc[page, :, row], qkv[t, hq + hkv:])
+    q = torch.randn((2, hq, 128), generator=gen(4), device=DEV)
+    out = torch.empty((2, hq, 128), dtype=torch.bfloat16, device=DEV)
+    ws = L.alloc_prefix_workspace(dims, 0, DEV)
+    L.locks_prefix_attention(dims, q, kc, vc, None, None, None, table, torch.tensor(own, dtype=torch.int32, device=DEV),
+                             out, ws)
+    assert L.locks_get_device_status(ws) == 0
+    at = [0, 45, 65]
+    for b in range(2):
+        x = f64(qkv[at[b]:at[b + 1]])
+        for h in range(hkv):
+            want = ref.attend(f64(q[b, 4 * h:4 * h + 4]), x[:, hq + h], x[:, hq + hkv + h])[0]
+            assert np.abs(f64(out[b, 4 * h:4 * h + 4]) - want).max() < 2e-2
+
+
 def test_prefix_long_split_over_all_ctas():
     check_prefix(prefix_case([(5, 70001)], [3000, 1, 0, 20, 555], 8, 1, seed=11))
 
