@@ -39,7 +39,7 @@ _lib: Optional[ctypes.CDLL] = None
 _native = None
 
 
-def _library() -> ctypes.CDLL:
+def load_library() -> ctypes.CDLL:
     """The library with this module's signatures; _marshal bound to its entry points."""
     global _lib, _native
     if _lib is None:
@@ -73,20 +73,26 @@ def _library() -> ctypes.CDLL:
 # The tensors' checks and addresses are _marshal's (csrc/marshal.cpp): of a decode step's small
 # calls, reading them through Python was most of the time.
 
-def _call(entry: str, name: str, device: int, stream, *args) -> None:
+def _place(device: int, stream):
+    """The stream's handle, and whether the device has to be made current first."""
     if _native is None:
-        _library()
-    if device < 0:                       # refused there, after what else may be wrong
-        stream = 0
-    elif stream is None:
+        load_library()
+    if device < 0:                       # host tensors: refused by the call, after what else may be wrong
+        return 0, False
+    if stream is None:
         stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device < 0 or torch.cuda.current_device() == device:
-        status = getattr(_native, entry)(device, stream, *args)
-    else:
+    return stream, _current_device() != device
+
+
+def _call(entry: str, name: str, device: int, stream, *args) -> None:
+    stream, elsewhere = _place(device, stream)
+    if elsewhere:
         with torch.cuda.device(device):
             status = getattr(_native, entry)(device, stream, *args)
+    else:
+        status = getattr(_native, entry)(device, stream, *args)
     if status != 0:
         raise LocksError(name, status)
 
@@ -95,7 +101,9 @@ def _raw_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)   # the same without a Stream object
+# the same without a Stream object, and without the check that CUDA is up (a CUDA tensor is)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 # -------------------------------------------------------------- entry points
@@ -130,7 +138,7 @@ def locks_append_tokens(dims: locks_dims_t, rope: Optional[locks_rope_t], q: Opt
 def locks_prefix_workspace_size(dims: locks_dims_t, num_groups: int) -> int:
     out = ctypes.c_size_t(0)
     _check("locks_prefix_workspace_size",
-           _library().locks_prefix_workspace_size(ctypes.byref(dims), num_groups, ctypes.byref(out)))
+           load_library().locks_prefix_workspace_size(ctypes.byref(dims), num_groups, ctypes.byref(out)))
     return out.value
 
 
@@ -153,7 +161,7 @@ def locks_prefix_attention(dims: locks_dims_t, q: torch.Tensor, k_cache: torch.T
 
 def locks_mass_workspace_size(dims: locks_dims_t) -> int:
     out = ctypes.c_size_t(0)
-    _check("locks_mass_workspace_size", _library().locks_mass_workspace_size(ctypes.byref(dims), ctypes.byref(out)))
+    _check("locks_mass_workspace_size", load_library().locks_mass_workspace_size(ctypes.byref(dims), ctypes.byref(out)))
     return out.value
 
 

@@ -22,7 +22,7 @@ def L():
     from sparse_kv_page_gb300 import build as b
     b.build()
     import sparse_kv_page_gb300 as L
-    L.cache._library()
+    L.cache.load_library()
     return L
 
 
