@@ -820,6 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&ctl->tmem, 512);
+    if (warp == 0 && (threadIdx.x & 31) == 0) prefetch_tensor_map(&a.tm_k);
+    if (warp == 3 && (threadIdx.x & 31) == 0) prefetch_tensor_map(&a.tm_v);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
