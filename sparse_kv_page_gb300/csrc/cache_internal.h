@@ -112,5 +112,11 @@ struct PrefixLayout {
 };
 PrefixLayout prefix_layout(int batch, int hq);
 cudaError_t launch_prefix(const PrefixArgs& a, int num_sms, cudaStream_t stream);
+// A cache [num_phys][hkv][16][128] as num_phys * hkv * 16 rows, in 64 x 16 boxes with 128-byte
+// swizzle.
+cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows);
+// The one-launch form for short lists and few sequences (prefix_small.cu).
+bool prefix_is_small(const PrefixArgs& a, int num_sms);
+cudaError_t launch_prefix_small(const PrefixArgs& a, cudaStream_t stream);
 
 }  // namespace locks

@@ -12,15 +12,16 @@
 // block of 128 rows, each item a run of tiles of 128 tokens. All tiles of the call form one
 // line, split evenly over one CTA per SM whatever the items are; an item cut by a CTA
 // boundary gives one partial (m, l, O) per piece. The line is found on the device from the
-// token counts, so a captured graph follows them.
+// token counts, so a captured graph follows them. Short lists of few sequences take one
+// launch of prefix_small.cu in place of this.
 //
 // CTA (16 warps): warp 14 finds the CTA's pieces and announces them to the others, warp 0
 // loads K and warp 3 V, warp 1 issues the products with K, warp 2 those with V, warps 4-7 and
 // 8-11 are two softmax groups, the other three bring the queries. The CTA's
 // tiles are one stream, whatever pieces they belong to: the scores of tile t + 1 are formed
 // while the groups weigh tile t, group x its 64 tokens x * 64.., each with a running maximum,
-// sum and accumulator of its own, so neither waits for the other, and each leaves a partial
-// of its own. A piece's accumulators are read while the next piece's scores are formed.
+// sum and accumulator of its own, so neither waits for the other; the two are joined into the
+// piece's one partial as they are read, while the next piece's scores are formed.
 // The roles are apart because each would hold up another: issuing a product or a load box
 // blocks until it is taken (one warp for both products took 3600 cycles a tile, one for all
 // 32 boxes 2400), and every role finding its own pieces spilled. The code is kept small: behind
@@ -43,12 +44,12 @@
 #include <cstring>
 
 #include "cache_internal.h"
+#include "prefix_units.cuh"
 #include "tcgen05.cuh"
 
 namespace locks {
 namespace {
 
-constexpr int kTile = 128;                        // tokens per tile, rows per block
 constexpr int kTilePages = kTile / kPage;
 constexpr int kHalfBytes = kTile * 128;           // 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalfBytes;
@@ -60,7 +61,6 @@ constexpr int kThreads = 512;
 constexpr int kQueryThreads = 96;
 constexpr int kPieces = 8;                        // pieces announced ahead
 constexpr int kPieceReaders = 15;                 // warps that follow them
-constexpr float kScaleLog2 = kInvSqrtD * kLog2e;  // raw score -> exponent of 2
 constexpr float kRescale = 8.f / kScaleLog2;      // a running maximum may lag by 2^8
 
 // Ring slots: what the queries leave of shared memory.
@@ -169,48 +169,6 @@ __device__ __forceinline__ int item_cost(int rows) { return rows > kNarrow ? kWi
 
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
 
-struct Unit {
-    int tokens, tiles, seq0, num_seqs;            // tiles per item
-    bool bad;
-};
-// The largest group bound ahead of this lane's, given the largest one before the warp's
-// (`bound`, at least 0), which moves on past the warp's own.
-__device__ __forceinline__ int bound_before(int mine, int& bound) {
-    const int lane = threadIdx.x & 31;
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto = max(upto, y);
-    }
-    const int before = __shfl_up_sync(0xffffffffu, upto, 1);
-    const int at = bound;
-    bound = max(bound, __shfl_sync(0xffffffffu, upto, 31));
-    return lane == 0 ? at : max(before, at);
-}
-// A group's prefix: sequences s..e, n tokens. Bounds may not fall: `before` is the largest one
-// ahead (bound_before).
-__device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int s, int e, int n, int before) {
-    const bool span = s >= before && e >= s && e <= a.batch;
-    const bool len = n >= 0 && n <= static_cast<int64_t>(a.max_prefix_pages) * kPage;
-    Unit r;
-    r.seq0 = span ? s : 0;
-    r.num_seqs = span ? e - s : 0;
-    r.tokens = span && len ? n : 0;
-    r.tiles = (r.tokens + kTile - 1) / kTile;
-    r.bad = !span || !len;
-    return r;
-}
-__device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b, int n) {
-    const bool len = n >= 0 && n <= static_cast<int64_t>(a.max_pages) * kPage;
-    Unit r;
-    r.seq0 = b;
-    r.num_seqs = 1;
-    r.tokens = len ? n : 0;
-    r.tiles = (r.tokens + kTile - 1) / kTile;
-    r.bad = !len;
-    return r;
-}
 // Steps of a unit on the line: an item's cost goes before its tiles.
 __device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
     const int rows = u.num_seqs * (a.group);
@@ -956,35 +914,6 @@ __global__ void __launch_bounds__(kJoinThreads, kWarps == 8 ? 2 : 4)
     if (a.lse && lane == 0) a.lse[row] = count > 0 ? fmaf(m, kInvSqrtD, logf(l)) : -INFINITY;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tiled_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-        }
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
-// A cache [num_phys][hkv][16][128] as num_phys * hkv * 16 rows, in 64 x 16 boxes.
-cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows) {
-    const auto fn = tiled_encoder();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kPage)};
-    const cuuint32_t steps[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box,
-                          steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <bool kSplitQ>
 cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) {
     cudaError_t e = ensure_kernel_attrs<prefix_kernel<kSplitQ>>(kSmemBytes<kSplitQ>);
@@ -1016,7 +945,36 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
     return cudaGetLastError();
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tiled_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
 }  // namespace
+
+// A cache [num_phys][hkv][16][128] as num_phys * hkv * 16 rows, in 64 x 16 boxes.
+cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows) {
+    const auto fn = tiled_encoder();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kPage)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box,
+                          steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 PrefixLayout prefix_layout(int batch, int hq) {
     // Partial rows: every unit has its own (the groups' are disjoint sequences, so at most
@@ -1040,6 +998,7 @@ cudaError_t launch_prefix(const PrefixArgs& args, int num_sms, cudaStream_t stre
     cudaError_t e = cache_map(&a.tm_k, a.k_cache, rows);
     if (e == cudaSuccess) e = cache_map(&a.tm_v, a.v_cache, rows);
     if (e != cudaSuccess) return e;
+    if (prefix_is_small(a, num_sms)) return launch_prefix_small(a, stream);
     const int grid = num_sms < kMaxPrefixCtas ? num_sms : kMaxPrefixCtas;
     return a.q_type == LOCKS_FP32 ? launch_prefix_t<true>(a, grid, stream) : launch_prefix_t<false>(a, grid, stream);
 }
