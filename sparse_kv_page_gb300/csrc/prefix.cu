@@ -13,7 +13,8 @@
 // line, split evenly over one CTA per SM whatever the items are; an item cut by a CTA
 // boundary gives one partial (m, l, O) per piece. The line is found on the device from the
 // token counts, so a captured graph follows them. Short lists of few sequences take one
-// launch of prefix_small.cu in place of this.
+// launch of prefix_pages.cu in place of this; own lists of few pages are left to the second
+// launch there, and the line holds the prefixes alone.
 //
 // CTA (16 warps): warp 14 finds the CTA's pieces and announces them to the others, warp 0
 // loads K and warp 3 V, warp 1 issues the products with K, warp 2 those with V, warps 4-7 and
@@ -55,7 +56,6 @@ constexpr int kHalfBytes = kTile * 128;           // 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kBoxBytes = kPage * 128;
 constexpr int kGroupTokens = kTile / 2;           // of a tile, per softmax group
-constexpr int kNarrow = 16;                       // rows of a piece that takes one query unit
 constexpr int kQueryUnits = kTile / kNarrow;
 constexpr int kThreads = 512;
 constexpr int kQueryThreads = 96;
@@ -161,21 +161,15 @@ __device__ __forceinline__ bool next_piece(Control* ctl, uint32_t& n, Piece& p, 
 
 // ----------------------------------------------------------------- the line of tiles
 
-// The line is counted in steps: one per tile, and ahead of an item's tiles what starting it
-// costs, in tiles: its queries, its partials, a pipeline that fills. A wide item's queries
-// wait for the ones before to be used up.
-constexpr int kNarrowCost = 1, kWideCost = 6;
-__device__ __forceinline__ int item_cost(int rows) { return rows > kNarrow ? kWideCost : kNarrowCost; }
-
-__device__ __forceinline__ int blocks_of(int rows) { return (rows + kTile - 1) / kTile; }
-
 // Steps of a unit on the line: an item's cost goes before its tiles.
 __device__ __forceinline__ int64_t unit_steps(const PrefixArgs& a, const Unit& u) {
     const int rows = u.num_seqs * (a.group);
     return u.tiles == 0 ? 0 : static_cast<int64_t>(u.tiles + item_cost(rows)) * blocks_of(rows) * a.hkv;
 }
 
-__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+// Units on the line: the groups' prefixes and, unless the second launch attends to them, the
+// sequences' own tokens.
+__device__ __forceinline__ int line_units(const PrefixArgs& a) { return a.num_groups + (a.own_apart ? 0 : a.batch); }
 
 // 32 units, one a lane, with their places on the line. Whole warps call everything here.
 struct Chunk {
@@ -189,7 +183,7 @@ struct Cursor {                     // what lies before a chunk
 };
 __device__ __noinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor& at) {
     const int lane = threadIdx.x & 31, u = first + lane;
-    const int units = a.num_groups + a.batch;
+    const int units = line_units(a);
     Chunk c;
     c.u = Unit{0, 0, 0, 0, false};
     const bool own = u >= a.num_groups && u < units;
@@ -219,21 +213,6 @@ __device__ __noinline__ Chunk load_chunk(const PrefixArgs& a, int first, Cursor&
     return c;
 }
 
-// First step of CTA c of n on a line of `total` steps, and the CTA of a step. (32-bit division
-// where it will do: a 64-bit one is a long routine, kept in one place.)
-__device__ __noinline__ int64_t divide64(int64_t x, int64_t y) { return x / y; }
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-    if (x < (1ll << 32) && y < (1ll << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return divide64(x, y);
-}
-__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int n) { return divide(total * c, n); }
-__device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
-    return static_cast<int>(divide((step + 1) * n - 1, total));
-}
-__device__ __forceinline__ int ctas_of(int64_t total, int grid) {
-    return total < grid ? static_cast<int>(total) : grid;
-}
-
 struct Walk {
     int64_t t, t_end;
     Cursor at;
@@ -261,7 +240,7 @@ __device__ __forceinline__ bool walk_begin(const PrefixArgs& a, Walk& w) {
             sum += unit_steps(a, group_unit(a, start, a.group_start[u + 1], a.prefix_tokens[u], before));
     }
 #pragma unroll 1
-    for (int b = max(32 - a.num_groups, 0) + lane; b < a.batch; b += 32) sum += unit_steps(a, own_unit(a, b, a.seq_tokens[b]));
+    for (int b = max(32 - a.num_groups, 0) + lane; b < line_units(a) - a.num_groups; b += 32) sum += unit_steps(a, own_unit(a, b, a.seq_tokens[b]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sum += w.at.steps;
@@ -712,7 +691,7 @@ __device__ __forceinline__ void run_pieces(const PrefixArgs& a, Control* ctl) {
 // Writes where every sequence's tiles lie for the second launch, and reports bad lengths and
 // bounds. One warp.
 __device__ __forceinline__ void write_plan(const PrefixArgs& a) {
-    const int lane = threadIdx.x & 31, units = a.num_groups + a.batch;
+    const int lane = threadIdx.x & 31, units = line_units(a);
     for (int b = lane; b < a.batch; b += 32) a.seqs[b].pre_tiles = 0;
     __syncwarp();
     Cursor at{0, 0, 0};
@@ -836,58 +815,17 @@ __global__ void __launch_bounds__(kJoinThreads, kWarps == 8 ? 2 : 4)
         first_o = cta_of(total, t, n);
         count_o = cta_of(total, t + s.own_tiles - 1, n) - first_o + 1;
     }
-    int first_p = 0, count_p = 0;                           // ... and of the prefix, for this row's block
-    int64_t row_p = 0;
-    if (s.pre_tiles > 0) {
-        const int rows = s.pre_num_seqs * g, row_in = (b - s.pre_seq0) * g + h;
-        const int64_t item = static_cast<int64_t>(kvh) * blocks_of(rows) + row_in / kTile;
-        const int cost = item_cost(rows);
-        const int64_t t = s.pre_step0 + item * (s.pre_tiles + cost) + cost;
-        first_p = cta_of(total, t, n);
-        count_p = cta_of(total, t + s.pre_tiles - 1, n) - first_p + 1;
-        row_p = static_cast<int64_t>(s.pre_row0) + kvh * rows + row_in;
-    }
-    const int count = live ? count_p + count_o : 0;
+    const PrefixRows p = prefix_rows(a, s, b, kvh, h, total, n);
+    const int count = live ? p.count + count_o : 0;
     const int64_t row_o = static_cast<int64_t>(s.own_row0) + kvh * g + h;
     auto part_row = [&](int i) {
-        return i < count_p ? row_p + static_cast<int64_t>(first_p + i) * kTile
-                           : row_o + static_cast<int64_t>(first_o + i - count_p) * kTile;
+        return i < p.count ? p.row + static_cast<int64_t>(i) * kTile
+                           : row_o + static_cast<int64_t>(first_o + i - p.count) * kTile;
     };
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = (warp % kWarps) * kJoinBatch; i0 < count; i0 += kWarps * kJoinBatch) {
-        const int here = min(kJoinBatch, count - i0);
-        const int64_t at = part_row(i0 + min(lane, here - 1));       // a partial a lane
-        float4 v[kJoinBatch];
-#pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) {
-            const int64_t r = shfl64(at, k);
-            if (k < here) v[k] = *reinterpret_cast<const float4*>(a.part_o + r * kD + lane * 4);
-        }
-        // either softmax group's maximum and sum; the accumulator goes by the larger maximum
-        float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (lane < here) ml = *reinterpret_cast<const float4*>(a.part_ml + at * 2);
-        const float mine = fmaxf(ml.x, ml.z);
-        float top = mine;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float to = fmaxf(m, top), base = to == -INFINITY ? 0.f : to;
-        const float f = fast_exp2((m - base) * kScaleLog2);
-        const float wgt = lane < here ? fast_exp2((mine - base) * kScaleLog2) : 0.f;
-        float sum = lane < here ? fast_exp2((ml.x - base) * kScaleLog2) * ml.y +
-                                      fast_exp2((ml.z - base) * kScaleLog2) * ml.w
-                                : 0.f;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l = l * f + sum;
-        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-        m = to;
-#pragma unroll
-        for (int k = 0; k < kJoinBatch; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, wgt, k);
-            if (k < here) o.x += wk * v[k].x, o.y += wk * v[k].y, o.z += wk * v[k].z, o.w += wk * v[k].w;
-        }
-    }
+    for (int i0 = (warp % kWarps) * kJoinBatch; i0 < count; i0 += kWarps * kJoinBatch)
+        join_partials<kJoinBatch>(a, part_row, i0, count, m, l, o);
     if (kWarps > 1) {
         if (lane == 0) ml_s[warp] = make_float2(m, l);
         o_s[warp][lane] = o;
@@ -929,6 +867,7 @@ cudaError_t launch_prefix_t(const PrefixArgs& a, int grid, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, prefix_kernel<kSplitQ>, a)) != cudaSuccess) return e;
+    if (a.own_apart) return launch_own(a, grid, stream);
     // The fewer rows, the more pieces each has: a prefix row of n blocks of 128 in all has about
     // grid / n. A CTA per row up to two rows an SM, half a CTA up to sixteen, a warp beyond. The
     // whole call, CTA / half CTA a row: 256 rows (1M x 8 sequences) 170.2 / 174.8 us, 2048 rows
@@ -1000,6 +939,8 @@ cudaError_t launch_prefix(const PrefixArgs& args, int num_sms, cudaStream_t stre
     if (e != cudaSuccess) return e;
     if (prefix_is_small(a, num_sms)) return launch_prefix_small(a, stream);
     const int grid = num_sms < kMaxPrefixCtas ? num_sms : kMaxPrefixCtas;
+    a.own_apart = own_by_pages(a, num_sms);
+    if (a.own_apart && a.num_groups == 0) return launch_own(a, grid, stream);
     return a.q_type == LOCKS_FP32 ? launch_prefix_t<true>(a, grid, stream) : launch_prefix_t<false>(a, grid, stream);
 }
 

@@ -1,7 +1,8 @@
-"""The shared-prefix attention's two forms on a GB300: one launch for short lists of few
-sequences, tiles for the rest. Which one a call takes follows its tables' widths, so every
-case of the first runs on the second too, through tables that are wider than their lists.
-Tolerances are test_gpu_cache's: both forms round queries, weights and outputs alike."""
+"""The shared-prefix attention's forms on a GB300: one launch for short lists of few
+sequences; tiles for the prefixes and pages for few own tokens; tiles for everything. Which one a
+call takes follows its tables' widths, so cases of the first run on the others too, through
+tables that are wider than their lists. Tolerances are test_gpu_cache's: all forms round queries,
+weights and outputs alike."""
 import numpy as np
 import pytest
 import torch
@@ -11,13 +12,13 @@ from tests import test_gpu_cache as T
 pytestmark = pytest.mark.gpu
 
 L = T.L
-WIDE = 300
+WIDE = 400
 
 
-def wide(c):
+def wide(c, names=("prefix_table", "page_table")):
     """The same case with tables of WIDE columns: behind the lists there is no page."""
     c = dict(c)
-    for name in ("prefix_table", "page_table"):
+    for name in names:
         t = c[name]
         if t.shape[1] < WIDE:
             c[name] = torch.nn.functional.pad(t, (0, WIDE - t.shape[1]), value=-1).contiguous()
@@ -42,7 +43,7 @@ CASES = [
     ([(1, 777)], [33], 128, 8),
     ([(2, 500), (0, 60), (1, 0), (4, 1025), (1, 7)], [0, 1, 200, 16, 0, 31, 128, 500, 9, 0, 77, 0], 20, 2),
     ([(2, 2049)], [495, 496], 32, 2),                           # 160 pages
-    ([(1, 4000)], [95], 16, 1),                                 # 256 pages
+    ([(1, 6000)], [140], 16, 1),                                # 384 pages
     ([], [511, 512, 513], 16, 4),                               # a page for each warp, one less, one more
     ([(1, 9 * i) for i in range(30)], [i % 19 for i in range(32)], 4, 1),
     ([(1, 40)] * 32, [5] * 33, 5, 1),
@@ -63,8 +64,8 @@ def test_both_forms(case, q_type):
 
 def test_calls_past_the_limits_take_tiles():
     for groups, own, hkv in (([(1, 1)] * 33, [0] * 33, 1),        # groups
-                             ([(1, 4065)], [17], 1),              # 257 pages
-                             ([], [16] * 39, 1)):                 # clusters
+                             ([(1, 6001)], [140], 1),             # 385 pages
+                             ([(39, 16)], [16] * 39, 1)):         # clusters
         c = T.prefix_case(groups, own, 4 * hkv, hkv, seed=60)
         T.check_prefix(c)
         assert not scratch_untouched(c)
@@ -128,3 +129,107 @@ def test_one_launch_in_a_graph_follows_its_lengths_and_two_calls_overlap():
         assert np.abs(T.f64(c["out"]) - want).max() < 2e-2
     T.check_prefix(d)
     assert scratch_untouched(c) and scratch_untouched(d)
+
+
+# ------------------------------------------------ own tokens by pages, behind the tiles
+
+@pytest.fixture
+def own_pages(monkeypatch):
+    """Cases of 32 / 8 heads whose prefix table alone is wide."""
+    case = T.prefix_case
+    monkeypatch.setattr(T, "prefix_case",
+                        lambda groups, own, hq, hkv, **k: wide(case(groups, own, 32, 8, **k), ("prefix_table",)))
+
+
+OWN = [T.test_prefix_groups_and_sequences_outside_them, T.test_prefix_steep_and_growing_scores,
+       T.test_prefix_nonfinite_values_stay_in_their_rows, T.test_prefix_bad_lengths_bounds_and_pages,
+       T.test_prefix_in_a_graph_follows_its_lengths_and_two_calls_overlap]
+
+
+@pytest.mark.parametrize("test", OWN, ids=lambda f: f.__name__[12:])
+def test_own_pages_at_small_sizes(test, own_pages):
+    test()
+
+
+OWN_CASES = [
+    # groups, own tokens, hq, hkv
+    ([(2, 333)], [45, 3], 32, 8),                                # eight warps a CTA or four, by the width
+    ([(2, 333)], [1024, 1009], 32, 8),
+    ([(5, 7000), (0, 3), (30, 50)], [(i * 97) % 1025 for i in range(38)], 32, 8),
+    ([(20, 200), (19, 0)], [i % 18 for i in range(45)], 64, 8),  # more than two CTAs an SM
+    ([(20, 600)], [(i * 7) % 300 for i in range(20)], 8, 8),
+    ([(60, 100)], [(i * 5) % 200 for i in range(61)], 20, 4),
+    ([(100, 40), (99, 900)], [(i * 3) % 70 for i in range(200)], 7, 1),
+    ([], [(i * 131) % 1025 for i in range(41)], 32, 8),          # no groups: no launch ahead
+    ([], [16, 0, 64, 63, 65] * 9, 4, 4),
+]
+
+
+@pytest.mark.parametrize("case", range(len(OWN_CASES)))
+@pytest.mark.parametrize("q_type", [torch.float32, torch.bfloat16])
+def test_own_pages(case, q_type):
+    groups, own, hq, hkv = OWN_CASES[case]
+    c = T.prefix_case(groups, own, hq, hkv, seed=80 + case, q_type=q_type)
+    T.check_prefix(wide(c, ("prefix_table",)))
+    if groups:
+        T.check_prefix(c)
+
+
+@pytest.mark.parametrize("groups", [[(2, 261), (38, 5)], []])
+def test_own_pages_rows_behind_the_end_are_never_used(groups):
+    own = [19, 0, 130, 16, 1] * 8
+    c = T.prefix_case(groups, own, 32, 8, seed=7, spare=2)
+    used = torch.zeros(c["k"].shape[0], 16, dtype=torch.bool, device=T.DEV)
+    for tab, n in list(zip(c["prefix_table"], [n for _, n in groups])) + list(zip(c["page_table"], own)):
+        for t in range(n):
+            used[int(tab[t // 16]), t % 16] = True
+    behind = ~used[:, None, :].expand(-1, 8, -1)
+    clean = {n: c[n].clone() for n in ("k", "v")}
+    T.run_prefix(c)
+    first, first_lse = c["out"].clone(), c["lse"].clone()
+    for kk, vv in ((float("nan"), float("nan")), (float("inf"), -float("inf"))):
+        c["k"], c["v"] = clean["k"].clone(), clean["v"].clone()
+        c["k"][behind] = kk
+        c["v"][behind] = vv
+        T.run_prefix(c)
+        assert torch.equal(first, c["out"]) and torch.equal(first_lse, c["lse"])
+
+
+@pytest.mark.parametrize("groups", [[(30, 300), (10, 90)], []])
+def test_tokens_appended_ahead_are_seen(groups):
+    """Append and attention back to back, in a captured graph: own tokens are read ahead of the
+    prefix launch's end, but not ahead of what came before it."""
+    own = [(i * 11) % 60 for i in range(40)]
+    c = T.prefix_case(groups, own, 32, 8, seed=21, spare=1)
+    d = {n: v.clone() if isinstance(v, torch.Tensor) else v for n, v in c.items()}
+    kv = torch.zeros((40, 16, 128), device=T.DEV).bfloat16()
+    index = torch.zeros(40, dtype=torch.int32, device=T.DEV)
+
+    def step(c, wait):
+        for i in range(4):                        # four layers' worth, all in one cache
+            L.locks_append_tokens(c["dims"], None, None, kv[:, :8], kv[:, 8:], None, index, c["page_table"], None, c["k"],
+                                  c["v"])
+            wait()
+            T.run_prefix(c)
+            wait()
+
+    step(c, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c, lambda: None)
+    for t in range(6):
+        kv.copy_(torch.randn(kv.shape, generator=T.gen(t), device=T.DEV))
+        for x in (c, d):
+            if t == 0:
+                x["k"].copy_(d["k"]), x["v"].copy_(d["v"])
+            index.copy_(x["seq_tokens"])
+            x["seq_tokens"] += 1
+            torch.cuda.synchronize()
+            if x is c:
+                graph.replay()
+            else:
+                step(d, torch.cuda.synchronize)
+            torch.cuda.synchronize()
+        assert torch.equal(c["out"], d["out"]) and torch.equal(c["lse"], d["lse"])
+    T.check_prefix(c)
