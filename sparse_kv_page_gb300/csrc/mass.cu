@@ -491,12 +491,21 @@ cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2*
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-    // More CTAs a sequence shorten the passes over its pages and lengthen every exchange.
-    // us a call with 1 / 8 / 16 CTAs a sequence: one sequence of 1024 pages 6.5 / 7.2 / 8.1, of
-    // 8192 15.9 / 6.2 / 7.8, of 16,384 - / 7.9 / 8.3, of 65,536 - / 18.3 / 14.0; eight of
-    // 65,536 - / 18.9 / 21.2. Sixteen also hold the longest tables (24,576 pages a CTA at most).
-    if (a.max_pages <= 1024) return launch_evict_t<1>(a, stream);
-    if (a.max_pages <= 16384 || (a.batch > 4 && a.max_pages <= 8 * kMaxShare)) return launch_evict_t<8>(a, stream);
+    // More CTAs a sequence shorten the passes over its pages and lengthen every exchange, and
+    // clusters that together pass a CTA per SM run one another's launches down. us a call with
+    // 1 / 2 / 4 / 8 CTAs a sequence: one sequence of 1100 pages 4.3 / 5.1 / 4.6 / 5.0, of 2000
+    // 5.9 / 5.3 / 4.7 / 5.0, of 4000 9.6 / 7.2 / 5.6 / 5.3; 19 of 4000 9.7 / 7.3 / 5.7 / 7.5;
+    // 64 of 2000 6.2 / 5.5 / 6.9 / 11.5, of 8000 16.8 / 11.8 / 10.8 / 13.5; 256 of 4000 15.3 /
+    // 16.1 / 19.4 / 37.5. With 8 / 16: one of 16,384 pages 7.9 / 8.3, of 65,536 18.3 / 14.0;
+    // eight of 65,536 18.9 / 21.2. Sixteen also hold the longest tables (24,576 pages a CTA at
+    // most).
+    if (a.max_pages <= 1536) return launch_evict_t<1>(a, stream);
+    if (a.max_pages <= 16384) {
+        if (a.batch <= 8 && a.max_pages > 2048) return launch_evict_t<8>(a, stream);
+        if (a.batch <= 24 || (a.batch <= 96 && a.max_pages > 4096)) return launch_evict_t<4>(a, stream);
+        return a.batch <= 96 ? launch_evict_t<2>(a, stream) : launch_evict_t<1>(a, stream);
+    }
+    if (a.batch > 4 && a.max_pages <= 8 * kMaxShare) return launch_evict_t<8>(a, stream);
     return launch_evict_t<16>(a, stream);
 }
 
