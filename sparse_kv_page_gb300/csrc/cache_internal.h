@@ -119,7 +119,7 @@ cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows);
 // By pages (prefix_pages.cu): the one-launch form for short lists and few sequences, and a
 // second launch that attends to own tokens and joins the prefix's partials to them.
 bool prefix_is_small(const PrefixArgs& a, int num_sms);
-cudaError_t launch_prefix_small(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_small(const PrefixArgs& a, int num_sms, cudaStream_t stream);
 bool own_by_pages(const PrefixArgs& a, int num_sms);
 cudaError_t launch_own(const PrefixArgs& a, int grid, cudaStream_t stream);
 

@@ -937,7 +937,7 @@ cudaError_t launch_prefix(const PrefixArgs& args, int num_sms, cudaStream_t stre
     cudaError_t e = cache_map(&a.tm_k, a.k_cache, rows);
     if (e == cudaSuccess) e = cache_map(&a.tm_v, a.v_cache, rows);
     if (e != cudaSuccess) return e;
-    if (prefix_is_small(a, num_sms)) return launch_prefix_small(a, stream);
+    if (prefix_is_small(a, num_sms)) return launch_prefix_small(a, num_sms, stream);
     const int grid = num_sms < kMaxPrefixCtas ? num_sms : kMaxPrefixCtas;
     a.own_apart = own_by_pages(a, num_sms);
     if (a.own_apart && a.num_groups == 0) return launch_own(a, grid, stream);

@@ -2,8 +2,8 @@
 // by pages on mma.sync, where a tile of 128 rows and 128 tokens would be mostly empty:
 //
 // 1. Short lists of few sequences, in one launch. One cluster of eight CTAs per (sequence, kv
-//    head): its 32 warps take the pages of the sequence's list (its group's prefix, then its
-//    own) in turn with an online softmax, and their partials meet in shared memory and then, a
+//    head): its 32 or 64 warps take the pages of the sequence's list (its group's prefix, then its
+//    own, up to 512) in turn with an online softmax, and their partials meet in shared memory and then, a
 //    query head per CTA, through distributed shared memory. A prefix is read once per sequence,
 //    which L2 serves; what the tiled kernel's evenly cut line, its pipeline and its second
 //    launch cost (10 us at the least) is what this one saves: 12.1 -> 4.8 us for two sequences
@@ -30,18 +30,14 @@ constexpr int kSlotBytes = 2 * kPageBytes;            // K and V of a page
 
 // The one-launch form: a cluster of CTAs per (sequence, kv head).
 constexpr int kCluster = 8;
-constexpr int kWarps = 4;
-constexpr int kDepth = 3;                             // pages a warp has in flight
-constexpr int kThreads = kWarps * 32;
-constexpr int kAllWarps = kCluster * kWarps;
-constexpr int kSmallPages = 384;                      // longest list taken, see prefix_is_small
-static_assert(kSmallPages <= 32 * kAllWarps, "a warp's page ids lie in its lanes");
+constexpr int kSmallPages = 512;                      // longest list taken, see prefix_is_small
+static_assert(kSmallPages <= 32 * kCluster * 4, "a warp's page ids lie in its lanes");
+template <int kWarps>
 struct Small {
     float m[kWarps][16], l[kWarps][16];               // warps' partials
     float cta_m[16], cta_l[16];                       // the CTA's
     float cta_o[16][kD];
 };
-constexpr int kSmemBytes = kWarps * kDepth * kSlotBytes + static_cast<int>(sizeof(Small));
 
 // Byte offset of 16-byte chunk c of a token's row: swizzled, for ldmatrix.
 __device__ __forceinline__ int chunk_offset(int token, int c) { return token * kRowBytes + ((c ^ (token & 7)) << 4); }
@@ -247,10 +243,12 @@ __device__ __forceinline__ int checked_page(const PrefixArgs& a, const int32_t* 
     return 0;
 }
 
-template <bool kSplitQ, int kBlocks>
-__global__ void __launch_bounds__(kThreads, 2) small_kernel(const __grid_constant__ PrefixArgs a) {
+template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
+__global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
+    small_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ __align__(1024) uint8_t slots[];
-    Small* sh = reinterpret_cast<Small*>(slots + kWarps * kDepth * kSlotBytes);
+    constexpr int kAllWarps = kCluster * kWarps;
+    auto* sh = reinterpret_cast<Small<kWarps>*>(slots + kWarps * kDepth * kSlotBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = static_cast<int>(cluster_ctarank());
     const int seg = blockIdx.x / kCluster, b = seg / a.hkv, kvh = seg % a.hkv, g = a.group;
@@ -276,9 +274,9 @@ __global__ void __launch_bounds__(kThreads, 2) small_kernel(const __grid_constan
     const Unit own = own_unit(a, b, a.seq_tokens[b]);
     if (own.bad && rank == 0 && threadIdx.x == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
     const int pre_pages = (pre_tokens + kPage - 1) / kPage, pages = pre_pages + (own.tokens + kPage - 1) / kPage;
-    const int first = rank * kWarps + warp;              // this warp's pages: first, first + 32, ...
+    const int first = rank * kWarps + warp;              // this warp's pages: first, first + kAllWarps, ...
     const int count = pages > first ? (pages - first + kAllWarps - 1) / kAllWarps : 0;
-    int ids = 0;                                         // of page first + 32 * lane
+    int ids = 0;                                         // of page first + kAllWarps * lane
     if (lane < count) {
         const int page = first + lane * kAllWarps;
         ids = checked_page(a, page < pre_pages ? a.prefix_table + static_cast<int64_t>(group) * a.max_prefix_pages + page
@@ -297,13 +295,14 @@ __global__ void __launch_bounds__(kThreads, 2) small_kernel(const __grid_constan
         if (lane == 0) sh->cta_m[r] = top, sh->cta_l[r] = sum;
     }
     cluster_sync_all();
-    for (int r = rank; r < g; r += kCluster) {           // a query head per CTA
+    const int dim = threadIdx.x % kD;
+    for (int r = rank + kCluster * (threadIdx.x / kD); r < g; r += kCluster * (kWarps * 32 / kD)) {   // a query head per CTA
         float cm[kCluster], cl[kCluster], co[kCluster], top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < kCluster; ++c) {
             cm[c] = ld_dsmem_f32(dsmem_addr(&sh->cta_m[r], c));
             cl[c] = ld_dsmem_f32(dsmem_addr(&sh->cta_l[r], c));
-            co[c] = ld_dsmem_f32(dsmem_addr(&sh->cta_o[r][threadIdx.x], c));
+            co[c] = ld_dsmem_f32(dsmem_addr(&sh->cta_o[r][dim], c));
         }
 #pragma unroll
         for (int c = 0; c < kCluster; ++c) top = fmaxf(top, cm[c]);
@@ -317,20 +316,21 @@ __global__ void __launch_bounds__(kThreads, 2) small_kernel(const __grid_constan
         }
         const int64_t row = static_cast<int64_t>(b) * a.hq + kvh * g + r;
         const float v = pages > 0 ? x / sum : 0.f;
-        reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + threadIdx.x] = __float2bfloat16_rn(v);
-        if (a.lse && threadIdx.x == 0) a.lse[row] = pages > 0 ? fmaf(top, kInvSqrtD, logf(sum)) : -INFINITY;
+        reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + dim] = __float2bfloat16_rn(v);
+        if (a.lse && dim == 0) a.lse[row] = pages > 0 ? fmaf(top, kInvSqrtD, logf(sum)) : -INFINITY;
     }
     cluster_sync_all();                                  // shared memory stays until every CTA has read it
 }
 
-template <bool kSplitQ, int kBlocks>
+template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
 cudaError_t launch_small_t(const PrefixArgs& a, cudaStream_t stream) {
-    cudaError_t e = ensure_kernel_attrs<small_kernel<kSplitQ, kBlocks>>(kSmemBytes);
+    constexpr int kBytes = kWarps * kDepth * kSlotBytes + static_cast<int>(sizeof(Small<kWarps>));
+    cudaError_t e = ensure_kernel_attrs<small_kernel<kSplitQ, kBlocks, kWarps, kDepth>>(kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.batch * a.hkv * kCluster, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -341,7 +341,7 @@ cudaError_t launch_small_t(const PrefixArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, small_kernel<kSplitQ, kBlocks>, a);
+    e = cudaLaunchKernelEx(&cfg, small_kernel<kSplitQ, kBlocks, kWarps, kDepth>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -359,7 +359,8 @@ constexpr int kOwnPages = 64;                         // longest list taken, see
 static_assert(kOwnPages <= 32 * 4, "a warp's page ids lie in its lanes");
 
 template <bool kSplitQ, int kWarps, int kDepth>
-__global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth)) own_kernel(const __grid_constant__ PrefixArgs a, int grid, bool alone) {
+__global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
+    own_kernel(const __grid_constant__ PrefixArgs a, int grid, bool alone) {
     extern __shared__ __align__(1024) uint8_t slots[];
     auto* sh = reinterpret_cast<Own<kWarps>*>(slots + kWarps * kDepth * kSlotBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -420,21 +421,38 @@ cudaError_t launch_own_t(const PrefixArgs& a, int grid, cudaStream_t stream) {
 
 }  // namespace
 
+// By the tables' widths, which is what the host knows, and up to two CTAs an SM. Measured (this
+// one / the tiled kernel and its second launch, us; kv heads x queries each): 1 sequence 8 x 4,
+// 515 pages 9.4 / 16.9; 4 sequences 8 x 4 (256 CTAs), 259 pages 10.3 / 13.5, 515 pages 15.3 /
+// 16.9; 1 sequence 2 x 16, 515 pages 12.6 / 12.8; 14 sequences 2 x 16 (224 CTAs), 378 pages
+// 17.2 / 17.0; 7 sequences 8 x 4 (448 CTAs), 67 pages 11.9 / 10.6. Groups are looked for by one
+// warp.
+static int64_t list_pages(const PrefixArgs& a) {
+    return static_cast<int64_t>(a.num_groups > 0 ? a.max_prefix_pages : 0) + a.max_pages;
+}
+static int64_t small_ctas(const PrefixArgs& a) { return static_cast<int64_t>(a.batch) * a.hkv * kCluster; }
+// Eight warps a CTA, one CTA an SM, for longer lists where the clusters fit side by side: 14
+// do, 16 run in two rounds (1024 tokens: 7.2 us, 9.3). Eight warps / four: 515 pages 9.4 / 11.1
+// us, 131 pages 6.2 / 6.1, 19 pages 5.0 / 4.4.
+static bool small_is_wide(const PrefixArgs& a, int num_sms) {
+    return 4 * small_ctas(a) <= 3 * static_cast<int64_t>(num_sms) && list_pages(a) > 192;
+}
 bool prefix_is_small(const PrefixArgs& a, int num_sms) {
-    // By the tables' widths, which is what the host knows, and up to two CTAs an SM. Measured
-    // (this one / the tiled kernel and its second launch, us; kv heads x queries each): 1
-    // sequence 8 x 4, 256 pages 7.8 / 13.3, 512 pages 11.1 / 16.7; 4 sequences 8 x 4 (256 CTAs),
-    // 256 pages 10.2 / 13.4, 375 pages 12.2 / 14.8; 14 sequences 2 x 16, 375 pages 17.2 / 17.0;
-    // 1 sequence 2 x 16, 512 pages 14.4 / 12.8; 7 sequences 8 x 4 (448 CTAs), 64 pages 11.8 /
-    // 10.6. Groups are looked for by one warp.
-    const int64_t pages = static_cast<int64_t>(a.num_groups > 0 ? a.max_prefix_pages : 0) + a.max_pages;
-    const int64_t ctas = static_cast<int64_t>(a.batch) * a.hkv * kCluster;
-    return a.num_groups <= 32 && pages <= kSmallPages && ctas <= 2 * static_cast<int64_t>(num_sms);
+    if (a.num_groups > 32 || small_ctas(a) > 2 * static_cast<int64_t>(num_sms)) return false;
+    return list_pages(a) <= (a.group <= 8 || small_is_wide(a, num_sms) ? kSmallPages : 384);
 }
 
-cudaError_t launch_prefix_small(const PrefixArgs& a, cudaStream_t stream) {
-    if (a.q_type == LOCKS_FP32) return a.group <= 8 ? launch_small_t<true, 1>(a, stream) : launch_small_t<true, 2>(a, stream);
-    return a.group <= 8 ? launch_small_t<false, 1>(a, stream) : launch_small_t<false, 2>(a, stream);
+cudaError_t launch_prefix_small(const PrefixArgs& a, int num_sms, cudaStream_t stream) {
+    const bool wide = small_is_wide(a, num_sms);
+    const auto launch = [&](auto split, auto blocks) {
+        constexpr bool kSplitQ = decltype(split)::value;
+        constexpr int kBlocks = decltype(blocks)::value;
+        return wide ? launch_small_t<kSplitQ, kBlocks, 8, 2>(a, stream) : launch_small_t<kSplitQ, kBlocks, 4, 3>(a, stream);
+    };
+    const auto by_group = [&](auto split) {
+        return a.group <= 8 ? launch(split, std::integral_constant<int, 1>()) : launch(split, std::integral_constant<int, 2>());
+    };
+    return a.q_type == LOCKS_FP32 ? by_group(std::true_type()) : by_group(std::false_type());
 }
 
 bool own_by_pages(const PrefixArgs& a, int num_sms) {

@@ -12,7 +12,7 @@ from tests import test_gpu_cache as T
 pytestmark = pytest.mark.gpu
 
 L = T.L
-WIDE = 400
+WIDE = 520
 
 
 def wide(c, names=("prefix_table", "page_table")):
@@ -43,7 +43,10 @@ CASES = [
     ([(1, 777)], [33], 128, 8),
     ([(2, 500), (0, 60), (1, 0), (4, 1025), (1, 7)], [0, 1, 200, 16, 0, 31, 128, 500, 9, 0, 77, 0], 20, 2),
     ([(2, 2049)], [495, 496], 32, 2),                           # 160 pages
-    ([(1, 6000)], [140], 16, 1),                                # 384 pages
+    ([(1, 8064)], [128], 16, 1),                                # 512 pages, eight warps a CTA
+    ([(14, 3000)], [i * 9 for i in range(14)], 8, 1),           # as many clusters as do so
+    ([(19, 8064)], [i * 5 for i in range(19)], 5, 1),           # 512 pages, four
+    ([(20, 6000)], [140] * 20, 16, 1),                          # 384 pages
     ([], [511, 512, 513], 16, 4),                               # a page for each warp, one less, one more
     ([(1, 9 * i) for i in range(30)], [i % 19 for i in range(32)], 4, 1),
     ([(1, 40)] * 32, [5] * 33, 5, 1),
@@ -64,7 +67,7 @@ def test_both_forms(case, q_type):
 
 def test_calls_past_the_limits_take_tiles():
     for groups, own, hkv in (([(1, 1)] * 33, [0] * 33, 1),        # groups
-                             ([(1, 6001)], [140], 1),             # 385 pages
+                             ([(1, 8065)], [128], 1),             # 513 pages
                              ([(39, 16)], [16] * 39, 1)):         # clusters
         c = T.prefix_case(groups, own, 4 * hkv, hkv, seed=60)
         T.check_prefix(c)
