@@ -92,6 +92,7 @@ struct PrefixArgs {
     int num_groups, max_prefix_pages, batch, hq, hkv, max_pages, num_phys, q_type;
     int group;                     // hq / hkv
     bool own_apart;                // the second launch attends to the sequences' own tokens
+    bool own_alone;                // ... and to the prefixes: there is no first
     // workspace regions (prefix_layout)
     int64_t* total;                // steps of the whole call
     struct PrefixSeq* seqs;        // [batch]
@@ -116,10 +117,12 @@ cudaError_t launch_prefix(const PrefixArgs& a, int num_sms, cudaStream_t stream)
 // A cache [num_phys][hkv][16][128] as num_phys * hkv * 16 rows, in 64 x 16 boxes with 128-byte
 // swizzle.
 cudaError_t cache_map(CUtensorMap* map, const uint16_t* base, int64_t rows);
-// By pages (prefix_pages.cu): the one-launch form for short lists and few sequences, and a
-// second launch that attends to own tokens and joins the prefix's partials to them.
+// By pages (prefix_pages.cu): one launch of clusters for few sequences, one of single CTAs for
+// short lists, and a second launch that attends to own tokens and joins the prefix's partials
+// to them.
 bool prefix_is_small(const PrefixArgs& a, int num_sms);
 cudaError_t launch_prefix_small(const PrefixArgs& a, int num_sms, cudaStream_t stream);
+bool list_by_pages(const PrefixArgs& a, int num_sms);
 bool own_by_pages(const PrefixArgs& a, int num_sms);
 cudaError_t launch_own(const PrefixArgs& a, int grid, cudaStream_t stream);
 

@@ -12,8 +12,8 @@
 // block of 128 rows, each item a run of tiles of 128 tokens. All tiles of the call form one
 // line, split evenly over one CTA per SM whatever the items are; an item cut by a CTA
 // boundary gives one partial (m, l, O) per piece. The line is found on the device from the
-// token counts, so a captured graph follows them. Short lists of few sequences take one
-// launch of prefix_pages.cu in place of this; own lists of few pages are left to the second
+// token counts, so a captured graph follows them. Short lists, and those of few sequences, take
+// one launch of prefix_pages.cu in place of this; own lists of few pages are left to the second
 // launch there, and the line holds the prefixes alone.
 //
 // CTA (16 warps): warp 14 finds the CTA's pieces and announces them to the others, warp 0
@@ -939,8 +939,9 @@ cudaError_t launch_prefix(const PrefixArgs& args, int num_sms, cudaStream_t stre
     if (e != cudaSuccess) return e;
     if (prefix_is_small(a, num_sms)) return launch_prefix_small(a, num_sms, stream);
     const int grid = num_sms < kMaxPrefixCtas ? num_sms : kMaxPrefixCtas;
+    a.own_alone = list_by_pages(a, num_sms);
+    if (a.own_alone) return launch_own(a, grid, stream);
     a.own_apart = own_by_pages(a, num_sms);
-    if (a.own_apart && a.num_groups == 0) return launch_own(a, grid, stream);
     return a.q_type == LOCKS_FP32 ? launch_prefix_t<true>(a, grid, stream) : launch_prefix_t<false>(a, grid, stream);
 }
 

@@ -9,10 +9,11 @@
 //    launch cost (10 us at the least) is what this one saves: 12.1 -> 4.8 us for two sequences
 //    behind 333 tokens. Latency bounds it.
 //
-// 2. The second launch behind the tiled kernel, where own tokens are few pages: attends to them
-//    and joins the prefix's partials. As items of the tiled kernel every (sequence, kv head)
-//    takes a tile's pipeline of its own, about 2.8 us of an SM: 96 sequences of up to 100 tokens
-//    behind a short prefix, 8 kv heads: 27.1 -> 17.6 us, 256 sequences 59.5 -> 34.7 us.
+// 2. Many sequences, in one launch where lists are short, else as the second launch behind the
+//    tiled kernel, which has the prefixes: a CTA per (sequence, kv head) attends to the pages and
+//    joins the prefix's partials, if any, to them. As items of the tiled kernel every (sequence,
+//    kv head) takes a tile's pipeline of its own, about 2.8 us of an SM: 96 sequences of up to
+//    100 tokens behind 16, 8 kv heads: 27.1 -> 8.9 us; behind 4000 tokens 38.2 -> 28.3.
 //
 // fp32 queries enter the products as a bf16 high and low part, weights are rounded to bf16 once
 // (at most 2^-8 of the sum of |weight * v|), as in the tiled kernel. What bounds a warp's page
@@ -52,19 +53,60 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// A sequence's tokens: its group's prefix, if any, and then its own.
+struct List {
+    int group, pre_tokens, own_tokens;
+    int pre_pages, pages;
+};
+// Whole warps; `report` on one that reports bad counts and bounds.
+__device__ __forceinline__ List find_list(const PrefixArgs& a, int b, bool report) {
+    const int lane = threadIdx.x & 31;
+    List r = {-1, 0, 0, 0, 0};
+    if (a.num_groups > 0) {                              // up to 32: a group a lane
+        Unit pre = {0, 0, 0, 0, false};
+        const bool on = lane < a.num_groups;
+        const int start = on ? __ldcg(a.group_start + lane) : 0, end = on ? __ldcg(a.group_start + lane + 1) : 0;
+        const int tokens = on ? __ldcg(a.prefix_tokens + lane) : 0;
+        int bound = 0;
+        const int before = bound_before(start, bound);
+        if (on) pre = group_unit(a, start, end, tokens, before);
+        if (pre.bad && report) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        r.group = __ffs(__ballot_sync(0xffffffffu, on && b >= pre.seq0 && b < pre.seq0 + pre.num_seqs)) - 1;
+        if (r.group >= 0) r.pre_tokens = __shfl_sync(0xffffffffu, pre.tokens, r.group);
+    }
+    return r;
+}
+// ... with the sequence's own tokens.
+__device__ __forceinline__ void add_own(const PrefixArgs& a, int b, bool report, List& r) {
+    const Unit own = own_unit(a, b, __ldcg(a.seq_tokens + b));
+    if (own.bad && report) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+    r.own_tokens = own.tokens;
+    r.pre_pages = (r.pre_tokens + kPage - 1) / kPage;
+    r.pages = r.pre_pages + (own.tokens + kPage - 1) / kPage;
+}
+__device__ __forceinline__ int page_id(const PrefixArgs& a, const List& list, int b, int page) {
+    const int x = __ldcg(page < list.pre_pages
+                             ? a.prefix_table + static_cast<int64_t>(list.group) * a.max_prefix_pages + page
+                             : a.page_table + static_cast<int64_t>(b) * a.max_pages + page - list.pre_pages);
+    if (x >= 0 && x < a.num_phys) return x;
+    report_error(a.st, LOCKS_ERR_BAD_INDEX);
+    return 0;
+}
+
 // A warp's pages of sequence b's list: page first + i * step for i < count (up to 32, the id of
-// page i in lane i) of a prefix's pre_pages pages and then its own. Products are formed with the
+// page i in lane i). Products are formed with the
 // queries as columns, S^T = K Q^T and O^T = V^T P^T, eight to a block: a group's few queries
 // would leave most of sixteen rows empty (4 queries: 24 products a page, 48 as rows). Leaves, per
 // column 2 * (lane % 4) + c of block n, the maximum m[n][c], this lane's part of the sum and the
 // accumulator o[n][16 dims][.].
 template <bool kSplitQ, int kBlocks, int kDepth>
 __device__ __forceinline__ void attend_pages(const PrefixArgs& a, int b, int kvh, uint8_t* mine, int ids, int first,
-                                             int step, int count, int pre_pages, int pre_tokens, int own_tokens,
-                                             float (&o)[kBlocks][8][4], float (&m)[kBlocks][2], float (&l)[kBlocks][2]) {
+                                             int step, int count, const List& list, float (&o)[kBlocks][8][4],
+                                             float (&m)[kBlocks][2], float (&l)[kBlocks][2]) {
     const int lane = threadIdx.x & 31;
     const auto valid_of = [&](int page) {
-        return min(kPage, page < pre_pages ? pre_tokens - page * kPage : own_tokens - (page - pre_pages) * kPage);
+        return min(kPage, page < list.pre_pages ? list.pre_tokens - page * kPage
+                                                : list.own_tokens - (page - list.pre_pages) * kPage);
     };
     const auto load = [&](int i, int slot) {             // page i of this warp, its tokens alone
         const int id = __shfl_sync(0xffffffffu, ids, i), valid = valid_of(first + i * step);
@@ -236,13 +278,6 @@ __device__ __forceinline__ float4 row_of_warps(const uint8_t* slots, const float
     return x;
 }
 
-__device__ __forceinline__ int checked_page(const PrefixArgs& a, const int32_t* id) {
-    const int x = __ldcg(id);
-    if (x >= 0 && x < a.num_phys) return x;
-    report_error(a.st, LOCKS_ERR_BAD_INDEX);
-    return 0;
-}
-
 template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
     small_kernel(const __grid_constant__ PrefixArgs a) {
@@ -256,35 +291,13 @@ __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
     grid_dependency_wait();
     allow_dependent_launch();
 
-    // the sequence's group, a group a lane
-    Unit pre = {0, 0, 0, 0, false};
-    int group = -1;
-    if (a.num_groups > 0) {
-        const bool on = lane < a.num_groups;
-        const int start = on ? a.group_start[lane] : 0, end = on ? a.group_start[lane + 1] : 0;
-        const int tokens = on ? a.prefix_tokens[lane] : 0;
-        int bound = 0;
-        const int before = bound_before(start, bound);
-        if (on) pre = group_unit(a, start, end, tokens, before);
-        if (pre.bad && rank == 0 && warp == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-        const unsigned in = __ballot_sync(0xffffffffu, on && b >= pre.seq0 && b < pre.seq0 + pre.num_seqs);
-        group = __ffs(in) - 1;
-    }
-    const int pre_tokens = group >= 0 ? __shfl_sync(0xffffffffu, pre.tokens, group) : 0;
-    const Unit own = own_unit(a, b, a.seq_tokens[b]);
-    if (own.bad && rank == 0 && threadIdx.x == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-    const int pre_pages = (pre_tokens + kPage - 1) / kPage, pages = pre_pages + (own.tokens + kPage - 1) / kPage;
+    List list = find_list(a, b, rank == 0 && warp == 0);
+    add_own(a, b, rank == 0 && threadIdx.x == 0, list);
     const int first = rank * kWarps + warp;              // this warp's pages: first, first + kAllWarps, ...
-    const int count = pages > first ? (pages - first + kAllWarps - 1) / kAllWarps : 0;
-    int ids = 0;                                         // of page first + kAllWarps * lane
-    if (lane < count) {
-        const int page = first + lane * kAllWarps;
-        ids = checked_page(a, page < pre_pages ? a.prefix_table + static_cast<int64_t>(group) * a.max_prefix_pages + page
-                                               : a.page_table + static_cast<int64_t>(b) * a.max_pages + page - pre_pages);
-    }
+    const int count = list.pages > first ? (list.pages - first + kAllWarps - 1) / kAllWarps : 0;
+    const int ids = lane < count ? page_id(a, list, b, first + lane * kAllWarps) : 0;
     float o[kBlocks][8][4], m[kBlocks][2], l[kBlocks][2];
-    attend_pages<kSplitQ, kBlocks, kDepth>(a, b, kvh, mine, ids, first, kAllWarps, count, pre_pages, pre_tokens, own.tokens,
-                          o, m, l);
+    attend_pages<kSplitQ, kBlocks, kDepth>(a, b, kvh, mine, ids, first, kAllWarps, count, list, o, m, l);
     put_partial<kBlocks>(mine, sh->m[warp], sh->l[warp], o, m, l);
     // the CTA's partial from the warps'
     __syncthreads();
@@ -315,9 +328,9 @@ __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
             x += f * co[c];
         }
         const int64_t row = static_cast<int64_t>(b) * a.hq + kvh * g + r;
-        const float v = pages > 0 ? x / sum : 0.f;
+        const float v = list.pages > 0 ? x / sum : 0.f;
         reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + dim] = __float2bfloat16_rn(v);
-        if (a.lse && dim == 0) a.lse[row] = pages > 0 ? fmaf(top, kInvSqrtD, logf(sum)) : -INFINITY;
+        if (a.lse && dim == 0) a.lse[row] = list.pages > 0 ? fmaf(top, kInvSqrtD, logf(sum)) : -INFINITY;
     }
     cluster_sync_all();                                  // shared memory stays until every CTA has read it
 }
@@ -350,15 +363,14 @@ cudaError_t launch_small_t(const PrefixArgs& a, cudaStream_t stream) {
 // partials and the prefix's. Own tokens need nothing from the first launch, every CTA of which
 // waited for what lies before it before it let this one start: so they are read ahead of the
 // wait, past L1, by the CTAs that find room while the first launch ends. `alone`: there is no
-// first launch.
+// first launch, and the list holds the prefix too.
 template <int kWarps>
 struct Own {
     float m[kWarps][16], l[kWarps][16];
 };
-constexpr int kOwnPages = 64;                         // longest list taken, see own_by_pages
-static_assert(kOwnPages <= 32 * 4, "a warp's page ids lie in its lanes");
+constexpr int kOwnPages = 32 * 4;                     // longest list taken: a warp's page ids lie in its lanes
 
-template <bool kSplitQ, int kWarps, int kDepth>
+template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
     own_kernel(const __grid_constant__ PrefixArgs a, int grid, bool alone) {
     extern __shared__ __align__(1024) uint8_t slots[];
@@ -366,15 +378,17 @@ __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / a.hkv, kvh = blockIdx.x % a.hkv, g = a.group;
     uint8_t* mine = slots + warp * kDepth * kSlotBytes;
-    if (alone) grid_dependency_wait();
-    const Unit own = own_unit(a, b, __ldcg(a.seq_tokens + b));
-    if (own.bad && threadIdx.x == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-    const int pages = (own.tokens + kPage - 1) / kPage;
-    const int count = pages > warp ? (pages - warp + kWarps - 1) / kWarps : 0;
-    const int ids = lane < count ? checked_page(a, a.page_table + static_cast<int64_t>(b) * a.max_pages + warp + lane * kWarps) : 0;
-    float o[1][8][4], m[1][2], l[1][2];
-    attend_pages<kSplitQ, 1, kDepth>(a, b, kvh, mine, ids, warp, kWarps, count, 0, 0, own.tokens, o, m, l);
-    put_partial<1>(mine, sh->m[warp], sh->l[warp], o, m, l);
+    List list = {-1, 0, 0, 0, 0};
+    if (alone) {
+        grid_dependency_wait();
+        list = find_list(a, b, warp == 0);
+    }
+    add_own(a, b, threadIdx.x == 0, list);
+    const int count = list.pages > warp ? (list.pages - warp + kWarps - 1) / kWarps : 0;
+    const int ids = lane < count ? page_id(a, list, b, warp + lane * kWarps) : 0;
+    float o[kBlocks][8][4], m[kBlocks][2], l[kBlocks][2];
+    attend_pages<kSplitQ, kBlocks, kDepth>(a, b, kvh, mine, ids, warp, kWarps, count, list, o, m, l);
+    put_partial<kBlocks>(mine, sh->m[warp], sh->l[warp], o, m, l);
     __syncthreads();
     if (!alone) grid_dependency_wait();
     allow_dependent_launch();
@@ -392,7 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
         const auto part_row = [&](int i) { return p.row + static_cast<int64_t>(i) * kTile; };
         for (int i = 0; i < p.count; i += 8) join_partials<8>(a, part_row, i, p.count, top, sum, x);
         const int64_t row = static_cast<int64_t>(b) * a.hq + kvh * g + r;
-        const bool some = pages > 0 || p.count > 0;
+        const bool some = list.pages > 0 || p.count > 0;
         const float inv = some ? 1.f / sum : 0.f;
         *reinterpret_cast<uint2*>(a.out + row * kD + lane * 4) =
             make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
@@ -400,10 +414,10 @@ __global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
     }
 }
 
-template <bool kSplitQ, int kWarps, int kDepth>
+template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
 cudaError_t launch_own_t(const PrefixArgs& a, int grid, cudaStream_t stream) {
     constexpr int kBytes = kWarps * kDepth * kSlotBytes + static_cast<int>(sizeof(Own<kWarps>));
-    cudaError_t e = ensure_kernel_attrs<own_kernel<kSplitQ, kWarps, kDepth>>(kBytes);
+    cudaError_t e = ensure_kernel_attrs<own_kernel<kSplitQ, kBlocks, kWarps, kDepth>>(kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -415,7 +429,7 @@ cudaError_t launch_own_t(const PrefixArgs& a, int grid, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, own_kernel<kSplitQ, kWarps, kDepth>, a, grid, a.num_groups == 0);
+    e = cudaLaunchKernelEx(&cfg, own_kernel<kSplitQ, kBlocks, kWarps, kDepth>, a, grid, a.own_alone);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -438,6 +452,7 @@ static bool small_is_wide(const PrefixArgs& a, int num_sms) {
     return 4 * small_ctas(a) <= 3 * static_cast<int64_t>(num_sms) && list_pages(a) > 192;
 }
 bool prefix_is_small(const PrefixArgs& a, int num_sms) {
+    if (list_pages(a) <= 16 && a.group <= 8) return false;    // list_by_pages: 3.3 - 4.2 us for 4.4
     if (a.num_groups > 32 || small_ctas(a) > 2 * static_cast<int64_t>(num_sms)) return false;
     return list_pages(a) <= (a.group <= 8 || small_is_wide(a, num_sms) ? kSmallPages : 384);
 }
@@ -455,13 +470,26 @@ cudaError_t launch_prefix_small(const PrefixArgs& a, int num_sms, cudaStream_t s
     return a.q_type == LOCKS_FP32 ? by_group(std::true_type()) : by_group(std::false_type());
 }
 
+// Measured (this / the other forms, us; 8 kv heads of 4 queries; tables of 1 + 7 pages): 7
+// sequences 3.9 / 9.9, 96 sequences 8.9 / 17.7, 256 sequences 22.6 / 34.0. Every sequence reads
+// the prefix for itself: 21 prefix pages and one of its own, 96 sequences 15.1 / 18.0, 256
+// sequences 34.4 / 29.5; 63 and one, 15 sequences 10.1 / 11.4 with four warps a CTA, 40
+// sequences 15.5 / 14.4. 1 + 119 pages: 96 sequences 64.1 / 71.8, 256 143.5 / 166.5. Sixteen
+// queries to a kv head, 2 kv heads, 96 sequences: 21 + 21 pages 17.5 / 19.3, 1 + 63 23.3 / 22.8.
+bool list_by_pages(const PrefixArgs& a, int num_sms) {
+    if (a.num_groups > 32 || list_pages(a) > (a.group > 8 ? 48 : kOwnPages)) return false;
+    const int64_t ctas = static_cast<int64_t>(a.batch) * a.hkv, room = 3 * static_cast<int64_t>(num_sms);
+    const int64_t prefix = a.num_groups > 0 ? a.max_prefix_pages : 0;
+    const int64_t most = a.group > 8 ? 24 : ctas <= num_sms ? 96 : 48;    // pages of a prefix, one wave of CTAs
+    return prefix * (ctas > room ? ctas : room) <= most * room;
+}
+
 bool own_by_pages(const PrefixArgs& a, int num_sms) {
     // Measured (this / as items of the tiled kernel, us; 8 kv heads of 4 queries, a prefix of
     // 4000 tokens): 96 sequences of up to 1 page 24.9 / 37.0, 32 pages 40.0 / 45.8, 125 pages
     // 82.8 / 79.1; 19 sequences 15.2 / 17.9, 19.3 / 21.5, 33.8 / 28.1. Sixteen queries to a kv
     // head (96 sequences, 2 kv heads) 26.1 / 27.1, 32.1 / 29.3.
-    if (a.group > 8 || a.max_pages > kOwnPages) return false;
-    if (a.num_groups == 0) return true;
+    if (a.group > 8 || a.max_pages > 64) return false;
     // A warp joins its rows one after the other, eight partials at a time, 0.7 us each; the
     // tiled kernel's own second launch has more warps for them. A prefix's block of rows has
     // about num_sms / (all blocks) partials.
@@ -475,12 +503,13 @@ cudaError_t launch_own(const PrefixArgs& a, int grid, cudaStream_t stream) {
     // sequences of up to 125 pages, 8 kv heads: 27.6 / 23.7 us; 96 sequences of one page 16.6 /
     // 19.2), or one of eight warps for long lists of few sequences (16 sequences of 64 pages
     // behind 128K tokens: 97.1, 94.4, 91.9).
-    const int64_t ctas = static_cast<int64_t>(a.batch) * a.hkv;
+    const int64_t ctas = static_cast<int64_t>(a.batch) * a.hkv, pages = a.own_alone ? list_pages(a) : a.max_pages;
     const auto launch = [&](auto split) {
         constexpr bool kSplitQ = decltype(split)::value;
-        return ctas > 2 * grid                    ? launch_own_t<kSplitQ, 4, 2>(a, grid, stream)
-               : ctas > grid || a.max_pages <= 32 ? launch_own_t<kSplitQ, 4, 3>(a, grid, stream)
-                                                  : launch_own_t<kSplitQ, 8, 2>(a, grid, stream);
+        if (a.group > 8) return launch_own_t<kSplitQ, 2, 4, 2>(a, grid, stream);
+        return ctas > 2 * grid                    ? launch_own_t<kSplitQ, 1, 4, 2>(a, grid, stream)
+               : ctas > grid || pages <= 32       ? launch_own_t<kSplitQ, 1, 4, 3>(a, grid, stream)
+                                                  : launch_own_t<kSplitQ, 1, 8, 2>(a, grid, stream);
     };
     return a.q_type == LOCKS_FP32 ? launch(std::true_type()) : launch(std::false_type());
 }

@@ -1,7 +1,7 @@
-"""The shared-prefix attention's forms on a GB300: one launch for short lists of few
-sequences; tiles for the prefixes and pages for few own tokens; tiles for everything. Which one a
-call takes follows its tables' widths, so cases of the first run on the others too, through
-tables that are wider than their lists. Tolerances are test_gpu_cache's: all forms round queries,
+"""The shared-prefix attention's forms on a GB300: one launch of clusters for few sequences; one
+of single CTAs for short lists; tiles for the prefixes and pages for few own tokens; tiles for
+everything. Which one a call takes follows its tables' widths, so cases of the first run on the
+others too, through tables that are wider than their lists. Tolerances are test_gpu_cache's: all forms round queries,
 weights and outputs alike."""
 import numpy as np
 import pytest
@@ -66,9 +66,9 @@ def test_both_forms(case, q_type):
 
 
 def test_calls_past_the_limits_take_tiles():
-    for groups, own, hkv in (([(1, 1)] * 33, [0] * 33, 1),        # groups
+    for groups, own, hkv in (([(1, 1)] * 33, [0] * 33, 1),        # groups (and own tokens by pages)
                              ([(1, 8065)], [128], 1),             # 513 pages
-                             ([(39, 16)], [16] * 39, 1)):         # clusters
+                             ([(39, 1600)], [16] * 39, 1)):       # clusters
         c = T.prefix_case(groups, own, 4 * hkv, hkv, seed=60)
         T.check_prefix(c)
         assert not scratch_untouched(c)
@@ -103,6 +103,18 @@ def test_tiles_at_small_sizes(test, tiles):
 @pytest.mark.parametrize("q_type", [torch.float32, torch.bfloat16])
 def test_tiles_head_layouts(hq, hkv, q_type, tiles):
     T.test_prefix_head_layouts(hq, hkv, q_type)
+
+
+@pytest.mark.parametrize("q_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("seqs", [32, 33, 70])
+def test_tiles_row_blocks(seqs, q_type, tiles):
+    T.test_prefix_row_blocks(seqs, q_type)
+
+
+@pytest.mark.parametrize("test", [T.test_prefix_many_sequences_many_groups, T.test_prefix_thousands_of_sequences],
+                         ids=lambda f: f.__name__[12:])
+def test_tiles_many(test, tiles):
+    test()
 
 
 @pytest.mark.parametrize("prefix", [1, 16, 100, 127, 128, 129, 256, 300, 2049])
@@ -236,3 +248,82 @@ def test_tokens_appended_ahead_are_seen(groups):
             torch.cuda.synchronize()
         assert torch.equal(c["out"], d["out"]) and torch.equal(c["lse"], d["lse"])
     T.check_prefix(c)
+
+
+# ------------------------------------------------ whole lists by pages, a CTA a kv head
+
+LIST_CASES = [
+    # groups, own tokens, hq, hkv
+    ([(1, 1)], [0], 1, 1),
+    ([(2, 33)], [45, 3], 32, 8),                                 # 6 pages, few sequences
+    ([(7, 200), (0, 90), (8, 16)], [i % 48 for i in range(17)], 8, 8),      # 16 pages
+    ([(5, 1536), (3, 1)], [512] * 10, 64, 8),                    # 128 pages, eight warps a CTA
+    ([(10, 700), (20, 768)], [i * 7 for i in range(40)], 32, 8),  # four, three a CTA in flight
+    ([(90, 160), (0, 3), (160, 90)], [i % 60 for i in range(256)], 28, 4),  # several waves of CTAs
+    ([(40, 380)], [i * 8 for i in range(48)], 32, 2),            # sixteen queries
+    ([(3, 30)] * 32, [i % 90 for i in range(100)], 8, 1),        # as many groups as there may be
+    ([], [(i * 50) % 2049 for i in range(60)], 16, 8),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LIST_CASES)))
+@pytest.mark.parametrize("q_type", [torch.float32, torch.bfloat16])
+def test_lists_by_pages(case, q_type):
+    groups, own, hq, hkv = LIST_CASES[case]
+    c = T.prefix_case(groups, own, hq, hkv, seed=120 + case, q_type=q_type)
+    T.check_prefix(c)
+    assert scratch_untouched(c)
+
+
+@pytest.fixture
+def many(monkeypatch):
+    """Cases of 32 / 8 heads with 40 more sequences, of no group and of one page at most."""
+    case = T.prefix_case
+    monkeypatch.setattr(T, "prefix_case",
+                        lambda groups, own, hq, hkv, **k: case(groups, list(own) + [i % 17 for i in range(40)], 32, 8, **k))
+
+
+@pytest.mark.parametrize("test", [T.test_prefix_groups_and_sequences_outside_them,
+                                  T.test_prefix_nonfinite_values_stay_in_their_rows,
+                                  T.test_prefix_in_a_graph_follows_its_lengths_and_two_calls_overlap],
+                         ids=lambda f: f.__name__[12:])
+def test_lists_by_pages_at_small_sizes(test, many):
+    test()
+
+
+def test_lists_by_pages_bad_lengths_bounds_and_pages():
+    c = T.prefix_case([(20, 100), (20, 60)], [i % 30 for i in range(40)], 32, 8, seed=9)
+    for name, at, value, as_if in (("seq_tokens", 1, 16 * c["dims"].max_pages_per_seq + 1, 0),
+                                   ("seq_tokens", 0, -1, 0), ("prefix_tokens", 0, -5, 0),
+                                   ("prefix_tokens", 1, 1 << 30, 0), ("group_start", 2, 41, 20),
+                                   ("page_table", (3, 0), -3, 0),
+                                   ("prefix_table", (1, 2), c["dims"].num_phys_pages, 0)):
+        kept = c[name].clone()
+        c[name][at] = value
+        c["ws"][:256] = 0
+        T.run_prefix(c)
+        assert L.locks_get_device_status(c["ws"]) == -6, name
+        got, got_lse = c["out"].clone(), c["lse"].clone()
+        c[name][at] = as_if
+        c["ws"][:256] = 0
+        T.check_prefix(c)
+        assert torch.equal(got, c["out"]) and torch.equal(got_lse, c["lse"]), name
+        c[name].copy_(kept)
+    assert scratch_untouched(c)
+
+
+def test_lists_by_pages_rows_behind_the_end_are_never_used():
+    groups, own = [(2, 261), (30, 5)], [19, 0, 30, 16, 1] * 8
+    c = T.prefix_case(groups, own, 32, 8, seed=7, spare=2)
+    used = torch.zeros(c["k"].shape[0], 16, dtype=torch.bool, device=T.DEV)
+    for tab, n in list(zip(c["prefix_table"], [n for _, n in groups])) + list(zip(c["page_table"], own)):
+        for t in range(n):
+            used[int(tab[t // 16]), t % 16] = True
+    behind = ~used[:, None, :].expand(-1, 8, -1)
+    T.run_prefix(c)
+    first, first_lse = c["out"].clone(), c["lse"].clone()
+    assert scratch_untouched(c)
+    c["k"][behind] = float("nan")
+    c["v"][behind] = float("-inf")
+    T.run_prefix(c)
+    assert torch.equal(first, c["out"]) and torch.equal(first_lse, c["lse"])
