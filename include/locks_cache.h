@@ -113,10 +113,14 @@ LOCKS_API int locks_prefix_workspace_size(const locks_dims_t* dims, int32_t num_
  * - page_table int32 [batch][max_pages_per_seq], not read when
  *   max_pages_per_seq is 0.
  * - out bf16 bits [batch][num_q_heads][128], 16-byte aligned; lse fp32, may be
- *   NULL. Two kernel launches.
- * The result does not depend on which sequences share a prefix but through
- * rounding (the order in which parts of the softmax are joined), and repeats
- * exactly for the same arguments.
+ *   NULL.
+ * One kernel launch, or two for long lists. Which form runs follows the batch,
+ * the heads and the widths of the tables (max_prefix_pages and
+ * max_pages_per_seq), so tables not much wider than the lists in them serve
+ * best.
+ * The result depends on which sequences share a prefix, on the batch and on
+ * those widths through rounding alone (the order in which parts of the softmax
+ * are joined), and repeats exactly for the same arguments.
  */
 LOCKS_API int locks_prefix_attention(const locks_dims_t* dims, const void* q, int32_t q_type,
                                      const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* prefix_table,

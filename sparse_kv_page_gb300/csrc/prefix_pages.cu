@@ -1,13 +1,13 @@
 // prefix_pages.cu - the parts of the shared-prefix attention (locks_prefix_attention) that go
 // by pages on mma.sync, where a tile of 128 rows and 128 tokens would be mostly empty:
 //
-// 1. Short lists of few sequences, in one launch. One cluster of eight CTAs per (sequence, kv
-//    head): its 32 or 64 warps take the pages of the sequence's list (its group's prefix, then its
-//    own, up to 512) in turn with an online softmax, and their partials meet in shared memory and then, a
-//    query head per CTA, through distributed shared memory. A prefix is read once per sequence,
-//    which L2 serves; what the tiled kernel's evenly cut line, its pipeline and its second
-//    launch cost (10 us at the least) is what this one saves: 12.1 -> 4.8 us for two sequences
-//    behind 333 tokens. Latency bounds it.
+// 1. Few sequences, lists of up to 512 pages, in one launch. One cluster of eight CTAs per
+//    (sequence, kv head): its 32 or 64 warps take the pages of the sequence's list (its group's
+//    prefix, then its own) in turn with an online softmax, and their partials meet in shared
+//    memory and then, a query head per CTA, through distributed shared memory. A prefix is read
+//    once per sequence, which L2 serves; what the tiled kernel's evenly cut line, its pipeline
+//    and its second launch cost (10 us at the least) is what this one saves: 12.1 -> 4.8 us for
+//    two sequences behind 333 tokens. Latency bounds it.
 //
 // 2. Many sequences, in one launch where lists are short, else as the second launch behind the
 //    tiled kernel, which has the prefixes: a CTA per (sequence, kv head) attends to the pages and
@@ -28,6 +28,10 @@ namespace {
 constexpr int kRowBytes = kD * 2;
 constexpr int kPageBytes = kPage * kRowBytes;
 constexpr int kSlotBytes = 2 * kPageBytes;            // K and V of a page
+
+// CTAs that an SM holds: 227 KB are 27 slots and the partials.
+template <int kWarps, int kDepth>
+constexpr int kCtasPerSm = 27 / (kWarps * kDepth);
 
 // The one-launch form: a cluster of CTAs per (sequence, kv head).
 constexpr int kCluster = 8;
@@ -279,7 +283,7 @@ __device__ __forceinline__ float4 row_of_warps(const uint8_t* slots, const float
 }
 
 template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
-__global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<kWarps, kDepth>)
     small_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ __align__(1024) uint8_t slots[];
     constexpr int kAllWarps = kCluster * kWarps;
@@ -371,7 +375,7 @@ struct Own {
 constexpr int kOwnPages = 32 * 4;                     // longest list taken: a warp's page ids lie in its lanes
 
 template <bool kSplitQ, int kBlocks, int kWarps, int kDepth>
-__global__ void __launch_bounds__(kWarps * 32, 27 / (kWarps * kDepth))
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<kWarps, kDepth>)
     own_kernel(const __grid_constant__ PrefixArgs a, int grid, bool alone) {
     extern __shared__ __align__(1024) uint8_t slots[];
     auto* sh = reinterpret_cast<Own<kWarps>*>(slots + kWarps * kDepth * kSlotBytes);
