@@ -97,7 +97,7 @@ struct Control {
     uint64_t joined;                              // both groups' maxima of a piece are in m
     uint32_t tmem;
     int abort;
-    float m[2][kTile];
+    float m[2][2][kTile];                         // [piece n % 2][group]: see run_softmax
     Piece pieces[kPieces];
 };
 template <bool kSplitQ>
@@ -622,8 +622,12 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
             if (lane == 0) mbar_arrive(&ctl->weights[x][b]);
         }
         // the piece's partial, once its last products are in: group x brings 64 dims of both
-        // groups' sums to the larger maximum
-        ctl->m[x][row] = m;
+        // groups' sums to the larger maximum. Pieces take turns with two copies of the maxima: a
+        // group may be done with the next piece's weights while the other has yet to read this
+        // one's, but the copy is written again only after `joined` of the piece between, where
+        // the other arrives after its read.
+        float(&tops)[2][kTile] = ctl->m[p.n & 1];
+        tops[x][row] = m;
         const int64_t at = p.part + row;
         if (row < p.rows) a.part_ml[at * 2 + x] = make_float2(m, l);
         __syncwarp();
@@ -632,7 +636,7 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
         if (!wait(&ctl->joined, p.n & 1)) return;
         tc_fence_after_sync();
         if (busy) {
-            const float m0 = ctl->m[0][row], m1 = ctl->m[1][row], top = fmaxf(m0, m1);
+            const float m0 = tops[0][row], m1 = tops[1][row], top = fmaxf(m0, m1);
             const float base = top == -INFINITY ? 0.f : top;
             const float f0 = fast_exp2((m0 - base) * kScaleLog2), f1 = fast_exp2((m1 - base) * kScaleLog2);
             const bool second = p.tiles > 1 || p.valid(0) > kGroupTokens;     // else group 1 holds nothing
