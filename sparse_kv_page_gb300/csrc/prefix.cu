@@ -97,6 +97,7 @@ struct Control {
     uint64_t joined;                              // both groups' maxima of a piece are in m
     uint32_t tmem;
     int abort;
+    uint32_t issued[2];                           // tiles whose K (V) loads were issued
     float m[2][2][kTile];                         // [piece n % 2][group]: see run_softmax
     Piece pieces[kPieces];
 };
@@ -340,13 +341,25 @@ __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Co
             ++t;
         }
     }
-    if (!ok) {
-        // giving up: the loads in flight write to this CTA's shared memory, so wait for them
-        for (uint32_t i = t > kN ? t - kN : 0; i < t; ++i) {
-            const uint32_t seq = kValues ? v_entry(i) : k_entry(i);
-            mbar_wait_bounded(&ctl->full[seq % kN], (seq / kN) & 1, kDrainNs);
-        }
+    if (lane == 0) ctl->issued[kValues] = t;
+}
+
+// After a role has given up, wherever it did: the loads in flight write to this CTA's shared
+// memory, which has to stay until they have landed. A warp, once every role has ended: lane s
+// waits for the last entry that was loaded into slot s (what was there before was used up, so
+// it had landed; entries of a slot follow one another without a gap, so entry e is its phase
+// e / kN). The last entry of a slot is among the last kN tiles of K or of V.
+template <bool kSplitQ>
+__device__ __noinline__ void drain_loads(Control* ctl) {
+    constexpr int kN = kSlots<kSplitQ>;
+    const int slot = threadIdx.x & 31;
+    int last = -1;
+    for (int back = 1; back <= kN; ++back) {
+        const int k = static_cast<int>(ctl->issued[0]) - back, v = static_cast<int>(ctl->issued[1]) - back;
+        if (k >= 0 && static_cast<int>(k_entry(k) % kN) == slot) last = max(last, static_cast<int>(k_entry(k)));
+        if (v >= 0 && static_cast<int>(v_entry(v) % kN) == slot) last = max(last, static_cast<int>(v_entry(v)));
     }
+    if (slot < kN && last >= 0) mbar_wait_bounded(&ctl->full[slot], (last / kN) & 1, kDrainNs);
 }
 
 // --------------------------------------------------------------------- the queries
@@ -784,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (warp == 0 && ctl->abort) drain_loads<kSplitQ>(ctl);
     if (warp == 1) tmem_free(ctl->tmem, 512);
 }
 

@@ -33,3 +33,44 @@ def test_short_pieces(case, q_type):
         c["out"].fill_(float("nan"))
         T.run_prefix(c)
         assert torch.equal(first, c["out"]) and torch.equal(first_lse, c["lse"])
+
+
+@pytest.fixture
+def wait_limit():
+    yield T.L.locks_set_wait_limit_ns
+    T.L.locks_set_wait_limit_ns(0)
+
+
+TIMEOUT = -5
+
+
+@pytest.mark.parametrize("q_type", [torch.float32, torch.bfloat16])
+def test_giving_up_leaves_nothing_in_flight(q_type, wait_limit):
+    """With a limit that waits for loads run past, a call either ends as ever or records that it gave
+    up. In both cases nothing of it may land in the shared memory of the calls behind it."""
+    c = wide(T.prefix_case([(40, 3000), (3, 20000)], [(i * 131) % 1500 for i in range(50)], 32, 8, seed=170, q_type=q_type))
+    d = T.prefix_case([(2, 333)], [45, 3], 32, 8, seed=171, q_type=q_type)
+    T.check_prefix(c)
+    T.check_prefix(d)
+    want = [x[n].clone() for x in (c, d) for n in ("out", "lse")]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=T.DEV)
+    for limit in (1, 1, 500, 2000, 5000):
+        for behind in (c, d):                     # other kernels, and the same
+            c["ws"][:256] = 0
+            d["out"].fill_(float("nan"))
+            flush.fill_(1)                        # the loads come from memory
+            wait_limit(limit)
+            T.run_prefix(c)
+            wait_limit(0)
+            status = T.L.locks_get_device_status(c["ws"])
+            assert status in (0, TIMEOUT)
+            if status == 0:
+                assert torch.equal(c["out"], want[0]) and torch.equal(c["lse"], want[1])
+            wait_limit(limit)
+            T.run_prefix(c)
+            wait_limit(0)
+            T.run_prefix(behind)
+            i = 0 if behind is c else 2
+            assert torch.equal(behind["out"], want[i]) and torch.equal(behind["lse"], want[i + 1])
+    c["ws"][:256] = 0
+    T.check_prefix(c)
