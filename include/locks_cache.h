@@ -144,8 +144,10 @@ LOCKS_API int locks_mass_workspace_size(const locks_dims_t* dims, size_t* bytes)
  *   (but may not overlap it otherwise). decay: finite; 1 sums, less forgets.
  *   With decay 0 the old mass is not read.
  * - lse_partials (may be NULL): the partials locks_score_pages wrote for these
- *   same scores and dims on this device; L_bh is then joined from them (their
- *   sums hold +inf scores too) and the scores are read once instead of twice.
+ *   same scores, dims and seq_pages on this device; L_bh is then joined from them
+ *   and the scores are read once instead of twice. What that call left of the
+ *   buffer as it was is not read. (The scorer leaves a +inf score out of its sums
+ *   together with the eight pages 8i .. 8i + 7 it lies among, so L_bh lacks those.)
  * - seq_pages[b] out of [0, max_pages_per_seq] records LOCKS_ERR_BAD_INDEX and
  *   the sequence is skipped. Two kernel launches.
  */

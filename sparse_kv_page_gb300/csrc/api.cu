@@ -282,8 +282,14 @@ int check_dims(const locks_dims_t* d) { return validate_dims(d); }
 int check_workspace(void* ws, size_t bytes, size_t need) { return check_ws(ws, bytes, need); }
 int current_sms() { return num_sms(current_device()); }
 DeviceStatus device_status(void* ws) { return status_of(ws); }
-int scorer_partials_row(const locks_dims_t* d, int sms) {
-    return scorer_grid(d, sms) * slot_warps(d->num_kv_heads, d->num_q_heads / d->num_kv_heads);
+ScorerSlots scorer_slots(const locks_dims_t* d, int sms) {
+    const int np = kStageUnits / d->num_kv_heads;
+    ScorerSlots s;
+    s.chunks = (d->max_pages_per_seq + np - 1) / np;
+    s.grid = std::max(1, scorer_grid(d, sms));
+    s.per = std::max(1, (d->batch * s.chunks + s.grid - 1) / s.grid);
+    s.warps = slot_warps(d->num_kv_heads, d->num_q_heads / d->num_kv_heads);
+    return s;
 }
 }  // namespace locks
 

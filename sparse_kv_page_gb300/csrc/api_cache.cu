@@ -255,8 +255,7 @@ int locks_accumulate_mass(const locks_dims_t* dims, const float* scores, const f
     if (lse_partials) {
         a.row = 1;
         s = cuda_status(locks::launch_mass_reduce(reinterpret_cast<const float2*>(lse_partials),
-                                                  locks::scorer_partials_row(dims, sms),
-                                                  static_cast<int64_t>(dims->batch) * dims->num_q_heads, own, st));
+                                                  locks::scorer_slots(dims, sms), a, own, st));
     } else {
         a.row = locks::mass_partials_row(dims->max_pages_per_seq);
         s = cuda_status(locks::launch_mass_partials(a, own, st));

@@ -12,7 +12,14 @@ int check_dims(const locks_dims_t* d);
 int check_workspace(void* ws, size_t bytes, size_t need);
 int current_sms();                       // SMs of the current device; 0: no device
 DeviceStatus device_status(void* ws);    // with the process's wait limit
-int scorer_partials_row(const locks_dims_t* d, int sms);   // (max, sum exp) pairs per (sequence, query head)
+// Where locks_score_pages puts its (max, sum exp) pairs, on a device of `sms` SMs: [batch][query
+// head][grid][warps]. A sequence is `chunks` items (sequence b the items from b * chunks on), and
+// scorer CTA c has items c * per .. (c + 1) * per and writes the pairs of the sequences they
+// belong to, no others.
+struct ScorerSlots {
+    int grid, warps, chunks, per;
+};
+ScorerSlots scorer_slots(const locks_dims_t* d, int sms);
 
 // ------------------------------------------------------------------ launchers
 struct AppendArgs {
@@ -54,8 +61,9 @@ struct MassArgs {
 // Pairs per (sequence, query head) that launch_mass_partials writes.
 int mass_partials_row(int max_pages);
 cudaError_t launch_mass_partials(const MassArgs& a, float2* partials, cudaStream_t stream);
-// Joins `row` pairs per (sequence, query head) to one.
-cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2* out, cudaStream_t stream);
+// Joins the scorer's pairs of each (sequence, query head) to one.
+cudaError_t launch_mass_reduce(const float2* in, const ScorerSlots& slots, const MassArgs& a, float2* out,
+                               cudaStream_t stream);
 // Follows one of the two on the same stream.
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream);
 

@@ -83,18 +83,27 @@ __global__ void __launch_bounds__(kThreads) partials_kernel(const MassArgs a, fl
     }
 }
 
-// The scorer's pairs, `row` per (sequence, query head), joined to one: a warp each.
-__global__ void __launch_bounds__(kThreads) reduce_kernel(const float2* in, int row, int64_t heads, float2* out) {
+// The scorer's pairs of each (sequence, query head), joined to one: a warp each. Only the slots
+// of the scorer CTAs whose items reach into the sequence are the scorer's: the others hold
+// whatever they held before. A pair whose sum is not above 0, or whose maximum is a NaN, holds
+// no scores (the selection's normaliser reads the same slots by the same rule).
+__global__ void __launch_bounds__(kThreads)
+    reduce_kernel(const float2* in, ScorerSlots slots, int hq, int64_t heads, float2* out) {
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t h = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (h >= heads) return;
+    const int64_t b = h / hq;
+    const int first = static_cast<int>(b * slots.chunks / slots.per);
+    const int last = min(slots.grid - 1, static_cast<int>(((b + 1) * slots.chunks - 1) / slots.per));
+    const float2* row = in + (h * slots.grid + first) * slots.warps;
+    const int n = (last - first + 1) * slots.warps;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 4
-    for (int i = lane; i < row; i += 32) {
-        const float2 v = in[h * row + i];
-        join(m, l, v.x, v.y);
+    for (int i = lane; i < n; i += 32) {
+        const float2 v = row[i];
+        if (v.y > 0.f && v.x == v.x) join(m, l, v.x, v.y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -485,9 +494,11 @@ cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream) {
     return launch_pdl(mass_kernel, dim3(blocks, a.batch, 1), kThreads, 0, stream, a, rows_aligned(a));
 }
 
-cudaError_t launch_mass_reduce(const float2* in, int row, int64_t heads, float2* out, cudaStream_t stream) {
+cudaError_t launch_mass_reduce(const float2* in, const ScorerSlots& slots, const MassArgs& a, float2* out,
+                               cudaStream_t stream) {
+    const int64_t heads = static_cast<int64_t>(a.batch) * a.hq;
     return launch_pdl(reduce_kernel, dim3(static_cast<unsigned>((heads + kWarps - 1) / kWarps)), kThreads, 0, stream, in,
-                      row, heads, out);
+                      slots, a.hq, heads, out);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
