@@ -97,9 +97,9 @@ LOCKS_API int locks_prefix_workspace_size(const locks_dims_t* dims, int32_t num_
  * tokens may end inside a page; rows behind the end are never used, whatever
  * they hold. No tokens at all: out = 0, lse = -inf.
  * - q: q_type LOCKS_FP32 or LOCKS_BF16, contiguous [batch][num_q_heads][128],
- *   16-byte aligned. fp32 queries enter the products as a bf16 high and low
- *   part (about 16 significant bits); weights are rounded to bf16 once before
- *   they meet the values; sums and softmax statistics are fp32.
+ *   16-byte aligned. fp32 queries, and the softmax weights where they meet the
+ *   values, enter the products as a bf16 high and low part (about 16 significant
+ *   bits); sums and softmax statistics are fp32.
  * - prefix_table int32 [num_groups][max_prefix_pages], prefix_tokens int32
  *   [num_groups] in [0, 16 * max_prefix_pages], group_start int32
  *   [num_groups + 1], not falling, in [0, batch]; seq_tokens int32 [batch] in

@@ -27,18 +27,22 @@
 // blocks until it is taken (one warp for both products took 3600 cycles a tile, one for all
 // 32 boxes 2400), and every role finding its own pieces spilled. The code is kept small: behind
 // a saturated HBM an instruction fetch from L2 takes microseconds.
-// Tensor memory: two score tiles (2 x 128 columns; the bf16 weights overwrite them) and the
-// groups' accumulators (2 x 128). Shared memory: the queries as a bf16 high part and, for
+// Tensor memory: two score tiles (2 x 128 columns; the weights, a bf16 high and low part each,
+// overwrite them) and the groups' accumulators (2 x 128). Shared memory: the queries as a bf16 high part and, for
 // fp32, a low part (32 KB each; 16 significant bits together), and a ring of 32 KB slots,
 // each a K or a V tile: eight pages of two 64-dim halves, one 2 KB TMA box each.
 // Pieces of up to 16 rows (a sequence's own tokens, small groups) take an eighth of the
 // query space each, so their queries come ahead of time; the products read 128 rows all the
 // same, and what the rows behind a piece's own hold reaches no row but theirs.
 //
-// Bound: per 128 x 128 tile the products take 128 * 128 * 128 * (2 + 1) multiply-adds (high
-// and low scores, then the values; one less for bf16 queries), 1536 cycles at the SM's 4096
-// a cycle; its 64 KB take about 2800 cycles at an SM's share of HBM. Up to 128 rows HBM
-// bounds it, above that the tensor cores.
+// The weights meet the values as two bf16 parts too (16 significant bits): as one, their
+// rounding would be as large in the output as the output's own, and put its error against 64
+// bits at 1.4 times that. One part / two, us: fp32 queries 128K tokens x 16 sequences 91 / 104,
+// 1M x 8 (32/2 heads) 170 / 195; bf16 queries 24K x 4 x 32 91.5 / 94.6, 64K x 64 94.7 / 98.2.
+// Bound: per 128 x 128 tile the products take 128 * 128 * 128 * (2 + 2) multiply-adds (high
+// and low scores, then the values with high and low weights; bf16 queries have no low scores),
+// 2048 cycles at the SM's 4096 a cycle; its 64 KB take about 2800 cycles at an SM's share of
+// HBM. Each block of 128 rows streams its prefix for itself.
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -108,6 +112,7 @@ static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024,
 // Tensor-memory columns: score tile b, accumulator of group x.
 __host__ __device__ constexpr uint32_t score_col(int b) { return b * 128; }
 __host__ __device__ constexpr uint32_t acc_col(int x) { return 256 + x * 128; }
+constexpr uint32_t kLowWeights = kGroupTokens / 2;   // a group's weights: high parts, then low parts
 
 // A wait that gives up after the limit, or once another warp of the CTA has. Out of line: the
 // roles' code together is larger than the nearer instruction caches, and behind a saturated
@@ -477,13 +482,14 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
             if (lane == 0) {
                 const uint32_t idesc = bf16_idesc(kTile, (p.valid(i) + kPage - 1) / kPage * kPage, false);
                 const uint32_t k_addr = ring_addr + slot * kTileBytes;
-#pragma unroll 1
+                const uint64_t q_desc = sw128_desc(q_at, 16, 1024), k_desc = sw128_desc(k_addr, 16, 1024);
+#pragma unroll
                 for (int part = 0; part < (kSplitQ ? 2 : 1); ++part)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-                        mma_ss(tmem + score_col(b), sw128_desc(q_at + part * kTileBytes + off, 16, 1024),
-                               sw128_desc(k_addr + off, 16, 1024), idesc, part + k > 0);
+                        const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                        mma_ss(tmem + score_col(b), q_desc + (part * (kTileBytes >> 4) + off), k_desc + off, idesc,
+                               part + k > 0);
                     }
                 mma_commit(&ctl->scores[b]);
                 mma_commit(&ctl->empty[slot]);
@@ -528,12 +534,19 @@ __device__ __forceinline__ void run_values(const PrefixArgs& a, uint8_t* ring, C
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (lane == 0) {
+                    const uint64_t v = sw128_desc(v_addr + x * (kTilePages / 2) * kBoxBytes, kHalfBytes, 1024);
+                    const uint32_t w = tmem + score_col(b) + x * kGroupTokens;
+                    const auto page = [&](int k) {                // 16 tokens
+                        mma_ts(tmem + acc_col(x), w + 8 * k, v + k * (kBoxBytes >> 4), kValues, i > 0 || k > 0);
+                        mma_ts(tmem + acc_col(x), w + kLowWeights + 8 * k, v + k * (kBoxBytes >> 4), kValues, true);
+                    };
+                    if (live == kTilePages) {
 #pragma unroll
-                    for (int k = 0; k < kTilePages / 2; ++k)      // 16 tokens: one page
-                        if (x * (kTilePages / 2) + k < live)
-                            mma_ts(tmem + acc_col(x), tmem + score_col(b) + x * kGroupTokens + 8 * k,
-                                   sw128_desc(v_addr + (x * (kTilePages / 2) + k) * kBoxBytes, kHalfBytes, 1024),
-                                   kValues, i > 0 || k > 0);
+                        for (int k = 0; k < kTilePages / 2; ++k) page(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < min(kTilePages / 2, live - x * (kTilePages / 2)); ++k) page(k);
+                    }
                 }
             }
             if (ok && lane == 0) {
@@ -560,6 +573,27 @@ __device__ __forceinline__ void help_queries(const PrefixArgs& a, uint8_t* q_s, 
     if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->q_first);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 d;\n\tfma.rn.f32x2 d, %2, %3, %4;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "l"(bits2(a)), "l"(bits2(make_float2(b, b))), "l"(bits2(c)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 d;\n\tadd.rn.f32x2 d, %2, %3;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "l"(bits2(a)), "l"(bits2(b)));
+    return r;
+}
+
 __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
     const int tid = threadIdx.x - 128;            // 0..255
     const int x = tid >> 7, row = tid & 127;      // softmax group, row of the block (= tensor-memory lane)
@@ -580,12 +614,11 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
             if (busy && valid > 0) {
                 const uint32_t tile = lane_base + score_col(b) + x * kGroupTokens;
                 float s[kGroupTokens];
+                {
+                    uint32_t r[kGroupTokens];
+                    tmem_load(r, tile);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32];
-                    tmem_load(r, tile + c * 32);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[e]);
+                    for (int e = 0; e < kGroupTokens; ++e) s[e] = __uint_as_float(r[e]);
                 }
                 if (valid < kGroupTokens) {
 #pragma unroll
@@ -617,17 +650,26 @@ __device__ __forceinline__ void run_softmax(const PrefixArgs& a, Control* ctl) {
                     m = to;
                 }
                 const float base = m == -INFINITY ? 0.f : m * kScaleLog2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t r[32];
+                float2 sum[4] = {};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float u = fast_exp2(fmaf(s[2 * e], kScaleLog2, -base));
-                    const float v = fast_exp2(fmaf(s[2 * e + 1], kScaleLog2, -base));
-                    sum[e & 3] += u + v;
-                    r[e] = pack_bf16x2(u, v);
+                for (int c = 0; c < kGroupTokens; c += 32) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 u =
+                            fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), kScaleLog2, make_float2(-base, -base));
+                        const float2 w = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+                        sum[e & 3] = add2(sum[e & 3], w);
+                        hi[e] = pack_bf16x2(w.x, w.y);
+                        const float2 rest = fma2(
+                            make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), -1.f, w);
+                        lo[e] = pack_bf16x2(rest.x, rest.y);
+                    }
+                    tmem_store(tile + c / 2, hi);
+                    tmem_store(tile + kLowWeights + c / 2, lo);
                 }
-                tmem_store(tile, r);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += all.x + all.y;
                 tmem_wait_store();
             }
             tc_fence_before_sync();

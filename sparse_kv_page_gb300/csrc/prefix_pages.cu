@@ -15,9 +15,9 @@
 //    kv head) takes a tile's pipeline of its own, about 2.8 us of an SM: 96 sequences of up to
 //    100 tokens behind 16, 8 kv heads: 27.1 -> 8.9 us; behind 4000 tokens 38.2 -> 28.3.
 //
-// fp32 queries enter the products as a bf16 high and low part, weights are rounded to bf16 once
-// (at most 2^-8 of the sum of |weight * v|), as in the tiled kernel. What bounds a warp's page
-// is its 24 products (fp32) and their chain, 0.3 us; copies of its next pages run beside them.
+// fp32 queries and the weights enter the products as a bf16 high and low part (what is left out
+// of a weight is at most 2^-16 of it), as in the tiled kernel. What bounds a warp's page is its
+// 32 products (fp32) and their chain, 0.3 us; copies of its next pages run beside them.
 #include <type_traits>
 
 #include "prefix_units.cuh"
@@ -100,7 +100,7 @@ __device__ __forceinline__ int page_id(const PrefixArgs& a, const List& list, in
 // A warp's pages of sequence b's list: page first + i * step for i < count (up to 32, the id of
 // page i in lane i). Products are formed with the
 // queries as columns, S^T = K Q^T and O^T = V^T P^T, eight to a block: a group's few queries
-// would leave most of sixteen rows empty (4 queries: 24 products a page, 48 as rows). Leaves, per
+// would leave most of sixteen rows empty (4 queries: 32 products a page, 64 as rows). Leaves, per
 // column 2 * (lane % 4) + c of block n, the maximum m[n][c], this lane's part of the sum and the
 // accumulator o[n][16 dims][.].
 template <bool kSplitQ, int kBlocks, int kDepth>
@@ -189,7 +189,7 @@ __device__ __forceinline__ void attend_pages(const PrefixArgs& a, int b, int kvh
                 else if (k % 2 == 1) mma_bf16_16816(t[n], r, qh[n][k][0], qh[n][k][1]);
             }
         }
-        uint32_t p[kBlocks][2];
+        uint32_t p[kBlocks][2], pl[kBlocks][2];          // high and low parts
         float f[kBlocks][2];
         bool same = true;
 #pragma unroll
@@ -211,8 +211,13 @@ __device__ __forceinline__ void attend_pages(const PrefixArgs& a, int b, int kvh
                 s[n][c + 2] = fast_exp2(fmaf(s[n][c + 2], kScaleLog2, -base));
                 l[n][c] = l[n][c] * f[n][c] + (s[n][c] + s[n][c + 2]);
             }
-            p[n][0] = movmatrix_trans(pack_bf16x2(s[n][0], s[n][1]));    // tokens down, queries along: turned
-            p[n][1] = movmatrix_trans(pack_bf16x2(s[n][2], s[n][3]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {                // tokens down, queries along: turned
+                const uint32_t hi = pack_bf16x2(s[n][2 * h], s[n][2 * h + 1]);
+                p[n][h] = movmatrix_trans(hi);
+                pl[n][h] = movmatrix_trans(pack_bf16x2(s[n][2 * h] - __uint_as_float(hi << 16),
+                                                       s[n][2 * h + 1] - __uint_as_float(hi & 0xffff0000u)));
+            }
         }
         if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
@@ -222,12 +227,21 @@ __device__ __forceinline__ void attend_pages(const PrefixArgs& a, int b, int kvh
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[n][d][e] *= f[n][e & 1];
         }
+        constexpr int kDims = kBlocks == 1 ? 4 : 2;      // sixteen dims at a time, between a sum's two products
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {                    // sixteen dims at a time
-            uint32_t r[4];
-            ldmatrix_x4_trans(r, slot + kPageBytes + chunk_offset((lane & 7) + (lane >> 4) * 8, 2 * d + ((lane >> 3) & 1)));
+        for (int d0 = 0; d0 < 8; d0 += kDims) {
+            uint32_t r[kDims][4];
 #pragma unroll
-            for (int n = 0; n < kBlocks; ++n) mma_bf16_16816(o[n][d], r, p[n][0], p[n][1]);
+            for (int d = 0; d < kDims; ++d)
+                ldmatrix_x4_trans(r[d], slot + kPageBytes + chunk_offset((lane & 7) + (lane >> 4) * 8,
+                                                                         2 * (d0 + d) + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int n = 0; n < kBlocks; ++n) {
+#pragma unroll
+                for (int d = 0; d < kDims; ++d) mma_bf16_16816(o[n][d0 + d], r[d], p[n][0], p[n][1]);
+#pragma unroll
+                for (int d = 0; d < kDims; ++d) mma_bf16_16816(o[n][d0 + d], r[d], pl[n][0], pl[n][1]);
+            }
         }
         __syncwarp();
         if (i + kDepth < count) load(i + kDepth, at);
