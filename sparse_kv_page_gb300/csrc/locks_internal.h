@@ -6,32 +6,25 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "locks_common.cuh"
+#include "raise_once.h"
 
 namespace locks {
 
 // Raises a kernel's dynamic shared-memory limit (and allows 16-CTA clusters
-// when asked) once per device instead of on every launch.
+// when asked) once per device and size instead of on every launch.
 template <auto Kern>
 cudaError_t ensure_kernel_attrs(int smem_bytes, bool nonportable_cluster = false) {
-    static std::atomic<int> done[64];
+    static RaiseOnce limits;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire) >= smem_bytes + 1) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
-    if (e != cudaSuccess) return e;
-    if (nonportable_cluster) {
-        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    int prev = done[dev].load();
-    while (prev < smem_bytes + 1 && !done[dev].compare_exchange_weak(prev, smem_bytes + 1)) {
-    }
-    return cudaSuccess;
+    if (dev < 0 || dev >= RaiseOnce::kDevices) return cudaErrorInvalidDevice;
+    return limits.raise(dev, smem_bytes, [&] {
+        const cudaError_t s = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+        if (s != cudaSuccess || !nonportable_cluster) return s;
+        return cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
 }
 
 // The scorer's persistent grid: one CTA per SM, at most kMaxScorerCtas (which bounds the
