@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "cache_internal.h"
+#include "rope_turns.h"
 
 namespace {
 
@@ -26,21 +27,6 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 // Two buffers that are the same one or have nothing in common.
 bool same_or_apart(const void* a, const void* b, size_t bytes) { return a == b || !overlap(a, bytes, b, bytes); }
-
-// x / (2 pi) as a fraction of a turn in units of 2^-64, whole turns dropped. The quotient is
-// formed as a double-double (1 / (2 pi) to 106 bits), so its fraction is good to 2^-64 turns
-// for any |x| up to thousands of radians per position.
-uint64_t turn_fraction(double x) {
-    constexpr double kHi = 0.15915494309189535, kLo = -9.8393378335251835e-18;   // 1 / (2 pi)
-    const double p = x * kHi;
-    const double err = std::fma(x, kHi, -p) + x * kLo;
-    double hi = p - std::floor(p);                          // exact: both are multiples of p's last bit
-    // hi in [0, 1] and err tiny: to 2^-64, in two exact 32-bit steps
-    const double a = std::floor(hi * 4294967296.0);
-    const double rest = (hi * 4294967296.0 - a) + err * 4294967296.0;   // in units of 2^-32
-    const double b = std::nearbyint(rest * 4294967296.0);   // may be negative or 2^32: the sum wraps
-    return (static_cast<uint64_t>(a) << 32) + static_cast<uint64_t>(static_cast<int64_t>(b));
-}
 
 struct MassLayout {
     size_t partials, total;
@@ -138,7 +124,7 @@ int locks_append_tokens(const locks_dims_t* dims, const locks_rope_t* rope, cons
         a.interleaved = rope->interleaved;
         a.rope_scale = rope->scale;
         for (int i = 0; i < rope->rot_dim / 2; ++i) {
-            a.turns[i] = turn_fraction(rope->inv_freq[i]);
+            a.turns[i] = locks::turn_fraction(rope->inv_freq[i]);
             a.axis[i] = static_cast<uint8_t>(rope->axis[i]);
         }
     }

@@ -76,3 +76,38 @@ def test_of_two_threads_the_smaller_size_does_not_stay(limits):
     a.join(10), b.join(10)
     limits(0, 5000, fast)
     assert now[0] == 5000
+
+
+# ------------------------------------------------------------ rope_turns.h
+
+def inverse_two_pi(bits):
+    """1 / (2 pi) * 2^bits, from pi = 16 atan(1/5) - 4 atan(1/239) in integers."""
+    one = 1 << (bits + 32)
+
+    def atan(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    return (one << bits) // (2 * (16 * atan(5) - 4 * atan(239)))
+
+
+def test_turns_per_position_to_the_last_bit(tmp_path):
+    lib = compiled(tmp_path, "turns", '''
+        #include "rope_turns.h"
+        extern "C" uint64_t turns(double x) { return locks::turn_fraction(x); }''')
+    lib.turns.argtypes, lib.turns.restype = [ctypes.c_double], ctypes.c_uint64
+    bits = 320
+    scale = inverse_two_pi(bits)
+    sizes = [0.75, 1.0, 0.1, 1e-3, 1e-6, 2.6e-6, 1e-12, 6.283185307179586, 6.3, 3.0, 100.0, 4095.9, 4096.0]
+    sizes += [500000.0 ** (-i / 64) for i in range(64)]
+    for x in [0.0, -0.0] + sizes + [-v for v in sizes]:
+        num, den = x.as_integer_ratio()
+        # units of 2^-64 turns, with 64 bits behind the point
+        exact = (num * scale << 64 >> (bits - 64)) // den
+        off = ((lib.turns(x) << 64) - exact) % (1 << 128)
+        off = min(off, (1 << 128) - off) / 2.0 ** 64
+        assert off <= 0.5 + 2.0 ** -20, (x, off)
