@@ -145,6 +145,15 @@ int32_t query_type(PyObject* o) {
     return o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() != at::kFloat ? LOCKS_BF16
                                                                                                     : LOCKS_FP32;
 }
+// The entry point's status. Other Python threads run meanwhile: a launch may wait for room in the
+// stream's queue, and what drains it (a host callback) may need the interpreter.
+template <typename F>
+int released(F entry) {
+    PyThreadState* const state = PyEval_SaveThread();
+    const int status = entry();
+    PyEval_RestoreThread(state);
+    return status;
+}
 // fp32, or the bf16 bits that int16 holds too.
 constexpr unsigned kQuery = kF32 | kBf16;
 
@@ -209,10 +218,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float* kw = c.get<float>(a[15], "k_weight", kF32, 128, true);
         size_t bytes;
         void* ws = c.workspace(a[17], &bytes);
+        const float eps = real(a[16]);
+        const int32_t in_type = kind == kF32 ? LOCKS_FP32 : kind == kF16 ? LOCKS_FP16 : LOCKS_BF16;
+        const int32_t q_type = query_type(a[10]);
+        void* stream = address<void>(a[1]);
         c.settle();
-        return g_append(d, rope, q, k, v, kind == kF32 ? LOCKS_FP32 : kind == kF16 ? LOCKS_FP16 : LOCKS_BF16, qs, ks, vs,
-                        static_cast<int32_t>(t), positions, seq, index, table, qw, kw, real(a[16]), q_out,
-                        query_type(a[10]), kc, vc, ws, bytes, address<void>(a[1]));
+        return released([&] {
+            return g_append(d, rope, q, k, v, in_type, qs, ks, vs, static_cast<int32_t>(t), positions, seq, index, table,
+                            qw, kw, eps, q_out, q_type, kc, vc, ws, bytes, stream);
+        });
     });
 }
 
@@ -249,9 +263,13 @@ PyObject* prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
         size_t bytes;
         void* ws = c.workspace(a[12], &bytes);
         float* lse = c.get<float>(a[13], "lse", kF32, b * d->num_q_heads, true);
+        const int32_t q_type = query_type(a[3]);
+        void* stream = address<void>(a[1]);
         c.settle();
-        return g_prefix(d, q, query_type(a[3]), kc, vc, table, tokens, start, static_cast<int32_t>(groups),
-                        static_cast<int32_t>(pages), own, seq, out, lse, ws, bytes, address<void>(a[1]));
+        return released([&] {
+            return g_prefix(d, q, q_type, kc, vc, table, tokens, start, static_cast<int32_t>(groups),
+                            static_cast<int32_t>(pages), own, seq, out, lse, ws, bytes, stream);
+        });
     });
 }
 
@@ -268,8 +286,10 @@ PyObject* mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
         size_t bytes;
         void* ws = c.workspace(a[7], &bytes);
         const float* partials = c.get<float>(a[9], "lse_partials", kF32, integer(a[10]), true);
+        const float decay = real(a[8]);
+        void* stream = address<void>(a[1]);
         c.settle();
-        return g_mass(d, scores, partials, seq, old, out, real(a[8]), ws, bytes, address<void>(a[1]));
+        return released([&] { return g_mass(d, scores, partials, seq, old, out, decay, ws, bytes, stream); });
     });
 }
 
@@ -296,10 +316,14 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* ne = c.get<int32_t>(a[11], "n_evicted", kI32, b);
         size_t bytes;
         void* ws = c.workspace(a[15], &bytes);
+        const int32_t keep = int32_of(a[6], "keep_pages"), sink = int32_of(a[12], "sink_pages");
+        const int32_t recent = int32_of(a[13], "recent_pages"), extra = int32_of(a[14], "extra_pages");
+        void* stream = address<void>(a[1]);
         c.settle();
-        return g_evict(d, m, table, seq, int32_of(a[6], "keep_pages"), int32_of(a[12], "sink_pages"),
-                       int32_of(a[13], "recent_pages"), int32_of(a[14], "extra_pages"), mo, to, so, ev,
-                       static_cast<int32_t>(cap), ne, ws, bytes, address<void>(a[1]));
+        return released([&] {
+            return g_evict(d, m, table, seq, keep, sink, recent, extra, mo, to, so, ev, static_cast<int32_t>(cap), ne, ws,
+                           bytes, stream);
+        });
     });
 }
 
