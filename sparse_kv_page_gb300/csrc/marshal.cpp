@@ -205,8 +205,17 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* v = c.rows(a[6], "v", type, t, d->num_kv_heads, &vs);
         const void* q = a[4] == Py_None ? nullptr : c.rows(a[4], "q", type, t, d->num_q_heads, &qs);
         const int64_t cache = static_cast<int64_t>(d->num_phys_pages) * d->num_kv_heads * 2048;
-        const int32_t* positions =
-            rope ? c.get<int32_t>(a[7], "positions", kI32, t * rope->num_axes, true) : nullptr;
+        const int32_t* positions = nullptr;
+        if (rope && a[7] != Py_None) {
+            const at::Tensor& p = tensor(a[7], "positions");
+            const bool rows = p.dim() == 2 && p.size(0) == rope->num_axes && p.size(1) == t;
+            if (!rows && !(p.dim() == 1 && rope->num_axes == 1 && p.size(0) == t)) {
+                PyErr_Format(PyExc_ValueError, "positions is not [%d][%lld]", static_cast<int>(rope->num_axes),
+                             static_cast<long long>(t));
+                throw Refused();
+            }
+            positions = c.get<int32_t>(a[7], "positions", kI32, t * rope->num_axes);
+        }
         const int32_t* index = c.get<int32_t>(a[8], "cache_index", kI32, t);
         const int32_t* table =
             c.get<int32_t>(a[9], "page_table", kI32, static_cast<int64_t>(d->batch) * d->max_pages_per_seq);
