@@ -15,6 +15,8 @@ struct Unit {
     int tokens, tiles, seq0, num_seqs;            // tiles per item
     bool bad;
 };
+// Lists may be as long as 2^31 - 16 tokens: no sum before the division.
+__device__ __forceinline__ int tiles_of(int tokens) { return tokens / kTile + (tokens % kTile != 0); }
 // The largest group bound ahead of this lane's, given the largest one before the warp's
 // (`bound`, at least 0), which moves on past the warp's own.
 __device__ __forceinline__ int bound_before(int mine, int& bound) {
@@ -39,7 +41,7 @@ __device__ __forceinline__ Unit group_unit(const PrefixArgs& a, int s, int e, in
     r.seq0 = span ? s : 0;
     r.num_seqs = span ? e - s : 0;
     r.tokens = span && len ? n : 0;
-    r.tiles = (r.tokens + kTile - 1) / kTile;
+    r.tiles = tiles_of(r.tokens);
     r.bad = !span || !len;
     return r;
 }
@@ -49,7 +51,7 @@ __device__ __forceinline__ Unit own_unit(const PrefixArgs& a, int b, int n) {
     r.seq0 = b;
     r.num_seqs = 1;
     r.tokens = len ? n : 0;
-    r.tiles = (r.tokens + kTile - 1) / kTile;
+    r.tiles = tiles_of(r.tokens);
     r.bad = !len;
     return r;
 }

@@ -2,6 +2,7 @@
 weighed while the softmax groups still join the sums of the one before, so each piece's
 maxima have to outlive the next one's. Tolerances are test_gpu_cache's; repeated calls
 have to agree to the bit."""
+import numpy as np
 import pytest
 import torch
 
@@ -74,3 +75,34 @@ def test_giving_up_leaves_nothing_in_flight(q_type, wait_limit):
             assert torch.equal(behind["out"], want[i]) and torch.equal(behind["lse"], want[i + 1])
     c["ws"][:256] = 0
     T.check_prefix(c)
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_longest_lists(own):
+    """2^31 - 16 tokens, seven pages over and over: the attention over those seven, whose sum is as
+    many times as large. Each CTA adds up to 2^24 / 152 tiles, eight products and two sums a
+    tile: that many last bits (2^-23) of sums of p |v| and of p."""
+    pages = (1 << 27) - 1                         # 7 * 19173961
+    tokens = 16 * pages
+    g = T.gen(5)
+    k = torch.randn((7, 1, 16, 128), generator=g, device=T.DEV).bfloat16()
+    v = torch.randn((7, 1, 16, 128), generator=g, device=T.DEV).bfloat16()
+    q = torch.randn((1, 2, 128), generator=g, device=T.DEV)
+    table = (torch.arange(pages, dtype=torch.int32, device=T.DEV) % 7).view(1, pages)
+    dims = T.L.make_dims(1, 2, 1, pages if own else 0, 7)
+    count = torch.tensor([tokens], dtype=torch.int32, device=T.DEV)
+    none = torch.zeros(1, dtype=torch.int32, device=T.DEV)
+    out, lse = torch.empty((1, 2, 128), device=T.DEV).bfloat16(), torch.empty((1, 2), device=T.DEV)
+    ws = T.L.alloc_prefix_workspace(dims, 1, T.DEV)
+    if own:
+        T.L.locks_prefix_attention(dims, q, k, v, None, None, None, table, count, out, ws, lse=lse)
+    else:
+        bounds = torch.tensor([0, 1], dtype=torch.int32, device=T.DEV)
+        T.L.locks_prefix_attention(dims, q, k, v, table, count, bounds, None, none, out, ws, lse=lse)
+    assert T.L.locks_get_device_status(ws) == 0
+    want, want_lse, w, size = T.ref.attend(T.f64(q[0]), T.f64(k).reshape(-1, 128), T.f64(v).reshape(-1, 128))
+    last_bits = 2.0 ** -23 * (2 ** 24 / 152 + 1)
+    e = 2.0 ** -15 * size
+    tol = (2 * e[:, None] + T.UB + 10 * last_bits) * w + T.UB * np.abs(want)
+    assert np.all(np.abs(T.f64(out)[0] - want) <= tol)
+    assert np.all(np.abs(T.f64(lse)[0] - np.log(pages // 7) - want_lse) <= e + 4 * last_bits)
