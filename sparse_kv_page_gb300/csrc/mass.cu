@@ -483,14 +483,15 @@ cudaError_t launch_evict_t(const EvictArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int mass_partials_row(int max_pages) { return (max_pages + kSlicePages - 1) / kSlicePages; }
+// No sum before the division: max_pages may be any int32.
+int mass_partials_row(int max_pages) { return max_pages / kSlicePages + (max_pages % kSlicePages != 0); }
 
 cudaError_t launch_mass_partials(const MassArgs& a, float2* partials, cudaStream_t stream) {
     return launch_pdl(partials_kernel, dim3(a.row, a.hq, a.batch), kThreads, 0, stream, a, partials, rows_aligned(a));
 }
 
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream) {
-    const int blocks = (a.max_pages + kMassPages - 1) / kMassPages;
+    const int blocks = a.max_pages / kMassPages + (a.max_pages % kMassPages != 0);
     return launch_pdl(mass_kernel, dim3(blocks, a.batch, 1), kThreads, 0, stream, a, rows_aligned(a));
 }
 
