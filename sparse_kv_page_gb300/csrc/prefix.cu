@@ -120,7 +120,7 @@ constexpr uint32_t kLowWeights = kGroupTokens / 2;   // a group's weights: high 
 __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status,
                                        uint64_t limit_ns) {
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
+    for (;;) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -130,13 +130,11 @@ __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile i
             : "r"(bar), "r"(parity)
             : "memory");
         if (ok) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (global_timer_ns() - t0 > limit_ns) {
-                *abort = 1;
-                if (status) atomicCAS(status, 0, LOCKS_ERR_TIMEOUT);
-                return false;
-            }
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            if (status) atomicCAS(status, 0, LOCKS_ERR_TIMEOUT);
+            return false;
         }
     }
 }

@@ -106,3 +106,18 @@ def test_longest_lists(own):
     tol = (2 * e[:, None] + T.UB + 10 * last_bits) * w + T.UB * np.abs(want)
     assert np.all(np.abs(T.f64(out)[0] - want) <= tol)
     assert np.all(np.abs(T.f64(lse)[0] - np.log(pages // 7) - want_lse) <= e + 4 * last_bits)
+
+
+def test_a_limit_that_every_load_passes_runs_out(wait_limit):
+    """A nanosecond: some wait of ten calls finds its load on the way and gives up."""
+    c = wide(T.prefix_case([(40, 3000), (3, 20000)], [7] * 50, 32, 8, seed=172))
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=T.DEV)
+    c["ws"][:256] = 0
+    for _ in range(10):
+        flush.fill_(1)
+        wait_limit(1)
+        T.run_prefix(c)
+        wait_limit(0)
+    assert T.L.locks_get_device_status(c["ws"]) == TIMEOUT
+    c["ws"][:256] = 0
+    T.check_prefix(c)
