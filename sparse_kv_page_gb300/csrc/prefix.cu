@@ -305,6 +305,12 @@ __device__ __forceinline__ uint32_t v_entry(uint32_t t) { return 2 * t + 2; }
 
 // The loads of K (kValues false) or of V, a warp each: a box takes about 75 cycles to issue,
 // so one warp for the 32 boxes of a tile would bound the supply.
+// With an odd ring the two take turns in a slot, and a wait for one use's end by its parity would
+// take the end of the use two before for it; so that one has to be seen before. Entry e's loader
+// last waited for entry e - 7. Where e is K of tile t, that is V of tile t - 5, whose products
+// followed that tile's scores, and e - 10, its K, was handed back ahead of the scores. Where e
+// is V of tile t, it is K of tile t - 2, whose scores followed the products of tile t - 4,
+// issued after e - 10, V of tile t - 5, had been handed back.
 template <bool kSplitQ, bool kValues>
 __device__ __forceinline__ void run_loads(const PrefixArgs& a, uint8_t* ring, Control* ctl) {
     constexpr uint32_t kN = kSlots<kSplitQ>;
@@ -489,8 +495,8 @@ __device__ __forceinline__ void run_scores(const PrefixArgs& a, uint32_t q_addr,
                         mma_ss(tmem + score_col(b), q_desc + (part * (kTileBytes >> 4) + off), k_desc + off, idesc,
                                part + k > 0);
                     }
+                mma_commit(&ctl->empty[slot]);          // first: see run_loads
                 mma_commit(&ctl->scores[b]);
-                mma_commit(&ctl->empty[slot]);
                 if (i == p.tiles - 1) mma_commit(&ctl->q_free[p.n % kQueryUnits]);
             }
         }
