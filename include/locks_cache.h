@@ -41,7 +41,7 @@ typedef struct {
     int32_t interleaved;   /* 0 or 1 */
     int32_t num_axes;      /* rows of positions, 1..LOCKS_MAX_AXES */
     float scale;           /* multiplies cos and sin (1: a plain rotation) */
-    double inv_freq[64];   /* radians per position; finite */
+    double inv_freq[64];   /* radians per position, from -4096 to 4096 */
     int32_t axis[64];      /* 0 <= axis[i] < num_axes */
 } locks_rope_t;
 
@@ -149,7 +149,8 @@ LOCKS_API int locks_mass_workspace_size(const locks_dims_t* dims, size_t* bytes)
  *   buffer as it was is not read. (The scorer leaves a +inf score out of its sums
  *   together with the eight pages 8i .. 8i + 7 it lies among, so L_bh lacks those.)
  * - seq_pages[b] out of [0, max_pages_per_seq] records LOCKS_ERR_BAD_INDEX and
- *   the sequence is skipped. Two kernel launches.
+ *   the sequence is skipped. batch at most 65535, else LOCKS_ERR_UNSUPPORTED. Two
+ *   kernel launches.
  */
 LOCKS_API int locks_accumulate_mass(const locks_dims_t* dims, const float* scores, const float* lse_partials,
                                     const int32_t* seq_pages, const float* mass, float* mass_out, float decay,

@@ -9,10 +9,14 @@ step::
     # the step's tokens: head norms, rotation, K/V into the cache, q in fp32
     locks_append_tokens(dims, rope, q_proj, k_proj, v_proj, positions, cache_index,
                         page_table, q, k_cache, v_cache)
-    locks_decode_step(dims, q, ..., scores=scores)      # or locks_prefix_attention
+    locks_decode_step(dims, q, ..., scores=scores)
     locks_accumulate_mass(dims, scores, seq_pages, mass, mass, mass_ws, decay=0.98)
     locks_evict_pages(dims, mass, page_table, seq_pages, keep_pages, mass, page_table,
                       seq_pages, evicted, n_evicted, sink_pages=1, recent_pages=4)
+
+``locks_prefix_attention`` attends in the step's place where a batch shares prompts. It goes
+over every token and writes no page scores: mass then needs ``locks_score_pages`` or
+``locks_exact_scores`` beside it.
 
 Every tensor of a call must be on one CUDA device; where that is not the current
 one, the call is made on it.

