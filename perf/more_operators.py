@@ -9,8 +9,8 @@ bits) or, where ``own`` is true, through this repository's library. Head dim 128
 context lengths run from a few tokens to the 1M tokens of the longest one.
 
 A packed unit, one page of one kv head, is 2432 bytes: the 4-bit codes of its keys and
-values in the order of the tensor cores' fragments, then bf16 (scale, zero) pairs, one to
-32 dims of a key and one to 64 dims of a value: value = zero + scale * code.
+values in the order of the tensor cores' fragments, then for every token bf16 scales and
+zeros, one of each to 32 dims of a key and to 64 dims of a value: value = zero + scale * code.
 """
 
 import math
@@ -148,7 +148,10 @@ def _packed_pool(units, g, dev):
         pool[u:u + n, :2048] = table[pick]
         scale = 0.29 * torch.exp(0.2 * torch.randn((n, 96), generator=g, device=dev))
         zero = -7.5 * scale + 0.1 * torch.randn((n, 96), generator=g, device=dev)
-        pool[u:u + n, 2048:] = torch.stack((scale, zero), -1).to(torch.bfloat16).view(n, 192).view(torch.uint8)
+        # a token's scales, then its zeros: four of either for its key, two for its value
+        both = [torch.stack([x[:, a:b].view(n, PAGE, -1) for x in (scale, zero)], 2)
+                for a, b in ((0, 64), (64, 96))]
+        pool[u:u + n, 2048:] = torch.cat([x.flatten(1) for x in both], 1).to(torch.bfloat16).view(torch.uint8)
     return pool
 
 
@@ -338,8 +341,8 @@ def _unpacked(units):
 
     def pairs(lo, groups):
         x = units[..., lo:lo + 64 * groups].contiguous().view(torch.bfloat16).float()
-        x = x.view(*lead, PAGE, groups, 1, 2)
-        return x[..., 0], x[..., 1]
+        x = x.view(*lead, PAGE, 2, groups, 1)
+        return x[..., 0, :, :], x[..., 1, :, :]
 
     def order(x, axes):
         return x.permute(*range(n), *(n + a for a in axes)).reshape(*lead, PAGE, D).float()
@@ -594,8 +597,8 @@ def _exact_attend(case, s):
     def of(units, byte, shift, lo, group):
         code = (units[:, byte.flatten()].int() >> shift.flatten()) & 15
         pair = units[:, lo:lo + 64 * (D // group)].contiguous().view(torch.bfloat16).double()
-        pair = pair.view(-1, PAGE, D // group, 2).repeat_interleave(group, 2)
-        return (pair[..., 1] + pair[..., 0] * code.view(-1, PAGE, D).double()).view(-1, D)
+        pair = pair.view(-1, PAGE, 2, D // group).repeat_interleave(group, 3)
+        return (pair[:, :, 1] + pair[:, :, 0] * code.view(-1, PAGE, D).double()).view(-1, D)
 
     pages, recent = _lengths(case)
     for b in range(B):
