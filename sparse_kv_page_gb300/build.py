@@ -1,8 +1,8 @@
 """Builds the in-tree CUDA library ``liblocks_gb300.so`` (sm_103a only).
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
-linked into one shared library exporting the C ABI of ``include/locks.h`` and
-``include/locks_cache.h``. ``csrc/marshal.cpp`` becomes the extension module ``_marshal``,
+linked into one shared library exporting the C ABI of ``include/locks.h``,
+``include/locks_cache.h`` and ``include/locks_pool.h``. ``csrc/marshal.cpp`` becomes the extension module ``_marshal``,
 the argument checks of the cache operators' Python binding (g++, torch's headers).
 Run as ``python -m sparse_kv_page_gb300.build`` or through
 ``__graft_entry__.build()``.

@@ -306,6 +306,7 @@ const char* locks_status_string(int status) {
         case LOCKS_ERR_CUDA: return "CUDA launch or runtime error";
         case LOCKS_ERR_TIMEOUT: return "device wait timed out";
         case LOCKS_ERR_BAD_INDEX: return "page index out of range on the device";
+        case LOCKS_ERR_NO_PAGES: return "too few free pages in the pool";
         default: return "unknown status";
     }
 }

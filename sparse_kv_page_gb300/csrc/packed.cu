@@ -1,0 +1,247 @@
+// packed.cu - pages of the bf16 pool to 4 bits and back (locks_pack_pages, locks_unpack_pages).
+//
+// A warp takes a unit (a page of one kv head): 8 KB of bf16 on one side, 2432 bytes on the
+// other, so HBM bounds both. The bf16 side is read and written 16 bytes a lane, two tokens to
+// an instruction; the codes go through a staging area in shared memory, because the order of
+// the attention's fragments spreads a lane's eight dims over four or eight words.
+#include <algorithm>
+
+#include "pool_internal.h"
+
+namespace locks {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {      // NaN if either is
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// Scale and zero (bf16 bits) of a group that kLanes neighbouring lanes hold, eight values each.
+template <int kLanes>
+__device__ __forceinline__ void group_scale(const uint4& x, uint32_t& scale, uint32_t& zero) {
+    uint32_t lo = bf16x2_min(bf16x2_min(x.x, x.y), bf16x2_min(x.z, x.w));
+    uint32_t hi = bf16x2_max(bf16x2_max(x.x, x.y), bf16x2_max(x.z, x.w));
+#pragma unroll
+    for (int o = 1; o < kLanes; o *= 2) {
+        lo = bf16x2_min(lo, __shfl_xor_sync(kAll, lo, o));
+        hi = bf16x2_max(hi, __shfl_xor_sync(kAll, hi, o));
+    }
+    lo = bf16x2_min(lo, lo >> 16 | lo << 16);
+    hi = bf16x2_max(hi, hi >> 16 | hi << 16);
+    scale = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(low_of(hi), low_of(lo)), 15.f)));
+    if (scale < 0x0080u) scale = 0;               // below 2^-126
+    zero = lo & 0xffffu;
+}
+
+// The eight codes of a lane's values, code i in the low 4 bits of c[i]. (x - zero) / scale is rounded as the fp32 quotient is. It is
+// formed with the reciprocal, off by less than 2^-18 (15 times 2^-24 for the reciprocal and
+// 2^-24 for the product); within that of a border between two codes the division decides
+// (bf16 values fall on borders often enough to matter: borders are 12-bit numbers themselves).
+// The quotient is within [0, 15.06], as the scale is rounded by at most 2^-9 of itself.
+constexpr float kRound = 12582912.f;              // 1.5 * 2^23: the sum's low bits are the rounded value
+__device__ __noinline__ uint32_t divided_code(float v, float s) {
+    return __float_as_uint(__fadd_rn(s == 0.f ? 0.f : __fdiv_rn(v, s), kRound));
+}
+__device__ __forceinline__ void codes_of(const uint4& x, uint32_t scale, uint32_t zero, uint32_t (&c)[8]) {
+    const float s = low_of(scale), z = low_of(zero), r = s == 0.f ? 0.f : __frcp_rn(s);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = __fmul_rn(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), r);
+        const float y = __fadd_rn(t, kRound);
+        far = fmaxf(far, fabsf(t - (y - kRound)));
+        c[i] = __float_as_uint(y);
+    }
+    if (far > 0.5f - 0x1p-17f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c[i] = divided_code(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), s);
+    }
+}
+
+// A unit's entries of the lists, or -1 where there is nothing to do.
+__device__ __forceinline__ bool find_pages(const PackArgs& a, int i, int& from, int& to) {
+    from = __ldg(a.src + i);
+    to = a.dst ? __ldg(a.dst + i) : from;
+    if (from < 0 || to < 0) return false;
+    if (from < a.num_src && to < a.num_dst) return true;
+    report_error(a.st, LOCKS_ERR_BAD_INDEX);
+    return false;
+}
+
+__global__ void __launch_bounds__(kWarps * 32) pack_kernel(const __grid_constant__ PackArgs a) {
+    __shared__ __align__(16) uint8_t stage[kWarps][kUnitBytes];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint8_t* const unit = stage[warp];
+    const int row = lane >> 4, chunk = lane & 15;             // of two tokens, 8 dims a lane
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t units = static_cast<int64_t>(a.n) * a.hkv;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+         u += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int i = static_cast<int>(u / a.hkv), h = static_cast<int>(u % a.hkv);
+        int from, to;
+        if (!find_pages(a, i, from, to)) continue;
+        const int64_t at = (static_cast<int64_t>(from) * a.hkv + h) * (kPage * kD) + lane * 8;
+        uint4 k[8], v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {                         // tokens 2j, 2j + 1
+            k[j] = __ldcs(reinterpret_cast<const uint4*>(a.k_in + at + j * 2 * kD));
+            v[j] = __ldcs(reinterpret_cast<const uint4*>(a.v_in + at + j * 2 * kD));
+        }
+        const int half = chunk & 1, w = chunk >> 1;
+        const int word = 512 * (w >> 2) + 4 * (w & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                         // tokens t and t + 8
+            const int t = 2 * j + row;
+            {
+                uint32_t c0[8], c1[8], s0, z0, s1, z1, full[4];
+                group_scale<4>(k[j], s0, z0);
+                group_scale<4>(k[j + 4], s1, z1);
+                codes_of(k[j], s0, z0, c0);
+                codes_of(k[j + 4], s1, z1, c1);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {                 // pair of dims: this half's bits of its word
+                    const uint32_t mine = (c0[2 * p] & 15) | (c0[2 * p + 1] & 15) << 16 | (c1[2 * p] & 15) << 8 |
+                                          (c1[2 * p + 1] & 15) << 24;
+                    full[p] = mine << (4 * half);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {                 // the even half keeps words 0, 1
+                    const uint32_t give = half ? full[p] : full[p + 2], keep = half ? full[p + 2] : full[p];
+                    const uint32_t all = keep | __shfl_xor_sync(kAll, give, 1);
+                    *reinterpret_cast<uint32_t*>(unit + word + 16 * (4 * t + 2 * half + p)) = all;
+                }
+                if ((chunk & 3) == 0) {
+                    uint16_t* sz = reinterpret_cast<uint16_t*>(unit + kUnitKScales + 16 * t) + (chunk >> 2);
+                    sz[0] = static_cast<uint16_t>(s0), sz[4] = static_cast<uint16_t>(z0);
+                    sz[64] = static_cast<uint16_t>(s1), sz[68] = static_cast<uint16_t>(z1);
+                }
+            }
+            {
+                uint32_t c0[8], c1[8], s0, z0, s1, z1, part[8];
+                group_scale<8>(v[j], s0, z0);
+                group_scale<8>(v[j + 4], s1, z1);
+                codes_of(v[j], s0, z0, c0);
+                codes_of(v[j + 4], s1, z1, c1);
+#pragma unroll
+                for (int d = 0; d < 8; ++d)                   // of tokens t, t + 8: a word a dim
+                    part[d] = ((c0[d] & 15) | (c1[d] & 15) << 8) << (16 * row + 4 * half);
+                uint32_t four[4];                             // dims 4 * half .. of both halves
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const uint32_t give = half ? part[d] : part[d + 4], keep = half ? part[d + 4] : part[d];
+                    four[d] = keep | __shfl_xor_sync(kAll, give, 1);
+                }
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {                 // ... and 2 * row .. of both tokens
+                    const uint32_t give = row ? four[d] : four[d + 2], keep = row ? four[d + 2] : four[d];
+                    const uint32_t all = keep | __shfl_xor_sync(kAll, give, 16);
+                    *reinterpret_cast<uint32_t*>(unit + kUnitVCodes + word +
+                                                 16 * (4 * (4 * half + 2 * row + d) + j)) = all;
+                }
+                if ((chunk & 7) == 0) {
+                    uint16_t* sz = reinterpret_cast<uint16_t*>(unit + kUnitVScales + 8 * t) + (chunk >> 3);
+                    sz[0] = static_cast<uint16_t>(s0), sz[2] = static_cast<uint16_t>(z0);
+                    sz[32] = static_cast<uint16_t>(s1), sz[34] = static_cast<uint16_t>(z1);
+                }
+            }
+        }
+        __syncwarp();
+        uint4* out = reinterpret_cast<uint4*>(a.packed + (static_cast<int64_t>(to) * a.hkv + h) * kUnitBytes);
+        for (int x = lane; x < kUnitBytes / 16; x += 32) out[x] = reinterpret_cast<const uint4*>(unit)[x];
+        __syncwarp();
+    }
+}
+
+// Two values of neighbouring dims as bf16: zero + scale * code, rounded once (the product of 8
+// and 4 bits is exact).
+__device__ __forceinline__ uint32_t pair_of(uint32_t c0, uint32_t c1, float s, float z) {
+    return pack_bf16x2(__fmaf_rn(s, static_cast<float>(c0), z), __fmaf_rn(s, static_cast<float>(c1), z));
+}
+
+__global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_constant__ PackArgs a) {
+    __shared__ __align__(16) uint8_t stage[kWarps][kUnitBytes];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint8_t* const unit = stage[warp];
+    const int row = lane >> 4, chunk = lane & 15;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t units = static_cast<int64_t>(a.n) * a.hkv;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+         u += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int i = static_cast<int>(u / a.hkv), h = static_cast<int>(u % a.hkv);
+        int from, to;
+        if (!find_pages(a, i, from, to)) continue;
+        const uint4* in = reinterpret_cast<const uint4*>(a.packed + (static_cast<int64_t>(from) * a.hkv + h) * kUnitBytes);
+        __syncwarp();
+        uint4 x[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            if (j < 4 || lane < kUnitBytes / 16 - 128) x[j] = __ldcs(in + j * 32 + lane);
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            if (j < 4 || lane < kUnitBytes / 16 - 128) reinterpret_cast<uint4*>(unit)[j * 32 + lane] = x[j];
+        __syncwarp();
+        const int half = chunk & 1, w = chunk >> 1;
+        const uint8_t* word = unit + 512 * (w >> 2) + 4 * (w & 3);
+        const int64_t at = (static_cast<int64_t>(to) * a.hkv + h) * (kPage * kD) + lane * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int t = 2 * j + row;
+            {
+                const uint16_t* sz = reinterpret_cast<const uint16_t*>(unit + kUnitKScales + 16 * t) + (chunk >> 2);
+                const float s = low_of(sz[0]), z = low_of(sz[4]);
+                uint32_t o[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const uint32_t c = *reinterpret_cast<const uint32_t*>(word + 16 * (4 * (t & 7) + p)) >>
+                                       (4 * half + 8 * (t >> 3));
+                    o[p] = pair_of(c & 15, c >> 16 & 15, s, z);
+                }
+                *reinterpret_cast<uint4*>(a.k_out + at + j * 2 * kD) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            {
+                const uint16_t* sz = reinterpret_cast<const uint16_t*>(unit + kUnitVScales + 8 * t) + (chunk >> 3);
+                const float s = low_of(sz[0]), z = low_of(sz[2]);
+                uint32_t c[8], o[4];
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    c[d] = *reinterpret_cast<const uint32_t*>(word + kUnitVCodes + 16 * (4 * d + (t & 7) / 2)) >>
+                               (16 * (t & 1) + 4 * half + 8 * (t >> 3)) &
+                           15;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) o[p] = pair_of(c[2 * p], c[2 * p + 1], s, z);
+                *reinterpret_cast<uint4*>(a.v_out + at + j * 2 * kD) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+}
+
+int grid_of(const PackArgs& a, int num_sms) {
+    const int64_t ctas = (static_cast<int64_t>(a.n) * a.hkv + kWarps - 1) / kWarps;
+    return static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(num_sms) * 8));
+}
+
+}  // namespace
+
+cudaError_t launch_pack(const PackArgs& a, int num_sms, cudaStream_t stream) {
+    return launch_dependent(pack_kernel, grid_of(a, num_sms), kWarps * 32, 0, stream, 1, a);
+}
+cudaError_t launch_unpack(const PackArgs& a, int num_sms, cudaStream_t stream) {
+    return launch_dependent(unpack_kernel, grid_of(a, num_sms), kWarps * 32, 0, stream, 1, a);
+}
+
+}  // namespace locks

@@ -41,10 +41,11 @@ RANK = 8
 _STATUS = {
     0: "LOCKS_OK", -1: "LOCKS_ERR_INVALID_ARG", -2: "LOCKS_ERR_UNSUPPORTED",
     -3: "LOCKS_ERR_WORKSPACE_TOO_SMALL", -4: "LOCKS_ERR_CUDA", -5: "LOCKS_ERR_TIMEOUT",
-    -6: "LOCKS_ERR_BAD_INDEX",
+    -6: "LOCKS_ERR_BAD_INDEX", -7: "LOCKS_ERR_NO_PAGES",
 }
 LOCKS_OK, LOCKS_ERR_INVALID_ARG, LOCKS_ERR_UNSUPPORTED = 0, -1, -2
 LOCKS_ERR_WORKSPACE_TOO_SMALL, LOCKS_ERR_CUDA, LOCKS_ERR_TIMEOUT, LOCKS_ERR_BAD_INDEX = -3, -4, -5, -6
+LOCKS_ERR_NO_PAGES = -7
 
 
 class LocksError(RuntimeError):
