@@ -106,7 +106,7 @@ LOCKS_API int locks_packed_workspace_size(const locks_dims_t* dims, size_t* byte
  *   is not read then and may be NULL. k_cap at least 1.
  * - recent_table int32 [batch][max_recent_pages], ids of bf16 pages, recent_tokens int32 [batch]
  *   in [0, 16 * max_recent_pages]; both not read, nor k_cache and v_cache, when
- *   max_recent_pages is 0.
+ *   max_recent_pages is 0 (num_phys_pages may then be 0 too).
  * - All counts, tables and lists are read on the device, so a captured graph may be replayed
  *   after they change. A count out of range counts as 0, a page id out of range is read as
  *   page 0; each records LOCKS_ERR_BAD_INDEX.

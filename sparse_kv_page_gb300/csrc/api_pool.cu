@@ -47,6 +47,16 @@ bool words(std::initializer_list<const void*> all) {
     return true;
 }
 
+// dims of the packed attention: num_phys_pages, the bf16 pool's, may be 0 where no recent tokens
+// are given.
+int check_packed(const locks_dims_t* d) {
+    if (!d) return LOCKS_ERR_INVALID_ARG;
+    locks_dims_t x = *d;
+    if (x.num_phys_pages == 0) x.num_phys_pages = 1;
+    const int s = locks::check_dims(&x);
+    return s == LOCKS_OK && x.batch > kMaxBatch ? LOCKS_ERR_UNSUPPORTED : s;
+}
+
 // What the calls that change tables have in common. Counts of tokens are int32, and a block
 // takes 1024 entries of a row.
 int check_table(const locks_dims_t* d) {
@@ -121,9 +131,8 @@ int locks_unpack_pages(const locks_dims_t* dims, const uint8_t* packed, int32_t 
 
 int locks_packed_workspace_size(const locks_dims_t* dims, size_t* bytes) {
     if (!bytes) return LOCKS_ERR_INVALID_ARG;
-    const int s = locks::check_dims(dims);
+    const int s = check_packed(dims);
     if (s != LOCKS_OK) return s;
-    if (dims->batch > kMaxBatch) return LOCKS_ERR_UNSUPPORTED;
     *bytes = locks::packed_layout(dims->num_q_heads / dims->num_kv_heads).bytes;
     return LOCKS_OK;
 }
@@ -134,13 +143,12 @@ int locks_packed_attention(const locks_dims_t* dims, const void* q, int32_t q_ty
                            const uint16_t* v_cache, const int32_t* recent_table, int32_t max_recent_pages,
                            const int32_t* recent_tokens, uint16_t* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream) {
-    int s = locks::check_dims(dims);
+    int s = check_packed(dims);
     if (s != LOCKS_OK) return s;
     if (q_type != LOCKS_FP32 && q_type != LOCKS_BF16) return LOCKS_ERR_INVALID_ARG;
     if (num_packed_pages < 0 || max_recent_pages < 0 || (selected && k_cap < 1)) return LOCKS_ERR_INVALID_ARG;
     // steps of a row are int32
-    if (dims->batch > kMaxBatch || max_recent_pages > INT_MAX / LOCKS_PAGE_SIZE / 2 ||
-        dims->max_pages_per_seq > INT_MAX / 4 || (selected && k_cap > INT_MAX / 4))
+    if (max_recent_pages > INT_MAX / LOCKS_PAGE_SIZE / 2 || dims->max_pages_per_seq > INT_MAX / 4 || (selected && k_cap > INT_MAX / 4))
         return LOCKS_ERR_UNSUPPORTED;
     const locks::PackedLayout w = locks::packed_layout(dims->num_q_heads / dims->num_kv_heads);
     if ((s = locks::check_workspace(workspace, workspace_bytes, w.bytes)) != LOCKS_OK) return s;

@@ -44,30 +44,31 @@ __device__ __forceinline__ void group_scale(const uint4& x, uint32_t& scale, uin
     zero = lo & 0xffffu;
 }
 
-// The eight codes of a lane's values, code i in the low 4 bits of c[i]. (x - zero) / scale is rounded as the fp32 quotient is. It is
-// formed with the reciprocal, off by less than 2^-18 (15 times 2^-24 for the reciprocal and
-// 2^-24 for the product); within that of a border between two codes the division decides
-// (bf16 values fall on borders often enough to matter: borders are 12-bit numbers themselves).
-// The quotient is within [0, 15.06], as the scale is rounded by at most 2^-9 of itself.
-constexpr float kRound = 12582912.f;              // 1.5 * 2^23: the sum's low bits are the rounded value
-__device__ __noinline__ uint32_t divided_code(float v, float s) {
-    return __float_as_uint(__fadd_rn(s == 0.f ? 0.f : __fdiv_rn(v, s), kRound));
-}
+// The eight codes of a lane's values as floats kRound + code, whose low bits are the code. The
+// quotient (x - zero) / scale is rounded as fp32 division rounds it, by Markstein's theorem (IBM J.
+// Res. Dev. 34, 1990): with the correctly rounded reciprocal r, q = v r and q + (v - s q) r is the
+// rounded v / s. It matters: bf16 values lie on borders between two codes often, and there the
+// product with the reciprocal alone may fall to either side. Scales so small or large that the
+// remainder or the reciprocal leave the normal numbers divide. The quotient is within [0, 15.06], as the
+// scale is rounded by at most 2^-8 of itself, so codes need no bounds.
+constexpr float kRound = 12582912.f;              // 1.5 * 2^23
+constexpr uint32_t kRoundBits = 0x4b400000u;
+__device__ __noinline__ float divided(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
 __device__ __forceinline__ void codes_of(const uint4& x, uint32_t scale, uint32_t zero, uint32_t (&c)[8]) {
-    const float s = low_of(scale), z = low_of(zero), r = s == 0.f ? 0.f : __frcp_rn(s);
+    const float s = low_of(scale), z = low_of(zero), r = __frcp_rn(s);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float far = 0.f;
+    if (s > 0x1p-90f && s < 0x1p120f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = __fmul_rn(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), r);
-        const float y = __fadd_rn(t, kRound);
-        far = fmaxf(far, fabsf(t - (y - kRound)));
-        c[i] = __float_as_uint(y);
-    }
-    if (far > 0.5f - 0x1p-17f) {
+        for (int i = 0; i < 8; ++i) {
+            const float v = __fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z);
+            const float q = __fmul_rn(v, r);
+            c[i] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-s, q, v), r, q), kRound));
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            c[i] = divided_code(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), s);
+            c[i] = __float_as_uint(
+                __fadd_rn(divided(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), s), kRound));
     }
 }
 
@@ -114,9 +115,8 @@ __global__ void __launch_bounds__(kWarps * 32) pack_kernel(const __grid_constant
                 codes_of(k[j + 4], s1, z1, c1);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {                 // pair of dims: this half's bits of its word
-                    const uint32_t mine = (c0[2 * p] & 15) | (c0[2 * p + 1] & 15) << 16 | (c1[2 * p] & 15) << 8 |
-                                          (c1[2 * p + 1] & 15) << 24;
-                    full[p] = mine << (4 * half);
+                    const uint32_t mine = c0[2 * p] + (c0[2 * p + 1] << 16) + (c1[2 * p] << 8) + (c1[2 * p + 1] << 24);
+                    full[p] = (mine - (kRoundBits + (kRoundBits << 8))) << (4 * half);
                 }
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {                 // the even half keeps words 0, 1
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kWarps * 32) pack_kernel(const __grid_constant
                 codes_of(v[j + 4], s1, z1, c1);
 #pragma unroll
                 for (int d = 0; d < 8; ++d)                   // of tokens t, t + 8: a word a dim
-                    part[d] = ((c0[d] & 15) | (c1[d] & 15) << 8) << (16 * row + 4 * half);
+                    part[d] = (c0[d] + (c1[d] << 8) - (kRoundBits + (kRoundBits << 8))) << (16 * row + 4 * half);
                 uint32_t four[4];                             // dims 4 * half .. of both halves
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {

@@ -1,10 +1,15 @@
 // packed_attend.cu - decode attention over packed pages (locks_packed_attention).
 //
-// All steps of the call, a page of a kv head each (a recent bf16 page counts kRecentSteps),
-// lie on one line, row after row (a row is a sequence and a kv head). The line is cut evenly
-// into CTAs and a CTA's part into warps, whatever the lengths of the rows, and a warp goes
-// through its pages with an online softmax. A row that ends up in several warps is joined in
-// shared memory at the CTA's end, one that goes past the CTA by a second kernel.
+// A CTA takes a part of a row (a sequence and a kv head), its warps every kWarps-th page of it
+// each, two pages at a time with an online softmax; the warps' partials meet in shared memory.
+// Two forms cut the rows into parts:
+//
+// 1. Short rows: a cluster of 1 to 8 CTAs a row, joined through distributed shared memory, in one
+//    launch. Latency bounds it.
+// 2. Long rows: all steps of the call, a page of a kv head each (a recent bf16 page counts
+//    kRecentSteps), lie on one line, row after row, that is cut evenly into as many CTAs as there
+//    are SMs, whatever the lengths of the rows. A row that goes past a CTA is joined by a second
+//    kernel from partials in the workspace.
 //
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
 // O^T = V^T P^T: few queries read a page, so HBM bounds the call as long as a page costs a warp
@@ -33,43 +38,34 @@ constexpr float kQueryShift = 0x1p100f, kRecentScore = 0x1p-73f;
 // Weights carry 2^40, so that their products with codes stay normal numbers.
 constexpr float kWeightBits = 40.f;
 constexpr float kSumUnit = 0x1p-40f, kOutUnit = 0x1p93f, kRecentWeight = 0x1p-133f;
+constexpr float kCodeUnit = 0x1p-133f, kMiddle = 7.5f;
+constexpr int kCentre = 8;                            // pairs of pages, a power of two
 constexpr float kSlack = 8.f;                         // log2 that a score may pass the maximum by
 
 // Variants: queries of a group in one block of 8 columns together with their low parts (kPair,
-// groups up to 4), in one block, or in two.
+// groups up to 4), in one block, or in two. 16 warps of 128 registers, or 12 of 168 for the
+// accumulators of two blocks; kDepth pages of each warp are in shared memory or on their way.
 template <int kKind>
-struct Shape;
-template <>
-struct Shape<0> {
-    static constexpr bool kPair = true;
-    static constexpr int kBlocks = 1, kWarps = 8, kCtas = 2, kDepth = 4, kRows = 4;
+struct Shape {
+    static constexpr bool kPair = kKind == 0;
+    static constexpr int kBlocks = kKind == 2 ? 2 : 1, kRows = kPair ? 4 : 8 * kBlocks;
+    static constexpr int kWarps = kKind == 2 ? 12 : 16, kDepth = kKind == 2 ? 6 : 5;
+    static constexpr int kThreads = kWarps * 32;
 };
-template <>
-struct Shape<1> {
-    static constexpr bool kPair = false;
-    static constexpr int kBlocks = 1, kWarps = 12, kCtas = 1, kDepth = 5, kRows = 8;
-};
-template <>
-struct Shape<2> {
-    static constexpr bool kPair = false;
-    static constexpr int kBlocks = 2, kWarps = 8, kCtas = 1, kDepth = 7, kRows = 16;
-};
-
+constexpr int kMaxCluster = 8;
 constexpr int kPartStride = kD + 4;                   // floats: columns' stores in different banks
-template <int kRows>
-constexpr int kPartBytes = kRows * kPartStride * 4;
 
-// Shared memory of a CTA besides the slots and the partials.
-template <int kWarps, int kRows>
+// Shared memory of a CTA besides the slots.
+template <int kKind>
 struct Control {
-    int64_t upto[kWarps * 32];                        // steps of the sequences up to each thread's last
-    int64_t warp_sum[kWarps];
-    struct Entry {
-        int64_t step0;                                // the row's first step on the line
-        int32_t row, len;                             // -1: unused; steps of the row
-        int32_t begins, ends;                         // the part holds the row's first / last step
-    } entry[kWarps * 2];                              // a warp's first row, and its last
-    float m[kWarps * 2][kRows], l[kWarps * 2][kRows];
+    using S = Shape<kKind>;
+    uint4 frag[S::kBlocks][8][32];                    // B fragments of the queries: high parts, low parts
+    uint2 sums[S::kBlocks][32];                       // ... of the groups' sums
+    float unit[S::kBlocks * 8];                       // a score's unit, by column
+    float m[S::kWarps][S::kRows], l[S::kWarps][S::kRows];
+    float cta_m[S::kRows], cta_l[S::kRows], cta_o[S::kRows][kD];
+    int64_t upto[S::kThreads];                        // steps of the sequences up to each thread's last
+    int64_t warp_sum[S::kWarps];
 };
 
 // 16 bytes, or zeros that read nothing.
@@ -88,6 +84,39 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// Two floats in one instruction.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void parts_of(Two x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// D = A B (no accumulator read).
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 struct Len {
     int pages, recent;                                // packed pages; recent tokens
@@ -101,9 +130,10 @@ __device__ __forceinline__ int checked(const PackedArgs& a, int n, int64_t most,
 }
 __device__ __forceinline__ Len row_len(const PackedArgs& a, int b, int h, bool report) {
     Len r;
-    r.pages = a.selected ? checked(a, __ldcg(a.n_selected + static_cast<int64_t>(b) * a.hkv + h), a.k_cap, report)
-                         : checked(a, __ldcg(a.seq_pages + b), a.max_pages, report);
-    r.recent = a.max_recent > 0 ? checked(a, __ldcg(a.recent_tokens + b), static_cast<int64_t>(a.max_recent) * kPage, report) : 0;
+    const int pages = a.selected ? __ldcg(a.n_selected + static_cast<int64_t>(b) * a.hkv + h) : __ldcg(a.seq_pages + b);
+    const int recent = a.max_recent > 0 ? __ldcg(a.recent_tokens + b) : 0;
+    r.pages = checked(a, pages, a.selected ? a.k_cap : a.max_pages, report);
+    r.recent = checked(a, recent, static_cast<int64_t>(a.max_recent) * kPage, report);
     return r;
 }
 // Steps of all rows of sequence b.
@@ -134,159 +164,172 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
     return static_cast<int>(((step + 1) * n - 1) / total);
 }
 
-// The queries of a row as B fragments, in bf16 parts, and what they need beside them.
+// One block of a row's queries as B fragments, in bf16 parts, by one warp.
 template <int kKind, bool kSplit>
-struct Queries {
+__device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int block, Control<kKind>& ctl) {
     using S = Shape<kKind>;
-    static constexpr bool kLow = kSplit && !S::kPair;    // low parts as fragments of their own
-    uint32_t hi[S::kBlocks][8][2];
-    uint32_t lo[kLow ? S::kBlocks : 1][8][2];
-    uint32_t sums[S::kBlocks][2];                     // B fragment of the groups' sums, in three parts
-    float unit[S::kBlocks][2];                        // a score's unit, of the accumulators' columns
-
-    __device__ __forceinline__ void load(const PackedArgs& a, int b, int h) {
-        const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const int query = S::kPair ? gid & 3 : block * 8 + gid;
+    const bool on = query < a.group;
+    const int64_t at = (static_cast<int64_t>(b) * a.hq + h * a.group + (on ? query : 0)) * kD + 2 * tig;
+    float2 x[8][2];
+    float big = 0.f;
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n) {
-            const int query = S::kPair ? gid & 3 : n * 8 + gid;
-            const bool on = query < a.group;
-            const int64_t at = (static_cast<int64_t>(b) * a.hq + h * a.group + (on ? query : 0)) * kD + 2 * tig;
-            float2 x[8][2];
-            float big = 0.f;
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int64_t e = at + 16 * k + 8 * c;
-                    if (a.q_type == LOCKS_FP32) {
-                        x[k][c] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + e));
-                    } else {
-                        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + e));
-                        x[k][c] = make_float2(low_of(w), high_of(w));
-                    }
-                    if (!on) x[k][c] = make_float2(0.f, 0.f);
-                    big = fmaxf(big, fmaxf(fabsf(x[k][c].x), fabsf(x[k][c].y)));
-                }
-            big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
-            const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -20), 60);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kQueryShift;
-            float sum[4];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (k % 2 == 0) sum[k / 2] = 0.f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float div = c == 0 ? up : up * 0.0625f;        // fields 4 bits up count 16 times
-                    const float y0 = x[k][c].x * div, y1 = x[k][c].y * div;
-                    uint32_t w = pack_bf16x2(y0, y1);
-                    if (kSplit) {
-                        const uint32_t v = pack_bf16x2(y0 - low_of(w), y1 - high_of(w));
-                        if (S::kPair) w = gid < 4 ? w : v;
-                        if (kLow) lo[n][k][c] = v;
-                    }
-                    hi[n][k][c] = w;
-                    float part = low_of(w) + high_of(w);
-                    if (kLow) part += low_of(lo[n][k][c]) + high_of(lo[n][k][c]);
-                    sum[k / 2] += c == 0 ? part : part * 16.f;
-                }
+        for (int c = 0; c < 2; ++c) {
+            const int64_t e = at + 16 * k + 8 * c;
+            if (a.q_type == LOCKS_FP32) {
+                x[k][c] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + e));
+            } else {
+                const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + e));
+                x[k][c] = make_float2(low_of(w), high_of(w));
             }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                sum[g] += __shfl_xor_sync(kAll, sum[g], 1);
-                sum[g] += __shfl_xor_sync(kAll, sum[g], 2);
-                sum[g] *= 0x1p-66f;                       // by 2^-133, as the codes are
-                sum[g] *= 0x1p-67f;
-            }
-            // rows k = 0..3 of the fragment: the groups' sums to 8 bits; 4..7: the next 8; 8..11
-            float s0 = tig & 1 ? sum[2] : sum[0], s1 = tig & 1 ? sum[3] : sum[1];
-            const uint32_t w0 = pack_bf16x2(s0, s1);
-            s0 -= low_of(w0), s1 -= high_of(w0);
-            const uint32_t w1 = pack_bf16x2(s0, s1);
-            s0 -= low_of(w1), s1 -= high_of(w1);
-            const uint32_t w2 = pack_bf16x2(s0, s1);
-            sums[n][0] = tig < 2 ? w0 : w1;
-            sums[n][1] = tig < 2 ? w2 : 0u;
-            const float back = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (0x1p33f * kScaleLog2);
-            unit[n][0] = __shfl_sync(kAll, back, 8 * tig);
-            unit[n][1] = __shfl_sync(kAll, back, 8 * tig + 4);
+            if (!on) x[k][c] = make_float2(0.f, 0.f);
+            big = fmaxf(big, fmaxf(fabsf(x[k][c].x), fabsf(x[k][c].y)));
         }
+    big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
+    const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -20), 60);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kQueryShift;
+    float sum[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k % 2 == 0) sum[k / 2] = 0.f;
+        uint32_t hi[2], lo[2] = {0u, 0u};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float by = c == 0 ? up : up * 0.0625f;          // fields 4 bits up count 16 times
+            const float y0 = x[k][c].x * by, y1 = x[k][c].y * by;
+            hi[c] = pack_bf16x2(y0, y1);
+            if (kSplit) {
+                lo[c] = pack_bf16x2(y0 - low_of(hi[c]), y1 - high_of(hi[c]));
+                if (S::kPair) {                                   // columns 4..7 are the low parts
+                    if (gid >= 4) hi[c] = lo[c];
+                    lo[c] = 0u;
+                }
+            }
+            const float part = low_of(hi[c]) + high_of(hi[c]) + (low_of(lo[c]) + high_of(lo[c]));
+            sum[k / 2] += c == 0 ? part : part * 16.f;
+        }
+        ctl.frag[block][k][lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
     }
-};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        sum[g] += __shfl_xor_sync(kAll, sum[g], 1);
+        sum[g] += __shfl_xor_sync(kAll, sum[g], 2);
+        sum[g] *= 0x1p-66f;                           // by 2^-133, as the codes are
+        sum[g] *= 0x1p-67f;
+    }
+    // rows k = 0..3 of the fragment: the groups' sums to 8 bits; 4..7: the next 8; 8..11
+    float s0 = tig & 1 ? sum[2] : sum[0], s1 = tig & 1 ? sum[3] : sum[1];
+    const uint32_t w0 = pack_bf16x2(s0, s1);
+    s0 -= low_of(w0), s1 -= high_of(w0);
+    const uint32_t w1 = pack_bf16x2(s0, s1);
+    s0 -= low_of(w1), s1 -= high_of(w1);
+    const uint32_t w2 = pack_bf16x2(s0, s1);
+    ctl.sums[block][lane] = make_uint2(tig < 2 ? w0 : w1, tig < 2 ? w2 : 0u);
+    if (tig == 0)
+        ctl.unit[block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (0x1p33f * kScaleLog2);
+}
 
-// A warp's running softmax over a row: columns 2 * tig + c of each block.
+// A warp's running softmax over a part of a row: columns 2 * tig + c of each block.
 template <int kKind, bool kSplit>
 struct Running {
     using S = Shape<kKind>;
-    using Q = Queries<kKind, kSplit>;
-    float o[S::kBlocks][8][4];                        // O^T of 16 dims each, in units of 2^-93 (dims + 8: 2^-89)
-    float m[S::kBlocks][2];                           // maximum, log2
-    float l[S::kBlocks][2];                           // this lane's part of the sum, times 2^40
-    float z[S::kBlocks][2][2];                        // [group]: of weights times zeros
+    static constexpr int kBlocks = S::kBlocks;
+    static constexpr bool kLow = kSplit && !S::kPair; // low parts as fragments of their own
+    float o[kBlocks][8][4];                           // O^T of 16 dims each, in units of 2^-93 (dims + 8: 2^-89)
+    float m[kBlocks][2];                              // maximum, log2
+    float unit[kBlocks][2];
+    Two l[kBlocks];                                   // this lane's part of the sum, times 2^40
+    Two z[kBlocks][2];                                // [group]: of weights times zeros
+    Two pw[kBlocks][2];                               // [group]: of weights times scales, since the last centre()
 
-    __device__ __forceinline__ void clear() {
+    __device__ __forceinline__ void clear(const Control<kKind>& ctl) {
+        const int tig = threadIdx.x & 3;
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n) {
+        for (int n = 0; n < kBlocks; ++n) {
 #pragma unroll
             for (int d = 0; d < 8; ++d) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, l[n][c] = 0.f, z[n][0][c] = z[n][1][c] = 0.f;
+            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, unit[n][c] = ctl.unit[n * 8 + 2 * tig + c];
+            l[n] = z[n][0] = z[n][1] = pw[n][0] = pw[n][1] = two(0.f, 0.f);
         }
     }
 
-    // Scores (tokens gid, gid + 8) to weights times 2^40. The maximum moves only when a score
-    // passes it by more than kSlack: weights and sums are floating-point numbers, so the slack
-    // costs no bits, and most pages pass with one vote.
-    __device__ __forceinline__ void weigh(float (&s)[S::kBlocks][4], const Q& q) {
+    // Scores (tokens gid, gid + 8 of kPages pages) to weights times 2^40. The maximum moves only
+    // when a score passes it by more than kSlack: weights and sums are floating-point numbers, so
+    // the slack costs no bits, and most pages pass with one vote.
+    template <int kPages>
+    __device__ __forceinline__ void weigh(float (&s)[kPages][kBlocks][4]) {
         bool over = false;
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n)
+        for (int n = 0; n < kBlocks; ++n) {
+            const float limit0 = m[n][0] + kSlack, limit1 = m[n][1] + kSlack;
+            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[n][i] *= q.unit[n][i & 1];
-                over |= s[n][i] > m[n][i & 1] + kSlack;
+            for (int p = 0; p < kPages; ++p) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[p][n][i] *= unit[n][i & 1];
+                top0 = fmaxf(top0, fmaxf(s[p][n][0], s[p][n][2]));
+                top1 = fmaxf(top1, fmaxf(s[p][n][1], s[p][n][3]));
             }
+            over |= top0 > limit0 || top1 > limit1;
+        }
         if (__any_sync(kAll, over)) {
 #pragma unroll
-            for (int n = 0; n < S::kBlocks; ++n)
+            for (int n = 0; n < kBlocks; ++n) {
+                float f[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float top = fmaxf(s[n][c], s[n][c + 2]);
+                    float top = m[n][c];
+#pragma unroll
+                    for (int p = 0; p < kPages; ++p) top = fmaxf(top, fmaxf(s[p][n][c], s[p][n][c + 2]));
 #pragma unroll
                     for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
-                    top = fmaxf(top, m[n][c]);
-                    const float f = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top);
+                    f[c] = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top);
                     m[n][c] = top;
-                    l[n][c] *= f;
-                    z[n][0][c] *= f;
-                    z[n][1][c] *= f;
-#pragma unroll
-                    for (int d = 0; d < 8; ++d) o[n][d][c] *= f, o[n][d][c + 2] *= f;
                 }
+                const Two f2 = two(f[0], f[1]);
+                l[n] = mul2(l[n], f2);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) z[n][g] = mul2(z[n][g], f2), pw[n][g] = mul2(pw[n][g], f2);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) o[n][d][0] *= f[0], o[n][d][1] *= f[1], o[n][d][2] *= f[0], o[n][d][3] *= f[1];
+            }
         }
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n)
+        for (int n = 0; n < kBlocks; ++n) {
+            const float base0 = m[n][0] == -INFINITY ? kWeightBits : kWeightBits - m[n][0];
+            const float base1 = m[n][1] == -INFINITY ? kWeightBits : kWeightBits - m[n][1];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float base = m[n][c] == -INFINITY ? kWeightBits : kWeightBits - m[n][c];
-                s[n][c] = fast_exp2(s[n][c] + base);
-                s[n][c + 2] = fast_exp2(s[n][c + 2] + base);
-                l[n][c] += s[n][c] + s[n][c + 2];
+            for (int p = 0; p < kPages; ++p) {
+                s[p][n][0] = fast_exp2(s[p][n][0] + base0);
+                s[p][n][1] = fast_exp2(s[p][n][1] + base1);
+                s[p][n][2] = fast_exp2(s[p][n][2] + base0);
+                s[p][n][3] = fast_exp2(s[p][n][3] + base1);
+                l[n] = add2(l[n], add2(two(s[p][n][0], s[p][n][1]), two(s[p][n][2], s[p][n][3])));
             }
+        }
     }
 
     // Weights as B fragments, tokens as rows: a high and a low part, in columns of their own
-    // (kPair) or apart. The high part is cut off rather than rounded, the low part of kPair
-    // too: what is left out is less than 2^-14 of a weight (2^-15 where the low part is rounded).
-    __device__ __forceinline__ static void parts(const float (&p)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-        const uint32_t low_columns = S::kPair && (threadIdx.x & 2) ? 0xffff0000u : 0u;
+    // (kPair) or apart. The high part is cut off, the low part rounded: half a step of it is 2^-15
+    // of a weight, up or down.
+    __device__ __forceinline__ static void split(const float (&p)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+        const uint32_t sign = threadIdx.x & 2 ? 0x80000000u : 0u;
+        const float low = threadIdx.x & 2 ? 1.f : 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint32_t a = __float_as_uint(p[2 * t]), b = __float_as_uint(p[2 * t + 1]);
             if (S::kPair) {
-                const float x = p[2 * t] - __uint_as_float(a & low_columns);
-                const float y = p[2 * t + 1] - __uint_as_float(b & low_columns);
-                hi[t] = movmatrix_trans(prmt(__float_as_uint(x), __float_as_uint(y), 0x7632u));
+                // the cut-off weight, or the weight less it
+                const Two x = fma2(two(low, low), two(p[2 * t], p[2 * t + 1]),
+                                   two(__uint_as_float((a & 0xffff0000u) ^ sign), __uint_as_float((b & 0xffff0000u) ^ sign)));
+                float x0, x1;
+                parts_of(x, x0, x1);
+                hi[t] = movmatrix_trans(pack_bf16x2(x0, x1));
             } else {
                 const uint32_t w = prmt(a, b, 0x7632u);
                 hi[t] = movmatrix_trans(w);
@@ -295,91 +338,158 @@ struct Running {
         }
     }
 
-    __device__ __forceinline__ void packed_page(const uint8_t* unit, const Q& q) {
+    // Two packed pages; the second one's tokens count only if `both` (it is read all the same).
+    __device__ __forceinline__ void packed_pages(const uint8_t* unit0, const uint8_t* unit1, bool both,
+                                                 const Control<kKind>& ctl) {
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-        float s[S::kBlocks][4];
+        const uint8_t* const units[2] = {unit0, unit1};
+        float s[2][kBlocks][4];
         {
-            const uint4 k0 = *reinterpret_cast<const uint4*>(unit + 16 * lane);
-            const uint4 k1 = *reinterpret_cast<const uint4*>(unit + 512 + 16 * lane);
-            const uint4 t0 = *reinterpret_cast<const uint4*>(unit + kUnitKScales + 16 * gid);
-            const uint4 t1 = *reinterpret_cast<const uint4*>(unit + kUnitKScales + 16 * (gid + 8));
-            const uint32_t z0 = tig & 1 ? t0.w : t0.z, z1 = tig & 1 ? t1.w : t1.z;
-            const uint32_t zeros[4] = {z0, z1, z0, z1};
+            uint32_t w[2][8], scale[2][2][2];
 #pragma unroll
-            for (int n = 0; n < S::kBlocks; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-                mma_bf16_16816(s[n], zeros, q.sums[n][0], q.sums[n][1]);
+            for (int p = 0; p < 2; ++p) {
+                const uint4 k0 = *reinterpret_cast<const uint4*>(units[p] + 16 * lane);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(units[p] + 512 + 16 * lane);
+                w[p][0] = k0.x, w[p][1] = k0.y, w[p][2] = k0.z, w[p][3] = k0.w;
+                w[p][4] = k1.x, w[p][5] = k1.y, w[p][6] = k1.z, w[p][7] = k1.w;
+                const uint4 t0 = *reinterpret_cast<const uint4*>(units[p] + kUnitKScales + 16 * gid);
+                const uint4 t1 = *reinterpret_cast<const uint4*>(units[p] + kUnitKScales + 16 * (gid + 8));
+                scale[p][0][0] = t0.x, scale[p][0][1] = t0.y, scale[p][1][0] = t1.x, scale[p][1][1] = t1.y;
+                const uint32_t z0 = tig & 1 ? t0.w : t0.z, z1 = tig & 1 ? t1.w : t1.z;
+                const uint32_t zeros[4] = {z0, z1, z0, z1};
+#pragma unroll
+                for (int n = 0; n < kBlocks; ++n) {
+                    const uint2 q = ctl.sums[n][lane];
+                    mma_first(s[p][n], zeros, q.x, q.y);
+                }
             }
-            const uint32_t w[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-            const uint32_t scale0[2] = {t0.x, t0.y}, scale1[2] = {t1.x, t1.y};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {             // 32 dims
-                float acc[S::kBlocks][4];
-#pragma unroll
-                for (int n = 0; n < S::kBlocks; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                float acc[2][kBlocks][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int k = 2 * g + i;
-                    const uint32_t up = w[k] >> 8;
-                    const uint32_t f[4] = {w[k] & 0x000f000fu, up & 0x000f000fu, w[k] & 0x00f000f0u, up & 0x00f000f0u};
+                    uint32_t f[2][4];
 #pragma unroll
-                    for (int n = 0; n < S::kBlocks; ++n) {
-                        mma_bf16_16816(acc[n], f, q.hi[n][k][0], q.hi[n][k][1]);
-                        if (Q::kLow) mma_bf16_16816(acc[n], f, q.lo[n][k][0], q.lo[n][k][1]);
+                    for (int p = 0; p < 2; ++p) {
+                        const uint32_t up = w[p][k] >> 8;
+                        f[p][0] = w[p][k] & 0x000f000fu, f[p][1] = up & 0x000f000fu;
+                        f[p][2] = w[p][k] & 0x00f000f0u, f[p][3] = up & 0x00f000f0u;
+                    }
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n) {
+                        uint4 q;
+                        if (kLow) {
+                            q = ctl.frag[n][k][lane];
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(&ctl.frag[n][k][lane]);
+                            q = make_uint4(x.x, x.y, 0u, 0u);
+                        }
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            if (i == 0) mma_first(acc[p][n], f[p], q.x, q.y);
+                            else mma_bf16_16816(acc[p][n], f[p], q.x, q.y);
+                        }
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+                            if (kLow) mma_bf16_16816(acc[p][n], f[p], q.z, q.w);
                     }
                 }
-                const float a0 = g & 1 ? high_of(scale0[g >> 1]) : low_of(scale0[g >> 1]);
-                const float a1 = g & 1 ? high_of(scale1[g >> 1]) : low_of(scale1[g >> 1]);
 #pragma unroll
-                for (int n = 0; n < S::kBlocks; ++n) {
-                    s[n][0] = fmaf(a0, acc[n][0], s[n][0]);
-                    s[n][1] = fmaf(a0, acc[n][1], s[n][1]);
-                    s[n][2] = fmaf(a1, acc[n][2], s[n][2]);
-                    s[n][3] = fmaf(a1, acc[n][3], s[n][3]);
-                }
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t x = scale[p][t][g >> 1];
+                        const float a = g & 1 ? high_of(x) : low_of(x);
+#pragma unroll
+                        for (int n = 0; n < kBlocks; ++n) {
+                            const Two y = fma2(two(a, a), two(acc[p][n][2 * t], acc[p][n][2 * t + 1]),
+                                               two(s[p][n][2 * t], s[p][n][2 * t + 1]));
+                            parts_of(y, s[p][n][2 * t], s[p][n][2 * t + 1]);
+                        }
+                    }
             }
         }
-        add_low(s);
-        weigh(s, q);
-        const uint4 v0 = *reinterpret_cast<const uint4*>(unit + kUnitVCodes + 16 * lane);
-        const uint4 v1 = *reinterpret_cast<const uint4*>(unit + kUnitVCodes + 512 + 16 * lane);
-        const uint2 t0 = *reinterpret_cast<const uint2*>(unit + kUnitVScales + 8 * gid);
-        const uint2 t1 = *reinterpret_cast<const uint2*>(unit + kUnitVScales + 8 * (gid + 8));
-        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        add_low<2>(s);
+        if (!both) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {                 // 64 dims
-            const float a0 = g ? high_of(t0.x) : low_of(t0.x), a1 = g ? high_of(t1.x) : low_of(t1.x);
-            const float z0 = g ? high_of(t0.y) : low_of(t0.y), z1 = g ? high_of(t1.y) : low_of(t1.y);
-            uint32_t hi[S::kBlocks][2], lo[S::kBlocks][2];
+            for (int n = 0; n < kBlocks; ++n) s[1][n][0] = s[1][n][1] = s[1][n][2] = s[1][n][3] = -INFINITY;
+        }
+        weigh<2>(s);
 #pragma unroll
-            for (int n = 0; n < S::kBlocks; ++n) {
-                const float p[4] = {s[n][0] * a0, s[n][1] * a0, s[n][2] * a1, s[n][3] * a1};
-                z[n][g][0] = fmaf(s[n][0], z0, fmaf(s[n][2], z1, z[n][g][0]));
-                z[n][g][1] = fmaf(s[n][1], z0, fmaf(s[n][3], z1, z[n][g][1]));
-                parts(p, hi[n], lo[n]);
-            }
+        for (int p = 0; p < 2; ++p) {
+            const uint4 v0 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 16 * lane);
+            const uint4 v1 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 512 + 16 * lane);
+            const uint2 t0 = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * gid);
+            const uint2 t1 = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8));
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int d = 4 * g + i;
-                const uint32_t up = w[d] >> 8;
-                const uint32_t f[4] = {w[d] & 0x000f000fu, w[d] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+            for (int g = 0; g < 2; ++g) {             // 64 dims
+                const float a0 = g ? high_of(t0.x) : low_of(t0.x), a1 = g ? high_of(t1.x) : low_of(t1.x);
+                const float z0 = g ? high_of(t0.y) : low_of(t0.y), z1 = g ? high_of(t1.y) : low_of(t1.y);
+                uint32_t hi[kBlocks][2], lo[kBlocks][2];
 #pragma unroll
-                for (int n = 0; n < S::kBlocks; ++n) {
-                    mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
-                    if (!S::kPair) mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
+                for (int n = 0; n < kBlocks; ++n) {
+                    const Two s0 = two(s[p][n][0], s[p][n][1]), s1 = two(s[p][n][2], s[p][n][3]);
+                    const Two p0 = mul2(s0, two(a0, a0)), p1 = mul2(s1, two(a1, a1));
+                    z[n][g] = fma2(s0, two(z0, z0), fma2(s1, two(z1, z1), z[n][g]));
+                    pw[n][g] = add2(pw[n][g], add2(p0, p1));
+                    float x[4];
+                    parts_of(p0, x[0], x[1]);
+                    parts_of(p1, x[2], x[3]);
+                    split(x, hi[n], lo[n]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int d = 4 * g + i;
+                    const uint32_t up = w[d] >> 8;
+                    const uint32_t f[4] = {w[d] & 0x000f000fu, w[d] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n) {
+                        mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
+                        if (!S::kPair) mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
+                    }
                 }
             }
         }
     }
 
+    // Codes are counted from 0, so the accumulators of the output and the sums with the zeros grow in
+    // opposite directions and cancel in the end, where a long row's output is far smaller than either
+    // and nothing would be left of it but their rounding. Every kCentre pairs of pages the codes'
+    // middle times the weights is moved from the one to the other.
+    __device__ __forceinline__ void centre() {
+#pragma unroll
+        for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const Two y = mul2(pw[n][g], two(kMiddle, kMiddle));
+                z[n][g] = add2(z[n][g], y);
+                pw[n][g] = two(0.f, 0.f);
+                float x[2];
+                parts_of(y, x[0], x[1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int i = 4; i < 32; i *= 2) x[c] += __shfl_xor_sync(kAll, x[c], i);
+                    x[c] *= S::kPair && (threadIdx.x & 2) ? 0.f : -kCodeUnit;    // not from the low parts' columns
+#pragma unroll
+                    for (int d = 4 * g; d < 4 * g + 4; ++d) {
+                        o[n][d][c] += x[c];
+                        o[n][d][c + 2] = fmaf(x[c], 16.f, o[n][d][c + 2]);
+                    }
+                }
+            }
+    }
+
     // A bf16 page in shared memory, K and then V, rows of 256 bytes swizzled by 16-byte chunks
     // (chunk_offset), zero from row `valid` on.
-    __device__ __forceinline__ void recent_page(const uint8_t* page, int valid, const Q& q) {
+    __device__ __forceinline__ void recent_page(const uint8_t* page, int valid, const Control<kKind>& ctl) {
         const int lane = threadIdx.x & 31, gid = lane >> 2;
         const uint32_t down = 0x21802180u, down16 = 0x23802380u;         // 2^-60, 2^-56: exponents 67, 71
-        float s[S::kBlocks][4];
+        float s[1][kBlocks][4];
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        for (int n = 0; n < kBlocks; ++n) s[0][n][0] = s[0][n][1] = s[0][n][2] = s[0][n][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             uint32_t f[4];
@@ -387,28 +497,29 @@ struct Running {
             f[0] = bf16x2_mul(f[0], down), f[1] = bf16x2_mul(f[1], down);
             f[2] = bf16x2_mul(f[2], down16), f[3] = bf16x2_mul(f[3], down16);
 #pragma unroll
-            for (int n = 0; n < S::kBlocks; ++n) {
-                mma_bf16_16816(s[n], f, q.hi[n][k][0], q.hi[n][k][1]);
-                if (Q::kLow) mma_bf16_16816(s[n], f, q.lo[n][k][0], q.lo[n][k][1]);
+            for (int n = 0; n < kBlocks; ++n) {
+                const uint4 q = ctl.frag[n][k][lane];
+                mma_bf16_16816(s[0][n], f, q.x, q.y);
+                if (kLow) mma_bf16_16816(s[0][n], f, q.z, q.w);
             }
         }
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n)
+        for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= kRecentScore;
-        add_low(s);
+            for (int i = 0; i < 4; ++i) s[0][n][i] *= kRecentScore;
+        add_low<1>(s);
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n)
+        for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (gid + 8 * (i >> 1) >= valid) s[n][i] = -INFINITY;
-        weigh(s, q);
-        uint32_t hi[S::kBlocks][2], lo[S::kBlocks][2];
+                if (gid + 8 * (i >> 1) >= valid) s[0][n][i] = -INFINITY;
+        weigh<1>(s);
+        uint32_t hi[kBlocks][2], lo[kBlocks][2];
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n) {
+        for (int n = 0; n < kBlocks; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= kRecentWeight;
-            parts(s[n], hi[n], lo[n]);
+            for (int i = 0; i < 4; ++i) s[0][n][i] *= kRecentWeight;
+            split(s[0][n], hi[n], lo[n]);
         }
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
@@ -418,7 +529,7 @@ struct Running {
                                      chunk_offset((lane & 7) + 8 * (lane >> 4), 2 * d + (lane >> 3 & 1)));
             f[1] = bf16x2_mul(f[1], 0x41804180u), f[3] = bf16x2_mul(f[3], 0x41804180u);      // 16
 #pragma unroll
-            for (int n = 0; n < S::kBlocks; ++n) {
+            for (int n = 0; n < kBlocks; ++n) {
                 mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
                 if (!S::kPair) mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
             }
@@ -426,44 +537,49 @@ struct Running {
     }
 
     // Low parts of the queries in columns of their own (bf16 queries fill those with copies).
-    __device__ __forceinline__ static void add_low(float (&s)[S::kBlocks][4]) {
+    template <int kPages>
+    __device__ __forceinline__ static void add_low(float (&s)[kPages][kBlocks][4]) {
         if (S::kPair && kSplit) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[0][i] += __shfl_xor_sync(kAll, s[0][i], 2);
+            for (int p = 0; p < kPages; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[p][0][i] += __shfl_xor_sync(kAll, s[p][0][i], 2);
         }
     }
     __device__ __forceinline__ static int chunk_offset(int token, int c) { return token * kD * 2 + ((c ^ (token & 7)) << 4); }
 
-    // The row's sums and unnormalised output, from all lanes: f(query, dim, value) for every
-    // query of the group, with m (log2) and l of each query by g(query, m, l).
-    template <typename F, typename G>
-    __device__ __forceinline__ void finish(int group, F f, G g) {
+    // The warp's partial: m (log2), l and the unnormalised output, a query a row of `part`.
+    __device__ __forceinline__ void put(int group, float* part, float* ms, float* ls) {
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
-        for (int n = 0; n < S::kBlocks; ++n)
+        for (int n = 0; n < kBlocks; ++n) {
+            float sum[2], zero[2][2];
+            parts_of(l[n], sum[0], sum[1]);
+            parts_of(z[n][0], zero[0][0], zero[0][1]);
+            parts_of(z[n][1], zero[1][0], zero[1][1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) {
-                    l[n][c] += __shfl_xor_sync(kAll, l[n][c], x);
-                    z[n][0][c] += __shfl_xor_sync(kAll, z[n][0][c], x);
-                    z[n][1][c] += __shfl_xor_sync(kAll, z[n][1][c], x);
+                    sum[c] += __shfl_xor_sync(kAll, sum[c], x);
+                    zero[0][c] += __shfl_xor_sync(kAll, zero[0][c], x);
+                    zero[1][c] += __shfl_xor_sync(kAll, zero[1][c], x);
                 }
                 const int query = S::kPair ? 2 * (tig & 1) + c : n * 8 + 2 * tig + c;
                 const bool on = query < group && !(S::kPair && tig >= 2);
-                const float sum = l[n][c] * kSumUnit;
-                if (on && gid == 0) g(query, m[n][c], sum);
+                if (on && gid == 0) ms[query] = m[n][c], ls[query] = sum[c] * kSumUnit;
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
                     float x0 = o[n][d][c], x1 = o[n][d][c + 2];
                     if (S::kPair) x0 += __shfl_xor_sync(kAll, x0, 2), x1 += __shfl_xor_sync(kAll, x1, 2);
-                    const float zero = z[n][d / 4][c] * kSumUnit;
+                    const float y = zero[d / 4][c] * kSumUnit;
                     if (on) {
-                        f(query, d * 16 + gid, fmaf(x0, kOutUnit, zero), sum);
-                        f(query, d * 16 + gid + 8, fmaf(x1, kOutUnit * 0.0625f, zero), sum);
+                        part[query * kPartStride + d * 16 + gid] = fmaf(x0, kOutUnit, y);
+                        part[query * kPartStride + d * 16 + gid + 8] = fmaf(x1, kOutUnit * 0.0625f, y);
                     }
                 }
             }
+        }
     }
 };
 
@@ -474,26 +590,187 @@ __device__ __forceinline__ void store_lse(const PackedArgs& a, int64_t row, floa
     if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
 }
 
+// A part of a row: packed pages page0 .. page1 and recent pages recent0 .. recent1.
+struct Part {
+    int b, h, page0, page1, recent0, recent1, recent;
+};
+
+// The pages of a part that are this warp's, index `mine` of `of` warps: every of-th one from
+// page0 + mine on; recent pages from the last warp down. All of the CTA calls it; leaves the
+// CTA's sums in ctl.m, ctl.l and the slots, by warp.
 template <int kKind, bool kSplit>
-__global__ void __launch_bounds__(Shape<kKind>::kWarps * 32, Shape<kKind>::kCtas)
-    attend_kernel(const __grid_constant__ PackedArgs a) {
+__device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& part, int mine, int of, uint8_t* slots,
+                                            Control<kKind>& ctl) {
     using S = Shape<kKind>;
-    constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kDepth = S::kDepth;
+    constexpr int kDepth = S::kDepth;
     static_assert(kDepth * kUnitBytes >= 4 * kPage * kD, "a recent page lies in the slots");
-    static_assert(kDepth * kUnitBytes >= kPartBytes<S::kRows>, "a partial lies in the slots");
-    extern __shared__ __align__(128) uint8_t slots[];
-    __shared__ Control<kWarps, S::kRows> ctl;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint8_t* const mine = slots + warp * kDepth * kUnitBytes;
-    // partials: a warp's first row beside the slots, its last row in its slots
-    const auto part = [&](int e) {
-        return reinterpret_cast<float*>(e & 1 ? slots + (e >> 1) * kDepth * kUnitBytes
-                                              : slots + kWarps * kDepth * kUnitBytes + (e >> 1) * kPartBytes<S::kRows>);
+    static_assert(kDepth * kUnitBytes >= S::kRows * kPartStride * 4, "a partial lies in the slots");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = part.b, h = part.h;
+    uint8_t* const own = slots + warp * kDepth * kUnitBytes;
+    const int first = part.page0 + mine;
+    const int count = part.page1 > first ? (part.page1 - first + of - 1) / of : 0;
+    const int64_t page_bytes = static_cast<int64_t>(a.hkv) * kUnitBytes;
+    const uint8_t* const base = a.packed + static_cast<int64_t>(h) * kUnitBytes + lane * 16;
+    int ids = lane < count ? packed_id(a, b, h, first + lane * of) : 0, next = 0;
+    int put = 0;                                      // slot of the next page to fetch
+    const auto load = [&](int i) {
+        if (i < count) {
+            if ((i & 31) == 0) {                      // ids of 32 pages, fetched 32 pages ahead
+                if (i > 0) ids = next;
+                if (i + 32 + lane < count) next = packed_id(a, b, h, first + (i + 32 + lane) * of);
+            }
+            const uint8_t* from = base + __shfl_sync(kAll, ids, i & 31) * page_bytes;
+            uint8_t* to = own + put * kUnitBytes + lane * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async_16(to + j * 512, from + j * 512);
+            if (lane < kUnitBytes / 16 - 128) cp_async_16(to + 2048, from + 2048);
+        }
+        copies_commit();
+        if (++put == kDepth) put = 0;
     };
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load(i);
+    if (warp < S::kBlocks) put_queries<kKind, kSplit>(a, b, h, warp, ctl);
+    __syncthreads();
+    Running<kKind, kSplit> run;
+    run.clear(ctl);
+    int at = 0;                                       // slot of the next page to use
+#pragma unroll 1
+    for (int i = 0; i < count; i += 2) {
+        copies_wait<kDepth - 2>();
+        __syncwarp();
+        const uint8_t* const unit0 = own + at * kUnitBytes;
+        if (++at == kDepth) at = 0;
+        const uint8_t* const unit1 = i + 1 < count ? own + at * kUnitBytes : unit0;
+        if (++at == kDepth) at = 0;
+        run.packed_pages(unit0, unit1, i + 1 < count, ctl);
+        if (((i / 2) & (kCentre - 1)) == kCentre - 1) run.centre();
+        __syncwarp();                                 // both are read
+        load(i + kDepth);
+        load(i + kDepth + 1);
+    }
+    run.centre();
+    copies_wait<0>();
+    __syncwarp();
+#pragma unroll 1
+    for (int r = part.recent0 + of - 1 - mine; r < part.recent1; r += of) {
+        const int valid = min(kPage, part.recent - r * kPage);
+        int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
+        if (id < 0 || id >= a.num_cache) {
+            report_error(a.st, LOCKS_ERR_BAD_INDEX);
+            id = 0;
+        }
+        const int64_t from = (static_cast<int64_t>(id) * a.hkv + h) * (kPage * kD) + lane * 8;
+#pragma unroll
+        for (int j = 0; j < kPage / 2; ++j) {         // two tokens
+            const int token = 2 * j + (lane >> 4), to = run.chunk_offset(token, lane & 15);
+            copy_or_zero(own + to, a.k_cache + from + j * 2 * kD, token < valid);
+            copy_or_zero(own + kPage * kD * 2 + to, a.v_cache + from + j * 2 * kD, token < valid);
+        }
+        copies_commit();
+        copies_wait<0>();
+        __syncwarp();
+        run.recent_page(own, valid, ctl);
+        __syncwarp();
+    }
+    run.put(a.group, reinterpret_cast<float*>(own), ctl.m[warp], ctl.l[warp]);
+    __syncthreads();
+}
+
+// Query `query`, dim `dim` of the CTA's part from its warps' partials.
+template <int kKind>
+__device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int query, int dim, float& top,
+                                            float& sum) {
+    using S = Shape<kKind>;
+    top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, ctl.m[w][query]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float x = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < S::kWarps; ++w) {
+        const float f = fast_exp2(ctl.m[w][query] - base);
+        x = fmaf(f, reinterpret_cast<const float*>(slots + w * S::kDepth * kUnitBytes)[query * kPartStride + dim], x);
+        sum = fmaf(f, ctl.l[w][query], sum);
+    }
+    return x;
+}
+
+// Short rows: cluster r / cluster size is a row.
+template <int kKind, bool kSplit>
+__global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __grid_constant__ PackedArgs a, int ctas) {
+    using S = Shape<kKind>;
+    extern __shared__ __align__(128) uint8_t slots[];
+    __shared__ Control<kKind> ctl;
+    const int warp = threadIdx.x >> 5, rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int r = blockIdx.x / ctas;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    Part part;
+    part.b = r / a.hkv;
+    part.h = r % a.hkv;
+    const Len len = row_len(a, part.b, part.h, rank == 0 && threadIdx.x == 0);
+    part.page0 = part.recent0 = 0;
+    part.page1 = len.pages;
+    part.recent1 = len.recent_pages();
+    part.recent = len.recent;
+    attend_part<kKind, kSplit>(a, part, rank * S::kWarps + warp, ctas * S::kWarps, slots, ctl);
+    const int64_t row = static_cast<int64_t>(part.b) * a.hq + part.h * a.group;
+    for (int i = threadIdx.x; i < a.group * kD; i += S::kThreads) {
+        const int query = i / kD, dim = i % kD;
+        float top, sum;
+        const float x = join_warps<kKind>(slots, ctl, query, dim, top, sum);
+        if (ctas == 1) {
+            store_row(a, row + query, x, sum, dim);
+            if (dim == 0) store_lse(a, row + query, top, sum);
+        } else {
+            ctl.cta_o[query][dim] = x;
+            if (dim == 0) ctl.cta_m[query] = top, ctl.cta_l[query] = sum;
+        }
+    }
+    if (ctas == 1) return;
+    cluster_sync_all();
+    for (int i = rank * S::kThreads + threadIdx.x; i < a.group * kD; i += ctas * S::kThreads) {
+        const int query = i / kD, dim = i % kD;
+        float m[kMaxCluster], l[kMaxCluster], x[kMaxCluster], top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            m[c] = -INFINITY;
+            l[c] = x[c] = 0.f;
+            if (c < ctas) {
+                m[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_m[query], c));
+                l[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_l[query], c));
+                x[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_o[query][dim], c));
+            }
+            top = fmaxf(top, m[c]);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        float value = 0.f, sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float f = fast_exp2(m[c] - base);
+            value = fmaf(f, x[c], value);
+            sum = fmaf(f, l[c], sum);
+        }
+        store_row(a, row + query, value, sum, dim);
+        if (dim == 0) store_lse(a, row + query, top, sum);
+    }
+    cluster_sync_all();                               // nobody leaves while its sums are read
+}
+
+// Long rows: the line of steps.
+template <int kKind, bool kSplit>
+__global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const __grid_constant__ PackedArgs a) {
+    using S = Shape<kKind>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+    extern __shared__ __align__(128) uint8_t slots[];
+    __shared__ Control<kKind> ctl;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool by_row = cuts_by_row(a, gridDim.x);
     grid_dependency_wait();
     allow_dependent_launch();
 
-    // the line of steps
     const int per = (a.batch + kThreads - 1) / kThreads;
     {
         int64_t sum = 0;
@@ -508,7 +785,6 @@ __global__ void __launch_bounds__(Shape<kKind>::kWarps * 32, Shape<kKind>::kCtas
             if (lane >= x) upto += y;
         }
         if (lane == 31) ctl.warp_sum[warp] = upto;
-        if (threadIdx.x < kWarps * 2) ctl.entry[threadIdx.x].row = -1;
         __syncthreads();
         for (int w = 0; w < warp; ++w) upto += ctl.warp_sum[w];
         ctl.upto[threadIdx.x] = upto;
@@ -523,159 +799,54 @@ __global__ void __launch_bounds__(Shape<kKind>::kWarps * 32, Shape<kKind>::kCtas
             for (int d = 0; d < kD; d += 8) *reinterpret_cast<uint4*>(a.out + row * kD + d) = make_uint4(0, 0, 0, 0);
             store_lse(a, row, 0.f, 0.f);
         }
+        if (by_row) a.cuts[r] = {-1, 0, 0};
     }
     __syncthreads();
     const int64_t total = ctl.upto[kThreads - 1];
     const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps));
-    const int64_t cta0 = ctas > 0 ? first_step(total, blockIdx.x, ctas) : 0;
-    const int64_t cta1 = static_cast<int>(blockIdx.x) < ctas ? first_step(total, blockIdx.x + 1, ctas) : cta0;
-    int64_t pos = cta0 + (cta1 - cta0) * warp / kWarps;
-    const int64_t end = cta0 + (cta1 - cta0) * (warp + 1) / kWarps;
-
-    if (pos < end) {
-        // the row at pos
-        int b = 0, h = 0, off = 0;
-        Len len;
-        {
-            int before = 0;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.upto[i * 32 + lane] <= pos));
-            int64_t at = pos - (before > 0 ? ctl.upto[before - 1] : 0);
-            b = before * per;
-            for (int64_t n; b < a.batch - 1 && at >= (n = seq_steps(a, b, false)); ++b) at -= n;
-            for (len = row_len(a, b, 0, false); h < a.hkv - 1 && at >= len.steps(); len = row_len(a, b, ++h, false))
-                at -= len.steps();
-            off = static_cast<int>(at);
-        }
-        Queries<kKind, kSplit> q;
-        Running<kKind, kSplit> run;
-        for (bool first = true; pos < end; first = false) {
-            const int steps = len.steps();
-            const int n = static_cast<int>(min(end - pos, static_cast<int64_t>(steps - off)));
-            // packed pages off .. off + count
-            const int count = max(0, min(off + n, len.pages) - off);
-            const int64_t unit0 = static_cast<int64_t>(h) * kUnitBytes, page_bytes = static_cast<int64_t>(a.hkv) * kUnitBytes;
-            int ids = lane < count ? packed_id(a, b, h, off + lane) : 0, next = 0;
-            const auto load = [&](int i, int slot) {
-                if ((i & 31) == 0) {                  // ids of 32 pages, fetched 32 pages ahead
-                    if (i > 0) ids = next;
-                    if (i + 32 + lane < count) next = packed_id(a, b, h, off + i + 32 + lane);
-                }
-                const uint8_t* from = a.packed + __shfl_sync(kAll, ids, i & 31) * page_bytes + unit0 + lane * 16;
-                uint8_t* to = mine + slot * kUnitBytes + lane * 16;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) cp_async_16(to + j * 512, from + j * 512);
-                if (lane < kUnitBytes / 16 - 128) cp_async_16(to + 2048, from + 2048);
-            };
-#pragma unroll
-            for (int i = 0; i < kDepth - 1; ++i) {
-                if (i < count) load(i, i);
-                copies_commit();
-            }
-            q.load(a, b, h);
-            run.clear();
-            int slot = 0;
-#pragma unroll 1
-            for (int i = 0; i < count; ++i) {
-                copies_wait<kDepth - 2>();
-                __syncwarp();                         // everyone's copies are there, and the slot ahead is read
-                if (i + kDepth - 1 < count) load(i + kDepth - 1, slot == 0 ? kDepth - 1 : slot - 1);
-                copies_commit();
-                run.packed_page(mine + slot * kUnitBytes, q);
-                if (++slot == kDepth) slot = 0;
-            }
-            copies_wait<0>();
-            __syncwarp();
-            // recent pages whose first step is among this part's
-            const int r0 = max(0, (off - len.pages + kRecentSteps - 1) / kRecentSteps);
-            const int r1 = min(len.recent_pages(), (off + n - len.pages + kRecentSteps - 1) / kRecentSteps);
-#pragma unroll 1
-            for (int r = r0; r < r1; ++r) {
-                const int valid = min(kPage, len.recent - r * kPage);
-                int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
-                if (id < 0 || id >= a.num_cache) {
-                    report_error(a.st, LOCKS_ERR_BAD_INDEX);
-                    id = 0;
-                }
-                const int64_t from = (static_cast<int64_t>(id) * a.hkv + h) * (kPage * kD) + lane * 8;
-#pragma unroll
-                for (int j = 0; j < kPage / 2; ++j) {  // two tokens
-                    const int token = 2 * j + (lane >> 4), to = run.chunk_offset(token, lane & 15);
-                    copy_or_zero(mine + to, a.k_cache + from + j * 2 * kD, token < valid);
-                    copy_or_zero(mine + kPage * kD * 2 + to, a.v_cache + from + j * 2 * kD, token < valid);
-                }
-                copies_commit();
-                copies_wait<0>();
-                __syncwarp();
-                run.recent_page(mine, valid, q);
-                __syncwarp();
-            }
-            const bool begins = off == 0, ends = off + n == steps;
-            if (begins && ends) {
-                const int64_t row = static_cast<int64_t>(b) * a.hq + h * a.group;
-                run.finish(
-                    a.group, [&](int query, int dim, float x, float sum) { store_row(a, row + query, x, sum, dim); },
-                    [&](int query, float m, float sum) { store_lse(a, row + query, m, sum); });
-            } else {
-                const int e = warp * 2 + (first ? 0 : 1);
-                float* o = part(e);
-                run.finish(
-                    a.group, [&](int query, int dim, float x, float) { o[query * kPartStride + dim] = x; },
-                    [&](int query, float m, float sum) { ctl.m[e][query] = m, ctl.l[e][query] = sum; });
-                if (lane == 0) {
-                    auto& entry = ctl.entry[e];
-                    entry.step0 = pos - off;
-                    entry.row = b * a.hkv + h;
-                    entry.len = steps;
-                    entry.begins = begins;
-                    entry.ends = ends;
-                }
-            }
-            pos += n;
-            off = 0;
-            if (pos < end) {
-                do {
-                    if (++h == a.hkv) ++b, h = 0;
-                    len = row_len(a, b, h, false);
-                } while (len.steps() == 0 && b < a.batch - 1);
-            }
-        }
+    int64_t pos = 0, end = 0;
+    if (static_cast<int>(blockIdx.x) < ctas) {
+        pos = first_step(total, blockIdx.x, ctas);
+        end = first_step(total, blockIdx.x + 1, ctas);
     }
+    if (!by_row && threadIdx.x == 0) a.cuts[blockIdx.x] = {-1, 0, 0};
+    if (pos >= end) return;
 
-    // rows that lie in several warps
-    __syncthreads();
-    int owned = -1, last = 0;                         // the row that goes on behind this CTA
-    for (int e = 0; e < kWarps * 2;) {
-        if (ctl.entry[e].row < 0) {
-            ++e;
-            continue;
-        }
-        const auto head = ctl.entry[e];
-        int stop = e;
-        bool ends = false;
-        for (int f = e; f < kWarps * 2; ++f) {
-            if (ctl.entry[f].row < 0) continue;
-            if (ctl.entry[f].row != head.row) break;
-            stop = f;
-            ends = ctl.entry[f].ends;
-        }
-        const bool whole = head.begins && ends;
-        if (head.begins && !ends) owned = head.row, last = cta_of(total, head.step0 + head.len - 1, ctas);
-        const int64_t row = static_cast<int64_t>(head.row / a.hkv) * a.hq + (head.row % a.hkv) * a.group;
-        const int slot = 2 * blockIdx.x + (head.begins ? 1 : 0);
+    // the row at pos
+    Part part;
+    Len len;
+    int off;
+    {
+        int before = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.upto[i * 32 + lane] <= pos));
+        int64_t at = pos - (before > 0 ? ctl.upto[before - 1] : 0);
+        part.b = before * per;
+        for (int64_t n; part.b < a.batch - 1 && at >= (n = seq_steps(a, part.b, false)); ++part.b) at -= n;
+        part.h = 0;
+        for (len = row_len(a, part.b, 0, false); part.h < a.hkv - 1 && at >= len.steps();
+             len = row_len(a, part.b, ++part.h, false))
+            at -= len.steps();
+        off = static_cast<int>(at);
+    }
+#pragma unroll 1
+    while (pos < end) {
+        const int steps = len.steps();
+        const int n = static_cast<int>(min(end - pos, static_cast<int64_t>(steps - off)));
+        part.page0 = min(off, len.pages);
+        part.page1 = min(off + n, len.pages);
+        // recent pages whose first step is among this part's
+        part.recent0 = max(0, (off - len.pages + kRecentSteps - 1) / kRecentSteps);
+        part.recent1 = min(len.recent_pages(), max(0, (off + n - len.pages + kRecentSteps - 1) / kRecentSteps));
+        part.recent = len.recent;
+        attend_part<kKind, kSplit>(a, part, warp, kWarps, slots, ctl);
+        const bool begins = off == 0, whole = begins && n == steps;
+        const int64_t row = static_cast<int64_t>(part.b) * a.hq + part.h * a.group;
+        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
         for (int i = threadIdx.x; i < a.group * kD; i += kThreads) {
             const int query = i / kD, dim = i % kD;
-            float top = -INFINITY;
-            for (int f = e; f <= stop; ++f)
-                if (ctl.entry[f].row >= 0) top = fmaxf(top, ctl.m[f][query]);
-            const float base = top == -INFINITY ? 0.f : top;
-            float x = 0.f, sum = 0.f;
-            for (int f = e; f <= stop; ++f)
-                if (ctl.entry[f].row >= 0) {
-                    const float w = fast_exp2(ctl.m[f][query] - base);
-                    x = fmaf(w, part(f)[query * kPartStride + dim], x);
-                    sum = fmaf(w, ctl.l[f][query], sum);
-                }
+            float top, sum;
+            const float x = join_warps<kKind>(slots, ctl, query, dim, top, sum);
             if (whole) {
                 store_row(a, row + query, x, sum, dim);
                 if (dim == 0) store_lse(a, row + query, top, sum);
@@ -684,25 +855,34 @@ __global__ void __launch_bounds__(Shape<kKind>::kWarps * 32, Shape<kKind>::kCtas
                 if (dim == 0) a.part_ml[slot * a.group + query] = make_float2(top, sum);
             }
         }
-        e = stop + 1;
-    }
-    if (threadIdx.x == 0) {
-        a.cuts[blockIdx.x].row = owned;
-        a.cuts[blockIdx.x].last = last;
+        if (begins && threadIdx.x == 0 && (by_row || !whole)) {
+            const int r = part.b * a.hkv + part.h;
+            const int last = cta_of(total, pos + steps - 1, ctas);
+            a.cuts[by_row ? r : static_cast<int>(blockIdx.x)] = {whole ? -1 : r, static_cast<int>(blockIdx.x), last};
+        }
+        pos += n;
+        off = 0;
+        if (pos < end) {
+            do {
+                if (++part.h == a.hkv) ++part.b, part.h = 0;
+                len = row_len(a, part.b, part.h, false);
+            } while (len.steps() == 0 && part.b < a.batch - 1);
+            __syncthreads();                          // the slots and sums are read
+        }
     }
 }
 
-// Joins the rows that lie in several CTAs: a block per (CTA that a row begins in, query).
+// Joins the rows that lie in several CTAs: a block per (cut, query).
 constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PackedArgs a) {
     __shared__ float weight[kMaxPackedCtas], sums[kJoinThreads / 32], tops[kJoinThreads / 32], acc[kJoinThreads];
-    const int c = blockIdx.x / a.group, query = blockIdx.x % a.group, tid = threadIdx.x;
+    const int query = blockIdx.x % a.group, tid = threadIdx.x;
     grid_dependency_wait();
     allow_dependent_launch();
-    const PackedCut cut = a.cuts[c];
+    const PackedCut cut = a.cuts[blockIdx.x / a.group];
     if (cut.row < 0) return;
-    const int n = cut.last - c + 1;                   // up to kMaxPackedCtas <= kJoinThreads
-    const auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    const int n = cut.last - cut.first + 1;           // up to kMaxPackedCtas <= kJoinThreads
+    const auto slot = [&](int i) { return i == 0 ? 2 * cut.first + 1 : 2 * (cut.first + i); };
     float2 ml = make_float2(-INFINITY, 0.f);
     if (tid < n) ml = a.part_ml[slot(tid) * a.group + query];
     float top = ml.x;
@@ -710,6 +890,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
     if (tid % 32 == 0) tops[tid / 32] = top;
     __syncthreads();
+#pragma unroll
     for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, tops[i]);
     const float w = tid < n ? fast_exp2(ml.x - (top == -INFINITY ? 0.f : top)) : 0.f;
     weight[tid] = w;
@@ -719,6 +900,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (tid % 32 == 0) sums[tid / 32] = sum;
     __syncthreads();
     sum = 0.f;
+#pragma unroll
     for (int i = 0; i < kJoinThreads / 32; ++i) sum += sums[i];
     const int dim = tid % kD;
     float x = 0.f;
@@ -736,20 +918,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 static_assert(kMaxPackedCtas <= kJoinThreads, "a thread per partial");
 
+// CTAs a row of the short form, 0: the line.
+int row_ctas(const PackedArgs& a, int warps, int num_sms) {
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.hkv;
+    const int64_t pages = (a.selected ? a.k_cap : a.max_pages) + static_cast<int64_t>(a.max_recent);
+    int n = 1;
+    while (n < kMaxCluster && rows * n * 2 <= num_sms && static_cast<int64_t>(n) * warps * 2 <= pages) n *= 2;
+    // pages a warp of the short form goes through, over all waves, against the line's
+    const int64_t waves = (rows * n + num_sms - 1) / num_sms;
+    const int64_t mine = waves * ((pages + n * warps - 1) / (n * warps));
+    const int64_t line = (rows * pages + num_sms * warps - 1) / (num_sms * warps);
+    return mine <= line + 8 ? n : 0;
+}
+
 template <int kKind, bool kSplit>
 cudaError_t launch_t(const PackedArgs& a, int num_sms, cudaStream_t stream) {
     using S = Shape<kKind>;
-    constexpr int kSmem = S::kWarps * (S::kDepth * kUnitBytes + kPartBytes<S::kRows>);
-    cudaError_t e = ensure_kernel_attrs<attend_kernel<kKind, kSplit>>(kSmem);
+    constexpr int kSmem = S::kWarps * S::kDepth * kUnitBytes;
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.hkv;
+    if (const int n = row_ctas(a, S::kWarps, num_sms)) {
+        const cudaError_t e = ensure_kernel_attrs<row_kernel<kKind, kSplit>>(kSmem);
+        return e != cudaSuccess ? e : launch_dependent(row_kernel<kKind, kSplit>, rows * n, S::kThreads, kSmem, stream, n, a, n);
+    }
+    cudaError_t e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
     if (e != cudaSuccess) return e;
-    // no more CTAs than the longest lists have steps for
-    const int64_t steps = static_cast<int64_t>(a.batch) * a.hkv *
-                          ((a.selected ? a.k_cap : a.max_pages) + static_cast<int64_t>(kRecentSteps) * a.max_recent);
-    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(std::min(num_sms * S::kCtas, kMaxPackedCtas),
-                                                                (steps + S::kWarps - 1) / S::kWarps));
-    e = launch_dependent(attend_kernel<kKind, kSplit>, ctas, S::kWarps * 32, kSmem, stream, 1, a);
+    const int ctas = std::min(num_sms, kMaxPackedCtas);
+    e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(join_kernel, ctas * a.group, kJoinThreads, 0, stream, 1, a);
+    return launch_dependent(join_kernel, std::min<int64_t>(rows, ctas) * a.group, kJoinThreads, 0, stream, 1, a);
 }
 
 }  // namespace

@@ -40,21 +40,23 @@ struct PackedArgs {
     float* lse;                    // nullable
     int q_type, k_cap, max_recent, batch, hq, hkv, group, max_pages, num_packed, num_cache;
     // workspace regions (packed_layout)
-    struct PackedCut* cuts;        // [kMaxPackedCtas]
+    struct PackedCut* cuts;        // [kMaxPackedCtas]: of each row, or where there are more rows of each CTA
     float2* part_ml;               // [2 * kMaxPackedCtas][group] (max, sum)
     float* part_o;                 // [2 * kMaxPackedCtas][group][128]
     DeviceStatus st;
 };
-// A row (sequence, kv head) that goes on past the end of the CTA it begins in: the row, and
-// the last CTA that has steps of it.
+// A row (sequence, kv head) that lies in several CTAs of the line, with the first and last of them.
 struct PackedCut {
-    int32_t row, last;             // row -1: none
+    int32_t row, first, last;      // row -1: none
 };
 constexpr int kMaxPackedCtas = 512;
 struct PackedLayout {
     size_t ml, o, bytes;           // offsets from the workspace (cuts at 256)
 };
 PackedLayout packed_layout(int group);
+__host__ __device__ inline bool cuts_by_row(const PackedArgs& a, int ctas) {
+    return static_cast<int64_t>(a.batch) * a.hkv <= ctas;
+}
 cudaError_t launch_packed_attention(const PackedArgs& a, int num_sms, cudaStream_t stream);
 
 struct CopyArgs {
