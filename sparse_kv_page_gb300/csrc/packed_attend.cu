@@ -14,13 +14,13 @@
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
 // O^T = V^T P^T: few queries read a page, so HBM bounds the call as long as a page costs a warp
 // few instructions. The codes lie in the pages in the order of the A fragments, so that a lane
-// loads its fragments with four 16-byte loads, and a pair of codes becomes a pair of bf16
-// values by one AND: a 4-bit field in the low byte of a bf16 is the subnormal (or first
-// normal) number field * 2^-133, exactly. Fields 4 bits further up count 16 times as much; the
-// queries' side is divided by 16 there, for values the output. What is left of 2^-133 after
-// the scaling of queries and weights by powers of two goes into the final factors. A token's
-// scales multiply the group's sums (keys) or the weights (values); zeros enter through a
-// product of their own with the queries' sums (keys) and through a sum per group (values).
+// loads its fragments with four 16-byte loads, and a pair of codes becomes a pair of fp16
+// values by one AND: a 4-bit field in the low bits of an fp16 is the subnormal number field *
+// 2^-24, exactly. Fields 4 bits further up count 16 times as much; the queries' side is divided
+// by 16 there, for values the output. Queries and weights are scaled by powers of two into fp16's
+// range. A token's scales multiply the group's sums (keys) or the weights (values); zeros enter
+// through a product of their own with the queries' sums (keys) and through a sum per group
+// (values).
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -31,19 +31,21 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRecentSteps = 3;                       // 8 KB against 2.4
 constexpr float kScaleLog2 = kInvSqrtD * kLog2e;
-// Queries are scaled by 2^(100 - e), e the exponent of the row's largest (within -20..60, so that
-// the factor is a number); scores are then in units of 2^(e - 33). Recent keys are scaled by 2^-60,
-// so that neither they nor their products leave fp32's range.
-constexpr float kQueryShift = 0x1p100f, kRecentScore = 0x1p-73f;
-// Weights carry 2^40, so that their products with codes stay normal numbers.
-constexpr float kWeightBits = 40.f;
-constexpr float kSumUnit = 0x1p-40f, kOutUnit = 0x1p93f, kRecentWeight = 0x1p-133f;
-constexpr float kCodeUnit = 0x1p-133f, kMiddle = 7.5f;
+// Queries are scaled by 2^(14 - e), e the exponent of the row's largest (within -100..100, so that
+// the factors are numbers); with codes of 2^-24 scores are in units of 2^(e + 10).
+constexpr float kQueryTop = 0x1p14f, kScoreUnit = 0x1p10f * kScaleLog2;
+constexpr float kCode = 0x1p-24f, kMiddle = 7.5f;
 constexpr int kCentre = 8;                            // pairs of pages, a power of two
 constexpr float kSlack = 8.f;                         // log2 that a score may pass the maximum by
+// Weights times a value's scale are fp16 (11 bits, rounded: 2^-11 of a weight at most, up or down;
+// the output has 8). A factor, a power of two, brings the largest scale so far to 2^5..2^6, and is
+// set anew when a scale times it passes 2^7: with kSlack weights stay below 2^15.
+constexpr int kScaleTop = 5;
+constexpr float kScaleLimit = 0x1p7f;
 
 // Variants: queries of a group in one block of 8 columns together with their low parts (kPair,
-// groups up to 4), in one block, or in two. 16 warps of 128 registers, or 12 of 168 for the
+// groups up to 4; bf16 queries have none and fill those columns with copies), in one block, or in
+// two. 16 warps of 128 registers, or 12 of 168 for the
 // accumulators of two blocks; kDepth pages of each warp are in shared memory or on their way.
 template <int kKind>
 struct Shape {
@@ -84,6 +86,11 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 f16x2_of(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 // Two floats in one instruction.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float a, float b) {
@@ -93,11 +100,6 @@ __device__ __forceinline__ Two two(float a, float b) {
 }
 __device__ __forceinline__ void parts_of(Two x, float& a, float& b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    Two d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 __device__ __forceinline__ Two mul2(Two a, Two b) {
     Two d;
@@ -110,9 +112,16 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
     return d;
 }
 // D = A B (no accumulator read).
-__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -164,7 +173,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
     return static_cast<int>(((step + 1) * n - 1) / total);
 }
 
-// One block of a row's queries as B fragments, in bf16 parts, by one warp.
+// One block of a row's queries as B fragments, in fp16 parts (fp32 queries keep 22 bits), by one warp.
 template <int kKind, bool kSplit>
 __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int block, Control<kKind>& ctl) {
     using S = Shape<kKind>;
@@ -190,8 +199,8 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
         }
     big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
     big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
-    const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -20), 60);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kQueryShift;
+    const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kQueryTop;
     float sum[4];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -201,15 +210,17 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
         for (int c = 0; c < 2; ++c) {
             const float by = c == 0 ? up : up * 0.0625f;          // fields 4 bits up count 16 times
             const float y0 = x[k][c].x * by, y1 = x[k][c].y * by;
-            hi[c] = pack_bf16x2(y0, y1);
+            hi[c] = pack_f16x2(y0, y1);
+            const float2 x0 = f16x2_of(hi[c]);
             if (kSplit) {
-                lo[c] = pack_bf16x2(y0 - low_of(hi[c]), y1 - high_of(hi[c]));
+                lo[c] = pack_f16x2(y0 - x0.x, y1 - x0.y);
                 if (S::kPair) {                                   // columns 4..7 are the low parts
                     if (gid >= 4) hi[c] = lo[c];
                     lo[c] = 0u;
                 }
             }
-            const float part = low_of(hi[c]) + high_of(hi[c]) + (low_of(lo[c]) + high_of(lo[c]));
+            const float2 x1 = f16x2_of(hi[c]), x2 = f16x2_of(lo[c]);
+            const float part = x1.x + x1.y + (x2.x + x2.y);
             sum[k / 2] += c == 0 ? part : part * 16.f;
         }
         ctl.frag[block][k][lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
@@ -218,8 +229,7 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
     for (int g = 0; g < 4; ++g) {
         sum[g] += __shfl_xor_sync(kAll, sum[g], 1);
         sum[g] += __shfl_xor_sync(kAll, sum[g], 2);
-        sum[g] *= 0x1p-66f;                           // by 2^-133, as the codes are
-        sum[g] *= 0x1p-67f;
+        sum[g] *= kCode;
     }
     // rows k = 0..3 of the fragment: the groups' sums to 8 bits; 4..7: the next 8; 8..11
     float s0 = tig & 1 ? sum[2] : sum[0], s1 = tig & 1 ? sum[3] : sum[1];
@@ -230,7 +240,7 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
     const uint32_t w2 = pack_bf16x2(s0, s1);
     ctl.sums[block][lane] = make_uint2(tig < 2 ? w0 : w1, tig < 2 ? w2 : 0u);
     if (tig == 0)
-        ctl.unit[block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (0x1p33f * kScaleLog2);
+        ctl.unit[block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kScoreUnit;
 }
 
 // A warp's running softmax over a part of a row: columns 2 * tig + c of each block.
@@ -239,12 +249,13 @@ struct Running {
     using S = Shape<kKind>;
     static constexpr int kBlocks = S::kBlocks;
     static constexpr bool kLow = kSplit && !S::kPair; // low parts as fragments of their own
-    float o[kBlocks][8][4];                           // O^T of 16 dims each, in units of 2^-93 (dims + 8: 2^-89)
+    float o[kBlocks][8][4];                           // O^T of 16 dims each, times factor * 2^-24 (dims + 8: 2^-20)
     float m[kBlocks][2];                              // maximum, log2
-    float unit[kBlocks][2];
-    Two l[kBlocks];                                   // this lane's part of the sum, times 2^40
-    Two z[kBlocks][2];                                // [group]: of weights times zeros
-    Two pw[kBlocks][2];                               // [group]: of weights times scales, since the last centre()
+    Two unit[kBlocks];
+    Two l[kBlocks];                                   // this lane's part of the sum
+    float z[kBlocks][2][2];                           // [group]: of weights times zeros
+    Two pw[kBlocks][2];                               // [group]: of weights times scales and factor, since the last centre()
+    float factor, scale_limit;                        // of the scales of values; the largest that it is good for
 
     __device__ __forceinline__ void clear(const Control<kKind>& ctl) {
         const int tig = threadIdx.x & 3;
@@ -253,31 +264,45 @@ struct Running {
 #pragma unroll
             for (int d = 0; d < 8; ++d) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, unit[n][c] = ctl.unit[n * 8 + 2 * tig + c];
-            l[n] = z[n][0] = z[n][1] = pw[n][0] = pw[n][1] = two(0.f, 0.f);
+            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, z[n][0][c] = z[n][1][c] = 0.f;
+            unit[n] = two(ctl.unit[n * 8 + 2 * tig], ctl.unit[n * 8 + 2 * tig + 1]);
+            l[n] = pw[n][0] = pw[n][1] = two(0.f, 0.f);
         }
+        factor = 1.f;
+        scale_limit = 0.f;
     }
 
-    // Scores (tokens gid, gid + 8 of kPages pages) to weights times 2^40. The maximum moves only
-    // when a score passes it by more than kSlack: weights and sums are floating-point numbers, so
-    // the slack costs no bits, and most pages pass with one vote.
+    // Scores (tokens gid, gid + 8 of kPages pages) to weights. The maximum moves only when a score
+    // passes it by more than kSlack, the factor when a scale (`scale`: this lane's largest) passes its
+    // limit: weights and sums are floating-point numbers, so the slack costs no bits, and most pages
+    // pass with one vote.
     template <int kPages>
-    __device__ __forceinline__ void weigh(float (&s)[kPages][kBlocks][4]) {
-        bool over = false;
+    __device__ __forceinline__ void weigh(float (&s)[kPages][kBlocks][4], float scale) {
+        bool over = scale > scale_limit;
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
             const float limit0 = m[n][0] + kSlack, limit1 = m[n][1] + kSlack;
             float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
             for (int p = 0; p < kPages; ++p) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[p][n][i] *= unit[n][i & 1];
+                parts_of(mul2(two(s[p][n][0], s[p][n][1]), unit[n]), s[p][n][0], s[p][n][1]);
+                parts_of(mul2(two(s[p][n][2], s[p][n][3]), unit[n]), s[p][n][2], s[p][n][3]);
                 top0 = fmaxf(top0, fmaxf(s[p][n][0], s[p][n][2]));
                 top1 = fmaxf(top1, fmaxf(s[p][n][1], s[p][n][3]));
             }
             over |= top0 > limit0 || top1 > limit1;
         }
         if (__any_sync(kAll, over)) {
+            float change = 1.f;
+#pragma unroll
+            for (int x = 1; x < 32; x *= 2) scale = fmaxf(scale, __shfl_xor_sync(kAll, scale, x));
+            if (scale > scale_limit) {                // 2^(kScaleTop - exponent), within 2^-100..2^100
+                const int e = min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, -95), 105);
+                const float next = __uint_as_float(static_cast<uint32_t>(127 + kScaleTop - e) << 23);
+                change = scale_limit == 0.f ? 0.f : next / factor;     // nothing to change yet
+                factor = next;
+                scale_limit = kScaleLimit / next;
+            }
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
                 float f[2];
@@ -290,50 +315,30 @@ struct Running {
                     for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
                     f[c] = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top);
                     m[n][c] = top;
+                    z[n][0][c] *= f[c];
+                    z[n][1][c] *= f[c];
                 }
+                l[n] = mul2(l[n], two(f[0], f[1]));
+                f[0] *= change, f[1] *= change;
                 const Two f2 = two(f[0], f[1]);
-                l[n] = mul2(l[n], f2);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) z[n][g] = mul2(z[n][g], f2), pw[n][g] = mul2(pw[n][g], f2);
+                pw[n][0] = mul2(pw[n][0], f2), pw[n][1] = mul2(pw[n][1], f2);
 #pragma unroll
                 for (int d = 0; d < 8; ++d) o[n][d][0] *= f[0], o[n][d][1] *= f[1], o[n][d][2] *= f[0], o[n][d][3] *= f[1];
             }
         }
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-            const float base0 = m[n][0] == -INFINITY ? kWeightBits : kWeightBits - m[n][0];
-            const float base1 = m[n][1] == -INFINITY ? kWeightBits : kWeightBits - m[n][1];
+            const Two base = two(m[n][0] == -INFINITY ? 0.f : -m[n][0], m[n][1] == -INFINITY ? 0.f : -m[n][1]);
 #pragma unroll
             for (int p = 0; p < kPages; ++p) {
-                s[p][n][0] = fast_exp2(s[p][n][0] + base0);
-                s[p][n][1] = fast_exp2(s[p][n][1] + base1);
-                s[p][n][2] = fast_exp2(s[p][n][2] + base0);
-                s[p][n][3] = fast_exp2(s[p][n][3] + base1);
-                l[n] = add2(l[n], add2(two(s[p][n][0], s[p][n][1]), two(s[p][n][2], s[p][n][3])));
-            }
-        }
-    }
-
-    // Weights as B fragments, tokens as rows: a high and a low part, in columns of their own
-    // (kPair) or apart. The high part is cut off, the low part rounded: half a step of it is 2^-15
-    // of a weight, up or down.
-    __device__ __forceinline__ static void split(const float (&p)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-        const uint32_t sign = threadIdx.x & 2 ? 0x80000000u : 0u;
-        const float low = threadIdx.x & 2 ? 1.f : 0.f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t a = __float_as_uint(p[2 * t]), b = __float_as_uint(p[2 * t + 1]);
-            if (S::kPair) {
-                // the cut-off weight, or the weight less it
-                const Two x = fma2(two(low, low), two(p[2 * t], p[2 * t + 1]),
-                                   two(__uint_as_float((a & 0xffff0000u) ^ sign), __uint_as_float((b & 0xffff0000u) ^ sign)));
-                float x0, x1;
-                parts_of(x, x0, x1);
-                hi[t] = movmatrix_trans(pack_bf16x2(x0, x1));
-            } else {
-                const uint32_t w = prmt(a, b, 0x7632u);
-                hi[t] = movmatrix_trans(w);
-                lo[t] = movmatrix_trans(pack_bf16x2(p[2 * t] - low_of(w), p[2 * t + 1] - high_of(w)));
+                for (int t = 0; t < 4; t += 2) {
+                    float x, y;
+                    parts_of(add2(two(s[p][n][t], s[p][n][t + 1]), base), x, y);
+                    s[p][n][t] = fast_exp2(x);
+                    s[p][n][t + 1] = fast_exp2(y);
+                    l[n] = add2(l[n], two(s[p][n][t], s[p][n][t + 1]));
+                }
             }
         }
     }
@@ -360,7 +365,7 @@ struct Running {
 #pragma unroll
                 for (int n = 0; n < kBlocks; ++n) {
                     const uint2 q = ctl.sums[n][lane];
-                    mma_first(s[p][n], zeros, q.x, q.y);
+                    mma_bf16_first(s[p][n], zeros, q.x, q.y);
                 }
             }
 #pragma unroll
@@ -387,12 +392,12 @@ struct Running {
                         }
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            if (i == 0) mma_first(acc[p][n], f[p], q.x, q.y);
-                            else mma_bf16_16816(acc[p][n], f[p], q.x, q.y);
+                            if (i == 0) mma_f16_first(acc[p][n], f[p], q.x, q.y);
+                            else mma_f16_16816(acc[p][n], f[p], q.x, q.y);
                         }
 #pragma unroll
                         for (int p = 0; p < 2; ++p)
-                            if (kLow) mma_bf16_16816(acc[p][n], f[p], q.z, q.w);
+                            if (kLow) mma_f16_16816(acc[p][n], f[p], q.z, q.w);
                     }
                 }
 #pragma unroll
@@ -403,9 +408,8 @@ struct Running {
                         const float a = g & 1 ? high_of(x) : low_of(x);
 #pragma unroll
                         for (int n = 0; n < kBlocks; ++n) {
-                            const Two y = fma2(two(a, a), two(acc[p][n][2 * t], acc[p][n][2 * t + 1]),
-                                               two(s[p][n][2 * t], s[p][n][2 * t + 1]));
-                            parts_of(y, s[p][n][2 * t], s[p][n][2 * t + 1]);
+                            s[p][n][2 * t] = fmaf(a, acc[p][n][2 * t], s[p][n][2 * t]);
+                            s[p][n][2 * t + 1] = fmaf(a, acc[p][n][2 * t + 1], s[p][n][2 * t + 1]);
                         }
                     }
             }
@@ -415,40 +419,43 @@ struct Running {
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) s[1][n][0] = s[1][n][1] = s[1][n][2] = s[1][n][3] = -INFINITY;
         }
-        weigh<2>(s);
+        uint2 t[2][2];                                // scales and zeros of the values of tokens gid, gid + 8
+        float scale = 0.f;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                t[p][i] = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8 * i));
+                scale = fmaxf(scale, fmaxf(low_of(t[p][i].x), high_of(t[p][i].x)));
+            }
+        weigh<2>(s, scale);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const uint4 v0 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 16 * lane);
             const uint4 v1 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 512 + 16 * lane);
-            const uint2 t0 = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * gid);
-            const uint2 t1 = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8));
             const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int g = 0; g < 2; ++g) {             // 64 dims
-                const float a0 = g ? high_of(t0.x) : low_of(t0.x), a1 = g ? high_of(t1.x) : low_of(t1.x);
-                const float z0 = g ? high_of(t0.y) : low_of(t0.y), z1 = g ? high_of(t1.y) : low_of(t1.y);
-                uint32_t hi[kBlocks][2], lo[kBlocks][2];
+                const float a0 = (g ? high_of(t[p][0].x) : low_of(t[p][0].x)) * factor;
+                const float a1 = (g ? high_of(t[p][1].x) : low_of(t[p][1].x)) * factor;
+                const float z0 = g ? high_of(t[p][0].y) : low_of(t[p][0].y), z1 = g ? high_of(t[p][1].y) : low_of(t[p][1].y);
+                uint32_t f[kBlocks][2];
 #pragma unroll
                 for (int n = 0; n < kBlocks; ++n) {
-                    const Two s0 = two(s[p][n][0], s[p][n][1]), s1 = two(s[p][n][2], s[p][n][3]);
-                    const Two p0 = mul2(s0, two(a0, a0)), p1 = mul2(s1, two(a1, a1));
-                    z[n][g] = fma2(s0, two(z0, z0), fma2(s1, two(z1, z1), z[n][g]));
-                    pw[n][g] = add2(pw[n][g], add2(p0, p1));
-                    float x[4];
-                    parts_of(p0, x[0], x[1]);
-                    parts_of(p1, x[2], x[3]);
-                    split(x, hi[n], lo[n]);
+                    const float x0 = s[p][n][0] * a0, x1 = s[p][n][1] * a0, x2 = s[p][n][2] * a1, x3 = s[p][n][3] * a1;
+                    z[n][g][0] = fmaf(s[p][n][0], z0, fmaf(s[p][n][2], z1, z[n][g][0]));
+                    z[n][g][1] = fmaf(s[p][n][1], z0, fmaf(s[p][n][3], z1, z[n][g][1]));
+                    pw[n][g] = add2(pw[n][g], add2(two(x0, x1), two(x2, x3)));
+                    f[n][0] = movmatrix_trans(pack_f16x2(x0, x1));       // tokens as rows
+                    f[n][1] = movmatrix_trans(pack_f16x2(x2, x3));
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int d = 4 * g + i;
                     const uint32_t up = w[d] >> 8;
-                    const uint32_t f[4] = {w[d] & 0x000f000fu, w[d] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+                    const uint32_t c[4] = {w[d] & 0x000f000fu, w[d] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
 #pragma unroll
-                    for (int n = 0; n < kBlocks; ++n) {
-                        mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
-                        if (!S::kPair) mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
-                    }
+                    for (int n = 0; n < kBlocks; ++n) mma_f16_16816(o[n][d], c, f[n][0], f[n][1]);
                 }
             }
         }
@@ -463,16 +470,16 @@ struct Running {
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const Two y = mul2(pw[n][g], two(kMiddle, kMiddle));
-                z[n][g] = add2(z[n][g], y);
-                pw[n][g] = two(0.f, 0.f);
                 float x[2];
-                parts_of(y, x[0], x[1]);
+                parts_of(pw[n][g], x[0], x[1]);
+                pw[n][g] = two(0.f, 0.f);
+                const float back = kMiddle / factor;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    z[n][g][c] = fmaf(x[c], back, z[n][g][c]);
 #pragma unroll
                     for (int i = 4; i < 32; i *= 2) x[c] += __shfl_xor_sync(kAll, x[c], i);
-                    x[c] *= S::kPair && (threadIdx.x & 2) ? 0.f : -kCodeUnit;    // not from the low parts' columns
+                    x[c] *= -kMiddle * kCode;
 #pragma unroll
                     for (int d = 4 * g; d < 4 * g + 4; ++d) {
                         o[n][d][c] += x[c];
@@ -483,44 +490,51 @@ struct Running {
     }
 
     // A bf16 page in shared memory, K and then V, rows of 256 bytes swizzled by 16-byte chunks
-    // (chunk_offset), zero from row `valid` on.
+    // (chunk_offset), zero from row `valid` on. Queries and weights meet it as two bf16 parts each.
     __device__ __forceinline__ void recent_page(const uint8_t* page, int valid, const Control<kKind>& ctl) {
         const int lane = threadIdx.x & 31, gid = lane >> 2;
-        const uint32_t down = 0x21802180u, down16 = 0x23802380u;         // 2^-60, 2^-56: exponents 67, 71
         float s[1][kBlocks][4];
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) s[0][n][0] = s[0][n][1] = s[0][n][2] = s[0][n][3] = 0.f;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
             uint32_t f[4];
             ldmatrix_x4(f, page + chunk_offset(lane & 15, 2 * k + (lane >> 4)));
-            f[0] = bf16x2_mul(f[0], down), f[1] = bf16x2_mul(f[1], down);
-            f[2] = bf16x2_mul(f[2], down16), f[3] = bf16x2_mul(f[3], down16);
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
                 const uint4 q = ctl.frag[n][k][lane];
-                mma_bf16_16816(s[0][n], f, q.x, q.y);
-                if (kLow) mma_bf16_16816(s[0][n], f, q.z, q.w);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float2 x = f16x2_of(c ? q.y : q.x), y = f16x2_of(c ? q.w : q.z);
+                    split(x.x + y.x, x.y + y.y, hi[c], lo[c]);
+                    if (c) hi[c] = bf16x2_mul(hi[c], 0x41804180u), lo[c] = bf16x2_mul(lo[c], 0x41804180u);      // 16
+                }
+                mma_bf16_16816(s[0][n], f, hi[0], hi[1]);
+                mma_bf16_16816(s[0][n], f, lo[0], lo[1]);
             }
         }
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[0][n][i] *= kRecentScore;
+            for (int i = 0; i < 4; ++i) s[0][n][i] *= kCode;
         add_low<1>(s);
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (gid + 8 * (i >> 1) >= valid) s[0][n][i] = -INFINITY;
-        weigh<1>(s);
+        weigh<1>(s, 0.f);
         uint32_t hi[kBlocks][2], lo[kBlocks][2];
+        const float unit_of_o = factor * kCode;
 #pragma unroll
-        for (int n = 0; n < kBlocks; ++n) {
+        for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[0][n][i] *= kRecentWeight;
-            split(s[0][n], hi[n], lo[n]);
-        }
+            for (int t = 0; t < 2; ++t) {
+                split(s[0][n][2 * t] * unit_of_o, s[0][n][2 * t + 1] * unit_of_o, hi[n][t], lo[n][t]);
+                hi[n][t] = movmatrix_trans(hi[n][t]);
+                lo[n][t] = movmatrix_trans(lo[n][t]);
+            }
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
             // rows of the fragment are dims: a0 (dims, tokens), a1 (dims + 8, tokens), a2 (dims, tokens + 8), a3
@@ -531,9 +545,14 @@ struct Running {
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
                 mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
-                if (!S::kPair) mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
+                mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
             }
         }
+    }
+    // x and y as a pair of bf16 high parts and one of low parts.
+    __device__ __forceinline__ static void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+        hi = pack_bf16x2(x, y);
+        lo = pack_bf16x2(x - low_of(hi), y - high_of(hi));
     }
 
     // Low parts of the queries in columns of their own (bf16 queries fill those with copies).
@@ -553,30 +572,24 @@ struct Running {
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-            float sum[2], zero[2][2];
+            float sum[2];
             parts_of(l[n], sum[0], sum[1]);
-            parts_of(z[n][0], zero[0][0], zero[0][1]);
-            parts_of(z[n][1], zero[1][0], zero[1][1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) {
                     sum[c] += __shfl_xor_sync(kAll, sum[c], x);
-                    zero[0][c] += __shfl_xor_sync(kAll, zero[0][c], x);
-                    zero[1][c] += __shfl_xor_sync(kAll, zero[1][c], x);
+                    z[n][0][c] += __shfl_xor_sync(kAll, z[n][0][c], x);
+                    z[n][1][c] += __shfl_xor_sync(kAll, z[n][1][c], x);
                 }
-                const int query = S::kPair ? 2 * (tig & 1) + c : n * 8 + 2 * tig + c;
-                const bool on = query < group && !(S::kPair && tig >= 2);
-                if (on && gid == 0) ms[query] = m[n][c], ls[query] = sum[c] * kSumUnit;
+                const int query = n * 8 + 2 * tig + c;
+                if (query >= group) continue;         // kPair: the second four columns too
+                if (gid == 0) ms[query] = m[n][c], ls[query] = sum[c];
+                const float back = 1.f / (factor * kCode);
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
-                    float x0 = o[n][d][c], x1 = o[n][d][c + 2];
-                    if (S::kPair) x0 += __shfl_xor_sync(kAll, x0, 2), x1 += __shfl_xor_sync(kAll, x1, 2);
-                    const float y = zero[d / 4][c] * kSumUnit;
-                    if (on) {
-                        part[query * kPartStride + d * 16 + gid] = fmaf(x0, kOutUnit, y);
-                        part[query * kPartStride + d * 16 + gid + 8] = fmaf(x1, kOutUnit * 0.0625f, y);
-                    }
+                    part[query * kPartStride + d * 16 + gid] = fmaf(o[n][d][c], back, z[n][d / 4][c]);
+                    part[query * kPartStride + d * 16 + gid + 8] = fmaf(o[n][d][c + 2], back * 0.0625f, z[n][d / 4][c]);
                 }
             }
         }
