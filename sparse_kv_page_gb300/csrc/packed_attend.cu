@@ -1,15 +1,16 @@
 // packed_attend.cu - decode attention over packed pages (locks_packed_attention).
 //
-// A CTA takes a part of a row (a sequence and a kv head), its warps every kWarps-th page of it
-// each, two pages at a time with an online softmax; the warps' partials meet in shared memory.
-// Two forms cut the rows into parts:
+// A CTA takes a part of a row (a sequence and a kv head), or of two neighbouring rows, its warps an
+// equal share each, two pages at a time with an online softmax; the warps' partials meet in shared
+// memory. Two forms cut the rows into parts:
 //
 // 1. Short rows: a cluster of 1 to 8 CTAs a row, joined through distributed shared memory, in one
 //    launch. Latency bounds it.
 // 2. Long rows: all steps of the call, a page of a kv head each (a recent bf16 page counts
 //    kRecentSteps), lie on one line, row after row, that is cut evenly into as many CTAs as there
-//    are SMs, whatever the lengths of the rows. A row that goes past a CTA is joined by a second
-//    kernel from partials in the workspace.
+//    are SMs, whatever the lengths of the rows. A CTA goes through its piece two rows at a time, so
+//    that where rows are long its warps meet once, at the end. A row that goes past a CTA is joined
+//    by a second kernel from partials in the workspace.
 //
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
 // O^T = V^T P^T: few queries read a page, so HBM bounds the call as long as a page costs a warp
@@ -38,8 +39,8 @@ constexpr float kCode = 0x1p-24f, kMiddle = 7.5f;
 constexpr int kCentre = 8;                            // pairs of pages, a power of two
 constexpr float kSlack = 8.f;                         // log2 that a score may pass the maximum by
 // Weights times a value's scale are fp16 (11 bits, rounded: 2^-11 of a weight at most, up or down;
-// the output has 8). A factor, a power of two, brings the largest scale so far to 2^5..2^6, and is
-// set anew when a scale times it passes 2^7: with kSlack weights stay below 2^15.
+// the output has 8). All weights carry a factor 2^lift that brings the largest scale so far to
+// 2^5..2^6, and is set anew when a scale times it passes 2^7: with kSlack they stay below 2^15.
 constexpr int kScaleTop = 5;
 constexpr float kScaleLimit = 0x1p7f;
 
@@ -61,13 +62,22 @@ constexpr int kPartStride = kD + 4;                   // floats: columns' stores
 template <int kKind>
 struct Control {
     using S = Shape<kKind>;
-    uint4 frag[S::kBlocks][8][32];                    // B fragments of the queries: high parts, low parts
-    uint2 sums[S::kBlocks][32];                       // ... of the groups' sums
-    float unit[S::kBlocks * 8];                       // a score's unit, by column
-    float m[S::kWarps][S::kRows], l[S::kWarps][S::kRows];
-    float cta_m[S::kRows], cta_l[S::kRows], cta_o[S::kRows][kD];
-    int64_t upto[S::kThreads];                        // steps of the sequences up to each thread's last
-    int64_t warp_sum[S::kWarps];
+    uint4 frag[2][S::kBlocks][8][32];                 // of both rows: B fragments of the queries: high parts, low parts
+    uint2 sums[2][S::kBlocks][32];                    // ... of the groups' sums
+    float unit[2][S::kBlocks * 8];                    // a score's unit, by column
+    // the warps' partials: which rows a warp had some of (bits), m and l; its output lies in its
+    // slots, or for the warp that had both rows that of the first in `both`
+    int32_t had[S::kWarps];
+    float m[2][S::kWarps][S::kRows], l[2][S::kWarps][S::kRows];
+    float both[S::kRows * kPartStride];
+    union {
+        struct {                                      // short rows: the CTA's partial
+            float m[S::kRows], l[S::kRows], o[S::kRows][kD];
+        } cta;
+        struct {                                      // long rows: steps of the sequences up to each thread's last
+            int64_t upto[S::kThreads], warp_sum[S::kWarps];
+        } line;
+    };
 };
 
 // 16 bytes, or zeros that read nothing.
@@ -84,6 +94,11 @@ __device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -106,25 +121,38 @@ __device__ __forceinline__ Two mul2(Two a, Two b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 __device__ __forceinline__ Two add2(Two a, Two b) {
     Two d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// D = A B (no accumulator read).
-__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+// D = A B + D and D = A B on mma.sync m16n8k16. Not volatile, as nothing but the operands counts:
+// the compiler may move products past one another, which saves it register copies.
+#define LOCKS_MMA(name, type)                                                                                        \
+    __device__ __forceinline__ void name(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {          \
+        asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "    \
+            "{%0,%1,%2,%3};"                                                                                         \
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                         \
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));                                         \
+    }                                                                                                                \
+    __device__ __forceinline__ void name##_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  \
+        asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "    \
+            "{%10,%10,%10,%10};"                                                                                     \
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                         \
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));                               \
+    }
+LOCKS_MMA(mma_f16, "f16")
+LOCKS_MMA(mma_bf16, "bf16")
+#undef LOCKS_MMA
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {          // of 8 x 8 16-bit elements
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 struct Len {
@@ -175,7 +203,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
 
 // One block of a row's queries as B fragments, in fp16 parts (fp32 queries keep 22 bits), by one warp.
 template <int kKind, bool kSplit>
-__device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int block, Control<kKind>& ctl) {
+__device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int which, int block, Control<kKind>& ctl) {
     using S = Shape<kKind>;
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     const int query = S::kPair ? gid & 3 : block * 8 + gid;
@@ -223,7 +251,7 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
             const float part = x1.x + x1.y + (x2.x + x2.y);
             sum[k / 2] += c == 0 ? part : part * 16.f;
         }
-        ctl.frag[block][k][lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+        ctl.frag[which][block][k][lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -238,9 +266,9 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
     const uint32_t w1 = pack_bf16x2(s0, s1);
     s0 -= low_of(w1), s1 -= high_of(w1);
     const uint32_t w2 = pack_bf16x2(s0, s1);
-    ctl.sums[block][lane] = make_uint2(tig < 2 ? w0 : w1, tig < 2 ? w2 : 0u);
+    ctl.sums[which][block][lane] = make_uint2(tig < 2 ? w0 : w1, tig < 2 ? w2 : 0u);
     if (tig == 0)
-        ctl.unit[block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kScoreUnit;
+        ctl.unit[which][block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kScoreUnit;
 }
 
 // A warp's running softmax over a part of a row: columns 2 * tig + c of each block.
@@ -249,27 +277,26 @@ struct Running {
     using S = Shape<kKind>;
     static constexpr int kBlocks = S::kBlocks;
     static constexpr bool kLow = kSplit && !S::kPair; // low parts as fragments of their own
-    float o[kBlocks][8][4];                           // O^T of 16 dims each, times factor * 2^-24 (dims + 8: 2^-20)
+    float o[kBlocks][8][4];                           // O^T of 16 dims each, in units of 2^-24 (dims + 8: 2^-20)
     float m[kBlocks][2];                              // maximum, log2
     Two unit[kBlocks];
     Two l[kBlocks];                                   // this lane's part of the sum
-    float z[kBlocks][2][2];                           // [group]: of weights times zeros
-    Two pw[kBlocks][2];                               // [group]: of weights times scales and factor, since the last centre()
-    float factor, scale_limit;                        // of the scales of values; the largest that it is good for
+    Two z[kBlocks][2];                                // [column], of both groups: of weights times zeros
+    Two pw[kBlocks][2];                               // ... of weights times scales, since the last centre()
+    float lift, scale_limit;                          // log2 of the weights' factor; the largest scale that it is good for
 
-    __device__ __forceinline__ void clear(const Control<kKind>& ctl) {
+    __device__ __forceinline__ void clear(const Control<kKind>& ctl, int which) {
         const int tig = threadIdx.x & 3;
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
 #pragma unroll
             for (int d = 0; d < 8; ++d) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, z[n][0][c] = z[n][1][c] = 0.f;
-            unit[n] = two(ctl.unit[n * 8 + 2 * tig], ctl.unit[n * 8 + 2 * tig + 1]);
-            l[n] = pw[n][0] = pw[n][1] = two(0.f, 0.f);
+            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, z[n][c] = pw[n][c] = two(0.f, 0.f);
+            unit[n] = two(ctl.unit[which][n * 8 + 2 * tig], ctl.unit[which][n * 8 + 2 * tig + 1]);
+            l[n] = two(0.f, 0.f);
         }
-        factor = 1.f;
-        scale_limit = 0.f;
+        lift = scale_limit = 0.f;
     }
 
     // Scores (tokens gid, gid + 8 of kPages pages) to weights. The maximum moves only when a score
@@ -293,15 +320,14 @@ struct Running {
             over |= top0 > limit0 || top1 > limit1;
         }
         if (__any_sync(kAll, over)) {
-            float change = 1.f;
+            float change = 0.f;                       // log2
 #pragma unroll
             for (int x = 1; x < 32; x *= 2) scale = fmaxf(scale, __shfl_xor_sync(kAll, scale, x));
-            if (scale > scale_limit) {                // 2^(kScaleTop - exponent), within 2^-100..2^100
-                const int e = min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, -95), 105);
-                const float next = __uint_as_float(static_cast<uint32_t>(127 + kScaleTop - e) << 23);
-                change = scale_limit == 0.f ? 0.f : next / factor;     // nothing to change yet
-                factor = next;
-                scale_limit = kScaleLimit / next;
+            if (scale > scale_limit) {                // kScaleTop - exponent, within -100..100
+                const int e = kScaleTop - min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, -95), 105);
+                change = static_cast<float>(e) - lift;
+                lift += change;
+                scale_limit = kScaleLimit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             }
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
@@ -313,22 +339,20 @@ struct Running {
                     for (int p = 0; p < kPages; ++p) top = fmaxf(top, fmaxf(s[p][n][c], s[p][n][c + 2]));
 #pragma unroll
                     for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
-                    f[c] = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top);
+                    f[c] = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top + change);
                     m[n][c] = top;
-                    z[n][0][c] *= f[c];
-                    z[n][1][c] *= f[c];
+                    const Two both = two(f[c], f[c]);
+                    z[n][c] = mul2(z[n][c], both);
+                    pw[n][c] = mul2(pw[n][c], both);
                 }
                 l[n] = mul2(l[n], two(f[0], f[1]));
-                f[0] *= change, f[1] *= change;
-                const Two f2 = two(f[0], f[1]);
-                pw[n][0] = mul2(pw[n][0], f2), pw[n][1] = mul2(pw[n][1], f2);
 #pragma unroll
                 for (int d = 0; d < 8; ++d) o[n][d][0] *= f[0], o[n][d][1] *= f[1], o[n][d][2] *= f[0], o[n][d][3] *= f[1];
             }
         }
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-            const Two base = two(m[n][0] == -INFINITY ? 0.f : -m[n][0], m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+            const Two base = two(m[n][0] == -INFINITY ? lift : lift - m[n][0], m[n][1] == -INFINITY ? lift : lift - m[n][1]);
 #pragma unroll
             for (int p = 0; p < kPages; ++p) {
 #pragma unroll
@@ -345,73 +369,78 @@ struct Running {
 
     // Two packed pages; the second one's tokens count only if `both` (it is read all the same).
     __device__ __forceinline__ void packed_pages(const uint8_t* unit0, const uint8_t* unit1, bool both,
-                                                 const Control<kKind>& ctl) {
+                                                 const Control<kKind>& ctl, int which) {
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
         const uint8_t* const units[2] = {unit0, unit1};
         float s[2][kBlocks][4];
         {
-            uint32_t w[2][8], scale[2][2][2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const uint4 k0 = *reinterpret_cast<const uint4*>(units[p] + 16 * lane);
-                const uint4 k1 = *reinterpret_cast<const uint4*>(units[p] + 512 + 16 * lane);
-                w[p][0] = k0.x, w[p][1] = k0.y, w[p][2] = k0.z, w[p][3] = k0.w;
-                w[p][4] = k1.x, w[p][5] = k1.y, w[p][6] = k1.z, w[p][7] = k1.w;
-                const uint4 t0 = *reinterpret_cast<const uint4*>(units[p] + kUnitKScales + 16 * gid);
-                const uint4 t1 = *reinterpret_cast<const uint4*>(units[p] + kUnitKScales + 16 * (gid + 8));
-                scale[p][0][0] = t0.x, scale[p][0][1] = t0.y, scale[p][1][0] = t1.x, scale[p][1][1] = t1.y;
-                const uint32_t z0 = tig & 1 ? t0.w : t0.z, z1 = tig & 1 ? t1.w : t1.z;
+                const int at = kUnitKScales + 16 * gid + 8 + 4 * (tig & 1);
+                const uint32_t z0 = *reinterpret_cast<const uint32_t*>(units[p] + at);
+                const uint32_t z1 = *reinterpret_cast<const uint32_t*>(units[p] + at + 128);
                 const uint32_t zeros[4] = {z0, z1, z0, z1};
 #pragma unroll
                 for (int n = 0; n < kBlocks; ++n) {
-                    const uint2 q = ctl.sums[n][lane];
+                    const uint2 q = ctl.sums[which][n][lane];
                     mma_bf16_first(s[p][n], zeros, q.x, q.y);
                 }
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {             // 32 dims
-                float acc[2][kBlocks][4];
+            for (int half = 0; half < 2; ++half) {    // 64 dims
+                uint32_t w[2][4], scale[2][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int k = 2 * g + i;
-                    uint32_t f[2][4];
+                for (int p = 0; p < 2; ++p) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(units[p] + 512 * half + 16 * lane);
+                    w[p][0] = x.x, w[p][1] = x.y, w[p][2] = x.z, w[p][3] = x.w;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint32_t up = w[p][k] >> 8;
-                        f[p][0] = w[p][k] & 0x000f000fu, f[p][1] = up & 0x000f000fu;
-                        f[p][2] = w[p][k] & 0x00f000f0u, f[p][3] = up & 0x00f000f0u;
-                    }
-#pragma unroll
-                    for (int n = 0; n < kBlocks; ++n) {
-                        uint4 q;
-                        if (kLow) {
-                            q = ctl.frag[n][k][lane];
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(&ctl.frag[n][k][lane]);
-                            q = make_uint4(x.x, x.y, 0u, 0u);
-                        }
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            if (i == 0) mma_f16_first(acc[p][n], f[p], q.x, q.y);
-                            else mma_f16_16816(acc[p][n], f[p], q.x, q.y);
-                        }
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-                            if (kLow) mma_f16_16816(acc[p][n], f[p], q.z, q.w);
-                    }
+                    for (int t = 0; t < 2; ++t)
+                        scale[p][t] = *reinterpret_cast<const uint32_t*>(units[p] + kUnitKScales + 16 * (gid + 8 * t) + 4 * half);
                 }
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                for (int g = 0; g < 2; ++g) {         // 32 dims
+                    float acc[2][kBlocks][4];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t x = scale[p][t][g >> 1];
-                        const float a = g & 1 ? high_of(x) : low_of(x);
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = 4 * half + 2 * g + i;
+                        uint32_t f[2][4];
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const uint32_t x = w[p][2 * g + i], up = x >> 8;
+                            f[p][0] = x & 0x000f000fu, f[p][1] = up & 0x000f000fu;
+                            f[p][2] = x & 0x00f000f0u, f[p][3] = up & 0x00f000f0u;
+                        }
 #pragma unroll
                         for (int n = 0; n < kBlocks; ++n) {
-                            s[p][n][2 * t] = fmaf(a, acc[p][n][2 * t], s[p][n][2 * t]);
-                            s[p][n][2 * t + 1] = fmaf(a, acc[p][n][2 * t + 1], s[p][n][2 * t + 1]);
+                            uint4 q;
+                            if (kLow) {
+                                q = ctl.frag[which][n][k][lane];
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2*>(&ctl.frag[which][n][k][lane]);
+                                q = make_uint4(x.x, x.y, 0u, 0u);
+                            }
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                if (i == 0) mma_f16_first(acc[p][n], f[p], q.x, q.y);
+                                else mma_f16(acc[p][n], f[p], q.x, q.y);
+                            }
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+                                if (kLow) mma_f16(acc[p][n], f[p], q.z, q.w);
                         }
                     }
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const float a = g ? high_of(scale[p][t]) : low_of(scale[p][t]);
+#pragma unroll
+                            for (int n = 0; n < kBlocks; ++n) {
+                                s[p][n][2 * t] = fmaf(a, acc[p][n][2 * t], s[p][n][2 * t]);
+                                s[p][n][2 * t + 1] = fmaf(a, acc[p][n][2 * t + 1], s[p][n][2 * t + 1]);
+                            }
+                        }
+                }
             }
         }
         add_low<2>(s);
@@ -420,42 +449,45 @@ struct Running {
             for (int n = 0; n < kBlocks; ++n) s[1][n][0] = s[1][n][1] = s[1][n][2] = s[1][n][3] = -INFINITY;
         }
         uint2 t[2][2];                                // scales and zeros of the values of tokens gid, gid + 8
-        float scale = 0.f;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                t[p][i] = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8 * i));
-                scale = fmaxf(scale, fmaxf(low_of(t[p][i].x), high_of(t[p][i].x)));
-            }
-        weigh<2>(s, scale);
+            for (int i = 0; i < 2; ++i) t[p][i] = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8 * i));
+        const uint32_t most = bf16x2_max(bf16x2_max(t[0][0].x, t[0][1].x), bf16x2_max(t[1][0].x, t[1][1].x));
+        weigh<2>(s, fmaxf(low_of(most), high_of(most)));
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const uint4 v0 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 16 * lane);
-            const uint4 v1 = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 512 + 16 * lane);
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            float x[kBlocks][4][2];                   // weights times scales: [token, column][group]
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Two scales = two(low_of(t[p][i].x), high_of(t[p][i].x)), zeros = two(low_of(t[p][i].y), high_of(t[p][i].y));
+#pragma unroll
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float y = s[p][n][2 * i + c];
+                        const Two weight = two(y, y), scaled = mul2(weight, scales);
+                        z[n][c] = fma2(weight, zeros, z[n][c]);
+                        pw[n][c] = add2(pw[n][c], scaled);
+                        parts_of(scaled, x[n][2 * i + c][0], x[n][2 * i + c][1]);
+                    }
+            }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {             // 64 dims
-                const float a0 = (g ? high_of(t[p][0].x) : low_of(t[p][0].x)) * factor;
-                const float a1 = (g ? high_of(t[p][1].x) : low_of(t[p][1].x)) * factor;
-                const float z0 = g ? high_of(t[p][0].y) : low_of(t[p][0].y), z1 = g ? high_of(t[p][1].y) : low_of(t[p][1].y);
+                const uint4 v = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 512 * g + 16 * lane);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t f[kBlocks][2];
 #pragma unroll
                 for (int n = 0; n < kBlocks; ++n) {
-                    const float x0 = s[p][n][0] * a0, x1 = s[p][n][1] * a0, x2 = s[p][n][2] * a1, x3 = s[p][n][3] * a1;
-                    z[n][g][0] = fmaf(s[p][n][0], z0, fmaf(s[p][n][2], z1, z[n][g][0]));
-                    z[n][g][1] = fmaf(s[p][n][1], z0, fmaf(s[p][n][3], z1, z[n][g][1]));
-                    pw[n][g] = add2(pw[n][g], add2(two(x0, x1), two(x2, x3)));
-                    f[n][0] = movmatrix_trans(pack_f16x2(x0, x1));       // tokens as rows
-                    f[n][1] = movmatrix_trans(pack_f16x2(x2, x3));
+                    f[n][0] = transposed(pack_f16x2(x[n][0][g], x[n][1][g]));       // tokens as rows
+                    f[n][1] = transposed(pack_f16x2(x[n][2][g], x[n][3][g]));
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int d = 4 * g + i;
-                    const uint32_t up = w[d] >> 8;
-                    const uint32_t c[4] = {w[d] & 0x000f000fu, w[d] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+                    const uint32_t up = w[i] >> 8;
+                    const uint32_t c[4] = {w[i] & 0x000f000fu, w[i] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
 #pragma unroll
-                    for (int n = 0; n < kBlocks; ++n) mma_f16_16816(o[n][d], c, f[n][0], f[n][1]);
+                    for (int n = 0; n < kBlocks; ++n) mma_f16(o[n][4 * g + i], c, f[n][0], f[n][1]);
                 }
             }
         }
@@ -469,21 +501,20 @@ struct Running {
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int c = 0; c < 2; ++c) {
+                z[n][c] = fma2(pw[n][c], two(kMiddle, kMiddle), z[n][c]);
                 float x[2];
-                parts_of(pw[n][g], x[0], x[1]);
-                pw[n][g] = two(0.f, 0.f);
-                const float back = kMiddle / factor;
+                parts_of(pw[n][c], x[0], x[1]);
+                pw[n][c] = two(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    z[n][g][c] = fmaf(x[c], back, z[n][g][c]);
+                for (int g = 0; g < 2; ++g) {
 #pragma unroll
-                    for (int i = 4; i < 32; i *= 2) x[c] += __shfl_xor_sync(kAll, x[c], i);
-                    x[c] *= -kMiddle * kCode;
+                    for (int i = 4; i < 32; i *= 2) x[g] += __shfl_xor_sync(kAll, x[g], i);
+                    x[g] *= -kMiddle * kCode;
 #pragma unroll
                     for (int d = 4 * g; d < 4 * g + 4; ++d) {
-                        o[n][d][c] += x[c];
-                        o[n][d][c + 2] = fmaf(x[c], 16.f, o[n][d][c + 2]);
+                        o[n][d][c] += x[g];
+                        o[n][d][c + 2] = fmaf(x[g], 16.f, o[n][d][c + 2]);
                     }
                 }
             }
@@ -491,7 +522,7 @@ struct Running {
 
     // A bf16 page in shared memory, K and then V, rows of 256 bytes swizzled by 16-byte chunks
     // (chunk_offset), zero from row `valid` on. Queries and weights meet it as two bf16 parts each.
-    __device__ __forceinline__ void recent_page(const uint8_t* page, int valid, const Control<kKind>& ctl) {
+    __device__ __forceinline__ void recent_page(const uint8_t* page, int valid, const Control<kKind>& ctl, int which) {
         const int lane = threadIdx.x & 31, gid = lane >> 2;
         float s[1][kBlocks][4];
 #pragma unroll
@@ -502,7 +533,7 @@ struct Running {
             ldmatrix_x4(f, page + chunk_offset(lane & 15, 2 * k + (lane >> 4)));
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
-                const uint4 q = ctl.frag[n][k][lane];
+                const uint4 q = ctl.frag[which][n][k][lane];
                 uint32_t hi[2], lo[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -510,8 +541,8 @@ struct Running {
                     split(x.x + y.x, x.y + y.y, hi[c], lo[c]);
                     if (c) hi[c] = bf16x2_mul(hi[c], 0x41804180u), lo[c] = bf16x2_mul(lo[c], 0x41804180u);      // 16
                 }
-                mma_bf16_16816(s[0][n], f, hi[0], hi[1]);
-                mma_bf16_16816(s[0][n], f, lo[0], lo[1]);
+                mma_bf16(s[0][n], f, hi[0], hi[1]);
+                mma_bf16(s[0][n], f, lo[0], lo[1]);
             }
         }
 #pragma unroll
@@ -526,14 +557,13 @@ struct Running {
                 if (gid + 8 * (i >> 1) >= valid) s[0][n][i] = -INFINITY;
         weigh<1>(s, 0.f);
         uint32_t hi[kBlocks][2], lo[kBlocks][2];
-        const float unit_of_o = factor * kCode;
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                split(s[0][n][2 * t] * unit_of_o, s[0][n][2 * t + 1] * unit_of_o, hi[n][t], lo[n][t]);
-                hi[n][t] = movmatrix_trans(hi[n][t]);
-                lo[n][t] = movmatrix_trans(lo[n][t]);
+                split(s[0][n][2 * t] * kCode, s[0][n][2 * t + 1] * kCode, hi[n][t], lo[n][t]);
+                hi[n][t] = transposed(hi[n][t]);
+                lo[n][t] = transposed(lo[n][t]);
             }
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
@@ -544,8 +574,8 @@ struct Running {
             f[1] = bf16x2_mul(f[1], 0x41804180u), f[3] = bf16x2_mul(f[3], 0x41804180u);      // 16
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
-                mma_bf16_16816(o[n][d], f, hi[n][0], hi[n][1]);
-                mma_bf16_16816(o[n][d], f, lo[n][0], lo[n][1]);
+                mma_bf16(o[n][d], f, hi[n][0], hi[n][1]);
+                mma_bf16(o[n][d], f, lo[n][0], lo[n][1]);
             }
         }
     }
@@ -572,24 +602,26 @@ struct Running {
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-            float sum[2];
+            float sum[2], zero[2][2];
             parts_of(l[n], sum[0], sum[1]);
+            parts_of(z[n][0], zero[0][0], zero[0][1]);
+            parts_of(z[n][1], zero[1][0], zero[1][1]);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(lift)) << 23);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) {
                     sum[c] += __shfl_xor_sync(kAll, sum[c], x);
-                    z[n][0][c] += __shfl_xor_sync(kAll, z[n][0][c], x);
-                    z[n][1][c] += __shfl_xor_sync(kAll, z[n][1][c], x);
+                    zero[c][0] += __shfl_xor_sync(kAll, zero[c][0], x);
+                    zero[c][1] += __shfl_xor_sync(kAll, zero[c][1], x);
                 }
                 const int query = n * 8 + 2 * tig + c;
                 if (query >= group) continue;         // kPair: the second four columns too
-                if (gid == 0) ms[query] = m[n][c], ls[query] = sum[c];
-                const float back = 1.f / (factor * kCode);
+                if (gid == 0) ms[query] = m[n][c], ls[query] = sum[c] * down;
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
-                    part[query * kPartStride + d * 16 + gid] = fmaf(o[n][d][c], back, z[n][d / 4][c]);
-                    part[query * kPartStride + d * 16 + gid + 8] = fmaf(o[n][d][c + 2], back * 0.0625f, z[n][d / 4][c]);
+                    part[query * kPartStride + d * 16 + gid] = down * fmaf(o[n][d][c], 1.f / kCode, zero[c][d / 4]);
+                    part[query * kPartStride + d * 16 + gid + 8] = down * fmaf(o[n][d][c + 2], 0.0625f / kCode, zero[c][d / 4]);
                 }
             }
         }
@@ -603,36 +635,31 @@ __device__ __forceinline__ void store_lse(const PackedArgs& a, int64_t row, floa
     if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
 }
 
-// A part of a row: packed pages page0 .. page1 and recent pages recent0 .. recent1.
+// Steps off .. off + steps of a row.
 struct Part {
-    int b, h, page0, page1, recent0, recent1, recent;
+    int b, h, off, steps;
+    Len len;
 };
 
-// The pages of a part that are this warp's, index `mine` of `of` warps: every of-th one from
-// page0 + mine on; recent pages from the last warp down. All of the CTA calls it; leaves the
-// CTA's sums in ctl.m, ctl.l and the slots, by warp.
+// Steps x0 .. x1 of a part, which are this warp's: leaves its sums at `out`, ms and ls.
 template <int kKind, bool kSplit>
-__device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& part, int mine, int of, uint8_t* slots,
-                                            Control<kKind>& ctl) {
+__device__ __forceinline__ void attend_steps(const PackedArgs& a, const Part part, int x0, int x1, int which, uint8_t* own,
+                                             bool ready, Control<kKind>& ctl, float* out, float* ms, float* ls) {
     using S = Shape<kKind>;
     constexpr int kDepth = S::kDepth;
-    static_assert(kDepth * kUnitBytes >= 4 * kPage * kD, "a recent page lies in the slots");
-    static_assert(kDepth * kUnitBytes >= S::kRows * kPartStride * 4, "a partial lies in the slots");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = part.b, h = part.h;
-    uint8_t* const own = slots + warp * kDepth * kUnitBytes;
-    const int first = part.page0 + mine;
-    const int count = part.page1 > first ? (part.page1 - first + of - 1) / of : 0;
-    const int64_t page_bytes = static_cast<int64_t>(a.hkv) * kUnitBytes;
+    const int lane = threadIdx.x & 31, b = part.b, h = part.h;
+    const int first = min(part.off + x0, part.len.pages), count = min(part.off + x1, part.len.pages) - first;
     const uint8_t* const base = a.packed + static_cast<int64_t>(h) * kUnitBytes + lane * 16;
-    int ids = lane < count ? packed_id(a, b, h, first + lane * of) : 0, next = 0;
+    uint32_t ids = lane < count ? packed_id(a, b, h, first + lane) : 0, next = 0;
+    const uint32_t stride = static_cast<uint32_t>(a.hkv) * kUnitBytes;
     int put = 0;                                      // slot of the next page to fetch
     const auto load = [&](int i) {
         if (i < count) {
             if ((i & 31) == 0) {                      // ids of 32 pages, fetched 32 pages ahead
                 if (i > 0) ids = next;
-                if (i + 32 + lane < count) next = packed_id(a, b, h, first + (i + 32 + lane) * of);
+                if (i + 32 + lane < count) next = packed_id(a, b, h, first + i + 32 + lane);
             }
-            const uint8_t* from = base + __shfl_sync(kAll, ids, i & 31) * page_bytes;
+            const uint8_t* from = base + static_cast<uint64_t>(__shfl_sync(kAll, ids, i & 31)) * stride;
             uint8_t* to = own + put * kUnitBytes + lane * 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j) cp_async_16(to + j * 512, from + j * 512);
@@ -643,10 +670,9 @@ __device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& par
     };
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) load(i);
-    if (warp < S::kBlocks) put_queries<kKind, kSplit>(a, b, h, warp, ctl);
-    __syncthreads();
+    if (!ready) __syncthreads();                      // the queries are there
     Running<kKind, kSplit> run;
-    run.clear(ctl);
+    run.clear(ctl, which);
     int at = 0;                                       // slot of the next page to use
 #pragma unroll 1
     for (int i = 0; i < count; i += 2) {
@@ -656,7 +682,7 @@ __device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& par
         if (++at == kDepth) at = 0;
         const uint8_t* const unit1 = i + 1 < count ? own + at * kUnitBytes : unit0;
         if (++at == kDepth) at = 0;
-        run.packed_pages(unit0, unit1, i + 1 < count, ctl);
+        run.packed_pages(unit0, unit1, i + 1 < count, ctl, which);
         if (((i / 2) & (kCentre - 1)) == kCentre - 1) run.centre();
         __syncwarp();                                 // both are read
         load(i + kDepth);
@@ -665,9 +691,12 @@ __device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& par
     run.centre();
     copies_wait<0>();
     __syncwarp();
+    // recent pages whose first step is among these
+    const int behind = part.off - part.len.pages + kRecentSteps - 1;
+    const int recent1 = min(part.len.recent_pages(), max(0, (behind + x1) / kRecentSteps));
 #pragma unroll 1
-    for (int r = part.recent0 + of - 1 - mine; r < part.recent1; r += of) {
-        const int valid = min(kPage, part.recent - r * kPage);
+    for (int r = max(0, (behind + x0) / kRecentSteps); r < recent1; ++r) {
+        const int valid = min(kPage, part.len.recent - r * kPage);
         int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
         if (id < 0 || id >= a.num_cache) {
             report_error(a.st, LOCKS_ERR_BAD_INDEX);
@@ -683,63 +712,102 @@ __device__ __forceinline__ void attend_part(const PackedArgs& a, const Part& par
         copies_commit();
         copies_wait<0>();
         __syncwarp();
-        run.recent_page(own, valid, ctl);
+        run.recent_page(own, valid, ctl, which);
         __syncwarp();
     }
-    run.put(a.group, reinterpret_cast<float*>(own), ctl.m[warp], ctl.l[warp]);
+    run.put(a.group, out, ms, ls);
+    __syncwarp();
+}
+
+// One or two parts (neighbouring rows) by all of the CTA, an equal share of the steps to a warp.
+// Leaves the warps' partials in shared memory, for join_warps.
+template <int kKind, bool kSplit>
+__device__ __forceinline__ void attend_parts(const PackedArgs& a, const Part (&part)[2], int parts, uint8_t* slots,
+                                             Control<kKind>& ctl) {
+    using S = Shape<kKind>;
+    static_assert(S::kDepth * kUnitBytes >= 4 * kPage * kD, "a recent page lies in the slots");
+    static_assert(S::kDepth * kUnitBytes >= S::kRows * kPartStride * 4, "a partial lies in the slots");
+    static_assert(2 * S::kBlocks <= S::kWarps, "a warp per block of queries");
+    const int warp = threadIdx.x >> 5;
+    uint8_t* const own = slots + warp * S::kDepth * kUnitBytes;
+    const int64_t all = static_cast<int64_t>(part[0].steps) + (parts > 1 ? part[1].steps : 0);
+    const int64_t x0 = all * warp / S::kWarps, x1 = all * (warp + 1) / S::kWarps;
+    if (warp < parts * S::kBlocks) {
+        const int which = warp / S::kBlocks;
+        put_queries<kKind, kSplit>(a, which ? part[1].b : part[0].b, which ? part[1].h : part[0].h, which, warp % S::kBlocks, ctl);
+    }
+    const bool has0 = x0 < x1 && x0 < part[0].steps, has1 = x0 < x1 && x1 > part[0].steps;
+    if ((threadIdx.x & 31) == 0) ctl.had[warp] = (has0 ? 1 : 0) | (has1 ? 2 : 0);
+    bool ready = false;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (!(which ? has1 : has0)) continue;
+        const int64_t base = which ? part[0].steps : 0;
+        const int s0 = static_cast<int>(max(x0 - base, static_cast<int64_t>(0)));
+        const int s1 = static_cast<int>(min(x1 - base, static_cast<int64_t>(which ? part[1].steps : part[0].steps)));
+        float* out = which == 0 && has1 ? ctl.both : reinterpret_cast<float*>(own);
+        attend_steps<kKind, kSplit>(a, which ? part[1] : part[0], s0, s1, which, own, ready, ctl, out, ctl.m[which][warp],
+                                    ctl.l[which][warp]);
+        ready = true;
+    }
+    if (!ready) __syncthreads();
     __syncthreads();
 }
 
-// Query `query`, dim `dim` of the CTA's part from its warps' partials.
+// Query `query`, dim `dim` of part `which` from its warps' partials.
 template <int kKind>
-__device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int query, int dim, float& top,
-                                            float& sum) {
+__device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int which, int query, int dim,
+                                            float& top, float& sum) {
     using S = Shape<kKind>;
     top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, ctl.m[w][query]);
+    for (int w = 0; w < S::kWarps; ++w)
+        if (ctl.had[w] >> which & 1) top = fmaxf(top, ctl.m[which][w][query]);
     const float base = top == -INFINITY ? 0.f : top;
     float x = 0.f;
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < S::kWarps; ++w) {
-        const float f = fast_exp2(ctl.m[w][query] - base);
-        x = fmaf(f, reinterpret_cast<const float*>(slots + w * S::kDepth * kUnitBytes)[query * kPartStride + dim], x);
-        sum = fmaf(f, ctl.l[w][query], sum);
+        const int had = ctl.had[w];
+        if (!(had >> which & 1)) continue;
+        const float f = fast_exp2(ctl.m[which][w][query] - base);
+        const float* o = which == 0 && had == 3 ? ctl.both : reinterpret_cast<const float*>(slots + w * S::kDepth * kUnitBytes);
+        x = fmaf(f, o[query * kPartStride + dim], x);
+        sum = fmaf(f, ctl.l[which][w][query], sum);
     }
     return x;
 }
 
-// Short rows: cluster r / cluster size is a row.
+// Short rows: cluster r is row r, its CTAs an equal share of it each.
 template <int kKind, bool kSplit>
 __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __grid_constant__ PackedArgs a, int ctas) {
     using S = Shape<kKind>;
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ Control<kKind> ctl;
-    const int warp = threadIdx.x >> 5, rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int r = blockIdx.x / ctas;
     grid_dependency_wait();
     allow_dependent_launch();
-    Part part;
-    part.b = r / a.hkv;
-    part.h = r % a.hkv;
-    const Len len = row_len(a, part.b, part.h, rank == 0 && threadIdx.x == 0);
-    part.page0 = part.recent0 = 0;
-    part.page1 = len.pages;
-    part.recent1 = len.recent_pages();
-    part.recent = len.recent;
-    attend_part<kKind, kSplit>(a, part, rank * S::kWarps + warp, ctas * S::kWarps, slots, ctl);
-    const int64_t row = static_cast<int64_t>(part.b) * a.hq + part.h * a.group;
+    Part part[2];
+    part[0].b = r / a.hkv;
+    part[0].h = r % a.hkv;
+    part[0].len = row_len(a, part[0].b, part[0].h, rank == 0 && threadIdx.x == 0);
+    const int64_t steps = part[0].len.steps();
+    part[0].off = static_cast<int>(steps * rank / ctas);
+    part[0].steps = static_cast<int>(steps * (rank + 1) / ctas) - part[0].off;
+    part[1] = part[0];
+    attend_parts<kKind, kSplit>(a, part, 1, slots, ctl);
+    const int64_t row = static_cast<int64_t>(part[0].b) * a.hq + part[0].h * a.group;
     for (int i = threadIdx.x; i < a.group * kD; i += S::kThreads) {
         const int query = i / kD, dim = i % kD;
         float top, sum;
-        const float x = join_warps<kKind>(slots, ctl, query, dim, top, sum);
+        const float x = join_warps<kKind>(slots, ctl, 0, query, dim, top, sum);
         if (ctas == 1) {
             store_row(a, row + query, x, sum, dim);
             if (dim == 0) store_lse(a, row + query, top, sum);
         } else {
-            ctl.cta_o[query][dim] = x;
-            if (dim == 0) ctl.cta_m[query] = top, ctl.cta_l[query] = sum;
+            ctl.cta.o[query][dim] = x;
+            if (dim == 0) ctl.cta.m[query] = top, ctl.cta.l[query] = sum;
         }
     }
     if (ctas == 1) return;
@@ -752,9 +820,9 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __
             m[c] = -INFINITY;
             l[c] = x[c] = 0.f;
             if (c < ctas) {
-                m[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_m[query], c));
-                l[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_l[query], c));
-                x[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta_o[query][dim], c));
+                m[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.m[query], c));
+                l[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.l[query], c));
+                x[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.o[query][dim], c));
             }
             top = fmaxf(top, m[c]);
         }
@@ -797,10 +865,10 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
             const int64_t y = __shfl_up_sync(kAll, upto, x);
             if (lane >= x) upto += y;
         }
-        if (lane == 31) ctl.warp_sum[warp] = upto;
+        if (lane == 31) ctl.line.warp_sum[warp] = upto;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += ctl.warp_sum[w];
-        ctl.upto[threadIdx.x] = upto;
+        for (int w = 0; w < warp; ++w) upto += ctl.line.warp_sum[w];
+        ctl.line.upto[threadIdx.x] = upto;
     }
     // rows without tokens are nobody's
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; r < static_cast<int64_t>(a.batch) * a.hkv;
@@ -815,7 +883,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
         if (by_row) a.cuts[r] = {-1, 0, 0};
     }
     __syncthreads();
-    const int64_t total = ctl.upto[kThreads - 1];
+    const int64_t total = ctl.line.upto[kThreads - 1];
     const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps));
     int64_t pos = 0, end = 0;
     if (static_cast<int>(blockIdx.x) < ctas) {
@@ -826,62 +894,68 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
     if (pos >= end) return;
 
     // the row at pos
-    Part part;
-    Len len;
-    int off;
+    Part part[2];
     {
+        Part& p = part[0];
         int before = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.upto[i * 32 + lane] <= pos));
-        int64_t at = pos - (before > 0 ? ctl.upto[before - 1] : 0);
-        part.b = before * per;
-        for (int64_t n; part.b < a.batch - 1 && at >= (n = seq_steps(a, part.b, false)); ++part.b) at -= n;
-        part.h = 0;
-        for (len = row_len(a, part.b, 0, false); part.h < a.hkv - 1 && at >= len.steps();
-             len = row_len(a, part.b, ++part.h, false))
-            at -= len.steps();
-        off = static_cast<int>(at);
+        for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.line.upto[i * 32 + lane] <= pos));
+        int64_t at = pos - (before > 0 ? ctl.line.upto[before - 1] : 0);
+        p.b = before * per;
+        for (int64_t n; p.b < a.batch - 1 && at >= (n = seq_steps(a, p.b, false)); ++p.b) at -= n;
+        p.h = 0;
+        for (p.len = row_len(a, p.b, 0, false); p.h < a.hkv - 1 && at >= p.len.steps(); p.len = row_len(a, p.b, ++p.h, false))
+            at -= p.len.steps();
+        p.off = static_cast<int>(at);
     }
+    // the row behind p's with any steps (there is one as long as steps are left)
+    const auto next_row = [&](const Part& p) {
+        Part r = p;
+        do {
+            if (++r.h == a.hkv) ++r.b, r.h = 0;
+            r.len = row_len(a, r.b, r.h, false);
+        } while (r.len.steps() == 0 && r.b < a.batch - 1);
+        r.off = 0;
+        return r;
+    };
 #pragma unroll 1
-    while (pos < end) {
-        const int steps = len.steps();
-        const int n = static_cast<int>(min(end - pos, static_cast<int64_t>(steps - off)));
-        part.page0 = min(off, len.pages);
-        part.page1 = min(off + n, len.pages);
-        // recent pages whose first step is among this part's
-        part.recent0 = max(0, (off - len.pages + kRecentSteps - 1) / kRecentSteps);
-        part.recent1 = min(len.recent_pages(), max(0, (off + n - len.pages + kRecentSteps - 1) / kRecentSteps));
-        part.recent = len.recent;
-        attend_part<kKind, kSplit>(a, part, warp, kWarps, slots, ctl);
-        const bool begins = off == 0, whole = begins && n == steps;
-        const int64_t row = static_cast<int64_t>(part.b) * a.hq + part.h * a.group;
-        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        for (int i = threadIdx.x; i < a.group * kD; i += kThreads) {
-            const int query = i / kD, dim = i % kD;
-            float top, sum;
-            const float x = join_warps<kKind>(slots, ctl, query, dim, top, sum);
-            if (whole) {
-                store_row(a, row + query, x, sum, dim);
-                if (dim == 0) store_lse(a, row + query, top, sum);
-            } else {
-                a.part_o[(static_cast<int64_t>(slot) * a.group + query) * kD + dim] = x;
-                if (dim == 0) a.part_ml[slot * a.group + query] = make_float2(top, sum);
+    while (true) {
+        part[0].steps = static_cast<int>(min(end - pos, static_cast<int64_t>(part[0].len.steps() - part[0].off)));
+        int parts = 1;
+        if (pos + part[0].steps < end) {
+            part[1] = next_row(part[0]);
+            part[1].steps = static_cast<int>(min(end - pos - part[0].steps, static_cast<int64_t>(part[1].len.steps())));
+            parts = 2;
+        }
+        attend_parts<kKind, kSplit>(a, part, parts, slots, ctl);
+#pragma unroll 1
+        for (int which = 0; which < parts; ++which) {
+            const Part& p = which ? part[1] : part[0];
+            const bool begins = p.off == 0, whole = begins && p.steps == p.len.steps();
+            const int64_t row = static_cast<int64_t>(p.b) * a.hq + p.h * a.group;
+            const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+            for (int i = threadIdx.x; i < a.group * kD; i += kThreads) {
+                const int query = i / kD, dim = i % kD;
+                float top, sum;
+                const float x = join_warps<kKind>(slots, ctl, which, query, dim, top, sum);
+                if (whole) {
+                    store_row(a, row + query, x, sum, dim);
+                    if (dim == 0) store_lse(a, row + query, top, sum);
+                } else {
+                    a.part_o[(static_cast<int64_t>(slot) * a.group + query) * kD + dim] = x;
+                    if (dim == 0) a.part_ml[slot * a.group + query] = make_float2(top, sum);
+                }
             }
+            if (begins && threadIdx.x == 0 && (by_row || !whole)) {
+                const int r = p.b * a.hkv + p.h;
+                const int last = cta_of(total, pos + p.len.steps() - 1, ctas);
+                a.cuts[by_row ? r : static_cast<int>(blockIdx.x)] = {whole ? -1 : r, static_cast<int>(blockIdx.x), last};
+            }
+            pos += p.steps;
         }
-        if (begins && threadIdx.x == 0 && (by_row || !whole)) {
-            const int r = part.b * a.hkv + part.h;
-            const int last = cta_of(total, pos + steps - 1, ctas);
-            a.cuts[by_row ? r : static_cast<int>(blockIdx.x)] = {whole ? -1 : r, static_cast<int>(blockIdx.x), last};
-        }
-        pos += n;
-        off = 0;
-        if (pos < end) {
-            do {
-                if (++part.h == a.hkv) ++part.b, part.h = 0;
-                len = row_len(a, part.b, part.h, false);
-            } while (len.steps() == 0 && part.b < a.batch - 1);
-            __syncthreads();                          // the slots and sums are read
-        }
+        if (pos >= end) break;
+        part[0] = next_row(part[parts - 1]);
+        __syncthreads();                              // the slots and sums are read
     }
 }
 
