@@ -145,7 +145,8 @@ LOCKS_API int locks_copy_pages(const locks_planes_t* planes, const int32_t* src_
                                int32_t max_pairs, const int32_t* n_pairs, void* workspace, size_t workspace_bytes,
                                void* stream);
 
-/* Workspace bytes of the three calls below for these dims (256-byte aligned). */
+/* Workspace bytes of locks_fork_sequences, locks_take_pages and locks_compact_pages for these dims
+ * (256-byte aligned). The pool they work on, of num_phys_pages pages, may have up to 2^30. */
 LOCKS_API int locks_pool_workspace_size(const locks_dims_t* dims, size_t* bytes);
 
 /*
@@ -187,7 +188,7 @@ LOCKS_API int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page
  * records LOCKS_ERR_BAD_INDEX.
  * - seq_tokens_out may be seq_tokens and refs_out refs; else no output may overlap another array.
  * - n_free (int32 [1], may be NULL) receives the number of pages that are free afterwards.
- * - batch at most 65536. One launch.
+ * - batch at most 65536. Two launches.
  */
 LOCKS_API int locks_take_pages(const locks_dims_t* dims, int32_t* page_table, const int32_t* seq_tokens,
                                const int32_t* new_tokens, const int32_t* refs, int32_t* seq_tokens_out,

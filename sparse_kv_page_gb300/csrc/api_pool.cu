@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int kMaxBatch = 65536;
+constexpr int kMaxPoolPages = 1 << 30;    // pages are counted a few rounds past the pool's end in int32
 constexpr size_t kStatusBytes = 256;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -58,12 +59,13 @@ int check_packed(const locks_dims_t* d) {
 }
 
 // What the calls that change tables have in common. Counts of tokens are int32, and a block
-// takes 1024 entries of a row.
+// takes 4096 entries of a row.
 int check_table(const locks_dims_t* d) {
     const int s = locks::check_dims(d);
     if (s != LOCKS_OK) return s;
     if (d->batch > kMaxBatch || d->max_pages_per_seq > INT_MAX / LOCKS_PAGE_SIZE) return LOCKS_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(d->batch) * (d->max_pages_per_seq / 1024 + 1) > INT_MAX) return LOCKS_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d->batch) * (d->max_pages_per_seq / 4096 + 1) > INT_MAX / 2) return LOCKS_ERR_UNSUPPORTED;
+    if (d->num_phys_pages > kMaxPoolPages) return LOCKS_ERR_UNSUPPORTED;
     return LOCKS_OK;
 }
 
@@ -74,11 +76,15 @@ locks::PoolArgs pool_args(const locks_dims_t* d, void* workspace) {
     a.max_pages = d->max_pages_per_seq;
     a.num_pages = d->num_phys_pages;
     uint8_t* base = static_cast<uint8_t*>(workspace);
-    const locks::PoolLayout w = locks::pool_layout(d->batch);
+    const locks::PoolLayout w = locks::pool_layout(d->batch, d->num_phys_pages);
+    a.needed = reinterpret_cast<int32_t*>(base + w.needed);
+    a.block_counts = reinterpret_cast<int32_t*>(base + w.block_counts);
     a.scan = reinterpret_cast<int32_t*>(base + w.scan);
-    a.children = reinterpret_cast<int32_t*>(base + w.children);
+    a.shift = reinterpret_cast<int32_t*>(base + w.shift);
+    a.children = a.shift;
     a.keeper = reinterpret_cast<int32_t*>(base + w.keeper);
     a.fresh = reinterpret_cast<int32_t*>(base + w.fresh);
+    a.flags = base + w.flags;
     a.st = locks::device_status(workspace);
     return a;
 }
@@ -233,7 +239,7 @@ int locks_pool_workspace_size(const locks_dims_t* dims, size_t* bytes) {
     if (!bytes) return LOCKS_ERR_INVALID_ARG;
     const int s = check_table(dims);
     if (s != LOCKS_OK) return s;
-    *bytes = locks::pool_layout(dims->batch).bytes;
+    *bytes = locks::pool_layout(dims->batch, dims->num_phys_pages).bytes;
     return LOCKS_OK;
 }
 
@@ -243,7 +249,7 @@ int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page_table, co
                          int32_t* n_copies, void* workspace, size_t workspace_bytes, void* stream) {
     int s = check_table(dims);
     if (s != LOCKS_OK) return s;
-    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch).bytes)) != LOCKS_OK)
+    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch, dims->num_phys_pages).bytes)) != LOCKS_OK)
         return s;
     if (!n_copies) return LOCKS_ERR_INVALID_ARG;
     const int64_t batch = dims->batch, cells = batch * dims->max_pages_per_seq, pages = dims->num_phys_pages;
@@ -257,8 +263,7 @@ int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page_table, co
                {ints(page_table_out, cells), ints(seq_tokens_out, batch), ints(refs_out, pages, refs),
                 ints(copy_src, batch), ints(copy_dst, batch), ints(n_copies, 1)}))
         return LOCKS_ERR_INVALID_ARG;
-    const int sms = locks::current_sms();
-    if (sms <= 0) return LOCKS_ERR_CUDA;
+    if (locks::current_sms() <= 0) return LOCKS_ERR_CUDA;
     locks::PoolArgs a = pool_args(dims, workspace);
     a.page_table = page_table;
     a.page_table_out = page_table_out;
@@ -270,7 +275,7 @@ int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page_table, co
     a.list_src = copy_src;
     a.list_dst = copy_dst;
     a.n_list = n_copies;
-    return cuda_status(locks::launch_fork(a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(locks::launch_fork(a, static_cast<cudaStream_t>(stream)));
 }
 
 int locks_take_pages(const locks_dims_t* dims, int32_t* page_table, const int32_t* seq_tokens,
@@ -278,7 +283,7 @@ int locks_take_pages(const locks_dims_t* dims, int32_t* page_table, const int32_
                      int32_t* n_free, void* workspace, size_t workspace_bytes, void* stream) {
     int s = check_table(dims);
     if (s != LOCKS_OK) return s;
-    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch).bytes)) != LOCKS_OK)
+    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch, dims->num_phys_pages).bytes)) != LOCKS_OK)
         return s;
     const int64_t batch = dims->batch, cells = batch * dims->max_pages_per_seq, pages = dims->num_phys_pages;
     if (batch > 0 && (!seq_tokens || !new_tokens || !seq_tokens_out)) return LOCKS_ERR_INVALID_ARG;
@@ -308,7 +313,7 @@ int locks_free_pages(const int32_t* refs, int32_t num_pages, const int32_t* page
                      void* stream) {
     int s;
     if (num_pages < 0 || stride < 0 || rows < 0) return LOCKS_ERR_INVALID_ARG;
-    if (stride > INT_MAX / 2) return LOCKS_ERR_UNSUPPORTED;
+    if (stride > INT_MAX / 2 || num_pages > kMaxPoolPages) return LOCKS_ERR_UNSUPPORTED;
     if (workspace && (s = locks::check_workspace(workspace, workspace_bytes, kStatusBytes)) != LOCKS_OK) return s;
     const int64_t cells = static_cast<int64_t>(rows) * stride;
     if (num_pages > 0 && (!refs || !refs_out)) return LOCKS_ERR_INVALID_ARG;
@@ -339,7 +344,7 @@ int locks_compact_pages(const locks_dims_t* dims, const int32_t* page_table, con
                         size_t workspace_bytes, void* stream) {
     int s = check_table(dims);
     if (s != LOCKS_OK) return s;
-    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch).bytes)) != LOCKS_OK)
+    if ((s = locks::check_workspace(workspace, workspace_bytes, locks::pool_layout(dims->batch, dims->num_phys_pages).bytes)) != LOCKS_OK)
         return s;
     const int64_t batch = dims->batch, cells = batch * dims->max_pages_per_seq, pages = dims->num_phys_pages;
     if (move_cap < 1 || move_cap < pages / 2) return LOCKS_ERR_INVALID_ARG;
@@ -353,8 +358,7 @@ int locks_compact_pages(const locks_dims_t* dims, const int32_t* page_table, con
                {ints(page_table_out, cells, page_table), ints(refs_out, pages, refs), ints(move_src, move_cap),
                 ints(move_dst, move_cap), ints(n_moves, 1), ints(new_page, pages)}))
         return LOCKS_ERR_INVALID_ARG;
-    const int sms = locks::current_sms();
-    if (sms <= 0) return LOCKS_ERR_CUDA;
+    if (locks::current_sms() <= 0) return LOCKS_ERR_CUDA;
     locks::PoolArgs a = pool_args(dims, workspace);
     a.page_table = page_table;
     a.page_table_out = page_table_out;
@@ -365,7 +369,7 @@ int locks_compact_pages(const locks_dims_t* dims, const int32_t* page_table, con
     a.list_dst = move_dst;
     a.n_list = n_moves;
     a.new_page = new_page;
-    return cuda_status(locks::launch_compact(a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(locks::launch_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

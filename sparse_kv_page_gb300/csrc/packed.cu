@@ -1,9 +1,11 @@
 // packed.cu - pages of the bf16 pool to 4 bits and back (locks_pack_pages, locks_unpack_pages).
 //
-// A warp takes a unit (a page of one kv head): 8 KB of bf16 on one side, 2432 bytes on the
-// other, so HBM bounds both. The bf16 side is read and written 16 bytes a lane, two tokens to
-// an instruction; the codes go through a staging area in shared memory, because the order of
-// the attention's fragments spreads a lane's eight dims over four or eight words.
+// 8 KB of bf16 on one side of a unit (a page of one kv head), 2432 bytes on the other, so HBM bounds
+// both. A warp packs the keys or the values of a unit, or unpacks both. The bf16 side is read and
+// written 16 bytes a lane, two tokens to an instruction; the codes go through a staging area in
+// shared memory, because the order of the attention's fragments spreads a lane's eight dims over
+// four or eight words. Packing takes about 5 instructions a value, most of them for two values at
+// once.
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -27,6 +29,35 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
+// Two floats in one instruction.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void parts_of(Two x, uint32_t& a, uint32_t& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Quotients below are rounded as fp32 division rounds them, by Markstein's theorem (IBM J. Res. Dev.
+// 34, 1990): with r the correctly rounded 1 / s, q = v r and q + (v - s q) r is the rounded v / s.
+
 // Scale and zero (bf16 bits) of a group that kLanes neighbouring lanes hold, eight values each.
 template <int kLanes>
 __device__ __forceinline__ void group_scale(const uint4& x, uint32_t& scale, uint32_t& zero) {
@@ -39,30 +70,30 @@ __device__ __forceinline__ void group_scale(const uint4& x, uint32_t& scale, uin
     }
     lo = bf16x2_min(lo, lo >> 16 | lo << 16);
     hi = bf16x2_max(hi, hi >> 16 | hi << 16);
-    scale = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(low_of(hi), low_of(lo)), 15.f)));
+    const float range = __fsub_rn(low_of(hi), low_of(lo)), by = 1.f / 15.f, q = __fmul_rn(range, by);
+    scale = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-15.f, q, range), by, q)));
     if (scale < 0x0080u) scale = 0;               // below 2^-126
     zero = lo & 0xffffu;
 }
 
-// The eight codes of a lane's values as floats kRound + code, whose low bits are the code. The
-// quotient (x - zero) / scale is rounded as fp32 division rounds it, by Markstein's theorem (IBM J.
-// Res. Dev. 34, 1990): with the correctly rounded reciprocal r, q = v r and q + (v - s q) r is the
-// rounded v / s. It matters: bf16 values lie on borders between two codes often, and there the
-// product with the reciprocal alone may fall to either side. Scales so small or large that the
-// remainder or the reciprocal leave the normal numbers divide. The quotient is within [0, 15.06], as the
-// scale is rounded by at most 2^-8 of itself, so codes need no bounds.
+// The eight codes of a lane's values as floats kRound + code, whose low bits are the code. How the
+// quotient (x - zero) / scale is rounded matters: bf16 values lie on borders between two codes often,
+// and there the product with the reciprocal alone may fall to either side. Scales so small or large
+// that the remainder or the reciprocal leave the normal numbers divide. The quotient is within
+// [0, 15.06], as the scale is rounded by at most 2^-8 of itself, so codes need no bounds.
 constexpr float kRound = 12582912.f;              // 1.5 * 2^23
 constexpr uint32_t kRoundBits = 0x4b400000u;
 __device__ __noinline__ float divided(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
 __device__ __forceinline__ void codes_of(const uint4& x, uint32_t scale, uint32_t zero, uint32_t (&c)[8]) {
-    const float s = low_of(scale), z = low_of(zero), r = __frcp_rn(s);
+    const float s = low_of(scale), z = low_of(zero);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     if (s > 0x1p-90f && s < 0x1p120f) {
+        const float r = __frcp_rn(s);
+        const Two zeros = two(-z, -z), scales = two(-s, -s), by = two(r, r), round = two(kRound, kRound);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = __fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z);
-            const float q = __fmul_rn(v, r);
-            c[i] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-s, q, v), r, q), kRound));
+        for (int i = 0; i < 4; ++i) {
+            const Two v = add2(two(low_of(w[i]), high_of(w[i])), zeros), q = mul2(v, by);
+            parts_of(add2(fma2(fma2(scales, q, v), by, q), round), c[2 * i], c[2 * i + 1]);
         }
     } else {
 #pragma unroll
@@ -82,86 +113,99 @@ __device__ __forceinline__ bool find_pages(const PackArgs& a, int i, int& from, 
     return false;
 }
 
+// Bits of codes c0 (token t or its pair's first) and c1 (token t + 8) at their places in a word.
+__device__ __forceinline__ uint32_t both_rows(uint32_t c0, uint32_t c1) {
+    return c0 + (c1 << 8) - (kRoundBits + (kRoundBits << 8));
+}
+
+// Keys: codes at 0 and scales at 1024 of `unit`.
+__device__ __forceinline__ void pack_keys(const uint4 (&x)[8], uint8_t* unit) {
+    const int lane = threadIdx.x & 31, row = lane >> 4, chunk = lane & 15, half = chunk & 1, w = chunk >> 1;
+    uint8_t* const words = unit + 512 * (w >> 2) + 4 * (w & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {                     // tokens t and t + 8
+        const int t = 2 * j + row;
+        uint32_t c0[8], c1[8], s0, z0, s1, z1, part[4];
+        group_scale<4>(x[j], s0, z0);
+        group_scale<4>(x[j + 4], s1, z1);
+        codes_of(x[j], s0, z0, c0);
+        codes_of(x[j + 4], s1, z1, c1);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)                   // pair of dims: this half's bits of its word
+            part[p] = (both_rows(c0[2 * p], c1[2 * p]) + (both_rows(c0[2 * p + 1], c1[2 * p + 1]) << 16)) << (4 * half);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {                 // the even half keeps words 0, 1
+            const uint32_t give = half ? part[p] : part[p + 2], keep = half ? part[p + 2] : part[p];
+            *reinterpret_cast<uint32_t*>(words + 16 * (4 * t + 2 * half + p)) = keep | __shfl_xor_sync(kAll, give, 1);
+        }
+        if ((chunk & 3) == 0) {
+            uint16_t* sz = reinterpret_cast<uint16_t*>(unit + 1024 + 16 * t) + (chunk >> 2);
+            sz[0] = static_cast<uint16_t>(s0), sz[4] = static_cast<uint16_t>(z0);
+            sz[64] = static_cast<uint16_t>(s1), sz[68] = static_cast<uint16_t>(z1);
+        }
+    }
+}
+
+// Values, the same way.
+__device__ __forceinline__ void pack_values(const uint4 (&x)[8], uint8_t* unit) {
+    const int lane = threadIdx.x & 31, row = lane >> 4, chunk = lane & 15, half = chunk & 1, w = chunk >> 1;
+    uint8_t* const words = unit + 512 * (w >> 2) + 4 * (w & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int t = 2 * j + row;
+        uint32_t c0[8], c1[8], s0, z0, s1, z1, part[8], four[4];
+        group_scale<8>(x[j], s0, z0);
+        group_scale<8>(x[j + 4], s1, z1);
+        codes_of(x[j], s0, z0, c0);
+        codes_of(x[j + 4], s1, z1, c1);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) part[d] = both_rows(c0[d], c1[d]) << (16 * row + 4 * half);     // a word a dim
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {                 // dims 4 * half .. of both halves
+            const uint32_t give = half ? part[d] : part[d + 4], keep = half ? part[d + 4] : part[d];
+            four[d] = keep | __shfl_xor_sync(kAll, give, 1);
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {                 // ... and 2 * row .. of both tokens
+            const uint32_t give = row ? four[d] : four[d + 2], keep = row ? four[d + 2] : four[d];
+            *reinterpret_cast<uint32_t*>(words + 16 * (4 * (4 * half + 2 * row + d) + j)) =
+                keep | __shfl_xor_sync(kAll, give, 16);
+        }
+        if ((chunk & 7) == 0) {
+            uint16_t* sz = reinterpret_cast<uint16_t*>(unit + 1024 + 8 * t) + (chunk >> 3);
+            sz[0] = static_cast<uint16_t>(s0), sz[2] = static_cast<uint16_t>(z0);
+            sz[32] = static_cast<uint16_t>(s1), sz[34] = static_cast<uint16_t>(z1);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kWarps * 32) pack_kernel(const __grid_constant__ PackArgs a) {
-    __shared__ __align__(16) uint8_t stage[kWarps][kUnitBytes];
+    __shared__ __align__(16) uint8_t stage[kWarps][1024 + 256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* const unit = stage[warp];
-    const int row = lane >> 4, chunk = lane & 15;             // of two tokens, 8 dims a lane
     grid_dependency_wait();
     allow_dependent_launch();
-    const int64_t units = static_cast<int64_t>(a.n) * a.hkv;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+    const int64_t items = 2 * static_cast<int64_t>(a.n) * a.hkv;         // a unit's keys, its values
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < items;
          u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int i = static_cast<int>(u / a.hkv), h = static_cast<int>(u % a.hkv);
+        const bool values = u & 1;
+        const int i = static_cast<int>((u >> 1) / a.hkv), h = static_cast<int>((u >> 1) % a.hkv);
         int from, to;
         if (!find_pages(a, i, from, to)) continue;
-        const int64_t at = (static_cast<int64_t>(from) * a.hkv + h) * (kPage * kD) + lane * 8;
-        uint4 k[8], v[8];
+        const uint16_t* in = (values ? a.v_in : a.k_in) + (static_cast<int64_t>(from) * a.hkv + h) * (kPage * kD) + lane * 8;
+        uint4 x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {                         // tokens 2j, 2j + 1
-            k[j] = __ldcs(reinterpret_cast<const uint4*>(a.k_in + at + j * 2 * kD));
-            v[j] = __ldcs(reinterpret_cast<const uint4*>(a.v_in + at + j * 2 * kD));
-        }
-        const int half = chunk & 1, w = chunk >> 1;
-        const int word = 512 * (w >> 2) + 4 * (w & 3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {                         // tokens t and t + 8
-            const int t = 2 * j + row;
-            {
-                uint32_t c0[8], c1[8], s0, z0, s1, z1, full[4];
-                group_scale<4>(k[j], s0, z0);
-                group_scale<4>(k[j + 4], s1, z1);
-                codes_of(k[j], s0, z0, c0);
-                codes_of(k[j + 4], s1, z1, c1);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {                 // pair of dims: this half's bits of its word
-                    const uint32_t mine = c0[2 * p] + (c0[2 * p + 1] << 16) + (c1[2 * p] << 8) + (c1[2 * p + 1] << 24);
-                    full[p] = (mine - (kRoundBits + (kRoundBits << 8))) << (4 * half);
-                }
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {                 // the even half keeps words 0, 1
-                    const uint32_t give = half ? full[p] : full[p + 2], keep = half ? full[p + 2] : full[p];
-                    const uint32_t all = keep | __shfl_xor_sync(kAll, give, 1);
-                    *reinterpret_cast<uint32_t*>(unit + word + 16 * (4 * t + 2 * half + p)) = all;
-                }
-                if ((chunk & 3) == 0) {
-                    uint16_t* sz = reinterpret_cast<uint16_t*>(unit + kUnitKScales + 16 * t) + (chunk >> 2);
-                    sz[0] = static_cast<uint16_t>(s0), sz[4] = static_cast<uint16_t>(z0);
-                    sz[64] = static_cast<uint16_t>(s1), sz[68] = static_cast<uint16_t>(z1);
-                }
-            }
-            {
-                uint32_t c0[8], c1[8], s0, z0, s1, z1, part[8];
-                group_scale<8>(v[j], s0, z0);
-                group_scale<8>(v[j + 4], s1, z1);
-                codes_of(v[j], s0, z0, c0);
-                codes_of(v[j + 4], s1, z1, c1);
-#pragma unroll
-                for (int d = 0; d < 8; ++d)                   // of tokens t, t + 8: a word a dim
-                    part[d] = (c0[d] + (c1[d] << 8) - (kRoundBits + (kRoundBits << 8))) << (16 * row + 4 * half);
-                uint32_t four[4];                             // dims 4 * half .. of both halves
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t give = half ? part[d] : part[d + 4], keep = half ? part[d + 4] : part[d];
-                    four[d] = keep | __shfl_xor_sync(kAll, give, 1);
-                }
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {                 // ... and 2 * row .. of both tokens
-                    const uint32_t give = row ? four[d] : four[d + 2], keep = row ? four[d + 2] : four[d];
-                    const uint32_t all = keep | __shfl_xor_sync(kAll, give, 16);
-                    *reinterpret_cast<uint32_t*>(unit + kUnitVCodes + word +
-                                                 16 * (4 * (4 * half + 2 * row + d) + j)) = all;
-                }
-                if ((chunk & 7) == 0) {
-                    uint16_t* sz = reinterpret_cast<uint16_t*>(unit + kUnitVScales + 8 * t) + (chunk >> 3);
-                    sz[0] = static_cast<uint16_t>(s0), sz[2] = static_cast<uint16_t>(z0);
-                    sz[32] = static_cast<uint16_t>(s1), sz[34] = static_cast<uint16_t>(z1);
-                }
-            }
-        }
+        for (int j = 0; j < 8; ++j) x[j] = __ldcs(reinterpret_cast<const uint4*>(in + j * 2 * kD));      // tokens 2j, 2j + 1
+        if (values) pack_values(x, unit);
+        else pack_keys(x, unit);
         __syncwarp();
-        uint4* out = reinterpret_cast<uint4*>(a.packed + (static_cast<int64_t>(to) * a.hkv + h) * kUnitBytes);
-        for (int x = lane; x < kUnitBytes / 16; x += 32) out[x] = reinterpret_cast<const uint4*>(unit)[x];
+        uint8_t* const out = a.packed + (static_cast<int64_t>(to) * a.hkv + h) * kUnitBytes + lane * 16;
+        uint8_t* const codes = out + (values ? kUnitVCodes : 0);
+        uint8_t* const scales = out + (values ? kUnitVScales : kUnitKScales);
+        const uint4* const from_stage = reinterpret_cast<const uint4*>(unit) + lane;
+        *reinterpret_cast<uint4*>(codes) = from_stage[0];
+        *reinterpret_cast<uint4*>(codes + 512) = from_stage[32];
+        if (lane < (values ? 8 : 16)) *reinterpret_cast<uint4*>(scales) = from_stage[64];
         __syncwarp();
     }
 }
@@ -230,18 +274,17 @@ __global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_consta
     }
 }
 
-int grid_of(const PackArgs& a, int num_sms) {
-    const int64_t ctas = (static_cast<int64_t>(a.n) * a.hkv + kWarps - 1) / kWarps;
-    return static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(num_sms) * 8));
+int grid_of(int64_t items, int num_sms) {
+    return static_cast<int>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 8));
 }
 
 }  // namespace
 
 cudaError_t launch_pack(const PackArgs& a, int num_sms, cudaStream_t stream) {
-    return launch_dependent(pack_kernel, grid_of(a, num_sms), kWarps * 32, 0, stream, 1, a);
+    return launch_dependent(pack_kernel, grid_of(2 * static_cast<int64_t>(a.n) * a.hkv, num_sms), kWarps * 32, 0, stream, 1, a);
 }
 cudaError_t launch_unpack(const PackArgs& a, int num_sms, cudaStream_t stream) {
-    return launch_dependent(unpack_kernel, grid_of(a, num_sms), kWarps * 32, 0, stream, 1, a);
+    return launch_dependent(unpack_kernel, grid_of(static_cast<int64_t>(a.n) * a.hkv, num_sms), kWarps * 32, 0, stream, 1, a);
 }
 
 }  // namespace locks

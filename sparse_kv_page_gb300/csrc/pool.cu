@@ -2,11 +2,11 @@
 // compacting pages.
 //
 // Which pages are free follows from the reference counts alone, so the calls that look for
-// free pages (fork, take) or rank the used ones (compact) scan them: one cluster of CTAs, a
-// contiguous segment of the pool to a warp, counts joined through distributed shared memory.
-// 4 bytes a page are little (1M pages: 4 MB, which L2 holds), and what bounds these calls is
-// latency: one round of loads to count, a barrier, one to place. Tables are rewritten by all
-// SMs in a second launch, which starts while the first runs.
+// free pages (fork, take) or rank the used ones (compact) scan them in two launches: one counts
+// them by blocks of the pool (and plans, in a block of its own, who needs how many pages), the
+// next knows every page's rank from the blocks' counts and places it. A call is short, a few MB at
+// most, so what bounds it are the launches and the loads that wait for one another; each launch
+// starts while the one before it runs.
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -16,34 +16,32 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
-constexpr int kScanRows = 4096;                       // rows whose prefix sums lie in shared memory
+constexpr int kRound = 4 * kThreads;                  // pages, or entries of a row, that a block takes at a time
+constexpr int kScanRows = 2048;                       // rows whose sums lie in shared memory
 
 __device__ __forceinline__ bool in_table(int tokens, int max_pages) {
     return tokens >= 0 && tokens <= static_cast<int64_t>(max_pages) * kPage;
 }
 __device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
 
-// This warp's segment of the pool: pages first .. last, a multiple of 128 but for the pool's end.
+// Block i of the pool: pages first .. last, a multiple of kRound but for the pool's end.
 struct Segment {
     int first, last;
 };
-__device__ __forceinline__ Segment segment_of(int pages) {
-    const int64_t warps = static_cast<int64_t>(cluster_size()) * kWarps;
-    const int64_t per = (pages + warps * 128 - 1) / (warps * 128) * 128;
-    const int64_t first = (static_cast<int64_t>(cluster_ctarank()) * kWarps + (threadIdx.x >> 5)) * per;
-    return {static_cast<int>(min(first, static_cast<int64_t>(pages))),
-            static_cast<int>(min(first + per, static_cast<int64_t>(pages)))};
+__host__ __device__ inline int pool_blocks(int pages) {
+    const int n = (pages + kRound - 1) / kRound;
+    return n < kMaxPoolBlocks ? n : kMaxPoolBlocks;
+}
+__device__ __forceinline__ Segment segment_of(int pages, int i) {
+    const int64_t blocks = max(1, pool_blocks(pages));
+    const int64_t per = (pages + blocks * kRound - 1) / (blocks * kRound) * kRound;
+    return {static_cast<int>(min(i * per, static_cast<int64_t>(pages))),
+            static_cast<int>(min((i + 1) * per, static_cast<int64_t>(pages)))};
 }
 // Counts of pages at .. at + 3 (a lane's), those past `last` as if held by nobody and not free.
 __device__ __forceinline__ int4 load4(const int32_t* refs, int at, int last) {
     if (at + 4 <= last) return __ldcg(reinterpret_cast<const int4*>(refs + at));
-    int4 r;
+    int4 r;                                           // (at may be past the end altogether)
     r.x = at < last ? __ldcg(refs + at) : INT32_MIN;
     r.y = at + 1 < last ? __ldcg(refs + at + 1) : INT32_MIN;
     r.z = at + 2 < last ? __ldcg(refs + at + 2) : INT32_MIN;
@@ -82,81 +80,88 @@ __device__ __forceinline__ int warp_upto(int x) {     // inclusive sum over the 
     return x;
 }
 
-// Counts pages of a kind (free4 or used4) in this warp's segment, and copies the counts to
-// refs_out on the way where that is another array.
-template <typename Kind>
-__device__ __forceinline__ int count_segment(const PoolArgs& a, const Segment& seg, Kind kind) {
-    const int lane = threadIdx.x & 31;
-    int n = 0;
-    const bool copy = a.refs_out != a.refs;
-#pragma unroll 4
-    for (int at = seg.first + 4 * lane; at < seg.last; at += 128) {
-        const int4 r = load4(a.refs, at, seg.last);
-        n += __popc(kind(r));
-        if (copy) store4(a.refs_out, at, seg.last, r);
-    }
-    return warp_sum(n);
+__device__ __forceinline__ int block_sum(int x, int* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = warp_sum(x);
+    if (lane == 0) scratch[warp] = x;
+    __syncthreads();
+    x = warp_sum(scratch[lane]);
+    __syncthreads();
+    return x;
 }
 
-// Calls f(page, rank) for the pages of a kind in this warp's segment, ranks counted from `rank`;
-// stops behind rank `most`.
-template <typename Kind, typename F>
-__device__ __forceinline__ void walk_segment(const PoolArgs& a, const Segment& seg, Kind kind, int rank, int most, F f) {
-    const int lane = threadIdx.x & 31;
+// Counts pages of a kind (free4 or used4) in block i of the pool, and copies the counts to refs_out
+// on the way where that is another array. `flags`: keeps which they are, four pages a byte (the next
+// launch may change the counts in place while it looks for the pages).
+template <typename Kind>
+__device__ __forceinline__ int count_block(const PoolArgs& a, int i, Kind kind, bool flags, int* scratch) {
+    const Segment seg = segment_of(a.num_pages, i);
+    const bool copy = a.refs_out != a.refs;
+    int n = 0;
 #pragma unroll 2
-    for (int at0 = seg.first; at0 < seg.last; at0 += 128) {
-        if (rank >= most) return;
-        const int at = at0 + 4 * lane;
-        const unsigned bits = at < seg.last ? kind(load4(a.refs, at, seg.last)) : 0u;
+    for (int at = seg.first + 4 * threadIdx.x; at < seg.last; at += kRound) {
+        const int4 r = load4(a.refs, at, seg.last);
+        const unsigned bits = kind(r);
+        n += __popc(bits);
+        if (flags) a.flags[at / 4] = static_cast<uint8_t>(bits);
+        if (copy) store4(a.refs_out, at, seg.last, r);
+    }
+    n = block_sum(n, scratch);
+    if (threadIdx.x == 0) a.block_counts[i] = n;
+    return n;
+}
+
+// How many of the kind are before block i of the pool, and in all.
+__device__ __forceinline__ void join_counts(const PoolArgs& a, int i, int* scratch, int& before, int& total) {
+    const int blocks = pool_blocks(a.num_pages), tid = threadIdx.x;
+    const int n = tid < blocks ? __ldcg(a.block_counts + tid) : 0;
+    before = block_sum(tid < i ? n : 0, scratch);
+    total = block_sum(n, scratch);
+}
+static_assert(kMaxPoolBlocks <= kThreads, "a thread per block of the pool");
+
+// Calls f(page, rank) for the flagged pages in a segment, ranks counted from `rank`; stops behind
+// rank `most`.
+template <typename F>
+__device__ __forceinline__ void walk_segment(const PoolArgs& a, const Segment& seg, int rank, int most, int* scratch,
+                                             F f) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int at0 = seg.first; at0 < seg.last && rank < most; at0 += kRound) {
+        const int at = at0 + 4 * threadIdx.x;
+        const unsigned bits = at < seg.last ? __ldcg(a.flags + at / 4) : 0u;
         const int upto = warp_upto(__popc(bits));
-        int r = rank + upto - __popc(bits);
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        const int sums = scratch[lane];
+        int r = rank + upto - __popc(bits) + warp_sum(lane < warp ? sums : 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (bits >> k & 1u) {
                 if (r < most) f(at + k, r);
                 ++r;
             }
-        rank += __shfl_sync(kAll, upto, 31);
+        rank += warp_sum(sums);
+        __syncthreads();
     }
 }
 
-// What the cluster's CTAs share: the warps' counts and the CTA's.
-struct Counts {
-    int warp[kWarps];
-    int cta;
-    int extra;                                        // compact: used pages below the end of the used ones
-};
-// From the warps' counts: how many of the kind are before this warp's segment, and in all.
-__device__ __forceinline__ void join_counts(Counts& c, int mine, int& before, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) c.warp[warp] = mine;
-    __syncthreads();
-    if (warp == 0) {
-        const int n = warp_sum(c.warp[lane]);
-        if (lane == 0) c.cta = n;
-    }
-    cluster_sync_all();
-    const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
-    const int x = lane < ctas ? static_cast<int>(ld_dsmem_u32(dsmem_addr(&c.cta, lane))) : 0;
-    total = warp_sum(x);
-    before = warp_sum(lane < rank ? x : 0) + warp_sum(lane < warp ? c.warp[lane] : 0);
-}
-
-// Sums over the batch, by one CTA: calls put(b, sum of count(0..b)) for every row in turn of
-// its thread, and returns the sum of all.
+// Sums over the batch, by one block: calls put(b, sum of count(0..b), count(b), extra) for every row in
+// turn of its thread, with the extra number that count(b, extra) gave; returns the sum of all.
 template <typename Count, typename Put>
 __device__ __forceinline__ int scan_rows(int batch, int* scratch, Count count, Put put) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int base = 0;
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        const int mine = b < batch ? count(b) : 0;
+        int extra = 0;
+        const int mine = b < batch ? count(b, extra) : 0;
         int upto = warp_upto(mine);
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
         const int sums = scratch[lane];
         upto += base + warp_sum(lane < warp ? sums : 0);
-        if (b < batch) put(b, upto, mine);
+        if (b < batch) put(b, upto, mine, extra);
         base += warp_sum(sums);
         __syncthreads();
     }
@@ -172,52 +177,80 @@ __device__ __forceinline__ int pages_needed(const PoolArgs& a, int b) {
     return pages_of(now) - pages_of(old);
 }
 
-__global__ void __launch_bounds__(kThreads) take_kernel(const __grid_constant__ PoolArgs a) {
-    __shared__ Counts counts;
-    __shared__ int scratch[kWarps], near_scan[kScanRows], served;
-    const int tid = threadIdx.x, rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_size());
+// First launch: free pages, by block of the pool; pages needed by rows 0..b, and what turns the rank
+// of a free page into its place in the row.
+__global__ void __launch_bounds__(kThreads) take_count_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps];
     grid_dependency_wait();
     allow_dependent_launch();
-    const Segment seg = segment_of(a.num_pages);
-    const int free_here = count_segment(a, seg, free4);
-    // pages needed by rows 0..b: in every CTA, or where the rows are many by one for all
-    const bool near = a.batch <= kScanRows;
-    int* const scan = near ? near_scan : a.scan;
-    if (tid == 0) served = 0;
-    if (near || rank == 0)
-        scan_rows(a.batch, scratch, [&](int b) { return max(0, pages_needed(a, b)); },
-                  [&](int b, int upto, int) { scan[b] = upto; });
+    if (blockIdx.x > 0) {
+        count_block(a, blockIdx.x - 1, free4, true, scratch);
+        return;
+    }
+    scan_rows(a.batch, scratch,
+              [&](int b, int& old) {
+                  const int need = pages_needed(a, b);
+                  old = need > 0 ? pages_of(__ldcg(a.seq_tokens + b)) : 0;
+                  return max(0, need);
+              },
+              [&](int b, int sum, int mine, int old) {
+                  a.scan[b] = sum;
+                  a.shift[b] = old - (sum - mine);
+              });
+}
+
+__global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps], near_upto[kScanRows], near_shift[kScanRows], served;
+    const int tid = threadIdx.x, blocks = pool_blocks(a.num_pages), block = blockIdx.x;
+    grid_dependency_wait();
+    allow_dependent_launch();
     int before, free;
-    join_counts(counts, free_here, before, free);
+    join_counts(a, block, scratch, before, free);
     // rows whose pages are all there: those before the first that lacks some
-    int mine = 0;
-    for (int b = tid; b < a.batch; b += kThreads)
-        if (scan[b] <= free) mine = max(mine, scan[b]);
-    if (mine > 0) atomicMax(&served, mine);
-    __syncthreads();
-    const int taken = served;
-    walk_segment(a, seg, free4, before, taken, [&](int page, int r) {
-        int lo = 0, hi = a.batch - 1;                 // the first row whose sum passes r
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (scan[mid] > r) hi = mid;
-            else lo = mid + 1;
+    int taken = a.batch > 0 ? __ldcg(a.scan + a.batch - 1) : 0;
+    if (taken > free) {
+        if (tid == 0) served = 0;
+        __syncthreads();
+        int mine = 0;
+        for (int b = tid; b < a.batch; b += kThreads) {
+            const int upto = __ldcg(a.scan + b);
+            if (upto <= free) mine = max(mine, upto);
         }
-        const int j = pages_of(__ldcg(a.seq_tokens + lo)) + r - (lo > 0 ? scan[lo - 1] : 0);
-        a.page_table_out[static_cast<int64_t>(lo) * a.max_pages + j] = page;
-        a.refs_out[page] = 1;
-    });
-    // seq_tokens is read above by every CTA (and may be seq_tokens_out)
-    cluster_sync_all();
-    for (int b = rank * kThreads + tid; b < a.batch; b += ctas * kThreads) {
+        if (mine > 0) atomicMax(&served, mine);
+        __syncthreads();
+        taken = served;
+    }
+    if (block < blocks && before < taken) {
+        const bool near = a.batch <= kScanRows;
+        if (near) {
+            for (int b = tid; b < a.batch; b += kThreads) near_upto[b] = __ldcg(a.scan + b), near_shift[b] = __ldcg(a.shift + b);
+            __syncthreads();
+        }
+        const int* const upto = near ? near_upto : a.scan;
+        const int* const shift = near ? near_shift : a.shift;
+        int lo = 0;                                   // the first row whose sum passes r, which only grows
+        walk_segment(a, segment_of(a.num_pages, block), before, taken, scratch, [&](int page, int r) {
+            if (upto[lo] <= r) {
+                int hi = a.batch - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (upto[mid] > r) hi = mid;
+                    else lo = mid + 1;
+                }
+            }
+            a.page_table_out[static_cast<int64_t>(lo) * a.max_pages + shift[lo] + r] = page;
+            a.refs_out[page] = 1;
+        });
+    }
+    for (int b = block * kThreads + tid; b < a.batch; b += gridDim.x * kThreads) {
         const int need = pages_needed(a, b);
         int tokens = __ldcg(a.seq_tokens + b);
         if (need < 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-        else if (need > 0 && scan[b] > free) report_error(a.st, LOCKS_ERR_NO_PAGES);
+        else if (need > 0 && __ldcg(a.scan + b) > free) report_error(a.st, LOCKS_ERR_NO_PAGES);
         else tokens = __ldcg(a.new_tokens + b);
         a.seq_tokens_out[b] = tokens;
     }
-    if (a.n_free && rank == 0 && tid == 0) *a.n_free = free - taken;
+    if (a.n_free && block == 0 && tid == 0) *a.n_free = free - taken;
 }
 
 // ------------------------------------------------------------------ fork
@@ -236,93 +269,98 @@ __device__ __forceinline__ bool needs_page(const PoolArgs& a, int b) {
     return p >= 0 && tokens_of(a, p) % kPage != 0 && __ldcg(a.keeper + p) != b;
 }
 
-__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PoolArgs a) {
-    __shared__ Counts counts;
-    __shared__ int scratch[kWarps], needed;
-    const int tid = threadIdx.x, rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_size());
+// First launch: free pages, by block of the pool; the rows' children and who needs a page.
+__global__ void __launch_bounds__(kThreads) fork_count_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps];
+    const int tid = threadIdx.x;
     grid_dependency_wait();
     allow_dependent_launch();
-    const Segment seg = segment_of(a.num_pages);
-    const int free_here = count_segment(a, seg, free4);
-    if (rank == 0) {
-        for (int b = tid; b < a.batch; b += kThreads) {
-            a.children[b] = 0;
-            a.keeper[b] = a.batch;
-            const int n = __ldcg(a.seq_tokens + b), p = __ldcg(a.parents + b);
-            if (!in_table(n, a.max_pages) || p < -1 || p >= a.batch) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-        }
-        __syncthreads();
-        for (int b = tid; b < a.batch; b += kThreads) {
-            const int p = parent_of(a, b);
-            if (p < 0) continue;
-            atomicAdd(a.children + p, 1);
-            atomicMin(a.keeper + p, b == p ? -1 : b);
-        }
-        __syncthreads();
-        for (int b = tid; b < a.batch; b += kThreads)
-            if (__ldcg(a.keeper + b) < 0) a.keeper[b] = b;
-        __syncthreads();
-        const int n = scan_rows(a.batch, scratch, [&](int b) { return needs_page(a, b) ? 1 : 0; },
-                                [&](int b, int upto, int mine) {
-                                    if (mine) a.fresh[upto - 1] = b;
-                                    a.scan[b] = upto;
-                                });
-        if (tid == 0) needed = n;
+    if (blockIdx.x > 0) {
+        count_block(a, blockIdx.x - 1, free4, true, scratch);
+        return;
     }
-    int before, free;
-    join_counts(counts, free_here, before, free);
-    const int want = static_cast<int>(ld_dsmem_u32(dsmem_addr(&needed, 0)));
-    const int n = min(want, free);
-    walk_segment(a, seg, free4, before, n, [&](int page, int r) {
-        const int b = __ldcg(a.fresh + r), p = parent_of(a, b), at = tokens_of(a, p) / kPage;
-        a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
-        a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(p) * a.max_pages + at);
-        a.list_dst[r] = page;
-        a.refs_out[page] = 1;
-    });
-    for (int b = rank * kThreads + tid; b < a.batch; b += ctas * kThreads) {
+    for (int b = tid; b < a.batch; b += kThreads) {
+        a.children[b] = 0;
+        a.keeper[b] = a.batch;
+        const int n = __ldcg(a.seq_tokens + b), p = __ldcg(a.parents + b);
+        if (!in_table(n, a.max_pages) || p < -1 || p >= a.batch) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+    }
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += kThreads) {
         const int p = parent_of(a, b);
-        int tokens = p >= 0 ? tokens_of(a, p) : 0;
-        if (needs_page(a, b) && __ldcg(a.scan + b) > free) {
-            report_error(a.st, LOCKS_ERR_NO_PAGES);
-            tokens = tokens / kPage * kPage;
-        }
-        a.seq_tokens_out[b] = tokens;
+        if (p < 0) continue;
+        atomicAdd(a.children + p, 1);
+        atomicMin(a.keeper + p, b == p ? -1 : b);
     }
-    if (rank == 0 && tid == 0) *a.n_list = n;
-    cluster_sync_all();                               // `needed` is read by all
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += kThreads)
+        if (__ldcg(a.keeper + b) < 0) a.keeper[b] = b;
+    __syncthreads();
+    const int n = scan_rows(a.batch, scratch, [&](int b, int&) { return needs_page(a, b) ? 1 : 0; },
+                            [&](int b, int upto, int mine, int) {
+                                if (mine) a.fresh[upto - 1] = b;
+                                a.scan[b] = upto;
+                            });
+    if (tid == 0) *a.needed = n;
 }
 
-// The tables' rows, and what their holds change by. A block takes a piece of a row.
-constexpr int kRowThreads = 256, kRowPiece = 4 * kRowThreads;
-__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const __grid_constant__ PoolArgs a, int pieces) {
-    const int b = blockIdx.x / pieces, j0 = (blockIdx.x % pieces) * kRowPiece + threadIdx.x;
+// Second launch: the first blocks place the free pages; of the others each takes a piece of a row: the
+// tables' rows, and what their holds change by.
+__global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_constant__ PoolArgs a, int pieces) {
+    __shared__ int scratch[kWarps];
+    const int tid = threadIdx.x, blocks = pool_blocks(a.num_pages);
     grid_dependency_wait();
     allow_dependent_launch();
+    if (static_cast<int>(blockIdx.x) <= blocks) {     // (a block more, for a pool without pages)
+        const int block = blockIdx.x;
+        int before, free;
+        join_counts(a, block, scratch, before, free);
+        const int n = min(__ldcg(a.needed), free);
+        if (block < blocks)
+            walk_segment(a, segment_of(a.num_pages, block), before, n, scratch, [&](int page, int r) {
+                const int b = __ldcg(a.fresh + r), p = parent_of(a, b), at = tokens_of(a, p) / kPage;
+                a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
+                a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(p) * a.max_pages + at);
+                a.list_dst[r] = page;
+                a.refs_out[page] = 1;                 // nobody's until now: the rows' blocks leave it alone
+            });
+        for (int b = block * kThreads + tid; b < a.batch; b += (blocks + 1) * kThreads) {
+            const int p = parent_of(a, b);
+            int tokens = p >= 0 ? tokens_of(a, p) : 0;
+            if (needs_page(a, b) && __ldcg(a.scan + b) > free) {
+                report_error(a.st, LOCKS_ERR_NO_PAGES);
+                tokens = tokens / kPage * kPage;
+            }
+            a.seq_tokens_out[b] = tokens;
+        }
+        if (block == 0 && tid == 0) *a.n_list = n;
+        return;
+    }
+    const int x = blockIdx.x - blocks - 1, b = x / pieces, j0 = (x % pieces) * kRound + tid;
     const int p = parent_of(a, b);
     const int64_t row = static_cast<int64_t>(b) * a.max_pages;
     if (p >= 0) {                                     // row b of the new table
         const int n = tokens_of(a, p), full = n / kPage;
         const int end = full + (n % kPage != 0 && __ldcg(a.keeper + p) == b ? 1 : 0);
         const int32_t* from = a.page_table + static_cast<int64_t>(p) * a.max_pages;
-        int x[4];
+        int page[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = j0 + i * kRowThreads;
-            if (j < end) x[i] = __ldcg(from + j);
+            const int j = j0 + i * kThreads;
+            if (j < end) page[i] = __ldcg(from + j);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = j0 + i * kRowThreads;
-            if (j < end) a.page_table_out[row + j] = x[i];
+            const int j = j0 + i * kThreads;
+            if (j < end) a.page_table_out[row + j] = page[i];
         }
     }
-    const int n = tokens_of(a, b), full = n / kPage, children = __ldcg(a.children + b);
+    const int n = tokens_of(a, b), children = __ldcg(a.children + b);
     if (children == 1) return;                        // every page has as many holders as before
-    const int end = children == 0 ? pages_of(n) : full;   // a last page is kept by one child
+    const int end = children == 0 ? pages_of(n) : n / kPage;      // a last page is kept by one child
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kRowThreads;
+        const int j = j0 + i * kThreads;
         if (j >= end) continue;
         const int page = __ldcg(a.page_table + row + j);
         if (page >= 0 && page < a.num_pages) atomicAdd(a.refs_out + page, children - 1);
@@ -332,6 +370,7 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const __grid_con
 
 // ------------------------------------------------------------------ free
 
+constexpr int kRowThreads = 256, kRowPiece = 4 * kRowThreads;
 __global__ void __launch_bounds__(kRowThreads) copy_refs_kernel(const __grid_constant__ PoolArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -370,64 +409,85 @@ __global__ void __launch_bounds__(kRowThreads) free_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ compact
 
-__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ PoolArgs a) {
-    __shared__ Counts counts;
-    const int tid = threadIdx.x, lane = tid & 31, rank = static_cast<int>(cluster_ctarank());
-    const int ctas = static_cast<int>(cluster_size());
+__global__ void __launch_bounds__(kThreads) compact_count_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps];
     grid_dependency_wait();
     allow_dependent_launch();
-    const Segment seg = segment_of(a.num_pages);
-    if (tid == 0) counts.extra = 0;
-    const int used_here = count_segment(a, seg, used4);
-    int before, used;
-    join_counts(counts, used_here, before, used);
-    // used pages below id `used`: known where that lies
-    if (seg.first <= used && used < seg.last) {
-        int n = 0;
-        for (int at = seg.first + 4 * lane; at < used; at += 128) {
-            const unsigned bits = used4(load4(a.refs, at, seg.last));
-            n += __popc(bits & (at + 4 <= used ? 15u : (1u << (used - at)) - 1u));
-        }
-        n = warp_sum(n);
-        if (lane == 0) counts.extra = before + n;
+    count_block(a, blockIdx.x, used4, false, scratch);
+}
+
+// How many pages are used, and how many of those lie below the id of that number: all others move.
+// A pool of one block is counted here, which saves it a launch.
+__device__ __forceinline__ void find_moves(const PoolArgs& a, int i, int* scratch, int& before, int& used, int& low) {
+    const bool one = pool_blocks(a.num_pages) == 1;
+    before = 0;
+    if (one) used = count_block(a, 0, used4, false, scratch);
+    else join_counts(a, i, scratch, before, used);
+    low = used;
+    if (used >= a.num_pages) return;
+    const int64_t per = segment_of(a.num_pages, 0).last;
+    const int edge = static_cast<int>(used / per);    // the block that `used` lies in
+    int ahead = 0, n = 0;
+    if (!one) join_counts(a, edge, scratch, ahead, n);
+    n = 0;
+    const Segment seg = segment_of(a.num_pages, edge);
+    for (int at = seg.first + 4 * threadIdx.x; at < used; at += kRound) {
+        const unsigned bits = used4(load4(a.refs, at, seg.last));
+        n += __popc(bits & (at + 4 <= used ? 15u : (1u << (used - at)) - 1u));
     }
-    cluster_sync_all();
-    int low = lane < ctas ? static_cast<int>(ld_dsmem_u32(dsmem_addr(&counts.extra, lane))) : 0;
-    low = used < a.num_pages ? warp_sum(low) : used;  // one CTA's, 0 in the others
-    const int moves = used - low;
-    // the k-th hole below `used` and the k-th used page from there on
-    int rank_used = before;
-    for (int at0 = seg.first; at0 < seg.last; at0 += 128) {
-        const int at = at0 + 4 * lane;
-        const unsigned bits = at < seg.last ? used4(load4(a.refs, at, seg.last)) : 0u;
+    low = ahead + block_sum(n, scratch);
+}
+
+// Second launch: the k-th hole below `used` and the k-th used page from there on. A page that moves
+// has -1 - k for its new id until the third launch.
+__global__ void __launch_bounds__(kThreads) compact_place_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int rank, used, low;
+    find_moves(a, blockIdx.x, scratch, rank, used, low);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_list = used - low;
+    const Segment seg = segment_of(a.num_pages, blockIdx.x);
+#pragma unroll 1
+    for (int at0 = seg.first; at0 < seg.last; at0 += kRound) {
+        const int at = at0 + 4 * threadIdx.x;
+        const unsigned bits = used4(load4(a.refs, at, seg.last));
         const int upto = warp_upto(__popc(bits));
-        int u = rank_used + upto - __popc(bits);      // used pages before at + k
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        const int sums = scratch[lane];
+        int u = rank + upto - __popc(bits) + warp_sum(lane < warp ? sums : 0);     // used pages before at + k
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int page = at + k;
-            if (page >= seg.last) break;
             const bool on = bits >> k & 1u;
-            if (on && page >= used) a.list_src[u - low] = page;
-            if (!on && page < used) a.list_dst[page - u] = page;
-            a.new_page[page] = page;
+            if (page < seg.last) {
+                if (on && page >= used) a.list_src[u - low] = page;
+                if (!on && page < used) a.list_dst[page - u] = page;
+                a.new_page[page] = on && page >= used ? -1 - (u - low) : page;
+            }
             u += on;
         }
-        rank_used += __shfl_sync(kAll, upto, 31);
+        rank += warp_sum(sums);
+        __syncthreads();
     }
-    cluster_sync_all();
-    for (int i = rank * kThreads + tid; i < moves; i += ctas * kThreads) {
+}
+
+// Third launch: a block takes a piece of a row of the tables, and all of them the moves. (An entry
+// of new_page that another block is just setting is as good before as after.)
+__global__ void __launch_bounds__(kThreads) renumber_kernel(const __grid_constant__ PoolArgs a, int pieces) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int moves = __ldcg(a.n_list);
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < moves; i += gridDim.x * kThreads) {
         const int from = __ldcg(a.list_src + i), to = __ldcg(a.list_dst + i);
         a.new_page[from] = to;
         a.refs_out[to] = __ldcg(a.refs + from);
         a.refs_out[from] = 0;
     }
-    if (rank == 0 && tid == 0) *a.n_list = moves;
-}
-
-__global__ void __launch_bounds__(kRowThreads) renumber_kernel(const __grid_constant__ PoolArgs a, int pieces) {
-    const int b = blockIdx.x / pieces, j0 = (blockIdx.x % pieces) * kRowPiece + threadIdx.x;
-    grid_dependency_wait();
-    allow_dependent_launch();
+    const int b = blockIdx.x / pieces, j0 = (blockIdx.x % pieces) * kRound + threadIdx.x;
+    if (b >= a.batch) return;
     const int n = __ldcg(a.seq_tokens + b);
     if (!in_table(n, a.max_pages)) {
         if (j0 == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
@@ -438,19 +498,23 @@ __global__ void __launch_bounds__(kRowThreads) renumber_kernel(const __grid_cons
     int x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kRowThreads;
+        const int j = j0 + i * kThreads;
         x[i] = j < end ? __ldcg(a.page_table + row + j) : 0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kRowThreads;
+        const int j = j0 + i * kThreads;
         if (j >= end) continue;
-        if (x[i] >= 0 && x[i] < a.num_pages) x[i] = __ldcg(a.new_page + x[i]);
-        else report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        if (x[i] >= 0 && x[i] < a.num_pages) {
+            x[i] = __ldcg(a.new_page + x[i]);
+            if (x[i] < 0) x[i] = __ldcg(a.list_dst + (-1 - x[i]));
+        } else {
+            report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kRowThreads;
+        const int j = j0 + i * kThreads;
         if (j < end) a.page_table_out[row + j] = x[i];
     }
 }
@@ -512,47 +576,46 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     }
 }
 
-// CTAs of the cluster that scans the pool: each takes about 8192 pages, two loads a thread.
-int cluster_of(int pages) {
-    int n = 1;
-    while (n < kMaxCluster && static_cast<int64_t>(n) * 8192 < pages) n *= 2;
-    return n;
-}
-template <auto Kern>
-cudaError_t launch_scan(const PoolArgs& a, cudaStream_t stream) {
-    const int n = cluster_of(a.num_pages);
-    const cudaError_t e = ensure_kernel_attrs<Kern>(0, true);
-    return e != cudaSuccess ? e : launch_dependent(Kern, n, kThreads, 0, stream, n, a);
-}
-int pieces_of(int max_pages) { return (max_pages + kRowPiece - 1) / kRowPiece; }
+int pieces_of(int max_pages, int piece) { return std::max(1, (max_pages + piece - 1) / piece); }
 
 }  // namespace
 
-PoolLayout pool_layout(int batch) {
+PoolLayout pool_layout(int batch, int pages) {
     const size_t row = (static_cast<size_t>(batch) * 4 + 255) / 256 * 256;
     PoolLayout w;
-    w.scan = 256;
-    w.children = w.scan + row;
-    w.keeper = w.children + row;
+    w.needed = 256;
+    w.block_counts = w.needed + 256;
+    w.scan = w.block_counts + kMaxPoolBlocks * sizeof(int32_t);
+    w.shift = w.scan + row;
+    w.keeper = w.shift + row;
     w.fresh = w.keeper + row;
-    w.bytes = w.fresh + row;
+    w.flags = w.fresh + row;
+    w.bytes = w.flags + (static_cast<size_t>(pages) / 4 + 256) / 256 * 256;
     return w;
 }
 
-cudaError_t launch_take(const PoolArgs& a, cudaStream_t stream) { return launch_scan<take_kernel>(a, stream); }
-
-cudaError_t launch_fork(const PoolArgs& a, int, cudaStream_t stream) {
-    const cudaError_t e = launch_scan<fork_kernel>(a, stream);
-    const int pieces = pieces_of(a.max_pages);
-    if (e != cudaSuccess || pieces == 0 || a.batch == 0) return e;
-    return launch_dependent(fork_rows_kernel, static_cast<int64_t>(a.batch) * pieces, kRowThreads, 0, stream, 1, a, pieces);
+cudaError_t launch_take(const PoolArgs& a, cudaStream_t stream) {
+    const int blocks = pool_blocks(a.num_pages);
+    const cudaError_t e = launch_dependent(take_count_kernel, blocks + 1, kThreads, 0, stream, 1, a);
+    return e != cudaSuccess ? e : launch_dependent(take_place_kernel, blocks + 1, kThreads, 0, stream, 1, a);
 }
 
-cudaError_t launch_compact(const PoolArgs& a, int, cudaStream_t stream) {
-    const cudaError_t e = launch_scan<compact_kernel>(a, stream);
-    const int pieces = pieces_of(a.max_pages);
-    if (e != cudaSuccess || pieces == 0 || a.batch == 0) return e;
-    return launch_dependent(renumber_kernel, static_cast<int64_t>(a.batch) * pieces, kRowThreads, 0, stream, 1, a, pieces);
+cudaError_t launch_fork(const PoolArgs& a, cudaStream_t stream) {
+    const int blocks = pool_blocks(a.num_pages), pieces = pieces_of(a.max_pages, kRound);
+    const cudaError_t e = launch_dependent(fork_count_kernel, blocks + 1, kThreads, 0, stream, 1, a);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = a.max_pages > 0 ? static_cast<int64_t>(a.batch) * pieces : 0;
+    return launch_dependent(fork_place_kernel, blocks + 1 + rows, kThreads, 0, stream, 1, a, pieces);
+}
+
+cudaError_t launch_compact(const PoolArgs& a, cudaStream_t stream) {
+    const int blocks = std::max(1, pool_blocks(a.num_pages)), pieces = pieces_of(a.max_pages, kRound);
+    cudaError_t e = blocks > 1 ? launch_dependent(compact_count_kernel, blocks, kThreads, 0, stream, 1, a) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(compact_place_kernel, blocks, kThreads, 0, stream, 1, a);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = std::max<int64_t>(1, a.max_pages > 0 ? static_cast<int64_t>(a.batch) * pieces : 0);
+    return launch_dependent(renumber_kernel, rows, kThreads, 0, stream, 1, a, pieces);
 }
 
 cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream) {
@@ -562,7 +625,7 @@ cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     if (a.rows == 0 || a.stride == 0) return cudaSuccess;
-    const int pieces = pieces_of(a.stride);
+    const int pieces = pieces_of(a.stride, kRowPiece);
     const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(a.rows) * pieces, static_cast<int64_t>(num_sms) * 64);
     return launch_dependent(free_kernel, ctas, kRowThreads, 0, stream, 1, a, pieces);
 }

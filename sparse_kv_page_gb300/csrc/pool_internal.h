@@ -90,20 +90,25 @@ struct PoolArgs {
     int rows, stride;              // free
     int batch, max_pages, num_pages;
     // workspace regions (pool_layout)
-    int32_t* scan;                 // [batch]: take: pages needed by rows 0..b
-    int32_t* children;             // fork: [batch] rows that continue row p
+    int32_t* needed;               // fork: fresh pages
+    int32_t* block_counts;         // [kMaxPoolBlocks] free or used pages of each block of the pool
+    int32_t* scan;                 // [batch] pages needed by rows 0..b
+    int32_t* shift;                // take: [batch] from a page's rank to its place in the row
+    int32_t* children;             // fork: [batch] rows that continue row p (the same region)
     int32_t* keeper;               // fork: [batch] the child that keeps p's last page
     int32_t* fresh;                // fork: [batch] row of the i-th fresh page
+    uint8_t* flags;                // [pages / 4]: bits of the free pages
     DeviceStatus st;
 };
+constexpr int kMaxPoolBlocks = 512;
 struct PoolLayout {
-    size_t scan, children, keeper, fresh, bytes;
+    size_t needed, block_counts, scan, shift, keeper, fresh, flags, bytes;
 };
-PoolLayout pool_layout(int batch);
-cudaError_t launch_fork(const PoolArgs& a, int num_sms, cudaStream_t stream);
+PoolLayout pool_layout(int batch, int pages);
+cudaError_t launch_fork(const PoolArgs& a, cudaStream_t stream);
 cudaError_t launch_take(const PoolArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const PoolArgs& a, cudaStream_t stream);
 cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_compact(const PoolArgs& a, int num_sms, cudaStream_t stream);
 
 // kernel<<<ctas, threads, smem>>> that may start while the kernel before it on the stream is
 // still running (it has to call grid_dependency_wait before its first global access), in
