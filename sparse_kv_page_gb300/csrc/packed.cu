@@ -36,8 +36,8 @@ __device__ __forceinline__ Two two(float a, float b) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
     return d;
 }
-__device__ __forceinline__ void parts_of(Two x, uint32_t& a, uint32_t& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+__device__ __forceinline__ void parts_of(Two x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     Two d;
@@ -57,49 +57,74 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
 
 // Quotients below are rounded as fp32 division rounds them, by Markstein's theorem (IBM J. Res. Dev.
 // 34, 1990): with r the correctly rounded 1 / s, q = v r and q + (v - s q) r is the rounded v / s.
+// (Newton's step makes r of the approximate reciprocal; for the 8-bit scales here it is the rounded
+// one, for each of them.) How a quotient is rounded matters: bf16 values lie on borders between two
+// codes often, and there the product with the reciprocal alone may fall to either side.
 
-// Scale and zero (bf16 bits) of a group that kLanes neighbouring lanes hold, eight values each.
-template <int kLanes>
-__device__ __forceinline__ void group_scale(const uint4& x, uint32_t& scale, uint32_t& zero) {
-    uint32_t lo = bf16x2_min(bf16x2_min(x.x, x.y), bf16x2_min(x.z, x.w));
-    uint32_t hi = bf16x2_max(bf16x2_max(x.x, x.y), bf16x2_max(x.z, x.w));
-#pragma unroll
-    for (int o = 1; o < kLanes; o *= 2) {
-        lo = bf16x2_min(lo, __shfl_xor_sync(kAll, lo, o));
-        hi = bf16x2_max(hi, __shfl_xor_sync(kAll, hi, o));
-    }
-    lo = bf16x2_min(lo, lo >> 16 | lo << 16);
-    hi = bf16x2_max(hi, hi >> 16 | hi << 16);
-    const float range = __fsub_rn(low_of(hi), low_of(lo)), by = 1.f / 15.f, q = __fmul_rn(range, by);
-    scale = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-15.f, q, range), by, q)));
-    if (scale < 0x0080u) scale = 0;               // below 2^-126
-    zero = lo & 0xffffu;
+// Least and greatest of eight values as a pair (least, -greatest): both are then minima.
+__device__ __forceinline__ uint32_t extremes(const uint4& x) {
+    const uint32_t lo = bf16x2_min(bf16x2_min(x.x, x.y), bf16x2_min(x.z, x.w));
+    const uint32_t hi = bf16x2_max(bf16x2_max(x.x, x.y), bf16x2_max(x.z, x.w)) ^ 0x80008000u;
+    return bf16x2_min(prmt(lo, hi, 0x5410u), prmt(lo, hi, 0x7632u));
 }
 
-// The eight codes of a lane's values as floats kRound + code, whose low bits are the code. How the
-// quotient (x - zero) / scale is rounded matters: bf16 values lie on borders between two codes often,
-// and there the product with the reciprocal alone may fall to either side. Scales so small or large
-// that the remainder or the reciprocal leave the normal numbers divide. The quotient is within
-// [0, 15.06], as the scale is rounded by at most 2^-8 of itself, so codes need no bounds.
-constexpr float kRound = 12582912.f;              // 1.5 * 2^23
-constexpr uint32_t kRoundBits = 0x4b400000u;
-__device__ __noinline__ float divided(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
-__device__ __forceinline__ void codes_of(const uint4& x, uint32_t scale, uint32_t zero, uint32_t (&c)[8]) {
-    const float s = low_of(scale), z = low_of(zero);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    if (s > 0x1p-90f && s < 0x1p120f) {
-        const float r = __frcp_rn(s);
-        const Two zeros = two(-z, -z), scales = two(-s, -s), by = two(r, r), round = two(kRound, kRound);
+// Two groups, of kLanes neighbouring lanes with eight values each: scales and zeros as bf16 bits,
+// those of the first group in the low half.
+template <int kLanes>
+__device__ __forceinline__ void group_scales(const uint4& x0, const uint4& x1, uint32_t& scales, uint32_t& zeros) {
+    uint32_t e0 = extremes(x0), e1 = extremes(x1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Two v = add2(two(low_of(w[i]), high_of(w[i])), zeros), q = mul2(v, by);
-            parts_of(add2(fma2(fma2(scales, q, v), by, q), round), c[2 * i], c[2 * i + 1]);
+    for (int o = 1; o < kLanes; o *= 2) {
+        e0 = bf16x2_min(e0, __shfl_xor_sync(kAll, e0, o));
+        e1 = bf16x2_min(e1, __shfl_xor_sync(kAll, e1, o));
+    }
+    const Two least = two(low_of(e0), low_of(e1)), most = two(-high_of(e0), -high_of(e1));
+    const float by = 1.f / 15.f;
+    const Two range = fma2(least, two(-1.f, -1.f), most), q = mul2(range, two(by, by));
+    float s0, s1;
+    parts_of(fma2(fma2(two(-15.f, -15.f), q, range), two(by, by), q), s0, s1);
+    scales = pack_bf16x2(s0, s1);
+    if ((scales & 0xffffu) < 0x0080u) scales &= 0xffff0000u;      // below 2^-126
+    if ((scales >> 16) < 0x0080u) scales &= 0x0000ffffu;
+    zeros = prmt(e0, e1, 0x5410u);
+}
+
+// The codes of two groups' values, element i of x0 and of x1, as floats kRound + code, whose low bytes
+// are the codes. Scales so small or large that the remainder or the reciprocal leave the normal
+// numbers divide. The quotient is within [0, 15.06], as the scale is rounded by at most 2^-8 of
+// itself, so codes need no bounds.
+constexpr float kRound = 12582912.f;              // 1.5 * 2^23
+__device__ __noinline__ float divided(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
+}
+__device__ __forceinline__ bool ordinary(float s) { return s > 0x1p-90f && s < 0x1p120f; }
+__device__ __forceinline__ void codes_of(const uint4& x0, const uint4& x1, uint32_t scales, uint32_t zeros,
+                                         uint32_t (&c0)[8], uint32_t (&c1)[8]) {
+    const float s0 = low_of(scales), s1 = high_of(scales);
+    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+    const Two z = two(-low_of(zeros), -high_of(zeros));
+    if (ordinary(s0) && ordinary(s1)) {
+        const Two by = two(reciprocal(s0), reciprocal(s1)), minus = two(-s0, -s1), round = two(kRound, kRound);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = w0[i >> 1], b = w1[i >> 1];
+            const Two v = add2(i & 1 ? two(high_of(a), high_of(b)) : two(low_of(a), low_of(b)), z), q = mul2(v, by);
+            float y0, y1;
+            parts_of(add2(fma2(fma2(minus, q, v), by, q), round), y0, y1);
+            c0[i] = __float_as_uint(y0), c1[i] = __float_as_uint(y1);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[i] = __float_as_uint(
-                __fadd_rn(divided(__fsub_rn(i & 1 ? high_of(w[i >> 1]) : low_of(w[i >> 1]), z), s), kRound));
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = w0[i >> 1], b = w1[i >> 1];
+            float v0, v1;
+            parts_of(add2(i & 1 ? two(high_of(a), high_of(b)) : two(low_of(a), low_of(b)), z), v0, v1);
+            c0[i] = __float_as_uint(__fadd_rn(divided(v0, s0), kRound));
+            c1[i] = __float_as_uint(__fadd_rn(divided(v1, s1), kRound));
+        }
     }
 }
 
@@ -113,9 +138,11 @@ __device__ __forceinline__ bool find_pages(const PackArgs& a, int i, int& from, 
     return false;
 }
 
-// Bits of codes c0 (token t or its pair's first) and c1 (token t + 8) at their places in a word.
-__device__ __forceinline__ uint32_t both_rows(uint32_t c0, uint32_t c1) {
-    return c0 + (c1 << 8) - (kRoundBits + (kRoundBits << 8));
+// A word whose codes of the even half lie four bits below those of the odd one: this lane's half, and the
+// other's from the neighbour, which gets `give` in return.
+__device__ __forceinline__ uint32_t both_halves(uint32_t keep, uint32_t give, int half) {
+    const uint32_t got = __shfl_xor_sync(kAll, give, 1);
+    return keep * (half ? 16u : 1u) + got * (half ? 1u : 16u);
 }
 
 // Keys: codes at 0 and scales at 1024 of `unit`.
@@ -125,23 +152,20 @@ __device__ __forceinline__ void pack_keys(const uint4 (&x)[8], uint8_t* unit) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {                     // tokens t and t + 8
         const int t = 2 * j + row;
-        uint32_t c0[8], c1[8], s0, z0, s1, z1, part[4];
-        group_scale<4>(x[j], s0, z0);
-        group_scale<4>(x[j + 4], s1, z1);
-        codes_of(x[j], s0, z0, c0);
-        codes_of(x[j + 4], s1, z1, c1);
+        uint32_t c0[8], c1[8], scales, zeros, part[4];
+        group_scales<4>(x[j], x[j + 4], scales, zeros);
+        codes_of(x[j], x[j + 4], scales, zeros, c0, c1);
 #pragma unroll
-        for (int p = 0; p < 4; ++p)                   // pair of dims: this half's bits of its word
-            part[p] = (both_rows(c0[2 * p], c1[2 * p]) + (both_rows(c0[2 * p + 1], c1[2 * p + 1]) << 16)) << (4 * half);
+        for (int p = 0; p < 4; ++p)                   // a pair of dims to a word: the codes' bytes at 0, 8, 16, 24
+            part[p] = prmt(c0[2 * p], c1[2 * p], 0x1140u) | prmt(c0[2 * p + 1], c1[2 * p + 1], 0x4011u);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {                 // the even half keeps words 0, 1
-            const uint32_t give = half ? part[p] : part[p + 2], keep = half ? part[p + 2] : part[p];
-            *reinterpret_cast<uint32_t*>(words + 16 * (4 * t + 2 * half + p)) = keep | __shfl_xor_sync(kAll, give, 1);
-        }
+        for (int p = 0; p < 2; ++p)                   // the even half keeps words 0, 1
+            *reinterpret_cast<uint32_t*>(words + 16 * (4 * t + 2 * half + p)) =
+                both_halves(half ? part[p + 2] : part[p], half ? part[p] : part[p + 2], half);
         if ((chunk & 3) == 0) {
             uint16_t* sz = reinterpret_cast<uint16_t*>(unit + 1024 + 16 * t) + (chunk >> 2);
-            sz[0] = static_cast<uint16_t>(s0), sz[4] = static_cast<uint16_t>(z0);
-            sz[64] = static_cast<uint16_t>(s1), sz[68] = static_cast<uint16_t>(z1);
+            sz[0] = static_cast<uint16_t>(scales), sz[4] = static_cast<uint16_t>(zeros);
+            sz[64] = static_cast<uint16_t>(scales >> 16), sz[68] = static_cast<uint16_t>(zeros >> 16);
         }
     }
 }
@@ -150,21 +174,18 @@ __device__ __forceinline__ void pack_keys(const uint4 (&x)[8], uint8_t* unit) {
 __device__ __forceinline__ void pack_values(const uint4 (&x)[8], uint8_t* unit) {
     const int lane = threadIdx.x & 31, row = lane >> 4, chunk = lane & 15, half = chunk & 1, w = chunk >> 1;
     uint8_t* const words = unit + 512 * (w >> 2) + 4 * (w & 3);
+    const uint32_t place = row ? 0x4011u : 0x1140u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int t = 2 * j + row;
-        uint32_t c0[8], c1[8], s0, z0, s1, z1, part[8], four[4];
-        group_scale<8>(x[j], s0, z0);
-        group_scale<8>(x[j + 4], s1, z1);
-        codes_of(x[j], s0, z0, c0);
-        codes_of(x[j + 4], s1, z1, c1);
+        uint32_t c0[8], c1[8], scales, zeros, part[8], four[4];
+        group_scales<8>(x[j], x[j + 4], scales, zeros);
+        codes_of(x[j], x[j + 4], scales, zeros, c0, c1);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) part[d] = both_rows(c0[d], c1[d]) << (16 * row + 4 * half);     // a word a dim
+        for (int d = 0; d < 8; ++d) part[d] = prmt(c0[d], c1[d], place);        // a word a dim: bytes at 0, 8 or 16, 24
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {                 // dims 4 * half .. of both halves
-            const uint32_t give = half ? part[d] : part[d + 4], keep = half ? part[d + 4] : part[d];
-            four[d] = keep | __shfl_xor_sync(kAll, give, 1);
-        }
+        for (int d = 0; d < 4; ++d)                   // dims 4 * half .. of both halves
+            four[d] = both_halves(half ? part[d + 4] : part[d], half ? part[d] : part[d + 4], half);
 #pragma unroll
         for (int d = 0; d < 2; ++d) {                 // ... and 2 * row .. of both tokens
             const uint32_t give = row ? four[d] : four[d + 2], keep = row ? four[d + 2] : four[d];
@@ -173,8 +194,8 @@ __device__ __forceinline__ void pack_values(const uint4 (&x)[8], uint8_t* unit) 
         }
         if ((chunk & 7) == 0) {
             uint16_t* sz = reinterpret_cast<uint16_t*>(unit + 1024 + 8 * t) + (chunk >> 3);
-            sz[0] = static_cast<uint16_t>(s0), sz[2] = static_cast<uint16_t>(z0);
-            sz[32] = static_cast<uint16_t>(s1), sz[34] = static_cast<uint16_t>(z1);
+            sz[0] = static_cast<uint16_t>(scales), sz[2] = static_cast<uint16_t>(zeros);
+            sz[32] = static_cast<uint16_t>(scales >> 16), sz[34] = static_cast<uint16_t>(zeros >> 16);
         }
     }
 }
