@@ -69,10 +69,12 @@ struct Control {
     // slots, or for the warp that had both rows that of the first in `both`
     int32_t had[S::kWarps];
     float m[2][S::kWarps][S::kRows], l[2][S::kWarps][S::kRows];
+    float factor[2][S::kWarps][S::kRows];             // of the warps' partials when they are joined
+    float top[2][S::kRows], sum[2][S::kRows];         // the CTA's m and l
     float both[S::kRows * kPartStride];
     union {
         struct {                                      // short rows: the CTA's partial
-            float m[S::kRows], l[S::kRows], o[S::kRows][kD];
+            float o[S::kRows][kD];
         } cta;
         struct {                                      // long rows: steps of the sequences up to each thread's last
             int64_t upto[S::kThreads], warp_sum[S::kWarps];
@@ -201,9 +203,10 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
     return static_cast<int>(((step + 1) * n - 1) / total);
 }
 
-// One block of a row's queries as B fragments, in fp16 parts (fp32 queries keep 22 bits), by one warp.
+// Dims 32 g .. 32 g + 31 of one block of a row's queries as B fragments, in fp16 parts (fp32 queries
+// keep 22 bits), by one warp.
 template <int kKind, bool kSplit>
-__device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int which, int block, Control<kKind>& ctl) {
+__device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, int which, int block, int g, Control<kKind>& ctl) {
     using S = Shape<kKind>;
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     const int query = S::kPair ? gid & 3 : block * 8 + gid;
@@ -229,10 +232,10 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
     big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
     const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 100);
     const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kQueryTop;
-    float sum[4];
+    float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        if (k % 2 == 0) sum[k / 2] = 0.f;
+        if (k / 2 != g) continue;
         uint32_t hi[2], lo[2] = {0u, 0u};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -249,26 +252,35 @@ __device__ __forceinline__ void put_queries(const PackedArgs& a, int b, int h, i
             }
             const float2 x1 = f16x2_of(hi[c]), x2 = f16x2_of(lo[c]);
             const float part = x1.x + x1.y + (x2.x + x2.y);
-            sum[k / 2] += c == 0 ? part : part * 16.f;
+            sum += c == 0 ? part : part * 16.f;
         }
         ctl.frag[which][block][k][lane] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
     }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        sum[g] += __shfl_xor_sync(kAll, sum[g], 1);
-        sum[g] += __shfl_xor_sync(kAll, sum[g], 2);
-        sum[g] *= kCode;
+    sum += __shfl_xor_sync(kAll, sum, 1);
+    sum += __shfl_xor_sync(kAll, sum, 2);
+    sum *= kCode;
+    // the sum's fragment: rows k = g, 4 + g and 8 + g are its first 8 bits, the next 8, and the next
+    if (tig < 3) {
+        const float s0 = __bfloat162float(__float2bfloat16_rn(sum)), s1 = __bfloat162float(__float2bfloat16_rn(sum - s0));
+        const float mine = tig == 0 ? s0 : tig == 1 ? s1 : sum - s0 - s1;
+        const int k = 4 * tig + g;                    // of lane 4 gid + k % 8 / 2, half k % 2, register k / 8
+        reinterpret_cast<uint16_t*>(&ctl.sums[which][block][4 * gid + k % 8 / 2])[2 * (k / 8) + k % 2] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(mine));
+    } else {                                          // rows 12 .. 15 are zero
+        const int k = 12 + g;
+        reinterpret_cast<uint16_t*>(&ctl.sums[which][block][4 * gid + k % 8 / 2])[2 * (k / 8) + k % 2] = 0;
     }
-    // rows k = 0..3 of the fragment: the groups' sums to 8 bits; 4..7: the next 8; 8..11
-    float s0 = tig & 1 ? sum[2] : sum[0], s1 = tig & 1 ? sum[3] : sum[1];
-    const uint32_t w0 = pack_bf16x2(s0, s1);
-    s0 -= low_of(w0), s1 -= high_of(w0);
-    const uint32_t w1 = pack_bf16x2(s0, s1);
-    s0 -= low_of(w1), s1 -= high_of(w1);
-    const uint32_t w2 = pack_bf16x2(s0, s1);
-    ctl.sums[which][block][lane] = make_uint2(tig < 2 ? w0 : w1, tig < 2 ? w2 : 0u);
-    if (tig == 0)
+    if (tig == 0 && g == 0)
         ctl.unit[which][block * 8 + gid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kScoreUnit;
+}
+// ... of all blocks and dims of the CTA's rows, by its first warps.
+template <int kKind, bool kSplit>
+__device__ __forceinline__ void put_all_queries(const PackedArgs& a, int b0, int h0, int b1, int h1, int rows, Control<kKind>& ctl) {
+    using S = Shape<kKind>;
+    for (int i = threadIdx.x >> 5; i < rows * S::kBlocks * 4; i += S::kWarps) {
+        const int which = i / (S::kBlocks * 4);
+        put_queries<kKind, kSplit>(a, which ? b1 : b0, which ? h1 : h0, which, i / 4 % S::kBlocks, i % 4, ctl);
+    }
 }
 
 // A warp's running softmax over a part of a row: columns 2 * tig + c of each block.
@@ -635,29 +647,32 @@ __device__ __forceinline__ void store_lse(const PackedArgs& a, int64_t row, floa
     if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
 }
 
-// Steps off .. off + steps of a row.
-struct Part {
-    int b, h, off, steps;
-    Len len;
+// What a warp has of a row: packed pages first, first + step, ... (`count` of them, the ids of the first
+// 32 by lane in `ids`) and recent pages recent0, recent0 + step, ... before recent1.
+struct Share {
+    int b, h, first, step, count;
+    uint32_t ids;
+    int recent0, recent1, recent;                     // `recent` tokens in all
 };
 
-// Steps x0 .. x1 of a part, which are this warp's: leaves its sums at `out`, ms and ls.
-template <int kKind, bool kSplit>
-__device__ __forceinline__ void attend_steps(const PackedArgs& a, const Part part, int x0, int x1, int which, uint8_t* own,
-                                             bool ready, Control<kKind>& ctl, float* out, float* ms, float* ls) {
+// Leaves the share's sums at `out`, ms and ls. `ahead` is called once the first copies are on their way.
+template <int kKind, bool kSplit, typename Ahead>
+__device__ __forceinline__ void attend_share(const PackedArgs& a, const Share share, int which, uint8_t* own,
+                                             Control<kKind>& ctl, float* out, float* ms, float* ls, Ahead ahead) {
     using S = Shape<kKind>;
     constexpr int kDepth = S::kDepth;
-    const int lane = threadIdx.x & 31, b = part.b, h = part.h;
-    const int first = min(part.off + x0, part.len.pages), count = min(part.off + x1, part.len.pages) - first;
+    static_assert(kDepth * kUnitBytes >= 4 * kPage * kD, "a recent page lies in the slots");
+    static_assert(kDepth * kUnitBytes >= S::kRows * kPartStride * 4, "a partial lies in the slots");
+    const int lane = threadIdx.x & 31, b = share.b, h = share.h, count = share.count;
     const uint8_t* const base = a.packed + static_cast<int64_t>(h) * kUnitBytes + lane * 16;
-    uint32_t ids = lane < count ? packed_id(a, b, h, first + lane) : 0, next = 0;
     const uint32_t stride = static_cast<uint32_t>(a.hkv) * kUnitBytes;
+    uint32_t ids = share.ids, next = 0;
     int put = 0;                                      // slot of the next page to fetch
     const auto load = [&](int i) {
         if (i < count) {
             if ((i & 31) == 0) {                      // ids of 32 pages, fetched 32 pages ahead
                 if (i > 0) ids = next;
-                if (i + 32 + lane < count) next = packed_id(a, b, h, first + i + 32 + lane);
+                if (i + 32 + lane < count) next = packed_id(a, b, h, share.first + (i + 32 + lane) * share.step);
             }
             const uint8_t* from = base + static_cast<uint64_t>(__shfl_sync(kAll, ids, i & 31)) * stride;
             uint8_t* to = own + put * kUnitBytes + lane * 16;
@@ -670,7 +685,7 @@ __device__ __forceinline__ void attend_steps(const PackedArgs& a, const Part par
     };
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) load(i);
-    if (!ready) __syncthreads();                      // the queries are there
+    ahead();
     Running<kKind, kSplit> run;
     run.clear(ctl, which);
     int at = 0;                                       // slot of the next page to use
@@ -691,12 +706,9 @@ __device__ __forceinline__ void attend_steps(const PackedArgs& a, const Part par
     run.centre();
     copies_wait<0>();
     __syncwarp();
-    // recent pages whose first step is among these
-    const int behind = part.off - part.len.pages + kRecentSteps - 1;
-    const int recent1 = min(part.len.recent_pages(), max(0, (behind + x1) / kRecentSteps));
 #pragma unroll 1
-    for (int r = max(0, (behind + x0) / kRecentSteps); r < recent1; ++r) {
-        const int valid = min(kPage, part.len.recent - r * kPage);
+    for (int r = share.recent0; r < share.recent1; r += share.step) {
+        const int valid = min(kPage, share.recent - r * kPage);
         int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
         if (id < 0 || id >= a.num_cache) {
             report_error(a.st, LOCKS_ERR_BAD_INDEX);
@@ -719,95 +731,97 @@ __device__ __forceinline__ void attend_steps(const PackedArgs& a, const Part par
     __syncwarp();
 }
 
-// One or two parts (neighbouring rows) by all of the CTA, an equal share of the steps to a warp.
-// Leaves the warps' partials in shared memory, for join_warps.
-template <int kKind, bool kSplit>
-__device__ __forceinline__ void attend_parts(const PackedArgs& a, const Part (&part)[2], int parts, uint8_t* slots,
-                                             Control<kKind>& ctl) {
+// The CTA's m and l of each query of `rows` rows, and the factors that the warps' partials are joined
+// with. All of the CTA calls it, once the partials are there.
+template <int kKind>
+__device__ __forceinline__ void join_sums(const PackedArgs& a, int rows, Control<kKind>& ctl) {
     using S = Shape<kKind>;
-    static_assert(S::kDepth * kUnitBytes >= 4 * kPage * kD, "a recent page lies in the slots");
-    static_assert(S::kDepth * kUnitBytes >= S::kRows * kPartStride * 4, "a partial lies in the slots");
-    static_assert(2 * S::kBlocks <= S::kWarps, "a warp per block of queries");
-    const int warp = threadIdx.x >> 5;
-    uint8_t* const own = slots + warp * S::kDepth * kUnitBytes;
-    const int64_t all = static_cast<int64_t>(part[0].steps) + (parts > 1 ? part[1].steps : 0);
-    const int64_t x0 = all * warp / S::kWarps, x1 = all * (warp + 1) / S::kWarps;
-    if (warp < parts * S::kBlocks) {
-        const int which = warp / S::kBlocks;
-        put_queries<kKind, kSplit>(a, which ? part[1].b : part[0].b, which ? part[1].h : part[0].h, which, warp % S::kBlocks, ctl);
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < rows * a.group; i += S::kWarps) {        // a warp a query, a lane a partial
+        const int which = i / a.group, query = i % a.group;
+        const bool on = lane < S::kWarps && (ctl.had[lane] >> which & 1);
+        const float m = on ? ctl.m[which][lane][query] : -INFINITY;
+        float top = m;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
+        const float f = on ? fast_exp2(m - (top == -INFINITY ? 0.f : top)) : 0.f;
+        float sum = on ? f * ctl.l[which][lane][query] : 0.f;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(kAll, sum, x);
+        if (lane < S::kWarps) ctl.factor[which][lane][query] = f;
+        if (lane == 0) ctl.top[which][query] = top, ctl.sum[which][query] = sum;
     }
-    const bool has0 = x0 < x1 && x0 < part[0].steps, has1 = x0 < x1 && x1 > part[0].steps;
-    if ((threadIdx.x & 31) == 0) ctl.had[warp] = (has0 ? 1 : 0) | (has1 ? 2 : 0);
-    bool ready = false;
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        if (!(which ? has1 : has0)) continue;
-        const int64_t base = which ? part[0].steps : 0;
-        const int s0 = static_cast<int>(max(x0 - base, static_cast<int64_t>(0)));
-        const int s1 = static_cast<int>(min(x1 - base, static_cast<int64_t>(which ? part[1].steps : part[0].steps)));
-        float* out = which == 0 && has1 ? ctl.both : reinterpret_cast<float*>(own);
-        attend_steps<kKind, kSplit>(a, which ? part[1] : part[0], s0, s1, which, own, ready, ctl, out, ctl.m[which][warp],
-                                    ctl.l[which][warp]);
-        ready = true;
-    }
-    if (!ready) __syncthreads();
     __syncthreads();
 }
-
-// Query `query`, dim `dim` of part `which` from its warps' partials.
+// Query `query`, dim `dim` of row `which` from the warps' partials.
 template <int kKind>
-__device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int which, int query, int dim,
-                                            float& top, float& sum) {
+__device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int which, int query, int dim) {
     using S = Shape<kKind>;
-    top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < S::kWarps; ++w)
-        if (ctl.had[w] >> which & 1) top = fmaxf(top, ctl.m[which][w][query]);
-    const float base = top == -INFINITY ? 0.f : top;
     float x = 0.f;
-    sum = 0.f;
 #pragma unroll
     for (int w = 0; w < S::kWarps; ++w) {
         const int had = ctl.had[w];
         if (!(had >> which & 1)) continue;
-        const float f = fast_exp2(ctl.m[which][w][query] - base);
         const float* o = which == 0 && had == 3 ? ctl.both : reinterpret_cast<const float*>(slots + w * S::kDepth * kUnitBytes);
-        x = fmaf(f, o[query * kPartStride + dim], x);
-        sum = fmaf(f, ctl.l[which][w][query], sum);
+        x = fmaf(ctl.factor[which][w][query], o[query * kPartStride + dim], x);
     }
     return x;
 }
 
-// Short rows: cluster r is row r, its CTAs an equal share of it each.
+// Short rows: cluster r is row r, and its warps take its pages in turn, so that their ids are on the way
+// before the row's length is known; recent pages go to the last warps.
 template <int kKind, bool kSplit>
 __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __grid_constant__ PackedArgs a, int ctas) {
     using S = Shape<kKind>;
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ Control<kKind> ctl;
-    const int rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int r = blockIdx.x / ctas;
     grid_dependency_wait();
     allow_dependent_launch();
-    Part part[2];
-    part[0].b = r / a.hkv;
-    part[0].h = r % a.hkv;
-    part[0].len = row_len(a, part[0].b, part[0].h, rank == 0 && threadIdx.x == 0);
-    const int64_t steps = part[0].len.steps();
-    part[0].off = static_cast<int>(steps * rank / ctas);
-    part[0].steps = static_cast<int>(steps * (rank + 1) / ctas) - part[0].off;
-    part[1] = part[0];
-    attend_parts<kKind, kSplit>(a, part, 1, slots, ctl);
-    const int64_t row = static_cast<int64_t>(part[0].b) * a.hq + part[0].h * a.group;
+    Share share;
+    share.b = r / a.hkv;
+    share.h = r % a.hkv;
+    share.first = rank * S::kWarps + warp;
+    share.step = ctas * S::kWarps;
+    const int mine = share.first + lane * share.step;
+    const bool some = mine < (a.selected ? a.k_cap : a.max_pages);
+    int id = -1;
+    if (some) {
+        int j = mine;
+        if (a.selected) j = __ldcg(a.selected + (static_cast<int64_t>(share.b) * a.hkv + share.h) * a.k_cap + mine);
+        if (j >= 0 && j < a.max_pages) id = __ldcg(a.page_table + static_cast<int64_t>(share.b) * a.max_pages + j);
+    }
+    const Len len = row_len(a, share.b, share.h, rank == 0 && threadIdx.x == 0);
+    share.count = len.pages > share.first ? (len.pages - share.first + share.step - 1) / share.step : 0;
+    if (lane < share.count && (id < 0 || id >= a.num_packed)) {
+        report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        id = 0;
+    }
+    share.ids = id;
+    share.recent0 = share.step - 1 - share.first;
+    share.recent1 = len.recent_pages();
+    share.recent = len.recent;
+    uint8_t* const own = slots + warp * S::kDepth * kUnitBytes;
+    const bool has = share.count > 0 || share.recent0 < share.recent1;
+    if (lane == 0) ctl.had[warp] = has ? 1 : 0;
+    const auto queries = [&] {
+        put_all_queries<kKind, kSplit>(a, share.b, share.h, 0, 0, 1, ctl);
+        __syncthreads();
+    };
+    if (has) attend_share<kKind, kSplit>(a, share, 0, own, ctl, reinterpret_cast<float*>(own), ctl.m[0][warp], ctl.l[0][warp], queries);
+    else queries();
+    __syncthreads();
+    join_sums<kKind>(a, 1, ctl);
+    const int64_t row = static_cast<int64_t>(share.b) * a.hq + share.h * a.group;
     for (int i = threadIdx.x; i < a.group * kD; i += S::kThreads) {
         const int query = i / kD, dim = i % kD;
-        float top, sum;
-        const float x = join_warps<kKind>(slots, ctl, 0, query, dim, top, sum);
+        const float x = join_warps<kKind>(slots, ctl, 0, query, dim);
         if (ctas == 1) {
-            store_row(a, row + query, x, sum, dim);
-            if (dim == 0) store_lse(a, row + query, top, sum);
+            store_row(a, row + query, x, ctl.sum[0][query], dim);
+            if (dim == 0) store_lse(a, row + query, ctl.top[0][query], ctl.sum[0][query]);
         } else {
             ctl.cta.o[query][dim] = x;
-            if (dim == 0) ctl.cta.m[query] = top, ctl.cta.l[query] = sum;
         }
     }
     if (ctas == 1) return;
@@ -820,12 +834,13 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __
             m[c] = -INFINITY;
             l[c] = x[c] = 0.f;
             if (c < ctas) {
-                m[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.m[query], c));
-                l[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.l[query], c));
+                m[c] = ld_dsmem_f32(dsmem_addr(&ctl.top[0][query], c));
+                l[c] = ld_dsmem_f32(dsmem_addr(&ctl.sum[0][query], c));
                 x[c] = ld_dsmem_f32(dsmem_addr(&ctl.cta.o[query][dim], c));
             }
-            top = fmaxf(top, m[c]);
         }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) top = fmaxf(top, m[c]);
         const float base = top == -INFINITY ? 0.f : top;
         float value = 0.f, sum = 0.f;
 #pragma unroll
@@ -838,6 +853,64 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __
         if (dim == 0) store_lse(a, row + query, top, sum);
     }
     cluster_sync_all();                               // nobody leaves while its sums are read
+}
+
+// Steps off .. off + steps of a row.
+struct Part {
+    int b, h, off, steps;
+    Len len;
+};
+
+// Steps x0 .. x1 of a part as a warp's share.
+__device__ __forceinline__ Share share_of(const PackedArgs& a, const Part part, int x0, int x1) {
+    const int lane = threadIdx.x & 31;
+    Share s;
+    s.b = part.b;
+    s.h = part.h;
+    s.step = 1;
+    s.first = min(part.off + x0, part.len.pages);
+    s.count = min(part.off + x1, part.len.pages) - s.first;
+    s.ids = lane < s.count ? packed_id(a, s.b, s.h, s.first + lane) : 0;
+    // recent pages whose first step is among these
+    const int behind = part.off - part.len.pages + kRecentSteps - 1;
+    s.recent0 = max(0, (behind + x0) / kRecentSteps);
+    s.recent1 = min(part.len.recent_pages(), max(0, (behind + x1) / kRecentSteps));
+    s.recent = part.len.recent;
+    return s;
+}
+
+// One or two parts (neighbouring rows) by all of the CTA, an equal share of the steps to a warp.
+// Leaves the warps' partials in shared memory, for join_warps.
+template <int kKind, bool kSplit>
+__device__ __forceinline__ void attend_parts(const PackedArgs& a, const Part (&part)[2], int parts, uint8_t* slots,
+                                             Control<kKind>& ctl) {
+    using S = Shape<kKind>;
+    const int warp = threadIdx.x >> 5;
+    uint8_t* const own = slots + warp * S::kDepth * kUnitBytes;
+    const int64_t all = static_cast<int64_t>(part[0].steps) + (parts > 1 ? part[1].steps : 0);
+    const int64_t x0 = all * warp / S::kWarps, x1 = all * (warp + 1) / S::kWarps;
+    const bool has0 = x0 < x1 && x0 < part[0].steps, has1 = x0 < x1 && x1 > part[0].steps;
+    if ((threadIdx.x & 31) == 0) ctl.had[warp] = (has0 ? 1 : 0) | (has1 ? 2 : 0);
+    bool ready = false;
+    const auto queries = [&] {
+        if (ready) return;
+        put_all_queries<kKind, kSplit>(a, part[0].b, part[0].h, part[1].b, part[1].h, parts, ctl);
+        __syncthreads();
+        ready = true;
+    };
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (!(which ? has1 : has0)) continue;
+        const int64_t base = which ? part[0].steps : 0;
+        const int s0 = static_cast<int>(max(x0 - base, static_cast<int64_t>(0)));
+        const int s1 = static_cast<int>(min(x1 - base, static_cast<int64_t>(which ? part[1].steps : part[0].steps)));
+        float* out = which == 0 && has1 ? ctl.both : reinterpret_cast<float*>(own);
+        attend_share<kKind, kSplit>(a, share_of(a, which ? part[1] : part[0], s0, s1), which, own, ctl, out, ctl.m[which][warp],
+                                    ctl.l[which][warp], queries);
+    }
+    queries();
+    __syncthreads();
+    join_sums<kKind>(a, parts, ctl);
 }
 
 // Long rows: the line of steps.
@@ -936,8 +1009,8 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             for (int i = threadIdx.x; i < a.group * kD; i += kThreads) {
                 const int query = i / kD, dim = i % kD;
-                float top, sum;
-                const float x = join_warps<kKind>(slots, ctl, which, query, dim, top, sum);
+                const float x = join_warps<kKind>(slots, ctl, which, query, dim);
+                const float top = ctl.top[which][query], sum = ctl.sum[which][query];
                 if (whole) {
                     store_row(a, row + query, x, sum, dim);
                     if (dim == 0) store_lse(a, row + query, top, sum);
