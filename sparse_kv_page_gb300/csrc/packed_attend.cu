@@ -641,7 +641,7 @@ struct Running {
 };
 
 __device__ __forceinline__ void store_row(const PackedArgs& a, int64_t row, float value, float sum, int dim) {
-    a.out[row * kD + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : value / sum));
+    a.out[row * kD + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : __fdividef(value, sum)));
 }
 __device__ __forceinline__ void store_lse(const PackedArgs& a, int64_t row, float m, float sum) {
     if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
@@ -683,8 +683,31 @@ __device__ __forceinline__ void attend_share(const PackedArgs& a, const Share sh
         copies_commit();
         if (++put == kDepth) put = 0;
     };
+    const auto load_recent = [&](int r) {
+        const int valid = min(kPage, share.recent - r * kPage);
+        int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
+        if (id < 0 || id >= a.num_cache) {
+            report_error(a.st, LOCKS_ERR_BAD_INDEX);
+            id = 0;
+        }
+        const int64_t from = (static_cast<int64_t>(id) * a.hkv + h) * (kPage * kD) + lane * 8;
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) load(i);
+        for (int j = 0; j < kPage / 2; ++j) {         // two tokens
+            const int token = 2 * j + (lane >> 4), to = Running<kKind, kSplit>::chunk_offset(token, lane & 15);
+            copy_or_zero(own + to, a.k_cache + from + j * 2 * kD, token < valid);
+            copy_or_zero(own + kPage * kD * 2 + to, a.v_cache + from + j * 2 * kD, token < valid);
+        }
+        copies_commit();
+    };
+    int recent = share.recent0;                       // the next recent page, and the one that is loaded
+    bool loaded = false;
+    if (count > 0) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) load(i);
+    } else if (recent < share.recent1) {
+        load_recent(recent);
+        loaded = true;
+    }
     ahead();
     Running<kKind, kSplit> run;
     run.clear(ctl, which);
@@ -703,30 +726,22 @@ __device__ __forceinline__ void attend_share(const PackedArgs& a, const Share sh
         load(i + kDepth);
         load(i + kDepth + 1);
     }
-    run.centre();
-    copies_wait<0>();
-    __syncwarp();
+    if (count > 0) run.centre();
 #pragma unroll 1
-    for (int r = share.recent0; r < share.recent1; r += share.step) {
-        const int valid = min(kPage, share.recent - r * kPage);
-        int id = __ldcg(a.recent_table + static_cast<int64_t>(b) * a.max_recent + r);
-        if (id < 0 || id >= a.num_cache) {
-            report_error(a.st, LOCKS_ERR_BAD_INDEX);
-            id = 0;
+    for (; recent < share.recent1; recent += share.step) {
+        if (!loaded) {
+            copies_wait<0>();
+            __syncwarp();                             // the slots are free
+            load_recent(recent);
         }
-        const int64_t from = (static_cast<int64_t>(id) * a.hkv + h) * (kPage * kD) + lane * 8;
-#pragma unroll
-        for (int j = 0; j < kPage / 2; ++j) {         // two tokens
-            const int token = 2 * j + (lane >> 4), to = run.chunk_offset(token, lane & 15);
-            copy_or_zero(own + to, a.k_cache + from + j * 2 * kD, token < valid);
-            copy_or_zero(own + kPage * kD * 2 + to, a.v_cache + from + j * 2 * kD, token < valid);
-        }
-        copies_commit();
+        loaded = false;
         copies_wait<0>();
         __syncwarp();
-        run.recent_page(own, valid, ctl, which);
+        run.recent_page(own, min(kPage, share.recent - recent * kPage), ctl, which);
         __syncwarp();
     }
+    copies_wait<0>();
+    __syncwarp();
     run.put(a.group, out, ms, ls);
     __syncwarp();
 }
@@ -754,16 +769,17 @@ __device__ __forceinline__ void join_sums(const PackedArgs& a, int rows, Control
     __syncthreads();
 }
 // Query `query`, dim `dim` of row `which` from the warps' partials.
-template <int kKind>
+template <int kKind, bool kTwo>
 __device__ __forceinline__ float join_warps(const uint8_t* slots, const Control<kKind>& ctl, int which, int query, int dim) {
     using S = Shape<kKind>;
+    const float* const o = reinterpret_cast<const float*>(slots) + query * kPartStride + dim;
     float x = 0.f;
 #pragma unroll
     for (int w = 0; w < S::kWarps; ++w) {
         const int had = ctl.had[w];
-        if (!(had >> which & 1)) continue;
-        const float* o = which == 0 && had == 3 ? ctl.both : reinterpret_cast<const float*>(slots + w * S::kDepth * kUnitBytes);
-        x = fmaf(ctl.factor[which][w][query], o[query * kPartStride + dim], x);
+        float y = o[w * (S::kDepth * kUnitBytes / 4)];
+        if (kTwo && which == 0 && had == 3) y = ctl.both[query * kPartStride + dim];
+        x = fmaf(ctl.factor[which][w][query], had >> which & 1 ? y : 0.f, x);
     }
     return x;
 }
@@ -816,7 +832,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __
     const int64_t row = static_cast<int64_t>(share.b) * a.hq + share.h * a.group;
     for (int i = threadIdx.x; i < a.group * kD; i += S::kThreads) {
         const int query = i / kD, dim = i % kD;
-        const float x = join_warps<kKind>(slots, ctl, 0, query, dim);
+        const float x = join_warps<kKind, false>(slots, ctl, 0, query, dim);
         if (ctas == 1) {
             store_row(a, row + query, x, ctl.sum[0][query], dim);
             if (dim == 0) store_lse(a, row + query, ctl.top[0][query], ctl.sum[0][query]);
@@ -1009,7 +1025,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             for (int i = threadIdx.x; i < a.group * kD; i += kThreads) {
                 const int query = i / kD, dim = i % kD;
-                const float x = join_warps<kKind>(slots, ctl, which, query, dim);
+                const float x = join_warps<kKind, true>(slots, ctl, which, query, dim);
                 const float top = ctl.top[which][query], sum = ctl.sum[which][query];
                 if (whole) {
                     store_row(a, row + query, x, sum, dim);
