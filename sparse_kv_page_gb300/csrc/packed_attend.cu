@@ -23,6 +23,7 @@
 // through a product of their own with the queries' sums (keys) and through a sum per group
 // (values).
 #include <algorithm>
+#include <atomic>
 
 #include "pool_internal.h"
 
@@ -78,6 +79,7 @@ struct Control {
         } cta;
         struct {                                      // long rows: steps of the sequences up to each thread's last
             int64_t upto[S::kThreads], warp_sum[S::kWarps];
+            int2 len[S::kThreads];                    // pages and recent tokens of sequence i, where that is enough
         } line;
     };
 };
@@ -194,13 +196,16 @@ __device__ __forceinline__ int packed_id(const PackedArgs& a, int b, int h, int 
     return 0;
 }
 
-// CTA c of n holds steps first(c) .. first(c + 1) of the line.
-__device__ __forceinline__ int64_t first_step(int64_t total, int c, int n) {
-    const int64_t x = total * c;
-    return x < (1ll << 32) ? static_cast<uint32_t>(x) / static_cast<uint32_t>(n) : x / n;
+// CTA c of n holds steps first(c) .. first(c + 1) of the line. (A 64-bit division is a long routine,
+// kept in one place.)
+static __device__ __noinline__ int64_t divide64(int64_t x, int64_t y) { return x / y; }
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    if (x < (1ll << 32) && y < (1ll << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return divide64(x, y);
 }
+__device__ __forceinline__ int64_t first_step(int64_t total, int c, int n) { return divide(total * c, n); }
 __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
-    return static_cast<int>(((step + 1) * n - 1) / total);
+    return static_cast<int>(divide((step + 1) * n - 1, total));
 }
 
 // Dims 32 g .. 32 g + 31 of one block of a row's queries as B fragments, in fp16 parts (fp32 queries
@@ -904,7 +909,7 @@ __device__ __forceinline__ void attend_parts(const PackedArgs& a, const Part (&p
     const int warp = threadIdx.x >> 5;
     uint8_t* const own = slots + warp * S::kDepth * kUnitBytes;
     const int64_t all = static_cast<int64_t>(part[0].steps) + (parts > 1 ? part[1].steps : 0);
-    const int64_t x0 = all * warp / S::kWarps, x1 = all * (warp + 1) / S::kWarps;
+    const int64_t x0 = divide(all * warp, S::kWarps), x1 = divide(all * (warp + 1), S::kWarps);
     const bool has0 = x0 < x1 && x0 < part[0].steps, has1 = x0 < x1 && x1 > part[0].steps;
     if ((threadIdx.x & 31) == 0) ctl.had[warp] = (has0 ? 1 : 0) | (has1 ? 2 : 0);
     bool ready = false;
@@ -941,12 +946,21 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
     grid_dependency_wait();
     allow_dependent_launch();
 
-    const int per = (a.batch + kThreads - 1) / kThreads;
+    // lengths: kept where they are the same for all kv heads and there is a thread for each sequence
+    const int per = (a.batch + kThreads - 1) / kThreads, tid = threadIdx.x;
+    const bool kept = !a.selected && per <= 1;
     {
         int64_t sum = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = threadIdx.x * per + i;
-            if (b < a.batch) sum += seq_steps(a, b, blockIdx.x == 0);
+        if (kept) {
+            Len len = {0, 0};
+            if (tid < a.batch) len = row_len(a, tid, 0, blockIdx.x == 0);
+            ctl.line.len[tid] = make_int2(len.pages, len.recent);
+            sum = static_cast<int64_t>(len.steps()) * a.hkv;
+        } else {
+            for (int i = 0; i < per; ++i) {
+                const int b = tid * per + i;
+                if (b < a.batch) sum += seq_steps(a, b, blockIdx.x == 0);
+            }
         }
         int64_t upto = sum;
 #pragma unroll
@@ -957,13 +971,17 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
         if (lane == 31) ctl.line.warp_sum[warp] = upto;
         __syncthreads();
         for (int w = 0; w < warp; ++w) upto += ctl.line.warp_sum[w];
-        ctl.line.upto[threadIdx.x] = upto;
+        ctl.line.upto[tid] = upto;
     }
+    const auto length = [&](int b, int h) {
+        if (!kept) return row_len(a, b, h, false);
+        const int2 x = ctl.line.len[b];
+        return Len{x.x, x.y};
+    };
     // rows without tokens are nobody's
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; r < static_cast<int64_t>(a.batch) * a.hkv;
-         r += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int b = static_cast<int>(r / a.hkv), h = static_cast<int>(r % a.hkv);
-        if (row_len(a, b, h, false).steps() != 0) continue;
+    for (int r = blockIdx.x * kThreads + tid; r < a.batch * a.hkv; r += gridDim.x * kThreads) {
+        const int b = r / a.hkv, h = r % a.hkv;
+        if (length(b, h).steps() != 0) continue;
         for (int q = 0; q < a.group; ++q) {
             const int64_t row = static_cast<int64_t>(b) * a.hq + h * a.group + q;
             for (int d = 0; d < kD; d += 8) *reinterpret_cast<uint4*>(a.out + row * kD + d) = make_uint4(0, 0, 0, 0);
@@ -979,7 +997,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
         pos = first_step(total, blockIdx.x, ctas);
         end = first_step(total, blockIdx.x + 1, ctas);
     }
-    if (!by_row && threadIdx.x == 0) a.cuts[blockIdx.x] = {-1, 0, 0};
+    if (!by_row && tid == 0) a.cuts[blockIdx.x] = {-1, 0, 0};
     if (pos >= end) return;
 
     // the row at pos
@@ -991,18 +1009,23 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
         for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.line.upto[i * 32 + lane] <= pos));
         int64_t at = pos - (before > 0 ? ctl.line.upto[before - 1] : 0);
         p.b = before * per;
-        for (int64_t n; p.b < a.batch - 1 && at >= (n = seq_steps(a, p.b, false)); ++p.b) at -= n;
-        p.h = 0;
-        for (p.len = row_len(a, p.b, 0, false); p.h < a.hkv - 1 && at >= p.len.steps(); p.len = row_len(a, p.b, ++p.h, false))
-            at -= p.len.steps();
-        p.off = static_cast<int>(at);
+        if (kept) {
+            p.len = length(p.b, 0);
+            p.h = static_cast<int>(divide(at, p.len.steps()));
+            p.off = static_cast<int>(at - static_cast<int64_t>(p.h) * p.len.steps());
+        } else {
+            for (int64_t n; p.b < a.batch - 1 && at >= (n = seq_steps(a, p.b, false)); ++p.b) at -= n;
+            p.h = 0;
+            for (p.len = length(p.b, 0); p.h < a.hkv - 1 && at >= p.len.steps(); p.len = length(p.b, ++p.h)) at -= p.len.steps();
+            p.off = static_cast<int>(at);
+        }
     }
     // the row behind p's with any steps (there is one as long as steps are left)
     const auto next_row = [&](const Part& p) {
         Part r = p;
         do {
             if (++r.h == a.hkv) ++r.b, r.h = 0;
-            r.len = row_len(a, r.b, r.h, false);
+            r.len = length(r.b, r.h);
         } while (r.len.steps() == 0 && r.b < a.batch - 1);
         r.off = 0;
         return r;
@@ -1094,17 +1117,64 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 static_assert(kMaxPackedCtas <= kJoinThreads, "a thread per partial");
 
-// CTAs a row of the short form, 0: the line.
-int row_ctas(const PackedArgs& a, int warps, int num_sms) {
+// Clusters of n CTAs of the short form that fit on the device at once (0: none), from the occupancy
+// API, kept per device.
+template <int kKind, bool kSplit>
+int resident_rows(int n, int num_sms, size_t smem) {
+    using S = Shape<kKind>;
+    if (n == 1) return num_sms;
+    static std::atomic<int> kept[RaiseOnce::kDevices][4];        // one more than the number; 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= RaiseOnce::kDevices) return 0;
+    std::atomic<int>& known = kept[dev][n == 2 ? 1 : n == 4 ? 2 : 3];
+    if (const int k = known.load()) return k - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n, 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = n;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, row_kernel<kKind, kSplit>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        clusters = 0;
+    }
+    known.store(clusters + 1);
+    return clusters;
+}
+
+// CTAs a row of the short form, or 0 for the line: what takes least by a fit to both (us). The short form
+// goes in waves of as many clusters as fit at once, `wave` each and 2 for a cluster's join, and `page` for
+// each page of a warp; the line takes `line`, `row` for each row of a CTA, and `page` with all pages spread
+// over all SMs' warps. Measured (line / 1 / 2 / 4 / 8 CTAs, us), 8 kv heads of 4 queries: 1 sequence of 128
+// pages 14.8 / 13.1 / 11.3 / 9.4 / 9.4, of 1024 17.1 / 60.6 / 35.7 / 22.3 / 15.3; 8 of 128 17.0 / 13.5 / 11.7
+// / 18.5 / 40.4, 96 of 128 84.2 / 82.5; 2 kv heads of 16: 1 of 128 17.1 / 21.7 / 17.8 / 13.5 / 12.5, 8 of 1024
+// 30.9 / 109 / 61.4 / 36.4 / 44.0, 96 of 128 52.6 / 42.0 / 52.1 / 79.2.
+struct FormCost {
+    double wave, page, line, row;
+};
+constexpr FormCost kFormCost[3] = {{5.5, 0.85, 13, 4.5}, {5.8, 0.91, 14, 6.5}, {8.8, 1.17, 16, 15}};
+template <int kKind, bool kSplit>
+int row_ctas(const PackedArgs& a, int num_sms, size_t smem) {
+    constexpr FormCost kCost = kFormCost[kKind];
+    constexpr int kWarps = Shape<kKind>::kWarps;
     const int64_t rows = static_cast<int64_t>(a.batch) * a.hkv;
     const int64_t pages = (a.selected ? a.k_cap : a.max_pages) + static_cast<int64_t>(a.max_recent);
-    int n = 1;
-    while (n < kMaxCluster && rows * n * 2 <= num_sms && static_cast<int64_t>(n) * warps * 2 <= pages) n *= 2;
-    // pages a warp of the short form goes through, over all waves, against the line's
-    const int64_t waves = (rows * n + num_sms - 1) / num_sms;
-    const int64_t mine = waves * ((pages + n * warps - 1) / (n * warps));
-    const int64_t line = (rows * pages + num_sms * warps - 1) / (num_sms * warps);
-    return mine <= line + 8 ? n : 0;
+    double best = kCost.line + kCost.row * static_cast<double>(rows) / num_sms +
+                  kCost.page * static_cast<double>(rows) * static_cast<double>(pages) / (num_sms * kWarps);
+    int ctas = 0;
+    for (int n = 1; n <= kMaxCluster; n *= 2) {
+        const int64_t at_once = resident_rows<kKind, kSplit>(n, num_sms, smem);
+        if (at_once == 0) continue;
+        const double wave = kCost.wave + (n > 1 ? 2 : 0) + kCost.page * static_cast<double>((pages + n * kWarps - 1) / (n * kWarps));
+        const double all = wave * static_cast<double>((rows + at_once - 1) / at_once);
+        if (all < best) best = all, ctas = n;
+    }
+    return ctas;
 }
 
 template <int kKind, bool kSplit>
@@ -1112,11 +1182,11 @@ cudaError_t launch_t(const PackedArgs& a, int num_sms, cudaStream_t stream) {
     using S = Shape<kKind>;
     constexpr int kSmem = S::kWarps * S::kDepth * kUnitBytes;
     const int64_t rows = static_cast<int64_t>(a.batch) * a.hkv;
-    if (const int n = row_ctas(a, S::kWarps, num_sms)) {
-        const cudaError_t e = ensure_kernel_attrs<row_kernel<kKind, kSplit>>(kSmem);
-        return e != cudaSuccess ? e : launch_dependent(row_kernel<kKind, kSplit>, rows * n, S::kThreads, kSmem, stream, n, a, n);
-    }
-    cudaError_t e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
+    cudaError_t e = ensure_kernel_attrs<row_kernel<kKind, kSplit>>(kSmem);
+    if (e != cudaSuccess) return e;
+    if (const int n = row_ctas<kKind, kSplit>(a, num_sms, kSmem))
+        return launch_dependent(row_kernel<kKind, kSplit>, rows * n, S::kThreads, kSmem, stream, n, a, n);
+    e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms, kMaxPackedCtas);
     e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
