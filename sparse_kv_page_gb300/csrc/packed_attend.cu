@@ -299,7 +299,8 @@ struct Running {
     Two unit[kBlocks];
     Two l[kBlocks];                                   // this lane's part of the sum
     Two z[kBlocks][2];                                // [column], of both groups: of weights times zeros
-    Two pw[kBlocks][2];                               // ... of weights times scales, since the last centre()
+    Two pw[kBlocks][2];                               // [group], of both columns: of weights times scales, as the
+                                                      // products take them, since the last centre()
     float lift, scale_limit;                          // log2 of the weights' factor; the largest scale that it is good for
 
     __device__ __forceinline__ void clear(const Control<kKind>& ctl, int which) {
@@ -358,11 +359,12 @@ struct Running {
                     for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
                     f[c] = m[n][c] == -INFINITY ? 0.f : fast_exp2(m[n][c] - top + change);
                     m[n][c] = top;
-                    const Two both = two(f[c], f[c]);
-                    z[n][c] = mul2(z[n][c], both);
-                    pw[n][c] = mul2(pw[n][c], both);
+                    z[n][c] = mul2(z[n][c], two(f[c], f[c]));
                 }
-                l[n] = mul2(l[n], two(f[0], f[1]));
+                const Two both = two(f[0], f[1]);
+                l[n] = mul2(l[n], both);
+                pw[n][0] = mul2(pw[n][0], both);
+                pw[n][1] = mul2(pw[n][1], both);
 #pragma unroll
                 for (int d = 0; d < 8; ++d) o[n][d][0] *= f[0], o[n][d][1] *= f[1], o[n][d][2] *= f[0], o[n][d][3] *= f[1];
             }
@@ -485,7 +487,6 @@ struct Running {
                         const float y = s[p][n][2 * i + c];
                         const Two weight = two(y, y), scaled = mul2(weight, scales);
                         z[n][c] = fma2(weight, zeros, z[n][c]);
-                        pw[n][c] = add2(pw[n][c], scaled);
                         parts_of(scaled, x[n][2 * i + c][0], x[n][2 * i + c][1]);
                     }
             }
@@ -495,10 +496,14 @@ struct Running {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t f[kBlocks][2];
 #pragma unroll
-                for (int n = 0; n < kBlocks; ++n) {
-                    f[n][0] = transposed(pack_f16x2(x[n][0][g], x[n][1][g]));       // tokens as rows
-                    f[n][1] = transposed(pack_f16x2(x[n][2][g], x[n][3][g]));
-                }
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t both = pack_f16x2(x[n][2 * i][g], x[n][2 * i + 1][g]);
+                        const float2 y = f16x2_of(both);
+                        pw[n][g] = add2(pw[n][g], two(y.x, y.y));
+                        f[n][i] = transposed(both);                      // tokens as rows
+                    }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t up = w[i] >> 8;
@@ -518,20 +523,22 @@ struct Running {
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                z[n][c] = fma2(pw[n][c], two(kMiddle, kMiddle), z[n][c]);
-                float x[2];
-                parts_of(pw[n][c], x[0], x[1]);
-                pw[n][c] = two(0.f, 0.f);
+            for (int g = 0; g < 2; ++g) {
+                float x[2], y[2];
+                parts_of(pw[n][g], x[0], x[1]);
+                pw[n][g] = two(0.f, 0.f);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
+                for (int c = 0; c < 2; ++c) {
+                    parts_of(z[n][c], y[0], y[1]);
+                    y[g] = fmaf(x[c], kMiddle, y[g]);
+                    z[n][c] = two(y[0], y[1]);
 #pragma unroll
-                    for (int i = 4; i < 32; i *= 2) x[g] += __shfl_xor_sync(kAll, x[g], i);
-                    x[g] *= -kMiddle * kCode;
+                    for (int i = 4; i < 32; i *= 2) x[c] += __shfl_xor_sync(kAll, x[c], i);
+                    x[c] *= -kMiddle * kCode;
 #pragma unroll
                     for (int d = 4 * g; d < 4 * g + 4; ++d) {
-                        o[n][d][c] += x[g];
-                        o[n][d][c + 2] = fmaf(x[g], 16.f, o[n][d][c + 2]);
+                        o[n][d][c] += x[c];
+                        o[n][d][c + 2] = fmaf(x[c], 16.f, o[n][d][c + 2]);
                     }
                 }
             }
