@@ -25,25 +25,12 @@
 #include <algorithm>
 #include <atomic>
 
-#include "pool_internal.h"
+#include "packed_units.cuh"
 
 namespace locks {
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
-constexpr int kRecentSteps = 3;                       // 8 KB against 2.4
-constexpr float kScaleLog2 = kInvSqrtD * kLog2e;
-// Queries are scaled by 2^(14 - e), e the exponent of the row's largest (within -100..100, so that
-// the factors are numbers); with codes of 2^-24 scores are in units of 2^(e + 10).
-constexpr float kQueryTop = 0x1p14f, kScoreUnit = 0x1p10f * kScaleLog2;
-constexpr float kCode = 0x1p-24f, kMiddle = 7.5f;
 constexpr int kCentre = 8;                            // pairs of pages, a power of two
-constexpr float kSlack = 8.f;                         // log2 that a score may pass the maximum by
-// Weights times a value's scale are fp16 (11 bits, rounded: 2^-11 of a weight at most, up or down;
-// the output has 8). All weights carry a factor 2^lift that brings the largest scale so far to
-// 2^5..2^6, and is set anew when a scale times it passes 2^7: with kSlack they stay below 2^15.
-constexpr int kScaleTop = 5;
-constexpr float kScaleLimit = 0x1p7f;
 
 // Variants: queries of a group in one block of 8 columns together with their low parts (kPair,
 // groups up to 4; bf16 queries have none and fill those columns with copies), in one block, or in
@@ -77,10 +64,7 @@ struct Control {
         struct {                                      // short rows: the CTA's partial
             float o[S::kRows][kD];
         } cta;
-        struct {                                      // long rows: steps of the sequences up to each thread's last
-            int64_t upto[S::kThreads], warp_sum[S::kWarps];
-            int2 len[S::kThreads];                    // pages and recent tokens of sequence i, where that is enough
-        } line;
+        LineShared<S::kThreads> line;                 // long rows
     };
 };
 
@@ -92,48 +76,6 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-__device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 f16x2_of(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
-// Two floats in one instruction.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float a, float b) {
-    Two d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void parts_of(Two x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-    Two d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    Two d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-    Two d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 // D = A B + D and D = A B on mma.sync m16n8k16. Not volatile, as nothing but the operands counts:
 // the compiler may move products past one another, which saves it register copies.
@@ -157,55 +99,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {          // of 8 x 
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-struct Len {
-    int pages, recent;                                // packed pages; recent tokens
-    __device__ int recent_pages() const { return (recent + kPage - 1) / kPage; }
-    __device__ int steps() const { return pages + kRecentSteps * recent_pages(); }
-};
-__device__ __forceinline__ int checked(const PackedArgs& a, int n, int64_t most, bool report) {
-    if (n >= 0 && n <= most) return n;
-    if (report) report_error(a.st, LOCKS_ERR_BAD_INDEX);
-    return 0;
-}
-__device__ __forceinline__ Len row_len(const PackedArgs& a, int b, int h, bool report) {
-    Len r;
-    const int pages = a.selected ? __ldcg(a.n_selected + static_cast<int64_t>(b) * a.hkv + h) : __ldcg(a.seq_pages + b);
-    const int recent = a.max_recent > 0 ? __ldcg(a.recent_tokens + b) : 0;
-    r.pages = checked(a, pages, a.selected ? a.k_cap : a.max_pages, report);
-    r.recent = checked(a, recent, static_cast<int64_t>(a.max_recent) * kPage, report);
-    return r;
-}
-// Steps of all rows of sequence b.
-__device__ __forceinline__ int64_t seq_steps(const PackedArgs& a, int b, bool report) {
-    if (!a.selected) return static_cast<int64_t>(row_len(a, b, 0, report).steps()) * a.hkv;
-    int64_t n = 0;
-    for (int h = 0; h < a.hkv; ++h) n += row_len(a, b, h, report).steps();
-    return n;
-}
-// Physical page of a row's packed page i.
-__device__ __forceinline__ int packed_id(const PackedArgs& a, int b, int h, int i) {
-    int j = i;
-    if (a.selected) j = __ldcg(a.selected + (static_cast<int64_t>(b) * a.hkv + h) * a.k_cap + i);
-    if (j >= 0 && j < a.max_pages) {
-        const int x = __ldcg(a.page_table + static_cast<int64_t>(b) * a.max_pages + j);
-        if (x >= 0 && x < a.num_packed) return x;
-    }
-    report_error(a.st, LOCKS_ERR_BAD_INDEX);
-    return 0;
-}
-
-// CTA c of n holds steps first(c) .. first(c + 1) of the line. (A 64-bit division is a long routine,
-// kept in one place.)
-static __device__ __noinline__ int64_t divide64(int64_t x, int64_t y) { return x / y; }
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-    if (x < (1ll << 32) && y < (1ll << 32)) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return divide64(x, y);
-}
-__device__ __forceinline__ int64_t first_step(int64_t total, int c, int n) { return divide(total * c, n); }
-__device__ __forceinline__ int cta_of(int64_t total, int64_t step, int n) {
-    return static_cast<int>(divide((step + 1) * n - 1, total));
 }
 
 // Dims 32 g .. 32 g + 31 of one block of a row's queries as B fragments, in fp16 parts (fp32 queries
@@ -652,13 +545,6 @@ struct Running {
     }
 };
 
-__device__ __forceinline__ void store_row(const PackedArgs& a, int64_t row, float value, float sum, int dim) {
-    a.out[row * kD + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : __fdividef(value, sum)));
-}
-__device__ __forceinline__ void store_lse(const PackedArgs& a, int64_t row, float m, float sum) {
-    if (a.lse) a.lse[row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
-}
-
 // What a warp has of a row: packed pages first, first + step, ... (`count` of them, the ids of the first
 // 32 by lane in `ids`) and recent pages recent0, recent0 + step, ... before recent1.
 struct Share {
@@ -883,12 +769,6 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) row_kernel(const __
     cluster_sync_all();                               // nobody leaves while its sums are read
 }
 
-// Steps off .. off + steps of a row.
-struct Part {
-    int b, h, off, steps;
-    Len len;
-};
-
 // Steps x0 .. x1 of a part as a warp's share.
 __device__ __forceinline__ Share share_of(const PackedArgs& a, const Part part, int x0, int x1) {
     const int lane = threadIdx.x & 31;
@@ -948,101 +828,29 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
     constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ Control<kKind> ctl;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool by_row = cuts_by_row(a, gridDim.x);
     grid_dependency_wait();
     allow_dependent_launch();
 
-    // lengths: kept where they are the same for all kv heads and there is a thread for each sequence
-    const int per = (a.batch + kThreads - 1) / kThreads, tid = threadIdx.x;
-    const bool kept = !a.selected && per <= 1;
-    {
-        int64_t sum = 0;
-        if (kept) {
-            Len len = {0, 0};
-            if (tid < a.batch) len = row_len(a, tid, 0, blockIdx.x == 0);
-            ctl.line.len[tid] = make_int2(len.pages, len.recent);
-            sum = static_cast<int64_t>(len.steps()) * a.hkv;
-        } else {
-            for (int i = 0; i < per; ++i) {
-                const int b = tid * per + i;
-                if (b < a.batch) sum += seq_steps(a, b, blockIdx.x == 0);
-            }
-        }
-        int64_t upto = sum;
-#pragma unroll
-        for (int x = 1; x < 32; x *= 2) {
-            const int64_t y = __shfl_up_sync(kAll, upto, x);
-            if (lane >= x) upto += y;
-        }
-        if (lane == 31) ctl.line.warp_sum[warp] = upto;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += ctl.line.warp_sum[w];
-        ctl.line.upto[tid] = upto;
-    }
-    const auto length = [&](int b, int h) {
-        if (!kept) return row_len(a, b, h, false);
-        const int2 x = ctl.line.len[b];
-        return Len{x.x, x.y};
-    };
-    // rows without tokens are nobody's
-    for (int r = blockIdx.x * kThreads + tid; r < a.batch * a.hkv; r += gridDim.x * kThreads) {
-        const int b = r / a.hkv, h = r % a.hkv;
-        if (length(b, h).steps() != 0) continue;
-        for (int q = 0; q < a.group; ++q) {
-            const int64_t row = static_cast<int64_t>(b) * a.hq + h * a.group + q;
-            for (int d = 0; d < kD; d += 8) *reinterpret_cast<uint4*>(a.out + row * kD + d) = make_uint4(0, 0, 0, 0);
-            store_lse(a, row, 0.f, 0.f);
-        }
-        if (by_row) a.cuts[r] = {-1, 0, 0};
-    }
-    __syncthreads();
-    const int64_t total = ctl.line.upto[kThreads - 1];
+    Line<kThreads> line{a, ctl.line};
+    line.scan(by_row);
+    const int64_t total = line.total();
     const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps));
     int64_t pos = 0, end = 0;
     if (static_cast<int>(blockIdx.x) < ctas) {
         pos = first_step(total, blockIdx.x, ctas);
         end = first_step(total, blockIdx.x + 1, ctas);
     }
-    if (!by_row && tid == 0) a.cuts[blockIdx.x] = {-1, 0, 0};
+    if (!by_row && threadIdx.x == 0) a.cuts[blockIdx.x] = {-1, 0, 0};
     if (pos >= end) return;
-
-    // the row at pos
     Part part[2];
-    {
-        Part& p = part[0];
-        int before = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) before += __popc(__ballot_sync(kAll, ctl.line.upto[i * 32 + lane] <= pos));
-        int64_t at = pos - (before > 0 ? ctl.line.upto[before - 1] : 0);
-        p.b = before * per;
-        if (kept) {
-            p.len = length(p.b, 0);
-            p.h = static_cast<int>(divide(at, p.len.steps()));
-            p.off = static_cast<int>(at - static_cast<int64_t>(p.h) * p.len.steps());
-        } else {
-            for (int64_t n; p.b < a.batch - 1 && at >= (n = seq_steps(a, p.b, false)); ++p.b) at -= n;
-            p.h = 0;
-            for (p.len = length(p.b, 0); p.h < a.hkv - 1 && at >= p.len.steps(); p.len = length(p.b, ++p.h)) at -= p.len.steps();
-            p.off = static_cast<int>(at);
-        }
-    }
-    // the row behind p's with any steps (there is one as long as steps are left)
-    const auto next_row = [&](const Part& p) {
-        Part r = p;
-        do {
-            if (++r.h == a.hkv) ++r.b, r.h = 0;
-            r.len = length(r.b, r.h);
-        } while (r.len.steps() == 0 && r.b < a.batch - 1);
-        r.off = 0;
-        return r;
-    };
+    part[0] = line.at(pos);
 #pragma unroll 1
     while (true) {
         part[0].steps = static_cast<int>(min(end - pos, static_cast<int64_t>(part[0].len.steps() - part[0].off)));
         int parts = 1;
         if (pos + part[0].steps < end) {
-            part[1] = next_row(part[0]);
+            part[1] = line.next(part[0]);
             part[1].steps = static_cast<int>(min(end - pos - part[0].steps, static_cast<int64_t>(part[1].len.steps())));
             parts = 2;
         }
@@ -1073,7 +881,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
             pos += p.steps;
         }
         if (pos >= end) break;
-        part[0] = next_row(part[parts - 1]);
+        part[0] = line.next(part[parts - 1]);
         __syncthreads();                              // the slots and sums are read
     }
 }
@@ -1193,10 +1001,16 @@ cudaError_t launch_t(const PackedArgs& a, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (const int n = row_ctas<kKind, kSplit>(a, num_sms, kSmem))
         return launch_dependent(row_kernel<kKind, kSplit>, rows * n, S::kThreads, kSmem, stream, n, a, n);
-    e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
-    if (e != cudaSuccess) return e;
-    const int ctas = std::min(num_sms, kMaxPackedCtas);
-    e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
+    int ctas;
+    if constexpr (kKind == 2) {
+        ctas = packed_tiles_ctas(num_sms);
+        e = launch_packed_tiles(a, ctas, stream);
+    } else {
+        e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
+        if (e != cudaSuccess) return e;
+        ctas = std::min(num_sms, kMaxPackedCtas);
+        e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
+    }
     if (e != cudaSuccess) return e;
     return launch_dependent(join_kernel, std::min<int64_t>(rows, ctas) * a.group, kJoinThreads, 0, stream, 1, a);
 }
