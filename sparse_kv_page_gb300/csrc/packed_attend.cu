@@ -1001,16 +1001,10 @@ cudaError_t launch_t(const PackedArgs& a, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (const int n = row_ctas<kKind, kSplit>(a, num_sms, kSmem))
         return launch_dependent(row_kernel<kKind, kSplit>, rows * n, S::kThreads, kSmem, stream, n, a, n);
-    int ctas;
-    if constexpr (kKind == 2) {
-        ctas = packed_tiles_ctas(num_sms);
-        e = launch_packed_tiles(a, ctas, stream);
-    } else {
-        e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
-        if (e != cudaSuccess) return e;
-        ctas = std::min(num_sms, kMaxPackedCtas);
-        e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
-    }
+    e = ensure_kernel_attrs<line_kernel<kKind, kSplit>>(kSmem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(num_sms, kMaxPackedCtas);
+    e = launch_dependent(line_kernel<kKind, kSplit>, ctas, S::kThreads, kSmem, stream, 1, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(join_kernel, std::min<int64_t>(rows, ctas) * a.group, kJoinThreads, 0, stream, 1, a);
 }

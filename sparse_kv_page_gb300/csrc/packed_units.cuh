@@ -3,6 +3,7 @@
 #pragma once
 
 #include "pool_internal.h"
+#include "two_floats.cuh"
 
 namespace locks {
 namespace {
@@ -21,8 +22,6 @@ constexpr float kSlack = 8.f;                         // log2 that a score may p
 constexpr int kScaleTop = 5;
 constexpr float kScaleLimit = 0x1p7f;
 
-__device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -38,31 +37,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ float2 f16x2_of(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
-// Two floats in one instruction.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float a, float b) {
-    Two d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void parts_of(Two x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-    Two d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    Two d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-    Two d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 struct Len {
     int pages, recent;                                // packed pages; recent tokens
     __device__ int recent_pages() const { return (recent + kPage - 1) / kPage; }

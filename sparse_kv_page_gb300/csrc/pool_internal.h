@@ -57,9 +57,6 @@ PackedLayout packed_layout(int group);
 __host__ __device__ inline bool cuts_by_row(const PackedArgs& a, int ctas) {
     return static_cast<int64_t>(a.batch) * a.hkv <= ctas;
 }
-// Long rows of more than eight queries to a kv head (packed_tiles.cu); the joining launch follows.
-int packed_tiles_ctas(int num_sms);
-cudaError_t launch_packed_tiles(const PackedArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_packed_attention(const PackedArgs& a, int num_sms, cudaStream_t stream);
 
 struct CopyArgs {
