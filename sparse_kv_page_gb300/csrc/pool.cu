@@ -147,7 +147,20 @@ __device__ __forceinline__ void walk_segment(const PoolArgs& a, const Segment& s
 }
 
 // Sums over the batch, by one block: calls put(b, sum of count(0..b), count(b), extra) for every row in
-// turn of its thread, with the extra number that count(b, extra) gave; returns the sum of all.
+// turn of its thread, with the extra number that count(b, extra) gave; returns the sum of all. Sums stop
+// at kMany, which no pool has: all the rows' needs together may pass 31 bits.
+constexpr int kMany = (1 << 30) + 1;
+__device__ __forceinline__ int add_up(int x, int y) {
+    return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), static_cast<unsigned>(kMany)));
+}
+__device__ __forceinline__ int add_upto(int x) {      // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(kAll, x, o);
+        if ((threadIdx.x & 31) >= o) x = add_up(x, y);
+    }
+    return x;
+}
 template <typename Count, typename Put>
 __device__ __forceinline__ int scan_rows(int batch, int* scratch, Count count, Put put) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -156,13 +169,14 @@ __device__ __forceinline__ int scan_rows(int batch, int* scratch, Count count, P
         const int b = b0 + threadIdx.x;
         int extra = 0;
         const int mine = b < batch ? count(b, extra) : 0;
-        int upto = warp_upto(mine);
+        int upto = add_upto(mine);
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
-        const int sums = scratch[lane];
-        upto += base + warp_sum(lane < warp ? sums : 0);
+        const int sums = add_upto(scratch[lane]);
+        const int before = __shfl_sync(kAll, sums, max(warp - 1, 0));
+        upto = add_up(upto, add_up(base, warp > 0 ? before : 0));
         if (b < batch) put(b, upto, mine, extra);
-        base += warp_sum(sums);
+        base = add_up(base, __shfl_sync(kAll, sums, 31));
         __syncthreads();
     }
     return base;
@@ -352,7 +366,9 @@ __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int j = j0 + i * kThreads;
-            if (j < end) a.page_table_out[row + j] = page[i];
+            if (j >= end) continue;
+            a.page_table_out[row + j] = page[i];
+            if (page[i] < 0 || page[i] >= a.num_pages) report_error(a.st, LOCKS_ERR_BAD_INDEX);
         }
     }
     const int n = tokens_of(a, b), children = __ldcg(a.children + b);
@@ -452,7 +468,8 @@ __global__ void __launch_bounds__(kThreads) compact_place_kernel(const __grid_co
 #pragma unroll 1
     for (int at0 = seg.first; at0 < seg.last; at0 += kRound) {
         const int at = at0 + 4 * threadIdx.x;
-        const unsigned bits = used4(load4(a.refs, at, seg.last));
+        const int4 r = load4(a.refs, at, seg.last);
+        const unsigned bits = used4(r);
         const int upto = warp_upto(__popc(bits));
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
@@ -466,6 +483,7 @@ __global__ void __launch_bounds__(kThreads) compact_place_kernel(const __grid_co
                 if (on && page >= used) a.list_src[u - low] = page;
                 if (!on && page < used) a.list_dst[page - u] = page;
                 a.new_page[page] = on && page >= used ? -1 - (u - low) : page;
+                if (page >= used && (k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w) < 0) a.refs_out[page] = 0;
             }
             u += on;
         }
@@ -480,7 +498,8 @@ __global__ void __launch_bounds__(kThreads) renumber_kernel(const __grid_constan
     grid_dependency_wait();
     allow_dependent_launch();
     const int moves = __ldcg(a.n_list);
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < moves; i += gridDim.x * kThreads) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < moves;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
         const int from = __ldcg(a.list_src + i), to = __ldcg(a.list_dst + i);
         a.new_page[from] = to;
         a.refs_out[to] = __ldcg(a.refs + from);
@@ -619,7 +638,7 @@ cudaError_t launch_compact(const PoolArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.refs_out != a.refs) {
+    if (a.refs_out != a.refs && a.num_pages > 0) {
         const int64_t ctas = (static_cast<int64_t>(a.num_pages) + 4 * kRowThreads - 1) / (4 * kRowThreads);
         const cudaError_t e = launch_dependent(copy_refs_kernel, ctas, kRowThreads, 0, stream, 1, a);
         if (e != cudaSuccess) return e;
@@ -633,6 +652,7 @@ cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_copy_pages(const CopyArgs& a, int num_sms, cudaStream_t stream) {
     int64_t pieces = 0;
     for (int i = 0; i < a.num_planes; ++i) pieces += (a.page_bytes[i] + kCopyBytes - 1) / kCopyBytes;
+    if (pieces == 0) return cudaSuccess;              // pages of no bytes
     const int64_t ctas = std::min<int64_t>(pieces * a.max_pairs, static_cast<int64_t>(num_sms) * 8);
     return launch_dependent(copy_kernel, ctas, kCopyThreads, 0, stream, 1, a);
 }
