@@ -96,9 +96,12 @@ LOCKS_API int locks_packed_workspace_size(const locks_dims_t* dims, size_t* byte
  * used, whatever they hold. A NaN among the tokens' keys or values gives NaN to the rows that
  * attend to it, and so may an infinity.
  * - q: q_type LOCKS_FP32 or LOCKS_BF16, contiguous [batch][num_q_heads][128], 16-byte aligned,
- *   each head's of magnitudes from 2^-60 to 2^60 or 0. fp32 queries and the softmax weights enter the products as a bf16
- *   high and low part (at least 14 significant bits); sums and softmax statistics are fp32.
- *   Keys and values of magnitudes up to 2^50 are served.
+ *   each head's of magnitudes from 2^-60 to 2^60 or 0. fp32 queries enter the products as two
+ *   fp16 parts, 22 bits below each head's largest (over recent tokens as two bf16 parts, 16 bits).
+ *   The weights times the values' scales enter as fp16, rounded (11 bits; over recent tokens as
+ *   two bf16 parts). Sums and softmax statistics are fp32.
+ *   Keys and values of magnitudes up to 2^50 are served. Values in groups of scales below 2^-49
+ *   are off by up to 2^-75 each.
  * - page_table int32 [batch][max_pages_per_seq], ids of packed pages; not read when
  *   max_pages_per_seq is 0.
  * - selected int32 [batch][num_kv_heads][k_cap] (logical pages, in any order; the same one
@@ -223,7 +226,7 @@ LOCKS_API int locks_free_pages(const int32_t* refs, int32_t num_pages, const int
  *   another array.
  * - seq_tokens out of [0, 16 * max_pages_per_seq] record LOCKS_ERR_BAD_INDEX and the row is not
  *   written; an id out of range is handed on and records it too.
- * Two launches.
+ * Three launches, or two for a pool of up to 4096 pages.
  */
 LOCKS_API int locks_compact_pages(const locks_dims_t* dims, const int32_t* page_table, const int32_t* seq_tokens,
                                   const int32_t* refs, int32_t* page_table_out, int32_t* refs_out, int32_t* move_src,

@@ -234,8 +234,8 @@ struct Running {
             float change = 0.f;                       // log2
 #pragma unroll
             for (int x = 1; x < 32; x *= 2) scale = fmaxf(scale, __shfl_xor_sync(kAll, scale, x));
-            if (scale > scale_limit) {                // kScaleTop - exponent, within -100..100
-                const int e = kScaleTop - min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, -95), 105);
+            if (scale > scale_limit) {                // kScaleTop - exponent, within -100..54 (see kScaleLeast)
+                const int e = kScaleTop - min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, kScaleLeast), 105);
                 change = static_cast<float>(e) - lift;
                 lift += change;
                 scale_limit = kScaleLimit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);

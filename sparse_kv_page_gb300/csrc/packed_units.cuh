@@ -19,7 +19,9 @@ constexpr float kSlack = 8.f;                         // log2 that a score may p
 // Weights times a value's scale are fp16 (11 bits, rounded: 2^-11 of a weight at most, up or down;
 // the output has 8). All weights carry a factor 2^lift that brings the largest scale so far to
 // 2^5..2^6, and is set anew when a scale times it passes 2^7: with kSlack they stay below 2^15.
-constexpr int kScaleTop = 5;
+// Scales below 2^kScaleLeast count as that large, for the zeros, of up to 2^50, take the factor too:
+// 2^(54 + kSlack + 50) and the sums of it are numbers.
+constexpr int kScaleTop = 5, kScaleLeast = -49;
 constexpr float kScaleLimit = 0x1p7f;
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {

@@ -98,3 +98,23 @@ def test_compact_clears_counts_below_zero(pool, in_place):
     assert L.locks_get_device_status(ws) == 0
     assert host(n).tolist() == [2] and host(src).tolist()[:2] == [5, pool - 1] and host(dst).tolist()[:2] == [0, 1]
     assert host(ro).tolist() == [3, 4] + [0] * (pool - 2)
+
+
+def test_attention_over_large_zeros_and_tiny_scales():
+    """The first 64 dims of all values are 2^40 and the others below 2^-86: weights grow with the scales,
+    and their products with the zeros are numbers still. (Scales below 2^-49 count as fp16 numbers of
+    2^-54: a value's error is at most 15 * 2^-25 * 2^-54, and 2^10 tokens of them less than 2^-60.)"""
+    from tests.test_gpu_packed import make_case, run, tokens_of, f64
+    from tests import pool_ref as ref
+    c = make_case([40], [0], 8, 2, seed=31)
+    fields = c["packed"][..., 2304:].contiguous().view(torch.bfloat16).view(*c["packed"].shape[:2], 16, 4)
+    fields[..., 0], fields[..., 1], fields[..., 2], fields[..., 3] = 0.0, 2.0 ** -90, 2.0 ** 40, 2.0 ** -87
+    c["packed"][..., 2304:] = fields.view(*c["packed"].shape[:2], 64).view(torch.uint8)
+    run(c)
+    assert L.locks_get_device_status(c["ws"]) == 0
+    got, units, table = f64(c["out"]), c["packed"].cpu().numpy(), c["table"].cpu().numpy()
+    assert (np.abs(got[0, :, :64] - 2.0 ** 40) <= 2.0 ** 32).all()
+    for h in range(2):
+        want, want_lse, _, size = ref.attend(f64(c["q"])[0, 4 * h:4 * h + 4], *tokens_of(c, 0, h, units, table))
+        assert (np.abs(got[0, 4 * h:4 * h + 4, 64:] - want[:, 64:]) <= 2.0 ** -60).all()
+        assert (np.abs(f64(c["lse"])[0, 4 * h:4 * h + 4] - want_lse) <= 2.0 ** -15 * size + 2.0 ** -16).all()
