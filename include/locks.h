@@ -107,7 +107,6 @@ enum {
     LOCKS_ERR_TIMEOUT = -5,            /* device: a bounded wait ran out (status word) */
     LOCKS_ERR_BAD_INDEX = -6,          /* device: a page id or page-table entry out of range;
                                           the unit was skipped or read from page 0 instead */
-    LOCKS_ERR_NO_PAGES = -7,           /* device: a pool has too few free pages (locks_pool.h) */
 };
 
 typedef struct {

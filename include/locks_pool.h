@@ -54,6 +54,10 @@ extern "C" {
 #define LOCKS_PACKED_BYTES 2432
 #define LOCKS_MAX_PLANES 128
 
+enum {
+    LOCKS_ERR_NO_PAGES = -7,           /* device: a pool has too few free pages */
+};
+
 /*
  * Packs pages: unit (dst_pages[i], h) of the packed pool from page src_pages[i] of the bf16
  * pool, i < n_pages, h < num_kv_heads. For every group (32 dims of a key, 64 of a value):

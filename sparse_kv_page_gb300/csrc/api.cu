@@ -6,7 +6,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "cache_internal.h"
+#include "pool_internal.h"
 
 namespace {
 
