@@ -4,9 +4,10 @@
 // both. A warp packs the keys or the values of a unit, or unpacks both. The bf16 side is read and
 // written 16 bytes a lane, two tokens to an instruction; the codes go through a staging area in
 // shared memory, because the order of the attention's fragments spreads a lane's eight dims over
-// four or eight words. Packing takes about 5 instructions a value, most of them for two values at
-// once, and is bounded by their issue: 4096 pages of 8 kv heads in 73 us (4.8 TB/s of both sides);
-// unpacking them in 55 us, as fast as HBM copies.
+// four or eight words. Packing takes a warp 800 instructions for 64 values a lane, with most of the
+// arithmetic on two values at once, and is bounded by them (65% of the issue slots): 4096 pages of 8 kv heads
+// in 68 us (5.1 TB/s of both sides; 73 without the next values on their way meanwhile). Unpacking
+// them takes 55 - 57 us, as fast as HBM copies.
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -102,10 +103,8 @@ __device__ __forceinline__ void codes_of(const uint4& x0, const uint4& x1, uint3
     }
 }
 
-// A unit's entries of the lists, or -1 where there is nothing to do.
-__device__ __forceinline__ bool find_pages(const PackArgs& a, int i, int& from, int& to) {
-    from = __ldg(a.src + i);
-    to = a.dst ? __ldg(a.dst + i) : from;
+// Whether there is something to do for an entry of the lists.
+__device__ __forceinline__ bool find_pages(const PackArgs& a, int from, int to) {
     if (from < 0 || to < 0) return false;
     if (from < a.num_src && to < a.num_dst) return true;
     report_error(a.st, LOCKS_ERR_BAD_INDEX);
@@ -174,27 +173,55 @@ __device__ __forceinline__ void pack_values(const uint4 (&x)[8], uint8_t* unit) 
     }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) pack_kernel(const __grid_constant__ PackArgs a) {
+// A warp's next keys or values are on their way to shared memory while it packs these, and the ids
+// of those behind are too. Each lane reads what it has copied itself.
+constexpr int kPackCtas = 3;                          // of an SM, by their registers
+__global__ void __launch_bounds__(kWarps * 32, kPackCtas) pack_kernel(const __grid_constant__ PackArgs a) {
     __shared__ __align__(16) uint8_t stage[kWarps][1024 + 256];
+    __shared__ uint4 ahead[kWarps][8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* const unit = stage[warp];
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t items = 2 * static_cast<int64_t>(a.n) * a.hkv;         // a unit's keys, its values
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < items;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const bool values = u & 1;
-        const int i = static_cast<int>((u >> 1) / a.hkv), h = static_cast<int>((u >> 1) % a.hkv);
-        int from, to;
-        if (!find_pages(a, i, from, to)) continue;
-        const uint16_t* in = (values ? a.v_in : a.k_in) + (static_cast<int64_t>(from) * a.hkv + h) * (kPage * kD) + lane * 8;
-        uint4 x[8];
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int heads = __ffs(a.hkv) - 1;               // a power of two
+    int src = -1, dst = -1;                           // pages of the next item
+    const auto ids = [&](int64_t v) {
+        if (v >= items) return;
+        const int i = static_cast<int>(v >> (1 + heads));
+        src = __ldg(a.src + i);
+        dst = a.dst ? __ldg(a.dst + i) : src;
+    };
+    // Starts on item v; the page that it goes to, or -1.
+    const auto fetch = [&](int64_t v) {
+        if (v >= items || !find_pages(a, src, dst)) return -1;
+        const int h = static_cast<int>(v >> 1) & (a.hkv - 1);
+        const uint16_t* in = (v & 1 ? a.v_in : a.k_in) + (static_cast<int64_t>(src) * a.hkv + h) * (kPage * kD) + lane * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __ldcs(reinterpret_cast<const uint4*>(in + j * 2 * kD));      // tokens 2j, 2j + 1
+        for (int j = 0; j < 8; ++j) cp_async_16(&ahead[warp][j][lane], in + j * 2 * kD);      // tokens 2j, 2j + 1
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return dst;
+    };
+    ids(u);
+    int to = fetch(u);
+    ids(u + stride);
+    for (; u < items; u += stride) {
+        const bool values = u & 1;
+        const int h = static_cast<int>(u >> 1) & (a.hkv - 1), here = to;
+        uint4 x[8];
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = ahead[warp][j][lane];
+        __syncwarp();
+        to = fetch(u + stride);
+        ids(u + 2 * stride);
+        if (here < 0) continue;
         if (values) pack_values(x, unit);
         else pack_keys(x, unit);
         __syncwarp();
-        uint8_t* const out = a.packed + (static_cast<int64_t>(to) * a.hkv + h) * kUnitBytes + lane * 16;
+        uint8_t* const out = a.packed + (static_cast<int64_t>(here) * a.hkv + h) * kUnitBytes + lane * 16;
         uint8_t* const codes = out + (values ? kUnitVCodes : 0);
         uint8_t* const scales = out + (values ? kUnitVScales : kUnitKScales);
         const uint4* const from_stage = reinterpret_cast<const uint4*>(unit) + lane;
@@ -215,15 +242,15 @@ __global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_consta
     __shared__ __align__(16) uint8_t stage[kWarps][kUnitBytes];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* const unit = stage[warp];
-    const int row = lane >> 4, chunk = lane & 15;
+    const int row = lane >> 4, chunk = lane & 15, heads = __ffs(a.hkv) - 1;
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t units = static_cast<int64_t>(a.n) * a.hkv;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
          u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int i = static_cast<int>(u / a.hkv), h = static_cast<int>(u % a.hkv);
-        int from, to;
-        if (!find_pages(a, i, from, to)) continue;
+        const int i = static_cast<int>(u >> heads), h = static_cast<int>(u) & (a.hkv - 1);
+        const int from = __ldg(a.src + i), to = a.dst ? __ldg(a.dst + i) : from;
+        if (!find_pages(a, from, to)) continue;
         const uint4* in = reinterpret_cast<const uint4*>(a.packed + (static_cast<int64_t>(from) * a.hkv + h) * kUnitBytes);
         __syncwarp();
         uint4 x[5];
@@ -269,17 +296,17 @@ __global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_consta
     }
 }
 
-int grid_of(int64_t items, int num_sms) {
-    return static_cast<int>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 8));
+int grid_of(int64_t items, int num_sms, int per_sm) {
+    return static_cast<int>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * per_sm));
 }
 
 }  // namespace
 
 cudaError_t launch_pack(const PackArgs& a, int num_sms, cudaStream_t stream) {
-    return launch_dependent(pack_kernel, grid_of(2 * static_cast<int64_t>(a.n) * a.hkv, num_sms), kWarps * 32, 0, stream, 1, a);
+    return launch_dependent(pack_kernel, grid_of(2 * static_cast<int64_t>(a.n) * a.hkv, num_sms, kPackCtas), kWarps * 32, 0, stream, 1, a);
 }
 cudaError_t launch_unpack(const PackArgs& a, int num_sms, cudaStream_t stream) {
-    return launch_dependent(unpack_kernel, grid_of(static_cast<int64_t>(a.n) * a.hkv, num_sms), kWarps * 32, 0, stream, 1, a);
+    return launch_dependent(unpack_kernel, grid_of(static_cast<int64_t>(a.n) * a.hkv, num_sms, 8), kWarps * 32, 0, stream, 1, a);
 }
 
 }  // namespace locks
