@@ -166,7 +166,7 @@ LOCKS_API int locks_pool_workspace_size(const locks_dims_t* dims, size_t* bytes)
  *   seq_tokens_out[b] = n, 0 where parents[b] is -1; further entries are not written
  *   copy_src[i], copy_dst[i], i < *n_copies: the pages whose first n % 16 rows the caller has
  *       to copy (locks_copy_pages), in ascending order of b
- *   refs_out: refs with the old rows' holds let go and the new rows' added
+ *   refs_out: refs with the old rows' holds let go and the new rows' added, 1 for the pages taken
  * Free are the pages with refs <= 0 before the call, taken in ascending order for ascending b;
  * pages that lose their last holder become free after it. Where there are too few,
  * LOCKS_ERR_NO_PAGES is recorded and the last ones go without: their rows keep the full pages
@@ -177,7 +177,7 @@ LOCKS_API int locks_pool_workspace_size(const locks_dims_t* dims, size_t* bytes)
  * - num_phys_pages is the size of the pool that the table names pages of.
  * - seq_tokens out of [0, 16 * max_pages_per_seq] count as 0, a parent out of [-1, batch) as -1,
  *   a page id out of range is handed on and not counted; each records LOCKS_ERR_BAD_INDEX.
- * - batch at most 65536. Two launches.
+ * - batch at most 65536. Two launches, or one for small pools.
  */
 LOCKS_API int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page_table, const int32_t* seq_tokens,
                                    const int32_t* parents, const int32_t* refs, int32_t* page_table_out,
@@ -195,7 +195,7 @@ LOCKS_API int locks_fork_sequences(const locks_dims_t* dims, const int32_t* page
  * records LOCKS_ERR_BAD_INDEX.
  * - seq_tokens_out may be seq_tokens and refs_out refs; else no output may overlap another array.
  * - n_free (int32 [1], may be NULL) receives the number of pages that are free afterwards.
- * - batch at most 65536. Two launches.
+ * - batch at most 65536. Two launches, or one for small pools.
  */
 LOCKS_API int locks_take_pages(const locks_dims_t* dims, int32_t* page_table, const int32_t* seq_tokens,
                                const int32_t* new_tokens, const int32_t* refs, int32_t* seq_tokens_out,
@@ -230,7 +230,7 @@ LOCKS_API int locks_free_pages(const int32_t* refs, int32_t num_pages, const int
  *   another array.
  * - seq_tokens out of [0, 16 * max_pages_per_seq] record LOCKS_ERR_BAD_INDEX and the row is not
  *   written; an id out of range is handed on and records it too.
- * Three launches, or two for a pool of up to 4096 pages.
+ * Three launches, or one or two for small pools.
  */
 LOCKS_API int locks_compact_pages(const locks_dims_t* dims, const int32_t* page_table, const int32_t* seq_tokens,
                                   const int32_t* refs, int32_t* page_table_out, int32_t* refs_out, int32_t* move_src,

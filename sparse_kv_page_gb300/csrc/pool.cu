@@ -4,11 +4,12 @@
 // Which pages are free follows from the reference counts alone, so the calls that look for
 // free pages (fork, take) or rank the used ones (compact) scan them in two launches: one counts
 // them by blocks of the pool (and plans, in a block of its own, who needs how many pages), the
-// next knows every page's rank from the blocks' counts and places it. A call is short, a few MB at
-// most, so what bounds it are the launches and the loads that wait for one another; each launch
-// starts while the one before it runs. Measured: freeing pages of 3 sequences and taking some for 29
-// others in a pool of 16K pages 10.4 us; of 48 x 8192 pages in a pool of 1M 19.6; forking 2 x 64 rows
-// of 8188 pages and copying the last ones 15.6; compacting a pool of 2048 pages, with the copies, 11.5.
+// next knows every page's rank from the blocks' counts and places it. For small pools one block does
+// both. A call is short, a few MB at most, so what bounds it are the launches and the loads that wait
+// for one another; each launch starts while the one before it runs. Measured: freeing pages of 3
+// sequences and taking some for 29 others in a pool of 16K pages 8.7 us; of 48 x 8192 pages in a pool
+// of 1M 19.5; forking 2 x 64 rows of 8188 pages and copying the last ones 15.3; compacting a pool of 2048
+// pages, with the copies, 8.7.
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -122,16 +123,15 @@ __device__ __forceinline__ void join_counts(const PoolArgs& a, int i, int* scrat
 }
 static_assert(kMaxPoolBlocks <= kThreads, "a thread per block of the pool");
 
-// Calls f(page, rank) for the flagged pages in a segment, ranks counted from `rank`; stops behind
-// rank `most`.
-template <typename F>
-__device__ __forceinline__ void walk_segment(const PoolArgs& a, const Segment& seg, int rank, int most, int* scratch,
-                                             F f) {
+// Calls f(page, rank) for the pages in a segment that bits_at(page of a lane's four) flags, ranks counted
+// from `rank`; stops behind rank `most`.
+template <typename Bits, typename F>
+__device__ __forceinline__ void walk_segment(const Segment& seg, int rank, int most, int* scratch, Bits bits_at, F f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
     for (int at0 = seg.first; at0 < seg.last && rank < most; at0 += kRound) {
         const int at = at0 + 4 * threadIdx.x;
-        const unsigned bits = at < seg.last ? __ldcg(a.flags + at / 4) : 0u;
+        const unsigned bits = at < seg.last ? bits_at(at) : 0u;
         const int upto = warp_upto(__popc(bits));
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
@@ -146,6 +146,10 @@ __device__ __forceinline__ void walk_segment(const PoolArgs& a, const Segment& s
         rank += warp_sum(sums);
         __syncthreads();
     }
+}
+
+__device__ __forceinline__ auto flags_at(const PoolArgs& a) {
+    return [&a](int at) -> unsigned { return __ldcg(a.flags + at / 4); };
 }
 
 // Sums over the batch, by one block: calls put(b, sum of count(0..b), count(b), extra) for every row in
@@ -182,6 +186,41 @@ __device__ __forceinline__ int scan_rows(int batch, int* scratch, Count count, P
         __syncthreads();
     }
     return base;
+}
+
+// ------------------------------------------------------------------ small pools
+//
+// One block does a call on a small pool whole, in one launch: the counts stay in its registers, what
+// the rows need in shared memory, and a warp takes a piece of a row. Measured (graphs of calls, us, one
+// block / two or three launches; pool, rows x entries): taking 500, 8 x 31 4.5 / 6.1, 16000, 32 x 250 5.4 /
+// 6.7; forking 500, 8 x 31 5.1 / 9.3, 8000, 32 x 125 7.8 / 9.1, 16000, 32 x 250 10.6 / 8.7; compacting 500,
+// 8 x 31 3.8 / 6.5, 8000, 32 x 125 8.7 / 10.6. (Freeing into another array, 500 2.4 / 2.7, 16000 4.9 / 2.9,
+// has two launches always.)
+constexpr int kOneRounds = 4, kTakePages = kOneRounds * kRound, kForkPages = 2 * kRound, kOneBatch = kThreads;
+constexpr int kMovePages = 2 * kRound;                // ids of 16 bits in shared memory
+constexpr int kWarpPiece = 4 * 32, kOnePieces = 2 * kWarps;
+__host__ __device__ inline int warp_pieces(int entries) { return entries > kWarpPiece ? (entries + kWarpPiece - 1) / kWarpPiece : 1; }
+
+// Bits (free4 or used4) of a lane's pages, four of each round, and the counts copied on the way.
+template <typename Kind>
+__device__ __forceinline__ unsigned one_bits(const PoolArgs& a, Kind kind) {
+    const bool copy = a.refs_out != a.refs;
+    int4 r[kOneRounds];
+    unsigned bits = 0u;
+#pragma unroll
+    for (int k = 0; k < kOneRounds; ++k) r[k] = load4(a.refs, k * kRound + 4 * threadIdx.x, a.num_pages);
+#pragma unroll
+    for (int k = 0; k < kOneRounds; ++k) {
+        bits |= kind(r[k]) << (4 * k);
+        if (copy) store4(a.refs_out, k * kRound + 4 * threadIdx.x, a.num_pages, r[k]);
+    }
+    return bits;
+}
+// f(row, first entry of this lane; its others are 32, 64 and 96 further on) for all pieces of all rows.
+template <typename F>
+__device__ __forceinline__ void each_piece(int rows, int entries, F f) {
+    const int pieces = warp_pieces(entries);
+    for (int x = threadIdx.x >> 5; x < rows * pieces; x += kWarps) f(x / pieces, (x % pieces) * kWarpPiece + (threadIdx.x & 31));
 }
 
 // ------------------------------------------------------------------ take
@@ -245,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_const
         const int* const upto = near ? near_upto : a.scan;
         const int* const shift = near ? near_shift : a.shift;
         int lo = 0;                                   // the first row whose sum passes r, which only grows
-        walk_segment(a, segment_of(a.num_pages, block), before, taken, scratch, [&](int page, int r) {
+        walk_segment(segment_of(a.num_pages, block), before, taken, scratch, flags_at(a), [&](int page, int r) {
             if (upto[lo] <= r) {
                 int hi = a.batch - 1;
                 while (lo < hi) {
@@ -267,6 +306,54 @@ __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_const
         a.seq_tokens_out[b] = tokens;
     }
     if (a.n_free && block == 0 && tid == 0) *a.n_free = free - taken;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) take_one_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps], upto[kOneBatch], shift[kOneBatch], served;
+    const int b = threadIdx.x;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (b == 0) served = 0;
+    const unsigned bits = one_bits(a, free4);
+    int need = 0;
+    const int all = scan_rows(a.batch, scratch,
+                              [&](int b, int& old) {
+                                  need = pages_needed(a, b);
+                                  old = need > 0 ? pages_of(__ldcg(a.seq_tokens + b)) : 0;
+                                  return max(0, need);
+                              },
+                              [&](int b, int sum, int mine, int old) {
+                                  upto[b] = sum;
+                                  shift[b] = old - (sum - mine);
+                              });
+    const int free = block_sum(__popc(bits), scratch);
+    int taken = all;
+    if (all > free) {                                 // rows whose pages are all there
+        if (b < a.batch && upto[b] <= free) atomicMax(&served, upto[b]);
+        __syncthreads();
+        taken = served;
+    }
+    int lo = 0;                                       // the first row whose sum passes r, which only grows
+    walk_segment({0, a.num_pages}, 0, taken, scratch, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, [&](int page, int r) {
+        if (upto[lo] <= r) {
+            int hi = a.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (upto[mid] > r) hi = mid;
+                else lo = mid + 1;
+            }
+        }
+        a.page_table_out[static_cast<int64_t>(lo) * a.max_pages + shift[lo] + r] = page;
+        a.refs_out[page] = 1;
+    });
+    if (b < a.batch) {
+        int tokens = __ldcg(a.seq_tokens + b);
+        if (need < 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        else if (need > 0 && upto[b] > free) report_error(a.st, LOCKS_ERR_NO_PAGES);
+        else tokens = __ldcg(a.new_tokens + b);
+        a.seq_tokens_out[b] = tokens;
+    }
+    if (a.n_free && b == 0) *a.n_free = free - taken;
 }
 
 // ------------------------------------------------------------------ fork
@@ -333,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_const
         join_counts(a, block, scratch, before, free);
         const int n = min(__ldcg(a.needed), free);
         if (block < blocks)
-            walk_segment(a, segment_of(a.num_pages, block), before, n, scratch, [&](int page, int r) {
+            walk_segment(segment_of(a.num_pages, block), before, n, scratch, flags_at(a), [&](int page, int r) {
                 const int b = __ldcg(a.fresh + r), p = parent_of(a, b), at = tokens_of(a, p) / kPage;
                 a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
                 a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(p) * a.max_pages + at);
@@ -384,6 +471,79 @@ __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_const
         if (page >= 0 && page < a.num_pages) atomicAdd(a.refs_out + page, children - 1);
         else report_error(a.st, LOCKS_ERR_BAD_INDEX);
     }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_one_kernel(const __grid_constant__ PoolArgs a) {
+    __shared__ int scratch[kWarps], tokens[kOneBatch], parent[kOneBatch], children[kOneBatch], keeper[kOneBatch], fresh[kOneBatch];
+    const int tid = threadIdx.x;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int p = -1;
+    if (tid < a.batch) {
+        const int n = __ldcg(a.seq_tokens + tid);
+        p = __ldcg(a.parents + tid);
+        if (!in_table(n, a.max_pages) || p < -1 || p >= a.batch) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        if (p < 0 || p >= a.batch) p = -1;
+        tokens[tid] = in_table(n, a.max_pages) ? n : 0;
+        parent[tid] = p;
+        children[tid] = 0;
+        keeper[tid] = a.batch;
+    }
+    const unsigned bits = one_bits(a, free4);
+    __syncthreads();
+    if (p >= 0) {
+        atomicAdd(&children[p], 1);
+        atomicMin(&keeper[p], tid == p ? -1 : tid);
+    }
+    __syncthreads();
+    if (tid < a.batch && keeper[tid] < 0) keeper[tid] = tid;
+    __syncthreads();
+    const bool needs = p >= 0 && tokens[p] % kPage != 0 && keeper[p] != tid;
+    int upto = 0;
+    const int needed = scan_rows(a.batch, scratch, [&](int, int&) { return needs ? 1 : 0; },
+                                 [&](int b, int sum, int mine, int) {
+                                     upto = sum;
+                                     if (mine) fresh[sum - 1] = b;
+                                 });
+    const int free = block_sum(__popc(bits), scratch), n = min(needed, free);
+    walk_segment({0, a.num_pages}, 0, n, scratch, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, [&](int page, int r) {
+        const int b = fresh[r], from = parent[b], at = tokens[from] / kPage;
+        a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
+        a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(from) * a.max_pages + at);
+        a.list_dst[r] = page;
+        a.refs_out[page] = 1;
+    });
+    if (tid < a.batch) {
+        int m = p >= 0 ? tokens[p] : 0;
+        if (needs && upto > free) {
+            report_error(a.st, LOCKS_ERR_NO_PAGES);
+            m = m / kPage * kPage;
+        }
+        a.seq_tokens_out[tid] = m;
+    }
+    if (tid == 0) *a.n_list = n;
+    each_piece(a.batch, a.max_pages, [&](int b, int j0) {
+        const int from = parent[b], m = tokens[b], c = children[b];
+        const int64_t row = static_cast<int64_t>(b) * a.max_pages;
+        const int32_t* const old = a.page_table + static_cast<int64_t>(from) * a.max_pages;
+        const int copied = from < 0 ? 0 : tokens[from] / kPage + (tokens[from] % kPage != 0 && keeper[from] == b ? 1 : 0);
+        const int held = c == 1 ? 0 : c == 0 ? pages_of(m) : m / kPage;
+        int x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 32 * i;
+            x[i] = j < copied ? __ldcg(old + j) : 0;
+            y[i] = j < held ? __ldcg(a.page_table + row + j) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 32 * i;
+            if (j < copied) a.page_table_out[row + j] = x[i];
+            if (j < held && y[i] >= 0 && y[i] < a.num_pages) atomicAdd(a.refs_out + y[i], c - 1);
+            if ((j < copied && (x[i] < 0 || x[i] >= a.num_pages)) || (j < held && (y[i] < 0 || y[i] >= a.num_pages)))
+                report_error(a.st, LOCKS_ERR_BAD_INDEX);
+        }
+    });
 }
 
 // ------------------------------------------------------------------ free
@@ -540,6 +700,90 @@ __global__ void __launch_bounds__(kThreads) renumber_kernel(const __grid_constan
     }
 }
 
+__global__ void __launch_bounds__(kThreads, 1) compact_one_kernel(const __grid_constant__ PoolArgs a) {
+    constexpr int kRounds = kMovePages / kRound;
+    constexpr unsigned kMoves = 0x8000u;              // an id that is still the number of a move
+    __shared__ int scratch[kWarps];
+    __shared__ uint16_t ids[kMovePages], to[kMovePages / 2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int4 r[kRounds];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) r[k] = load4(a.refs, k * kRound + 4 * tid, a.num_pages);
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) mine += __popc(used4(r[k]));
+    const int used = block_sum(mine, scratch);
+    mine = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += k * kRound + 4 * tid + i < used ? used4(r[k]) >> i & 1u : 0u;
+    const int low = block_sum(mine, scratch);         // of them, those that stay
+    int rank = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const unsigned bits = used4(r[k]);
+        const int upto = warp_upto(__popc(bits));
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        const int sums = scratch[lane];
+        int u = rank + upto - __popc(bits) + warp_sum(lane < warp ? sums : 0);     // used pages before this one
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int page = k * kRound + 4 * tid + i;
+            const bool on = bits >> i & 1u;
+            if (page < a.num_pages) {
+                ids[page] = static_cast<uint16_t>(on && page >= used ? kMoves | (u - low) : page);
+                if (on && page >= used) a.list_src[u - low] = page;
+                if (!on && page < used) to[page - u] = static_cast<uint16_t>(page), a.list_dst[page - u] = page;
+            }
+            u += on;
+        }
+        rank += warp_sum(sums);
+        __syncthreads();
+    }
+    if (tid == 0) *a.n_list = used - low;
+    const auto new_id = [&](int page) -> int {
+        const unsigned x = ids[page];
+        return x & kMoves ? to[x & (kMoves - 1)] : x;
+    };
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const int count[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                 // a page's count is written by whom it belongs to now
+            const int page = k * kRound + 4 * tid + i;
+            if (page >= a.num_pages) continue;
+            const int id = new_id(page);
+            a.new_page[page] = id;
+            if (count[i] > 0) a.refs_out[id] = count[i];
+            if (page >= used) a.refs_out[page] = 0;
+        }
+    }
+    each_piece(a.batch, a.max_pages, [&](int b, int j0) {
+        const int n = __ldcg(a.seq_tokens + b);
+        if (!in_table(n, a.max_pages)) {
+            if (j0 == 0) report_error(a.st, LOCKS_ERR_BAD_INDEX);
+            return;
+        }
+        const int end = pages_of(n);
+        const int64_t row = static_cast<int64_t>(b) * a.max_pages;
+        int x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = j0 + 32 * i < end ? __ldcg(a.page_table + row + j0 + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 32 * i;
+            if (j >= end) continue;
+            if (x[i] >= 0 && x[i] < a.num_pages) x[i] = new_id(x[i]);
+            else report_error(a.st, LOCKS_ERR_BAD_INDEX);
+            a.page_table_out[row + j] = x[i];
+        }
+    });
+}
+
 // ------------------------------------------------------------------ copy
 
 // A block takes a piece of up to kCopyBytes of a page of one array: eight 16-byte loads a
@@ -615,13 +859,20 @@ PoolLayout pool_layout(int batch, int pages) {
     return w;
 }
 
+// Whether one block does the call: a row to a thread, pieces of rows for two turns of its warps.
+static bool in_one(const PoolArgs& a, int pages, int64_t rows, int entries) {
+    return a.num_pages <= pages && a.batch <= kOneBatch && rows * warp_pieces(entries) <= kOnePieces;
+}
+
 cudaError_t launch_take(const PoolArgs& a, cudaStream_t stream) {
+    if (in_one(a, kTakePages, 0, 0)) return launch_dependent(take_one_kernel, 1, kThreads, 0, stream, 1, a);
     const int blocks = pool_blocks(a.num_pages);
     const cudaError_t e = launch_dependent(take_count_kernel, blocks + 1, kThreads, 0, stream, 1, a);
     return e != cudaSuccess ? e : launch_dependent(take_place_kernel, blocks + 1, kThreads, 0, stream, 1, a);
 }
 
 cudaError_t launch_fork(const PoolArgs& a, cudaStream_t stream) {
+    if (in_one(a, kForkPages, a.batch, a.max_pages)) return launch_dependent(fork_one_kernel, 1, kThreads, 0, stream, 1, a);
     const int blocks = pool_blocks(a.num_pages), pieces = pieces_of(a.max_pages, kRound);
     const cudaError_t e = launch_dependent(fork_count_kernel, blocks + 1, kThreads, 0, stream, 1, a);
     if (e != cudaSuccess) return e;
@@ -630,6 +881,7 @@ cudaError_t launch_fork(const PoolArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_compact(const PoolArgs& a, cudaStream_t stream) {
+    if (in_one(a, kMovePages, a.batch, a.max_pages)) return launch_dependent(compact_one_kernel, 1, kThreads, 0, stream, 1, a);
     const int blocks = std::max(1, pool_blocks(a.num_pages)), pieces = pieces_of(a.max_pages, kRound);
     cudaError_t e = blocks > 1 ? launch_dependent(compact_count_kernel, blocks, kThreads, 0, stream, 1, a) : cudaSuccess;
     if (e != cudaSuccess) return e;

@@ -107,6 +107,7 @@ def fork(table, tokens, parents, refs, table_out, tokens_out):
                 row.append(last)
             elif free:
                 row.append(free.pop(0))
+                new[row[-1]] = 0                     # whatever it was: its count is 1 then
                 src.append(last)
                 dst.append(row[-1])
             else:
@@ -144,7 +145,7 @@ def compact(table, tokens, refs, table_out):
     new[src] = dst
     after = refs.copy()
     after[dst] = refs[src]
-    after[src] = 0
+    after[len(used):] = 0
     for b, n in enumerate(tokens):
         for j in range(pages_of(n)):
             table_out[b, j] = new[table[b, j]]
