@@ -7,9 +7,9 @@
 // next knows every page's rank from the blocks' counts and places it. For small pools one block does
 // both. A call is short, a few MB at most, so what bounds it are the launches and the loads that wait
 // for one another; each launch starts while the one before it runs. Measured: freeing pages of 3
-// sequences and taking some for 29 others in a pool of 16K pages 8.7 us; of 48 x 8192 pages in a pool
-// of 1M 19.5; forking 2 x 64 rows of 8188 pages and copying the last ones 15.3; compacting a pool of 2048
-// pages, with the copies, 8.7.
+// sequences and taking some for 29 others in a pool of 16K pages 8.0 us; of 48 x 8192 pages in a pool
+// of 1M 18.3; forking 2 x 64 rows of 8188 pages and copying the last ones 14.6; compacting a pool of 2048
+// pages, with the copies, 8.6.
 #include <algorithm>
 
 #include "pool_internal.h"
@@ -124,9 +124,12 @@ __device__ __forceinline__ void join_counts(const PoolArgs& a, int i, int* scrat
 static_assert(kMaxPoolBlocks <= kThreads, "a thread per block of the pool");
 
 // Calls f(page, rank) for the pages in a segment that bits_at(page of a lane's four) flags, ranks counted
-// from `rank`; stops behind rank `most`.
-template <typename Bits, typename F>
-__device__ __forceinline__ void walk_segment(const Segment& seg, int rank, int most, int* scratch, Bits bits_at, F f) {
+// from `rank`, up to rank `most`: neighbouring threads get neighbouring ranks, through `list`, so that
+// what goes by the rank is written together (200K pages taken from 1M by each lane's own: 12.0 us,
+// through the list 10.2). own(page, bits) is called before by the lane whose four pages those are.
+template <typename Bits, typename Own, typename F>
+__device__ __forceinline__ void walk_segment(const Segment& seg, int rank, int most, int* scratch, uint16_t* list, Bits bits_at,
+                                             Own own, F f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
     for (int at0 = seg.first; at0 < seg.last && rank < most; at0 += kRound) {
@@ -135,19 +138,23 @@ __device__ __forceinline__ void walk_segment(const Segment& seg, int rank, int m
         const int upto = warp_upto(__popc(bits));
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
-        const int sums = scratch[lane];
-        int r = rank + upto - __popc(bits) + warp_sum(lane < warp ? sums : 0);
+        const int sums = scratch[lane], all = warp_sum(sums), n = min(all, most - rank);
+        int r = upto - __popc(bits) + warp_sum(lane < warp ? sums : 0);
+        unsigned taken = 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (bits >> k & 1u) {
-                if (r < most) f(at + k, r);
+                if (r < n) list[r] = static_cast<uint16_t>(4 * threadIdx.x + k), taken |= 1u << k;
                 ++r;
             }
-        rank += warp_sum(sums);
+        if (taken) own(at, taken);
+        __syncthreads();
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n; i += kThreads) f(at0 + list[i], rank + i);
+        rank += all;
         __syncthreads();
     }
 }
-
 __device__ __forceinline__ auto flags_at(const PoolArgs& a) {
     return [&a](int at) -> unsigned { return __ldcg(a.flags + at / 4); };
 }
@@ -192,9 +199,9 @@ __device__ __forceinline__ int scan_rows(int batch, int* scratch, Count count, P
 //
 // One block does a call on a small pool whole, in one launch: the counts stay in its registers, what
 // the rows need in shared memory, and a warp takes a piece of a row. Measured (graphs of calls, us, one
-// block / two or three launches; pool, rows x entries): taking 500, 8 x 31 4.5 / 6.1, 16000, 32 x 250 5.4 /
-// 6.7; forking 500, 8 x 31 5.1 / 9.3, 8000, 32 x 125 7.8 / 9.1, 16000, 32 x 250 10.6 / 8.7; compacting 500,
-// 8 x 31 3.8 / 6.5, 8000, 32 x 125 8.7 / 10.6. (Freeing into another array, 500 2.4 / 2.7, 16000 4.9 / 2.9,
+// block / two or three launches; pool, rows x entries): taking 500, 8 x 31 4.1 / 5.4, 16000, 32 x 250 4.5 /
+// 5.9; forking 500, 8 x 31 4.3 / 6.7, 8000, 32 x 125 7.0 / 7.2, 16000, 32 x 250 9.7 / 7.6; compacting 500,
+// 8 x 31 3.8 / 6.5, 8000, 32 x 125 8.6 / 10.6. (Freeing into another array, 500 2.4 / 2.7, 16000 4.9 / 2.9,
 // has two launches always.)
 constexpr int kOneRounds = 4, kTakePages = kOneRounds * kRound, kForkPages = 2 * kRound, kOneBatch = kThreads;
 constexpr int kMovePages = 2 * kRound;                // ids of 16 bits in shared memory
@@ -225,6 +232,17 @@ __device__ __forceinline__ void each_piece(int rows, int entries, F f) {
 
 // ------------------------------------------------------------------ take
 
+// A lane's four pages, of which `taken` get a holder. (Nobody else changes the counts meanwhile.)
+__device__ __forceinline__ auto hold_taken(const PoolArgs& a) {
+    return [&a](int at, unsigned taken) {
+        int4 r = load4(a.refs, at, a.num_pages);
+        if (taken & 1u) r.x = 1;
+        if (taken & 2u) r.y = 1;
+        if (taken & 4u) r.z = 1;
+        if (taken & 8u) r.w = 1;
+        store4(a.refs_out, at, a.num_pages, r);
+    };
+}
 // Pages that row b needs; -1: its counts are wrong.
 __device__ __forceinline__ int pages_needed(const PoolArgs& a, int b) {
     const int old = __ldcg(a.seq_tokens + b), now = __ldcg(a.new_tokens + b);
@@ -256,6 +274,7 @@ __global__ void __launch_bounds__(kThreads) take_count_kernel(const __grid_const
 
 __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_constant__ PoolArgs a) {
     __shared__ int scratch[kWarps], near_upto[kScanRows], near_shift[kScanRows], served;
+    __shared__ uint16_t list[kRound];
     const int tid = threadIdx.x, blocks = pool_blocks(a.num_pages), block = blockIdx.x;
     grid_dependency_wait();
     allow_dependent_launch();
@@ -284,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_const
         const int* const upto = near ? near_upto : a.scan;
         const int* const shift = near ? near_shift : a.shift;
         int lo = 0;                                   // the first row whose sum passes r, which only grows
-        walk_segment(segment_of(a.num_pages, block), before, taken, scratch, flags_at(a), [&](int page, int r) {
+        walk_segment(segment_of(a.num_pages, block), before, taken, scratch, list, flags_at(a), hold_taken(a), [&](int page, int r) {
             if (upto[lo] <= r) {
                 int hi = a.batch - 1;
                 while (lo < hi) {
@@ -294,7 +313,6 @@ __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_const
                 }
             }
             a.page_table_out[static_cast<int64_t>(lo) * a.max_pages + shift[lo] + r] = page;
-            a.refs_out[page] = 1;
         });
     }
     for (int b = block * kThreads + tid; b < a.batch; b += gridDim.x * kThreads) {
@@ -310,6 +328,7 @@ __global__ void __launch_bounds__(kThreads) take_place_kernel(const __grid_const
 
 __global__ void __launch_bounds__(kThreads, 1) take_one_kernel(const __grid_constant__ PoolArgs a) {
     __shared__ int scratch[kWarps], upto[kOneBatch], shift[kOneBatch], served;
+    __shared__ uint16_t list[kRound];
     const int b = threadIdx.x;
     grid_dependency_wait();
     allow_dependent_launch();
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) take_one_kernel(const __grid_cons
         taken = served;
     }
     int lo = 0;                                       // the first row whose sum passes r, which only grows
-    walk_segment({0, a.num_pages}, 0, taken, scratch, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, [&](int page, int r) {
+    walk_segment({0, a.num_pages}, 0, taken, scratch, list, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, hold_taken(a), [&](int page, int r) {
         if (upto[lo] <= r) {
             int hi = a.batch - 1;
             while (lo < hi) {
@@ -344,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1) take_one_kernel(const __grid_cons
             }
         }
         a.page_table_out[static_cast<int64_t>(lo) * a.max_pages + shift[lo] + r] = page;
-        a.refs_out[page] = 1;
     });
     if (b < a.batch) {
         int tokens = __ldcg(a.seq_tokens + b);
@@ -411,6 +429,7 @@ __global__ void __launch_bounds__(kThreads) fork_count_kernel(const __grid_const
 // tables' rows, and what their holds change by.
 __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_constant__ PoolArgs a, int pieces) {
     __shared__ int scratch[kWarps];
+    __shared__ uint16_t list[kRound];
     const int tid = threadIdx.x, blocks = pool_blocks(a.num_pages);
     grid_dependency_wait();
     allow_dependent_launch();
@@ -420,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_const
         join_counts(a, block, scratch, before, free);
         const int n = min(__ldcg(a.needed), free);
         if (block < blocks)
-            walk_segment(segment_of(a.num_pages, block), before, n, scratch, flags_at(a), [&](int page, int r) {
+            walk_segment(segment_of(a.num_pages, block), before, n, scratch, list, flags_at(a), [](int, unsigned) {}, [&](int page, int r) {
                 const int b = __ldcg(a.fresh + r), p = parent_of(a, b), at = tokens_of(a, p) / kPage;
                 a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
                 a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(p) * a.max_pages + at);
@@ -475,6 +494,7 @@ __global__ void __launch_bounds__(kThreads) fork_place_kernel(const __grid_const
 
 __global__ void __launch_bounds__(kThreads, 1) fork_one_kernel(const __grid_constant__ PoolArgs a) {
     __shared__ int scratch[kWarps], tokens[kOneBatch], parent[kOneBatch], children[kOneBatch], keeper[kOneBatch], fresh[kOneBatch];
+    __shared__ uint16_t list[kRound];
     const int tid = threadIdx.x;
     grid_dependency_wait();
     allow_dependent_launch();
@@ -506,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_one_kernel(const __grid_cons
                                      if (mine) fresh[sum - 1] = b;
                                  });
     const int free = block_sum(__popc(bits), scratch), n = min(needed, free);
-    walk_segment({0, a.num_pages}, 0, n, scratch, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, [&](int page, int r) {
+    walk_segment({0, a.num_pages}, 0, n, scratch, list, [&](int at) { return bits >> (at / kRound * 4) & 15u; }, [](int, unsigned) {}, [&](int page, int r) {
         const int b = fresh[r], from = parent[b], at = tokens[from] / kPage;
         a.page_table_out[static_cast<int64_t>(b) * a.max_pages + at] = page;
         a.list_src[r] = __ldcg(a.page_table + static_cast<int64_t>(from) * a.max_pages + at);
