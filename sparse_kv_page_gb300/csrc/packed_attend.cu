@@ -419,9 +419,9 @@ struct Running {
     // middle times the weights is moved from the one to the other, and `ahead` times as much again for
     // those to come (0 at the end): the products cut their sums towards 0, and errors of sums that grow
     // from below 0 to above cancel. With kAhead sums that grow evenly go from -0.38 to 0.62 of a turn's;
-    // the output of two rows of a million tokens is off by 0.0018 of itself, 0.0017 of them its rounding
-    // to bf16 (0.0019 without). Zeros with the middle in them from the start would leave 0.0017, and take
-    // 194 us for 187.
+    // the output of two rows of a million tokens is off by 0.0018 - 0.0019 of itself, 0.0017 of them its
+    // rounding to bf16. (The weights' roundings count with the codes' distances from 0 here; zeros with the
+    // middle in them from the start would leave 0.0017, and take 194 us for 187.)
     __device__ __forceinline__ void centre(float ahead) {
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
