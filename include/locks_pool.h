@@ -65,7 +65,8 @@ enum {
  *   scale = bf16((greatest - least) / 15), 0 where that is below 2^-126
  *   code  = round((x - zero) / scale), ties to even; 0 where scale is 0
  * with the quotients rounded as fp32 division rounds them. A group with a NaN or an infinity
- * (or whose range overflows fp32) unpacks to no finite value. dst_pages NULL: the same ids as
+ * (or whose range overflows fp32) has a NaN for its scale and codes 0, and unpacks to no finite
+ * value; other groups are not touched by it. dst_pages NULL: the same ids as
  * src_pages. A negative id in either list skips the entry; one out of range does too and
  * records LOCKS_ERR_BAD_INDEX. No packed page may be named twice in dst_pages.
  * workspace: optional, 256 bytes (status only). One launch.

@@ -67,9 +67,10 @@ __device__ __forceinline__ void group_scales(const uint4& x0, const uint4& x1, u
 // The codes of two groups' values, element i of x0 and of x1, as floats kRound + code, whose low bytes
 // are the codes. Scales so small or large that the remainder or the reciprocal leave the normal
 // numbers divide. The quotient is within [0, 15.06], as the scale is rounded by at most 2^-8 of
-// itself, so codes need no bounds.
+// itself, so codes need no bounds: where words are put together, all other bits of a result's two low
+// bytes count as 0. A group that is not finite, of NaN scale, gets codes 0.
 constexpr float kRound = 12582912.f;              // 1.5 * 2^23
-__device__ __noinline__ float divided(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
+__device__ __noinline__ float divided(float v, float s) { return s > 0.f ? __fdiv_rn(v, s) : 0.f; }
 __device__ __forceinline__ float reciprocal(float s) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));

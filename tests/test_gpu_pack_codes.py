@@ -1,0 +1,65 @@
+"""GPU tests of packing's codes where a neighbour may go wrong: groups that are not finite beside groups
+that are."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_kv_page_gb300 as L
+from tests import pool_ref as ref
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+UNIT = L.LOCKS_PACKED_BYTES
+
+
+def pack(k, v):
+    """Units of all pages of k and v (float64 arrays of bf16 values [pages][16][128])."""
+    k, v = (torch.from_numpy(x).to(DEV).bfloat16()[:, None].contiguous() for x in (k, v))
+    n = k.shape[0]
+    packed = torch.full((n, 1, UNIT), 0xA5, dtype=torch.uint8, device=DEV)
+    L.locks_pack_pages(L.make_dims(1, 1, 1, 1, n), k, v, torch.arange(n, dtype=torch.int32, device=DEV), None, n, packed)
+    return packed
+
+
+def unpack(packed):
+    n = packed.shape[0]
+    k, v = (torch.zeros((n, 1, 16, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    L.locks_unpack_pages(L.make_dims(1, 1, 1, 1, n), packed, torch.arange(n, dtype=torch.int32, device=DEV), None, n, k, v)
+    return [x[:, 0].double().cpu().numpy() for x in (k, v)]
+
+
+BAD = {"nan": ([0], [np.nan]), "inf": ([3], [np.inf]), "minus_inf": ([7], [-np.inf]),
+       "both_infs": ([1, 2], [np.inf, -np.inf]), "range": ([4, 9], [3e38, -3e38]), "all": (range(32), [np.nan] * 32)}
+
+
+@pytest.mark.parametrize("kind", list(BAD))
+def test_groups_that_are_not_finite_leave_the_others_alone(kind):
+    """Page 16 g + t has one bad group, g of token t; the last ones have several."""
+    g = torch.Generator()
+    g.manual_seed(7)
+    n = 16 * 4 + 6
+    k, v = (torch.randn((n, 16, 128), generator=g).bfloat16().double().numpy() for _ in range(2))
+    bad = [np.zeros((n, 16, groups), bool) for groups in (4, 2)]
+    for page in range(64):
+        for b, groups in zip(bad, (4, 2)):
+            b[page, page % 16, page // 16 % groups] = True
+    rng = np.random.default_rng(3)
+    for b in bad:
+        b[64:] = rng.random(b[64:].shape) < 0.3
+    at, values = BAD[kind]
+    clean = []
+    for x, b in zip((k, v), bad):
+        size = 128 // b.shape[-1]
+        clean.append(np.where(np.repeat(b, size, -1), 0.0, x))
+        for page, token, group in zip(*np.nonzero(b)):
+            x[page, token, [size * group + d for d in at]] = values
+    packed = pack(k, v)
+    units = packed[:, 0].cpu().numpy()
+    for x, b, got, out in zip(clean, bad, ref.fields(units), unpack(packed)):
+        size = 128 // b.shape[-1]
+        good = ~np.repeat(b, size, -1)
+        for a, w in zip(got, ref.codes_of(x, size)):
+            assert np.array_equal(a[good], w[good])
+        assert np.isfinite(out[good]).all() and not np.isfinite(out[~good]).any()
