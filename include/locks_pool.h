@@ -77,8 +77,8 @@ LOCKS_API int locks_pack_pages(const locks_dims_t* dims, const uint16_t* k_cache
 
 /*
  * Unpacks pages: page dst_pages[i] of the bf16 pool from page src_pages[i] of the packed pool,
- * bf16(zero + scale * code), for pages that go on being read as bf16 ones (summaries of
- * another kind, shared-prefix attention). Lists, errors and workspace as for packing.
+ * bf16(zero + scale * code), rounded once, for pages that go on being read as bf16 ones (summaries
+ * of another kind, shared-prefix attention). Lists, errors and workspace as for packing.
  */
 LOCKS_API int locks_unpack_pages(const locks_dims_t* dims, const uint8_t* packed, int32_t num_packed_pages,
                                  const int32_t* src_pages, const int32_t* dst_pages, int32_t n_pages,

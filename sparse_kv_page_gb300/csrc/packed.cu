@@ -233,10 +233,33 @@ __global__ void __launch_bounds__(kWarps * 32, kPackCtas) pack_kernel(const __gr
     }
 }
 
-// Two values of neighbouring dims as bf16: zero + scale * code, rounded once (the product of 8
-// and 4 bits is exact).
-__device__ __forceinline__ uint32_t pair_of(uint32_t c0, uint32_t c1, float s, float z) {
-    return pack_bf16x2(__fmaf_rn(s, static_cast<float>(c0), z), __fmaf_rn(s, static_cast<float>(c1), z));
+// Whether fp32 holds all bits of zero + scale * code: from the last one of either (8 bits each) to the
+// carry of the sum, whose code is below 2^4.
+__device__ __forceinline__ bool sums_fit(float s, float z) {
+    const int apart = static_cast<int>(__float_as_uint(z) >> 23 & 255u) - static_cast<int>(__float_as_uint(s) >> 23 & 255u);
+    return apart >= -11 && apart <= 15;
+}
+// zero + scale * code rounded to odd: of the two floats next to the exact sum (the product of 8 and 4 bits
+// is exact) the one whose last bit is 1, or the sum itself. Rounding that to bf16 is rounding the sum once
+// (fp32 has more than two bits on top of bf16's); rounded to nearest here, a sum just off the middle
+// between two bf16 values would fall on it.
+__device__ __forceinline__ float to_odd(float s, float c, float z) {
+    const float down = __fmaf_rd(s, c, z), up = __fmaf_ru(s, c, z);
+    return __float_as_uint(down) & 1u ? down : up;
+}
+// Eight values of a group as bf16, rounded once. (All of them by to_odd: the 64K-token prompt 126 us, packing
+// and unpacking, instead of 123.)
+__device__ __forceinline__ void put_values(uint16_t* out, const uint32_t (&code)[8], float s, float z) {
+    float x[8];
+    if (sums_fit(s, z)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(s, static_cast<float>(code[i]), z);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_odd(s, static_cast<float>(code[i]), z);
+    }
+    *reinterpret_cast<uint4*>(out) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 __global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_constant__ PackArgs a) {
@@ -271,27 +294,25 @@ __global__ void __launch_bounds__(kWarps * 32) unpack_kernel(const __grid_consta
             {
                 const uint16_t* sz = reinterpret_cast<const uint16_t*>(unit + kUnitKScales + 16 * t) + (chunk >> 2);
                 const float s = low_of(sz[0]), z = low_of(sz[4]);
-                uint32_t o[4];
+                uint32_t c[8];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const uint32_t c = *reinterpret_cast<const uint32_t*>(word + 16 * (4 * (t & 7) + p)) >>
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(word + 16 * (4 * (t & 7) + p)) >>
                                        (4 * half + 8 * (t >> 3));
-                    o[p] = pair_of(c & 15, c >> 16 & 15, s, z);
+                    c[2 * p] = x & 15, c[2 * p + 1] = x >> 16 & 15;
                 }
-                *reinterpret_cast<uint4*>(a.k_out + at + j * 2 * kD) = make_uint4(o[0], o[1], o[2], o[3]);
+                put_values(a.k_out + at + j * 2 * kD, c, s, z);
             }
             {
                 const uint16_t* sz = reinterpret_cast<const uint16_t*>(unit + kUnitVScales + 8 * t) + (chunk >> 3);
                 const float s = low_of(sz[0]), z = low_of(sz[2]);
-                uint32_t c[8], o[4];
+                uint32_t c[8];
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
                     c[d] = *reinterpret_cast<const uint32_t*>(word + kUnitVCodes + 16 * (4 * d + (t & 7) / 2)) >>
                                (16 * (t & 1) + 4 * half + 8 * (t >> 3)) &
                            15;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) o[p] = pair_of(c[2 * p], c[2 * p + 1], s, z);
-                *reinterpret_cast<uint4*>(a.v_out + at + j * 2 * kD) = make_uint4(o[0], o[1], o[2], o[3]);
+                put_values(a.v_out + at + j * 2 * kD, c, s, z);
             }
         }
     }

@@ -1,5 +1,8 @@
-"""GPU tests of packing's codes where a neighbour may go wrong: groups that are not finite beside groups
-that are."""
+"""GPU tests of packing's codes where a neighbour may go wrong (groups that are not finite beside groups
+that are), and of the rounding of unpacked values."""
+
+import itertools
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -63,3 +66,50 @@ def test_groups_that_are_not_finite_leave_the_others_alone(kind):
         for a, w in zip(got, ref.codes_of(x, size)):
             assert np.array_equal(a[good], w[good])
         assert np.isfinite(out[good]).all() and not np.isfinite(out[~good]).any()
+
+
+def bf16_of(x: Fraction) -> float:
+    """The bf16 value nearest to x (a number of its range), ties to the even one."""
+    if x == 0:
+        return 0.0
+    size = abs(x)
+    e = size.numerator.bit_length() - size.denominator.bit_length()
+    e -= size < Fraction(2) ** e
+    step = Fraction(2) ** (max(e, -126) - 7)
+    return float(round(x / step) * step)             # round() takes ties to even
+
+
+def test_unpacked_values_are_rounded_once():
+    """Products on a tie between two bf16 values, and zeros on either side that are too small for fp32 to
+    see beside them."""
+    scales = [Fraction(128 + m, 128) for m in (0, 1, 2, 5, 33, 64, 85, 101, 127)]
+    zeros = [sign * Fraction(128 + m, 128) * Fraction(2) ** e for sign in (1, -1) for m in (0, 77)
+             for e in (-40, -30, -24, -17, -16, -15, -13, -12, -11, -9, -8, -3, 0, 7, 14, 15, 16, 17, 20, 30)] + [Fraction(0)]
+    pairs = list(itertools.product(scales, zeros))
+    n = -(-len(pairs) // 32)
+    code = np.arange(128) % 16
+    units = np.zeros((n, UNIT), np.uint8)
+    want = np.zeros((2, n, 16, 128))
+    groups = []
+    for i in range(n * 16):                          # token i of all: pair 2i of its dims 0..63, pair 2i + 1 of the others
+        groups.append([pairs[(2 * i + j) % len(pairs)] for j in range(2)])
+    for values in (0, 1):
+        byte, bit = ref.PLACES[values]
+        for t in range(16):
+            for d in range(128):
+                units[:, byte[t, d]] |= np.uint8(int(code[d]) << int(bit[t, d]))
+        per = (4, 2)[values]
+        fields = np.zeros((n, 16, 2, per), np.float32)
+        for i, pair in enumerate(groups):
+            for g in range(per):
+                fields[i // 16, i % 16, :, g] = [float(x) for x in pair[g * 2 // per]]
+            for d in range(128):
+                s, z = pair[d // 64]
+                want[values, i // 16, i % 16, d] = bf16_of(z + s * int(code[d]))
+        bits = (fields.view(np.uint32) >> 16).astype(np.uint16)
+        at = (2048, 2304)[values]
+        units[:, at:at + 64 * per] = bits.reshape(n, -1).view(np.uint8)
+    got = unpack(torch.from_numpy(units).to(DEV)[:, None].contiguous())
+    for x, w in zip(got, want):
+        wrong = x != w
+        assert not wrong.any(), (int(wrong.sum()), x[wrong][:6], w[wrong][:6])
