@@ -32,8 +32,8 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
 
 // Quotients below are rounded as fp32 division rounds them, by Markstein's theorem (IBM J. Res. Dev.
 // 34, 1990): with r the correctly rounded 1 / s, q = v r and q + (v - s q) r is the rounded v / s.
-// (Newton's step makes r of the approximate reciprocal; for the 8-bit scales here it is the rounded
-// one, for each of them.) How a quotient is rounded matters: bf16 values lie on borders between two
+// (Newton's step makes r of the approximate reciprocal; for the 8-bit scales here the codes are the
+// rounded quotient's for each of the 128 mantissas, which a test goes through.) How a quotient is rounded matters: bf16 values lie on borders between two
 // codes often, and there the product with the reciprocal alone may fall to either side.
 
 // Least and greatest of eight values as a pair (least, -greatest): both are then minima.

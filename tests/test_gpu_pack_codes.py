@@ -1,6 +1,5 @@
-"""GPU tests of packing's codes where a neighbour may go wrong (groups that are not finite beside groups
-that are), and of the rounding of unpacked values."""
-
+"""GPU tests of packing's codes where a quotient or a neighbour may go wrong: groups that are not
+finite beside groups that are, every mantissa of a scale, and the rounding of unpacked values."""
 import itertools
 from fractions import Fraction
 
@@ -66,6 +65,40 @@ def test_groups_that_are_not_finite_leave_the_others_alone(kind):
         for a, w in zip(got, ref.codes_of(x, size)):
             assert np.array_equal(a[good], w[good])
         assert np.isfinite(out[good]).all() and not np.isfinite(out[~good]).any()
+
+
+@pytest.mark.parametrize("exponent", [-85, -20, 0, 31, 100])
+def test_codes_of_every_scale(exponent):
+    """For each of the 128 mantissas a scale can have: all bf16 values of a group of that scale, of which
+    many have quotients on a border between two codes, or next to one."""
+    tokens = []
+    for m in range(128):
+        scale = Fraction(128 + m, 128)
+        # the greatest value is 15 scales (12 bits) cut to 8, the least what is missing: the range is 15 scales
+        whole = 15 * scale
+        high = Fraction(int(whole * 8), 8)
+        low = high - whole
+        values = np.arange(0x3e80, 0x4200, dtype=np.uint16)         # 0.25 .. 32
+        x = ref.f32_of(values).astype(np.float64)
+        x = x[x < float(high)]
+        x = np.concatenate([x, -x[x < float(-low)]])
+        for i in range(0, len(x), 30):
+            row = np.full(32, float(high))
+            row[1] = float(low)
+            row[2:2 + len(x[i:i + 30])] = x[i:i + 30]
+            tokens.append(row)
+    tokens = np.array(tokens)
+    assert np.array_equal(ref.cache_ref.bf16(tokens), tokens)
+    n = -(-len(tokens) // 32)
+    k = np.resize(tokens, (n * 64, 32)).reshape(n, 16, 128) * 2.0 ** exponent
+    v = np.resize(tokens.repeat(2, 0), (n * 32, 64)).reshape(n, 16, 128) * 2.0 ** exponent
+    units = pack(k, v)[:, 0].cpu().numpy()
+    for x, size, (code, scale, zero) in zip((k, v), (32, 64), ref.fields(units)):
+        c, s, z = ref.codes_of(x, size)
+        assert len(np.unique(s)) == 128
+        assert np.array_equal(s, scale) and np.array_equal(z, zero)
+        wrong = c != code
+        assert not wrong.any(), (int(wrong.sum()), x[wrong][:4], s[wrong][:4], z[wrong][:4], code[wrong][:4], c[wrong][:4])
 
 
 def bf16_of(x: Fraction) -> float:
