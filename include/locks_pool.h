@@ -28,7 +28,7 @@
  *   0     codes of the keys, 4 bits each      1024  codes of the values
  *   2048  for token t: bf16 scales of its key's 4 groups of 32 dims, then their zeros
  *   2304  for token t: bf16 scales of its value's 2 groups of 64 dims, then their zeros
- * value = zero + scale * code, code 0..15. Codes lie in the order in which the attention's
+ * value = zero + scale * code, code 0..15; scales of either sign. Codes lie in the order in which the attention's
  * tensor-core fragments read them. That of token t and dim d lies in the four bits from bit
  * b of the 32-bit word at byte 512 * (w / 4) + 16 * l + 4 * (w % 4) of its 1024, w = d / 16:
  *   keys    l = 4 * (t % 8) + d % 8 / 2,  b = 16 * (d % 2) + 4 * (d / 8 % 2) + 8 * (t / 8)
@@ -103,10 +103,10 @@ LOCKS_API int locks_packed_workspace_size(const locks_dims_t* dims, size_t* byte
  * - q: q_type LOCKS_FP32 or LOCKS_BF16, contiguous [batch][num_q_heads][128], 16-byte aligned,
  *   each head's of magnitudes from 2^-60 to 2^60 or 0. fp32 queries enter the products as two
  *   fp16 parts, 22 bits below each head's largest (over recent tokens as two bf16 parts, 16 bits).
- *   The weights times the values' scales enter as fp16, rounded (11 bits; over recent tokens as
- *   two bf16 parts). Sums and softmax statistics are fp32.
- *   Keys and values of magnitudes up to 2^50 are served. Values in groups of scales below 2^-49
- *   are off by up to 2^-75 each.
+ *   The weights times the values' scales enter rounded to 11 bits, each off by 2^-11 of itself or
+ *   by 2^-21 of what a token of the largest weight would have, whichever is more, however far apart
+ *   the scales of tokens and groups are (over recent tokens as two bf16 parts, 16 bits). Sums and
+ *   softmax statistics are fp32. Keys and values of magnitudes up to 2^50 are served.
  * - page_table int32 [batch][max_pages_per_seq], ids of packed pages; not read when
  *   max_pages_per_seq is 0.
  * - selected int32 [batch][num_kv_heads][k_cap] (logical pages, in any order; the same one

@@ -12,8 +12,8 @@
 //    are SMs, whatever the lengths of the rows. A CTA goes through its piece two rows at a time, so
 //    that where rows are long its warps meet once, at the end. A row that goes past a CTA is joined
 //    by a second kernel from partials in the workspace. Sixteen sequences of up to 128K tokens take
-//    361 us, 95% of the copy rate; two of 1M with 2 kv heads of 16 queries 187 us, 47%: there a
-//    page takes a warp 50 products and 445 instructions (301 for 4 queries), at three warps a
+//    363 us, 94% of the copy rate; two of 1M with 2 kv heads of 16 queries 193 us, 46%: there a
+//    page takes a warp 50 products and 451 instructions (301 for 4 queries), at three warps a
 //    scheduler.
 //
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
@@ -25,7 +25,9 @@
 // by 16 there, for values the output. Queries and weights are scaled by powers of two into fp16's
 // range. A token's scales multiply the group's sums (keys) or the weights (values); zeros enter
 // through a product of their own with the queries' sums (keys) and through a sum per group
-// (values).
+// (values). Where values' scales are so far apart that one power of two does not bring them all
+// into fp16's range, what fp16 loses of the weights has a product of its own, on bf16 (the same
+// fields are subnormals of 2^-133 there).
 #include <algorithm>
 #include <atomic>
 
@@ -199,7 +201,8 @@ struct Running {
     Two z[kBlocks][2];                                // [column], of both groups: of weights times zeros
     Two pw[kBlocks][2];                               // [group], of both columns: of weights times scales, as the
                                                       // products take them, since the last centre()
-    float lift, scale_limit;                          // log2 of the weights' factor; the largest scale that it is good for
+    float lift;                                       // log2 of the weights' factor
+    uint32_t limit;                                   // the largest scale that it is good for, as two bf16s; 0: none yet
 
     __device__ __forceinline__ void clear(const Control<kKind>& ctl, int which) {
         const int tig = threadIdx.x & 3;
@@ -212,16 +215,18 @@ struct Running {
             unit[n] = two(ctl.unit[which][n * 8 + 2 * tig], ctl.unit[which][n * 8 + 2 * tig + 1]);
             l[n] = two(0.f, 0.f);
         }
-        lift = scale_limit = 0.f;
+        lift = 0.f;
+        limit = 0u;
     }
 
     // Scores (tokens gid, gid + 8 of kPages pages) to weights. The maximum moves only when a score
-    // passes it by more than kSlack, the factor when a scale (`scale`: this lane's largest) passes its
-    // limit: weights and sums are floating-point numbers, so the slack costs no bits, and most pages
-    // pass with one vote.
-    template <int kPages>
-    __device__ __forceinline__ void weigh(float (&s)[kPages][kBlocks][4], float scale) {
-        bool over = scale > scale_limit;
+    // passes it by more than kSlack, the factor when a scale passes its limit: weights and sums are
+    // floating-point numbers, so the slack costs no bits, and most pages pass with one vote. `most` and
+    // `least` are this lane's extreme scales, two bf16s each; `rest` is called, ahead of the weights, where
+    // one is too small for the factor, or below 0.
+    template <int kPages, typename Rest>
+    __device__ __forceinline__ void weigh(float (&s)[kPages][kBlocks][4], uint32_t most, uint32_t least, Rest rest) {
+        bool over = any_greater(most, limit) || any_less(least, low());
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
             const float limit0 = m[n][0] + kSlack, limit1 = m[n][1] + kSlack;
@@ -237,13 +242,14 @@ struct Running {
         }
         if (__any_sync(kAll, over)) {
             float change = 0.f;                       // log2
+            float scale = fmaxf(fmaxf(low_of(most), high_of(most)), -fminf(low_of(least), high_of(least)));
 #pragma unroll
             for (int x = 1; x < 32; x *= 2) scale = fmaxf(scale, __shfl_xor_sync(kAll, scale, x));
-            if (scale > scale_limit) {                // kScaleTop - exponent, within -100..54 (see kScaleLeast)
+            if (scale > low_of(limit)) {              // kScaleTop - exponent, within -100..54 (see kScaleLeast)
                 const int e = kScaleTop - min(max(static_cast<int>(__float_as_uint(scale) >> 23) - 127, kScaleLeast), 105);
                 change = static_cast<float>(e) - lift;
                 lift += change;
-                scale_limit = kScaleLimit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                limit = static_cast<uint32_t>(127 + kScaleLimit - e) * 0x00800080u;
             }
 #pragma unroll
             for (int n = 0; n < kBlocks; ++n) {
@@ -266,22 +272,29 @@ struct Running {
 #pragma unroll
                 for (int d = 0; d < 8; ++d) o[n][d][0] *= f[0], o[n][d][1] *= f[1], o[n][d][2] *= f[0], o[n][d][3] *= f[1];
             }
+            if (__any_sync(kAll, any_less(least, low()))) rest();
         }
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-            const Two base = two(m[n][0] == -INFINITY ? lift : lift - m[n][0], m[n][1] == -INFINITY ? lift : lift - m[n][1]);
+            const Two by = base(n);
 #pragma unroll
             for (int p = 0; p < kPages; ++p) {
 #pragma unroll
                 for (int t = 0; t < 4; t += 2) {
                     float x, y;
-                    parts_of(add2(two(s[p][n][t], s[p][n][t + 1]), base), x, y);
+                    parts_of(add2(two(s[p][n][t], s[p][n][t + 1]), by), x, y);
                     s[p][n][t] = fast_exp2(x);
                     s[p][n][t + 1] = fast_exp2(y);
                     l[n] = add2(l[n], two(s[p][n][t], s[p][n][t + 1]));
                 }
             }
         }
+    }
+    // The least scale that the factor is good for (where there is no factor yet, a number below all scales).
+    __device__ __forceinline__ uint32_t low() const { return limit - static_cast<uint32_t>(kScaleLimit - kScaleLow) * 0x00800080u; }
+    // What turns the scores of block n into log2 of weights.
+    __device__ __forceinline__ Two base(int n) const {
+        return two(m[n][0] == -INFINITY ? lift : lift - m[n][0], m[n][1] == -INFINITY ? lift : lift - m[n][1]);
     }
 
     // Two packed pages; the second one's tokens count only if `both` (it is read all the same).
@@ -371,7 +384,8 @@ struct Running {
 #pragma unroll
             for (int i = 0; i < 2; ++i) t[p][i] = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8 * i));
         const uint32_t most = bf16x2_max(bf16x2_max(t[0][0].x, t[0][1].x), bf16x2_max(t[1][0].x, t[1][1].x));
-        weigh<2>(s, fmaxf(low_of(most), high_of(most)));
+        const uint32_t least = bf16x2_min(bf16x2_min(t[0][0].x, t[0][1].x), bf16x2_min(t[1][0].x, t[1][1].x));
+        weigh<2>(s, most, least, [&] { add_rest(units, s, t); });
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             float x[kBlocks][4][2];                   // weights times scales: [token, column][group]
@@ -404,13 +418,57 @@ struct Running {
                     }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t up = w[i] >> 8;
-                    const uint32_t c[4] = {w[i] & 0x000f000fu, w[i] & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+                    uint32_t c[4];
+                    codes_of(w[i], c);
 #pragma unroll
                     for (int n = 0; n < kBlocks; ++n) mma_f16(o[n][4 * g + i], c, f[n][0], f[n][1]);
                 }
             }
         }
+    }
+    // 16 dims' codes of the values, as fp16 or bf16 numbers.
+    __device__ __forceinline__ static void codes_of(uint32_t w, uint32_t (&c)[4]) {
+        const uint32_t up = w >> 8;
+        c[0] = w & 0x000f000fu, c[1] = w & 0x00f000f0u, c[2] = up & 0x000f000fu, c[3] = up & 0x00f000f0u;
+    }
+    // The products of two pages' values with what the weights times scales lose as fp16 (all of it where
+    // they are too small for it), in two bf16 parts. (Measured: two bf16 parts of all weights in fp16's
+    // place, 16 x 128K tokens 375 us instead of 363, 2 x 1M with 16 queries 225 instead of 193; a branch
+    // of the whole turn 371 and 200.)
+    __device__ __forceinline__ void add_rest(const uint8_t* const (&units)[2], const float (&s)[2][kBlocks][4],
+                                             const uint2 (&t)[2][2]) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint4 v = *reinterpret_cast<const uint4*>(units[p] + kUnitVCodes + 512 * g + 16 * lane);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t hi[kBlocks][2], lo[kBlocks][2];
+#pragma unroll
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x, y;
+                        parts_of(add2(two(s[p][n][2 * i], s[p][n][2 * i + 1]), base(n)), x, y);
+                        const float scale = g ? high_of(t[p][i].x) : low_of(t[p][i].x);
+                        x = fast_exp2(x) * scale, y = fast_exp2(y) * scale;
+                        const float2 held = f16x2_of(pack_f16x2(x, y));
+                        split((x - held.x) * kWide, (y - held.y) * kWide, hi[n][i], lo[n][i]);
+                        hi[n][i] = transposed(hi[n][i]);
+                        lo[n][i] = transposed(lo[n][i]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t c[4];
+                    codes_of(w[i], c);
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n) {
+                        mma_bf16(o[n][4 * g + i], c, hi[n][0], hi[n][1]);
+                        mma_bf16(o[n][4 * g + i], c, lo[n][0], lo[n][1]);
+                    }
+                }
+            }
     }
 
     // Codes are counted from 0, so the accumulators of the output and the sums with the zeros grow in
@@ -421,7 +479,7 @@ struct Running {
     // from below 0 to above cancel. With kAhead sums that grow evenly go from -0.38 to 0.62 of a turn's;
     // the output of two rows of a million tokens is off by 0.0018 - 0.0019 of itself, 0.0017 of them its
     // rounding to bf16. (The weights' roundings count with the codes' distances from 0 here; zeros with the
-    // middle in them from the start would leave 0.0017, and take 194 us for 187.)
+    // middle in them from the start would leave 0.0017, and take 4% longer.)
     __device__ __forceinline__ void centre(float ahead) {
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)
@@ -483,7 +541,7 @@ struct Running {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (gid + 8 * (i >> 1) >= valid) s[0][n][i] = -INFINITY;
-        weigh<1>(s, 0.f);
+        weigh<1>(s, 0u, 0x7f807f80u, [] {});
         uint32_t hi[kBlocks][2], lo[kBlocks][2];
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n)

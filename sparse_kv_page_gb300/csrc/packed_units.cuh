@@ -19,10 +19,13 @@ constexpr float kSlack = 8.f;                         // log2 that a score may p
 // Weights times a value's scale are fp16 (11 bits, rounded: 2^-11 of a weight at most, up or down;
 // the output has 8). All weights carry a factor 2^lift that brings the largest scale so far to
 // 2^5..2^6, and is set anew when a scale times it passes 2^7: with kSlack they stay below 2^15.
+// fp16 ends at 2^-25, which is 2^-21 of a weight of 1 where a scale times the factor is 2^-4. For a
+// pair of pages with a scale below that (or below 0) what fp16 loses is added in two bf16 parts, 16
+// bits whatever the scale: they carry kWide, as codes are 2^-133 in bf16.
 // Scales below 2^kScaleLeast count as that large, for the zeros, of up to 2^50, take the factor too:
 // 2^(54 + kSlack + 50) and the sums of it are numbers.
-constexpr int kScaleTop = 5, kScaleLeast = -49;
-constexpr float kScaleLimit = 0x1p7f;
+constexpr int kScaleTop = 5, kScaleLimit = 7, kScaleLow = -4, kScaleLeast = -49;
+constexpr float kWide = 0x1p109f;
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -34,6 +37,16 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Whether either half of a is greater than (less than) b's.
+__device__ __forceinline__ bool any_greater(uint32_t a, uint32_t b) {
+    return !__hbleu2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+}
+__device__ __forceinline__ bool any_less(uint32_t a, uint32_t b) { return any_greater(b, a); }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

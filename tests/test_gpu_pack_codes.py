@@ -1,5 +1,6 @@
 """GPU tests of packing's codes where a quotient or a neighbour may go wrong: groups that are not
 finite beside groups that are, every mantissa of a scale, and the rounding of unpacked values."""
+
 import itertools
 from fractions import Fraction
 
