@@ -22,7 +22,17 @@
  * tokens lie in pages of the bf16 pool (recent_table). A page that fills is packed and its
  * bf16 page used again; summaries, being indexed by physical page, are those of the packed
  * page. Scoring, selection, mass and eviction go by the tables and take a packed pool's as
- * they are.
+ * they are, with dims whose num_phys_pages is num_packed_pages.
+ *
+ * locks_build_summaries reads bf16 pages and writes at their ids. For summaries at the packed
+ * pages' ids, the four summary arrays have num_packed_pages + num_phys_pages pages, first those
+ * of the packed pool, then those of the bf16 pool:
+ * - locks_build_summaries with the bf16 pool's dims and ids, and a locks_summaries_t of pointers
+ *   num_packed_pages pages into the arrays;
+ * - locks_copy_pages with the four whole arrays as planes, from num_packed_pages + bf16 page to
+ *   packed page, and locks_pack_pages from and to the same pages;
+ * - the arrays' fronts are what scoring and selection read, and what goes into the planes, beside
+ *   the packed pages, when a fork or a compaction moves packed pages.
  *
  * Packed unit: one page of one kv head, LOCKS_PACKED_BYTES = 2432 bytes
  *   0     codes of the keys, 4 bits each      1024  codes of the values

@@ -3,7 +3,10 @@
 Like ``cache``: argument marshalling only, on torch's current CUDA stream of the tensors'
 device unless a stream is given, no fallback. A cache in 4 bits around the decode step::
 
-    # bf16 pages that filled become packed pages; their summaries go by the packed page
+    # bf16 pages that filled become packed pages; their summaries go by the packed page: arrays of
+    # num_packed pages and then the bf16 pool's, `tail` being the latter (Summaries(mu[num_packed:], ...))
+    locks_build_summaries(dims, k_cache, filled, n, tail)
+    locks_copy_pages(make_planes([mu, basis, coef, scales]), filled + num_packed, packed_ids)
     locks_pack_pages(dims, k_cache, v_cache, filled, packed_ids, n, packed)
     locks_select_pages(...)                       # scores as ever, tables of packed pages
     locks_packed_attention(dims, q, packed, page_table, seq_pages, out, ws, selected=selected,
