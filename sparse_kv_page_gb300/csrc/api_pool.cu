@@ -322,7 +322,7 @@ int locks_free_pages(const int32_t* refs, int32_t num_pages, const int32_t* page
     if (!aligned(refs, 16) || !aligned(refs_out, 16) || !words({pages, counts})) return LOCKS_ERR_INVALID_ARG;
     if (!apart({ints(refs, num_pages), ints(pages, cells), ints(counts, rows)}, {ints(refs_out, num_pages, refs)}))
         return LOCKS_ERR_INVALID_ARG;
-    if (num_pages == 0 && cells == 0) return LOCKS_OK;
+    if (num_pages == 0 && rows == 0) return LOCKS_OK;
     const int sms = locks::current_sms();
     if (sms <= 0) return LOCKS_ERR_CUDA;
     locks::PoolArgs a;

@@ -917,7 +917,7 @@ cudaError_t launch_free(const PoolArgs& a, int num_sms, cudaStream_t stream) {
         const cudaError_t e = launch_dependent(copy_refs_kernel, ctas, kRowThreads, 0, stream, 1, a);
         if (e != cudaSuccess) return e;
     }
-    if (a.rows == 0 || a.stride == 0) return cudaSuccess;
+    if (a.rows == 0) return cudaSuccess;              // (rows without entries have their counts looked at)
     const int pieces = pieces_of(a.stride, kRowPiece);
     const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(a.rows) * pieces, static_cast<int64_t>(num_sms) * 64);
     return launch_dependent(free_kernel, ctas, kRowThreads, 0, stream, 1, a, pieces);
