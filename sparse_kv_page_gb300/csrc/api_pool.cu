@@ -222,8 +222,10 @@ int locks_copy_pages(const locks_planes_t* planes, const int32_t* src_pages, con
         a.page_bytes[i] = bytes;
         a.num_planes += 1;
     }
-    if (max_pairs == 0 || a.num_planes == 0) return LOCKS_OK;
-    if (!src_pages || !dst_pages || !words({src_pages, dst_pages, n_pairs})) return LOCKS_ERR_INVALID_ARG;
+    const bool nothing = max_pairs == 0 || a.num_planes == 0;
+    if (nothing && !n_pairs) return LOCKS_OK;
+    if (!nothing && (!src_pages || !dst_pages)) return LOCKS_ERR_INVALID_ARG;
+    if (!words({src_pages, dst_pages, n_pairs})) return LOCKS_ERR_INVALID_ARG;
     const int sms = locks::current_sms();
     if (sms <= 0) return LOCKS_ERR_CUDA;
     a.src = src_pages;

@@ -933,9 +933,10 @@ cudaError_t launch_copy_pages(const CopyArgs& a, int num_sms, cudaStream_t strea
         pieces += (a.page_bytes[i] + kCopyBytes - 1) / kCopyBytes;
         bytes += a.page_bytes[i];
     }
-    if (pieces == 0) return cudaSuccess;              // pages of no bytes
-    const bool large = bytes / pieces >= kCopyBytes / 2 && pieces * a.max_pairs >= 2048;
-    const int64_t ctas = std::min<int64_t>(pieces * a.max_pairs, static_cast<int64_t>(num_sms) * (large ? 64 : 4));
+    const int64_t items = pieces * a.max_pairs;
+    if (items == 0 && !a.n_pairs) return cudaSuccess; // (a count is looked at all the same)
+    const bool large = items >= 2048 && bytes / pieces >= kCopyBytes / 2;
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(items, static_cast<int64_t>(num_sms) * (large ? 64 : 4)));
     return launch_dependent(copy_kernel, ctas, kCopyThreads, 0, stream, 1, a);
 }
 
