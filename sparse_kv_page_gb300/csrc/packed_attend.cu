@@ -12,7 +12,7 @@
 //    are SMs, whatever the lengths of the rows. A CTA goes through its piece two rows at a time, so
 //    that where rows are long its warps meet once, at the end. A row that goes past a CTA is joined
 //    by a second kernel from partials in the workspace. Sixteen sequences of up to 128K tokens take
-//    363 us, 94% of the copy rate; two of 1M with 2 kv heads of 16 queries 193 us, 46%: there a
+//    357 us, 96% of the copy rate; two of 1M with 2 kv heads of 16 queries 196 us, 45%: there a
 //    page takes a warp 50 products and 451 instructions (301 for 4 queries), at three warps a
 //    scheduler.
 //
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
         part[0].steps = static_cast<int>(min(end - pos, static_cast<int64_t>(part[0].len.steps() - part[0].off)));
         int parts = 1;
         if (pos + part[0].steps < end) {
-            part[1] = line.next(part[0]);
+            part[1] = line.next(part[0], pos + part[0].steps);
             part[1].steps = static_cast<int>(min(end - pos - part[0].steps, static_cast<int64_t>(part[1].len.steps())));
             parts = 2;
         }
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(Shape<kKind>::kThreads, 1) line_kernel(const _
             pos += p.steps;
         }
         if (pos >= end) break;
-        part[0] = line.next(part[parts - 1]);
+        part[0] = line.next(part[parts - 1], pos);
         __syncthreads();                              // the slots and sums are read
     }
 }
@@ -1034,10 +1034,11 @@ int resident_rows(int n, int num_sms, size_t smem) {
 // CTAs a row of the short form, or 0 for the line: what takes least by a fit to both (us). The short form
 // goes in waves of as many clusters as fit at once, `wave` each and 2 for a cluster's join, and `page` for
 // each page of a warp; the line takes `line`, `row` for each row of a CTA, and `page` with all pages spread
-// over all SMs' warps. Measured (line / 1 / 2 / 4 / 8 CTAs, us), 8 kv heads of 4 queries: 1 sequence of 128
-// pages 14.8 / 13.1 / 11.3 / 9.4 / 9.4, of 1024 17.1 / 60.6 / 35.7 / 22.3 / 15.3; 8 of 128 17.0 / 13.5 / 11.7
-// / 18.5 / 40.4, 96 of 128 84.2 / 82.5; 2 kv heads of 16: 1 of 128 17.1 / 21.7 / 17.8 / 13.5 / 12.5, 8 of 1024
-// 30.9 / 109 / 61.4 / 36.4 / 44.0, 96 of 128 52.6 / 42.0 / 52.1 / 79.2.
+// over all SMs' warps. Measured (line / 1 / 2 / 4 / 8 CTAs, us, fp32 queries, no recent tokens), 8 kv heads of
+// 4 queries: 1 sequence of 128 pages 13.6 / 12.3 / 10.3 / 8.6 / 8.6, of 1024 17.0 / 59.0 / 34.4 / 21.1 / 14.1; 8 of
+// 128 17.6 / 12.5 / 10.7 / 17.0 / 40.0, 96 of 128 83.1 / 80.8. Of 8 queries, the same: 14.6 / 13.3 / 11.1 / 9.2 / 9.4,
+// 18.1 / 65.7 / 37.7 / 22.8 / 15.3; 19.1 / 13.5 / 11.5 / 18.2 / 43.2, 93.0 / 88.0. 2 kv heads of 16: 1 of 128 17.7 /
+// 21.5 / 16.8 / 13.8 / 11.3, 8 of 1024 33.5 / 112 / 62.7 / 36.4 / 44.4, 96 of 128 54.9 / 41.9 / 50.7 / 81.6.
 struct FormCost {
     double wave, page, line, row;
 };

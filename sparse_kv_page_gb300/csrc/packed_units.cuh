@@ -197,13 +197,14 @@ struct Line {
         p.steps = 0;
         return p;
     }
-    // The row behind p's with any steps (there is one as long as steps are left).
-    __device__ __forceinline__ Part next(const Part& p) const {
+    // The row behind p's with any steps, which begins at `pos` (there is one as long as steps are left). The
+    // very next one where that has some, else by the sums: two of 4096 sequences in use, at the ends, with the
+    // rows between them gone through one by one 8.6 ms.
+    __device__ __forceinline__ Part next(const Part& p, int64_t pos) const {
         Part r = p;
-        do {
-            if (++r.h == a.hkv) ++r.b, r.h = 0;
-            r.len = length(r.b, r.h);
-        } while (r.len.steps() == 0 && r.b < a.batch - 1);
+        if (++r.h == a.hkv) ++r.b, r.h = 0;
+        r.len = length(r.b, r.h);
+        if (r.len.steps() == 0) return at(pos);
         r.off = 0;
         return r;
     }

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_packed import DEV, check, i32, make_case
+import sparse_kv_page_gb300 as L
+from tests.test_gpu_packed import DEV, check, make_case
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,32 @@ def test_a_full_batch_of_short_selections():
     lists[7] = [[int(x) for x in rng.integers(0, pages[7], 128)] for _ in range(hkv)]
     lists[50][3] = [int(x) for x in rng.integers(0, pages[50], 128)]
     check(make_case(pages, [b % 21 for b in range(n)], 32, hkv, seed=6, selected=lists))
+
+
+@pytest.mark.parametrize("lists", [False, True])
+def test_unused_slots_are_not_gone_through_one_by_one(lists):
+    """4096 slots, the first and the last in use: 0.05 and 0.08 ms a call, against 0.014 ms for those two
+    alone; 8 ms and more where a CTA looks at every row between them."""
+    n, hkv, pages = 4096, 8, [101, 64]       # steps 0 .. 808 and 808 .. 1320 of 83 CTAs: one has both ends
+    packed = torch.zeros((sum(pages), hkv, L.LOCKS_PACKED_BYTES), dtype=torch.uint8, device=DEV)
+    table = torch.zeros((n, 512), dtype=torch.int32, device=DEV)
+    counts = torch.zeros(n, dtype=torch.int32, device=DEV)
+    for b, first, k in ((0, 0, pages[0]), (n - 1, pages[0], pages[1])):
+        table[b, :k] = torch.arange(first, first + k, device=DEV)
+        counts[b] = k
+    dims = L.make_dims(n, 4 * hkv, hkv, 512, 1)
+    ws = L.alloc_packed_workspace(dims, DEV)
+    q, out = torch.ones((n, 4 * hkv, 128), device=DEV), torch.ones((n, 4 * hkv, 128), dtype=torch.bfloat16, device=DEV)
+    kw = {}
+    if lists:
+        kw = dict(selected=torch.arange(512, dtype=torch.int32, device=DEV).expand(n, hkv, 512).contiguous(),
+                  n_selected=counts[:, None].expand(n, hkv).contiguous())
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for i in range(7):
+        if i == 2:
+            start.record()
+        L.locks_packed_attention(dims, q, packed, table, counts, out, ws, **kw)
+    end.record()
+    torch.cuda.synchronize()
+    assert L.locks_get_device_status(ws) == 0 and float(out.abs().max()) == 0
+    assert start.elapsed_time(end) / 5 < 1
