@@ -47,7 +47,8 @@
  * Reference counts
  * ----------------
  *   refs  int32 [pages], 16-byte aligned: how many holders (rows of tables and whoever else)
- *         a page of a pool has. A page with refs <= 0 is free; there is no list of free pages.
+ *         a page of a pool has, from -2^30 to 2^30. A page with refs <= 0 is free; there is no list
+ *         of free pages.
  * A sequence of n tokens holds the first ceil(n / 16) pages of its row. Its full pages may be
  * shared with other rows, a page that is not full never is. The calls below keep it so.
  * Pages are always taken in ascending order of their ids, so that results repeat exactly.

@@ -60,8 +60,8 @@ __device__ __forceinline__ void store4(int32_t* refs, int at, int last, const in
     if (at + 1 < last) refs[at + 1] = r.y;
     if (at + 2 < last) refs[at + 2] = r.z;
 }
-// Bit k: page at + k is free / used (neither past the end, whose counts are INT32_MIN; a count
-// that a caller let fall to that value is as good as any below 0 and reads as not free).
+// Bit k: page at + k is free / used (neither past the end, whose counts are INT32_MIN, below those a
+// caller may have).
 __device__ __forceinline__ unsigned free4(const int4& r) {
     const auto is = [](int x) { return x <= 0 && x != INT32_MIN; };
     return (is(r.x) ? 1u : 0u) | (is(r.y) ? 2u : 0u) | (is(r.z) ? 4u : 0u) | (is(r.w) ? 8u : 0u);
