@@ -5,7 +5,7 @@
 // written 16 bytes a lane, two tokens to an instruction; the codes go through a staging area in
 // shared memory, because the order of the attention's fragments spreads a lane's eight dims over
 // four or eight words. Packing takes a warp 800 instructions for 64 values a lane, with most of the
-// arithmetic on two values at once, and is bounded by them (65% of the issue slots): 4096 pages of 8 kv heads
+// arithmetic on two values at once, and is bounded by them (64% of the issue slots): 4096 pages of 8 kv heads
 // in 68 us (5.1 TB/s of both sides; 73 without the next values on their way meanwhile). Unpacking
 // them takes 55 - 57 us, as fast as HBM copies.
 #include <algorithm>

@@ -8,7 +8,7 @@
 // both. A call is short, a few MB at most, so what bounds it are the launches and the loads that wait
 // for one another; each launch starts while the one before it runs. Measured: freeing pages of 3
 // sequences and taking some for 29 others in a pool of 16K pages 7.9 us; of 48 x 8192 pages in a pool
-// of 1M 18.3; forking 2 x 64 rows of 8188 pages and copying the last ones 13.1; compacting a pool of 2048
+// of 1M 18.3; forking 2 x 64 rows of 8188 pages and copying the last ones 13.8; compacting a pool of 2048
 // pages, with the copies, 8.6.
 #include <algorithm>
 
