@@ -26,8 +26,8 @@
 // range. A token's scales multiply the group's sums (keys) or the weights (values); zeros enter
 // through a product of their own with the queries' sums (keys) and through a sum per group
 // (values). Where values' scales are so far apart that one power of two does not bring them all
-// into fp16's range, what fp16 loses of the weights has a product of its own, on bf16 (the same
-// fields are subnormals of 2^-133 there).
+// into fp16's range, the weights enter in two bf16 parts (the same fields are subnormals of 2^-133
+// there).
 #include <algorithm>
 #include <atomic>
 
@@ -385,7 +385,11 @@ struct Running {
             for (int i = 0; i < 2; ++i) t[p][i] = *reinterpret_cast<const uint2*>(units[p] + kUnitVScales + 8 * (gid + 8 * i));
         const uint32_t most = bf16x2_max(bf16x2_max(t[0][0].x, t[0][1].x), bf16x2_max(t[1][0].x, t[1][1].x));
         const uint32_t least = bf16x2_min(bf16x2_min(t[0][0].x, t[0][1].x), bf16x2_min(t[1][0].x, t[1][1].x));
-        weigh<2>(s, most, least, [&] { add_rest(units, s, t); });
+        weigh<2>(s, most, least, [&] {
+            add_wide(units, s, t);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) t[p][0].x = t[p][1].x = 0u;      // nothing is left for the products below
+        });
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             float x[kBlocks][4][2];                   // weights times scales: [token, column][group]
@@ -431,11 +435,12 @@ struct Running {
         const uint32_t up = w >> 8;
         c[0] = w & 0x000f000fu, c[1] = w & 0x00f000f0u, c[2] = up & 0x000f000fu, c[3] = up & 0x00f000f0u;
     }
-    // The products of two pages' values with what the weights times scales lose as fp16 (all of it where
-    // they are too small for it), in two bf16 parts. (Measured: two bf16 parts of all weights in fp16's
-    // place, 16 x 128K tokens 375 us instead of 363, 2 x 1M with 16 queries 225 instead of 193; a branch
-    // of the whole turn 371 and 200.)
-    __device__ __forceinline__ void add_rest(const uint8_t* const (&units)[2], const float (&s)[2][kBlocks][4],
+    // The products of two pages' values, with weights times scales in two bf16 parts. (All of the weights, not
+    // what fp16 loses of them: a product with an fp16 subnormal cuts off the sum that it is added to at a
+    // fixed place, and left small groups' sums 5 to 8 bits.) (Measured: all pages so,
+    // 16 x 128K tokens 375 us instead of 363, 2 x 1M with 16 queries 225 instead of 193; a branch of the whole
+    // turn 371 and 200.)
+    __device__ __forceinline__ void add_wide(const uint8_t* const (&units)[2], const float (&s)[2][kBlocks][4],
                                              const uint2 (&t)[2][2]) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -453,8 +458,8 @@ struct Running {
                         parts_of(add2(two(s[p][n][2 * i], s[p][n][2 * i + 1]), base(n)), x, y);
                         const float scale = g ? high_of(t[p][i].x) : low_of(t[p][i].x);
                         x = fast_exp2(x) * scale, y = fast_exp2(y) * scale;
-                        const float2 held = f16x2_of(pack_f16x2(x, y));
-                        split((x - held.x) * kWide, (y - held.y) * kWide, hi[n][i], lo[n][i]);
+                        pw[n][g] = add2(pw[n][g], two(x, y));
+                        split(x * kWide, y * kWide, hi[n][i], lo[n][i]);
                         hi[n][i] = transposed(hi[n][i]);
                         lo[n][i] = transposed(lo[n][i]);
                     }

@@ -20,8 +20,8 @@ constexpr float kSlack = 8.f;                         // log2 that a score may p
 // the output has 8). All weights carry a factor 2^lift that brings the largest scale so far to
 // 2^5..2^6, and is set anew when a scale times it passes 2^7: with kSlack they stay below 2^15.
 // fp16 ends at 2^-25, which is 2^-21 of a weight of 1 where a scale times the factor is 2^-4. For a
-// pair of pages with a scale below that (or below 0) what fp16 loses is added in two bf16 parts, 16
-// bits whatever the scale: they carry kWide, as codes are 2^-133 in bf16.
+// pair of pages with a scale below that (or below 0) weights enter in two bf16 parts, 16 bits
+// whatever the scale: they carry kWide, as codes are 2^-133 in bf16.
 // Scales below 2^kScaleLeast count as that large, for the zeros, of up to 2^50, take the factor too:
 // 2^(54 + kSlack + 50) and the sums of it are numbers.
 constexpr int kScaleTop = 5, kScaleLimit = 7, kScaleLow = -4, kScaleLeast = -49;

@@ -119,3 +119,21 @@ def test_scales_below_zero(hq, hkv, pages):
             x[:, :, ::3] *= 2.0 ** 12                # past fp16 with the sum's slack
         put(x)
     check(c)
+
+
+@pytest.mark.parametrize("hq,hkv,pages", [(4, 1, 30000), (8, 1, 30000), (16, 1, 30000), (16, 1, 4000)])
+def test_long_rows_of_small_groups(hq, hkv, pages):
+    """A group's scales and zeros times 2^-30 are its output times 2^-30, also where a long row's output is far
+    smaller than its values. (Both outputs are off by 2^-8 of themselves for their rounding, by 2^-10 at most
+    for everything ahead of it.)"""
+    c = make_case([pages], [0], hq, hkv, seed=35, steep=0.2)
+    run(c)
+    first = f64(c["out"])
+    x, put = value_fields(c)
+    x[..., 1] *= 2.0 ** -30
+    put(x)
+    run(c)
+    second = f64(c["out"])
+    for dims, size in ((slice(0, 64), 1.0), (slice(64, 128), 2.0 ** 30)):
+        a, b = first[..., dims], size * second[..., dims]
+        assert np.linalg.norm(a - b) <= (2.0 ** -7 + 2.0 ** -9) * np.linalg.norm(a)
