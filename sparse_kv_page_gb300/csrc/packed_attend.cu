@@ -12,8 +12,8 @@
 //    are SMs, whatever the lengths of the rows. A CTA goes through its piece two rows at a time, so
 //    that where rows are long its warps meet once, at the end. A row that goes past a CTA is joined
 //    by a second kernel from partials in the workspace. Sixteen sequences of up to 128K tokens take
-//    356 us, 96% of the copy rate; two of 1M with 2 kv heads of 16 queries 196 us, 45%: there a
-//    page takes a warp 50 products and 452 instructions (299 for 4 queries), at three warps a
+//    360 us, 95% of the copy rate; two of 1M with 2 kv heads of 16 queries 196 us, 45%: there a
+//    page takes a warp 50 products and 454 instructions (299 for 4 queries), at three warps a
 //    scheduler.
 //
 // The products are formed on mma.sync with the queries as columns, S^T = K Q^T and
