@@ -38,9 +38,10 @@
  *   0     codes of the keys, 4 bits each      1024  codes of the values
  *   2048  for token t: bf16 scales of its key's 4 groups of 32 dims, then their zeros
  *   2304  for token t: bf16 scales of its value's 2 groups of 64 dims, then their zeros
- * value = zero + scale * code, code 0..15; scales of either sign. Codes lie in the order in which the attention's
- * tensor-core fragments read them. That of token t and dim d lies in the four bits from bit
- * b of the 32-bit word at byte 512 * (w / 4) + 16 * l + 4 * (w % 4) of its 1024, w = d / 16:
+ * value = zero + scale * code, code 0..15; scales may be of either sign. Codes lie in the order
+ * in which the attention's tensor-core fragments read them. That of token t and dim d lies in the
+ * four bits from bit b of the 32-bit word at byte 512 * (w / 4) + 16 * l + 4 * (w % 4) of its 1024,
+ * w = d / 16:
  *   keys    l = 4 * (t % 8) + d % 8 / 2,  b = 16 * (d % 2) + 4 * (d / 8 % 2) + 8 * (t / 8)
  *   values  l = 4 * (d % 8) + t % 8 / 2,  b = 16 * (t % 2) + 4 * (d / 8 % 2) + 8 * (t / 8)
  *
@@ -77,9 +78,9 @@ enum {
  *   code  = round((x - zero) / scale), ties to even; 0 where scale is 0
  * with the quotients rounded as fp32 division rounds them. A group with a NaN or an infinity
  * (or whose range overflows fp32) has a NaN for its scale and codes 0, and unpacks to no finite
- * value; other groups are not touched by it. dst_pages NULL: the same ids as
- * src_pages. A negative id in either list skips the entry; one out of range does too and
- * records LOCKS_ERR_BAD_INDEX. No packed page may be named twice in dst_pages.
+ * value; other groups are not touched by it. dst_pages NULL: the same ids as src_pages. A negative
+ * id in either list skips the entry; one out of range does too and records LOCKS_ERR_BAD_INDEX. No
+ * packed page may be named twice in dst_pages.
  * workspace: optional, 256 bytes (status only). One launch.
  */
 LOCKS_API int locks_pack_pages(const locks_dims_t* dims, const uint16_t* k_cache, const uint16_t* v_cache,

@@ -202,7 +202,7 @@ struct Running {
     Two pw[kBlocks][2];                               // [group], of both columns: of weights times scales, as the
                                                       // products take them, since the last centre()
     float lift;                                       // log2 of the weights' factor
-    uint32_t limit;                                   // the largest scale that it is good for, as two bf16s; 0: none yet
+    uint32_t limit;                                   // the largest scale that it is good for, as two bf16s
 
     __device__ __forceinline__ void clear(const Control<kKind>& ctl, int which) {
         const int tig = threadIdx.x & 3;
@@ -215,8 +215,8 @@ struct Running {
             unit[n] = two(ctl.unit[which][n * 8 + 2 * tig], ctl.unit[which][n * 8 + 2 * tig + 1]);
             l[n] = two(0.f, 0.f);
         }
-        lift = 0.f;
-        limit = 0u;
+        lift = 0.f;                                   // until a scale is not 0: limit 2^-116, low 0
+        limit = kLimits;
     }
 
     // Scores (tokens gid, gid + 8 of kPages pages) to weights. The maximum moves only when a score
@@ -290,8 +290,9 @@ struct Running {
             }
         }
     }
-    // The least scale that the factor is good for (where there is no factor yet, a number below all scales).
-    __device__ __forceinline__ uint32_t low() const { return limit - static_cast<uint32_t>(kScaleLimit - kScaleLow) * 0x00800080u; }
+    // The least scale that the factor is good for.
+    static constexpr uint32_t kLimits = static_cast<uint32_t>(kScaleLimit - kScaleLow) * 0x00800080u;
+    __device__ __forceinline__ uint32_t low() const { return limit - kLimits; }
     // What turns the scores of block n into log2 of weights.
     __device__ __forceinline__ Two base(int n) const {
         return two(m[n][0] == -INFINITY ? lift : lift - m[n][0], m[n][1] == -INFINITY ? lift : lift - m[n][1]);
@@ -435,11 +436,11 @@ struct Running {
         const uint32_t up = w >> 8;
         c[0] = w & 0x000f000fu, c[1] = w & 0x00f000f0u, c[2] = up & 0x000f000fu, c[3] = up & 0x00f000f0u;
     }
-    // The products of two pages' values, with weights times scales in two bf16 parts. (All of the weights, not
-    // what fp16 loses of them: a product with an fp16 subnormal cuts off the sum that it is added to at a
-    // fixed place, and left small groups' sums 5 to 8 bits.) (Measured: all pages so,
-    // 16 x 128K tokens 375 us instead of 363, 2 x 1M with 16 queries 225 instead of 193; a branch of the whole
-    // turn 371 and 200.)
+    // The products of two pages' values, with weights times scales in two bf16 parts: all of the weights, not
+    // what fp16 loses of them, as a product with an fp16 subnormal cuts off the sum that it is added to at a
+    // fixed place, which left small groups' sums 5 to 8 bits. (Measured, all pages by two parts: 16 x 128K
+    // tokens 375 us instead of 363, 2 x 1M with 16 queries 225 instead of 193; a branch of the whole turn 371
+    // and 200.)
     __device__ __forceinline__ void add_wide(const uint8_t* const (&units)[2], const float (&s)[2][kBlocks][4],
                                              const uint2 (&t)[2][2]) {
         const int lane = threadIdx.x & 31;

@@ -137,3 +137,20 @@ def test_long_rows_of_small_groups(hq, hkv, pages):
     for dims, size in ((slice(0, 64), 1.0), (slice(64, 128), 2.0 ** 30)):
         a, b = first[..., dims], size * second[..., dims]
         assert np.linalg.norm(a - b) <= (2.0 ** -7 + 2.0 ** -9) * np.linalg.norm(a)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** -30])
+def test_scales_below_zero_behind_flat_groups(hq, hkv, size):
+    """Four pages of five have scales 0, so that warps meet one below 0 before any above."""
+    n = 9000
+    c = make_case([n], [0], hq, hkv, seed=36)
+    x, put = value_fields(c)
+    x *= size
+    x[..., 1, :] += 15 * x[..., 0, :]
+    x[..., 0, :] *= -1
+    flat = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    flat[c["table"][0].long()[4::5]] = False
+    x[flat, :, :, 0] = 0
+    put(x)
+    check(c)
